@@ -31,6 +31,12 @@ __all__ = [
     "ozk_int4int8gemm_fp4awe", "ozk_int4int8gemm_fp4awe_workspace_size",
     "ozk_dgemm_workspace_size", "ozk_dgemv_workspace_size",
     "ozk_int8gemm_fp4limb_workspace_size", "ozk_deconstruct_workspace_size",
+    "OZK_ACT_NONE", "OZK_ACT_RELU", "OZK_ACT_GELU", "OZK_ACT_GELU_TANH", "OZK_ACT_SILU",
+    "OZK_F64", "OZK_F32", "OZK_F16", "OZK_BF16",
+    "ozk_dgemm_epilogue", "ozk_dgemm_epilogue_grad", "ozk_dgemm_epilogue_grad_workspace_size",
+    "ozk_int8linear", "ozk_int8linear_workspace_size",
+    "ozk_int8quant_rows", "ozk_layernorm", "ozk_layernorm_backward",
+    "ozk_layernorm_backward_workspace_size",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libozk.so")
@@ -38,6 +44,7 @@ OZK_PLANE_K = 64
 OZK_NOALLOC_SCRATCH_BYTES = 64 << 20   # scratch array of ozk_dgemv_noalloc, per GPU
 
 _i64 = ctypes.c_int64
+_f64 = ctypes.c_double
 _i32 = ctypes.c_int32
 _int = ctypes.c_int
 _ptr = ctypes.c_void_p
@@ -95,12 +102,44 @@ _SIGNATURES = {
     "ozk_int4int8gemm_fp4awe_workspace_size": (_int, [_i64, _i64, _i64, _ptr]),
     "ozk_int4int8gemm_fp4awe": (_int, [_i64, _i64, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr,
                                        _size, _ptr]),
+    "ozk_dgemm_epilogue": (_int, [_i64, _i64, _i64, _ptr, _i64, _ptr, _i64, _ptr, _int, _ptr,
+                                  _i64, _ptr, _i64, _ptr, _i64, _int, _int, _ptr, _size, _ptr]),
+    "ozk_dgemm_epilogue_grad_workspace_size": (_int, [_i64, _i64, _i64, _int, _ptr]),
+    "ozk_dgemm_epilogue_grad": (_int, [_i64, _i64, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr,
+                                       _i64, _int, _ptr, _i64, _ptr, _i64, _ptr, _int, _int, _ptr,
+                                       _size, _ptr]),
+    "ozk_int8linear_workspace_size": (_int, [_i64, _i64, _i64, _ptr]),
+    "ozk_int8linear": (_int, [_i64, _i64, _i64, _ptr, _i64, _ptr, _ptr, _i64, _ptr, _ptr, _int,
+                              _ptr, _i64, _int, _ptr, _i64, _ptr, _size, _ptr]),
+    "ozk_int8quant_rows": (_int, [_i64, _i64, _int, _ptr, _i64, _int, _ptr, _ptr, _f64, _ptr,
+                                  _i64, _ptr, _ptr]),
+    "ozk_layernorm": (_int, [_i64, _i64, _int, _ptr, _i64, _ptr, _ptr, _f64, _ptr, _i64, _ptr,
+                             _ptr, _ptr]),
+    "ozk_layernorm_backward_workspace_size": (_int, [_i64, _i64, _int, _ptr]),
+    "ozk_layernorm_backward": (_int, [_i64, _i64, _int, _ptr, _i64, _ptr, _i64, _ptr, _ptr, _ptr,
+                                      _ptr, _i64, _ptr, _ptr, _ptr, _size, _ptr]),
 }
 
 _LIB = None
 
 OZK_SCALING_MAX = 0   # per-line maximum (the default of every entry point)
 OZK_SCALING_NORM = 1  # per-line 2-norm (Cauchy-Schwarz)
+
+
+OZK_ACT_NONE, OZK_ACT_RELU, OZK_ACT_GELU, OZK_ACT_GELU_TANH, OZK_ACT_SILU = range(5)
+OZK_F64, OZK_F32, OZK_F16, OZK_BF16 = range(4)
+_TYPES = {torch.float64: OZK_F64, torch.float32: OZK_F32, torch.float16: OZK_F16,
+          torch.bfloat16: OZK_BF16}
+_ACTS = {"none": OZK_ACT_NONE, "relu": OZK_ACT_RELU, "gelu": OZK_ACT_GELU,
+         "gelu_tanh": OZK_ACT_GELU_TANH, "silu": OZK_ACT_SILU}
+
+
+def _act(act) -> int:
+    if isinstance(act, str):
+        if act not in _ACTS:
+            raise ValueError(f"unknown activation {act!r}")
+        return _ACTS[act]
+    return int(act)
 
 
 def _scaling(scaling) -> int:
@@ -606,3 +645,276 @@ def ozk_int4int8gemm_fp4awe(a: torch.Tensor, b: torch.Tensor, out: torch.Tensor 
           _dev_ptr(out), _ld(out), _dev_ptr(workspace), workspace.numel(),
           _stream(stream, out, workspace))
     return out
+
+
+# ------------------------------------------------------------ layers around the products
+def _check_rows(t: torch.Tensor, dtype, name: str):
+    """A matrix operand of the layer operators.  Rows that overlap (an expanded or unfolded
+    view) have no leading dimension the library takes."""
+    _check(t, dtype, name)
+    if t.shape[0] > 1 and t.shape[1] > 0 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}'s rows overlap")
+
+
+def _check_like(t: torch.Tensor | None, shape: tuple, dtype, name: str, device):
+    """An operand of the layer operators that may be absent: shape, dtype, device, strides."""
+    if t is None:
+        return
+    if len(shape) == 2:
+        _check_rows(t, dtype, name)
+    else:
+        _check(t, dtype, name, len(shape))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _check_workspace(t: torch.Tensor | None, device):
+    if t is None:
+        return
+    _check(t, torch.uint8, "workspace", 1)
+    if t.device != device:
+        raise ValueError(f"workspace is on {t.device}, expected {device}")
+
+
+class _On:
+    """The calls of a `with` block go to `device`: its current stream (or `stream`), its
+    context.  Switching costs a few microseconds and is left out on the current device."""
+
+    def __init__(self, device):
+        self._guard = (None if device.index == torch.cuda.current_device()
+                       else torch.cuda.device(device))
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def ozk_dgemm_epilogue_grad_workspace_size(m: int, n: int, k: int, r: int) -> int:
+    return _size_query("ozk_dgemm_epilogue_grad_workspace_size", m, n, k, r)
+
+
+def ozk_int8linear_workspace_size(m: int, n: int, k: int) -> int:
+    return _size_query("ozk_int8linear_workspace_size", m, n, k)
+
+
+def ozk_layernorm_backward_workspace_size(rows: int, cols: int, dtype) -> int:
+    return _size_query("ozk_layernorm_backward_workspace_size", rows, cols, _type(dtype))
+
+
+def _type(dtype) -> int:
+    if dtype not in _TYPES:
+        raise TypeError(f"unsupported element type {dtype}")
+    return _TYPES[dtype]
+
+
+def _ld_opt(t: torch.Tensor | None) -> int:
+    return 0 if t is None else _ld(t)
+
+
+def ozk_dgemm_epilogue(a: torch.Tensor, b: torch.Tensor, r: int,
+                       bias: torch.Tensor | None = None, act="none",
+                       residual: torch.Tensor | None = None, scaling="max",
+                       preact: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Emulated fp64 C = act(A B + bias) + residual ("none", "relu", "gelu", "gelu_tanh",
+    "silu" or OZK_ACT_*); preact (m x n) receives A B + bias for the gradient.  residual may
+    be out."""
+    _check_rows(a, torch.float64, "A")
+    _check(b, torch.float64, "B")
+    _check_like(b, (a.shape[1], b.shape[-1]), torch.float64, "B", a.device)
+    m, k = a.shape
+    n = b.shape[1]
+    _check_like(bias, (n,), torch.float64, "bias", a.device)
+    for t, name in ((residual, "residual"), (preact, "preact"), (out, "out")):
+        _check_like(t, (m, n), torch.float64, name, a.device)
+    _check_workspace(workspace, a.device)
+    with _On(a.device):
+        if out is None:
+            out = torch.empty((m, n), dtype=torch.float64, device=a.device)
+        if workspace is None:
+            workspace = _workspace(ozk_dgemm_workspace_size(m, n, k, r), a.device)
+        _call("ozk_dgemm_epilogue", m, n, k, _dev_ptr(a), _ld(a), _dev_ptr(b), _ld(b),
+              _dev_ptr(bias), _act(act), _dev_ptr(residual), _ld_opt(residual),
+              _dev_ptr(preact), _ld_opt(preact), _dev_ptr(out), _ld(out), r, _scaling(scaling),
+              _dev_ptr(workspace), workspace.numel(), _stream(stream, out, workspace))
+    return out
+
+
+def ozk_dgemm_epilogue_grad(dc: torch.Tensor, a: torch.Tensor, b: torch.Tensor, r: int,
+                            preact: torch.Tensor | None = None, act="none", scaling="max",
+                            need_da: bool = True, need_db: bool = True, need_dbias: bool = True,
+                            da: torch.Tensor | None = None, db: torch.Tensor | None = None,
+                            dbias: torch.Tensor | None = None,
+                            workspace: torch.Tensor | None = None, stream=None):
+    """(dA, dB, dbias) of ozk_dgemm_epilogue from the gradient of its output (the residual's
+    gradient is dc itself); None where not needed.  preact as the forward wrote it."""
+    act = _act(act)
+    _check_rows(dc, torch.float64, "dC")
+    _check(a, torch.float64, "A")
+    m, n = dc.shape
+    _check_like(a, (m, a.shape[-1]), torch.float64, "A", dc.device)
+    k = a.shape[1]
+    _check_like(b, (k, n), torch.float64, "B", dc.device)
+    if preact is None and act != OZK_ACT_NONE:
+        raise ValueError("preact is needed for an activation's gradient")
+    _check_like(preact, (m, n), torch.float64, "preact", dc.device)
+    _check_like(da, (m, k), torch.float64, "da", dc.device)
+    _check_like(db, (k, n), torch.float64, "db", dc.device)
+    _check_like(dbias, (n,), torch.float64, "dbias", dc.device)
+    _check_workspace(workspace, dc.device)
+    with _On(dc.device):
+        new = lambda *shape: torch.empty(shape, dtype=torch.float64, device=dc.device)
+        da = (new(m, k) if da is None else da) if need_da else None
+        db = (new(k, n) if db is None else db) if need_db else None
+        dbias = (new(n) if dbias is None else dbias) if need_dbias else None
+        if workspace is None:
+            workspace = _workspace(ozk_dgemm_epilogue_grad_workspace_size(m, n, k, r), dc.device)
+        _call("ozk_dgemm_epilogue_grad", m, n, k, _dev_ptr(dc), _ld(dc), _dev_ptr(a), _ld(a),
+              _dev_ptr(b), _ld(b), _dev_ptr(preact), _ld_opt(preact), act, _dev_ptr(da),
+              _ld_opt(da), _dev_ptr(db), _ld_opt(db), _dev_ptr(dbias), r, _scaling(scaling),
+              _dev_ptr(workspace), workspace.numel(), _stream(stream, da, db, dbias, workspace))
+    return da, db, dbias
+
+
+def ozk_int8linear(x: torch.Tensor, scale_x: torch.Tensor, w: torch.Tensor,
+                   scale_w: torch.Tensor, bias: torch.Tensor | None = None, act="none",
+                   residual: torch.Tensor | None = None, dtype=torch.bfloat16,
+                   out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """C = act(scale_x scale_w^T * (X W^T) + bias) + residual for int8 X (m x k) and W (n x k)
+    with fp32 row scales; C, bias and residual in `dtype` (float32, float16 or bfloat16; the
+    type of `out` where that is given).  residual may be out."""
+    if out is not None:
+        dtype = out.dtype
+    code = _type(dtype)
+    if code == OZK_F64:
+        raise TypeError("the int8 layer's output is float32, float16 or bfloat16")
+    _check_rows(x, torch.int8, "X")
+    _check(w, torch.int8, "W")
+    m, k = x.shape
+    _check_like(w, (w.shape[0], k), torch.int8, "W", x.device)
+    n = w.shape[0]
+    _check_like(scale_x, (m,), torch.float32, "scale_x", x.device)
+    _check_like(scale_w, (n,), torch.float32, "scale_w", x.device)
+    _check_like(bias, (n,), dtype, "bias", x.device)
+    _check_like(residual, (m, n), dtype, "residual", x.device)
+    _check_like(out, (m, n), dtype, "out", x.device)
+    _check_workspace(workspace, x.device)
+    with _On(x.device):
+        if out is None:
+            out = torch.empty((m, n), dtype=dtype, device=x.device)
+        ws_bytes = ozk_int8linear_workspace_size(m, n, k)
+        if workspace is None and ws_bytes > 0:
+            workspace = _workspace(ws_bytes, x.device)
+        _call("ozk_int8linear", m, n, k, _dev_ptr(x), _ld(x), _dev_ptr(scale_x), _dev_ptr(w),
+              _ld(w), _dev_ptr(scale_w), _dev_ptr(bias), _act(act), _dev_ptr(residual),
+              _ld_opt(residual), code, _dev_ptr(out), _ld(out), _dev_ptr(workspace),
+              0 if workspace is None else workspace.numel(), _stream(stream, out, workspace))
+    return out
+
+
+def _check_x(x) -> int:
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a CUDA/HIP tensor")
+    code = _type(x.dtype)
+    _check_rows(x, x.dtype, "x")
+    return code
+
+
+def _check_norm_weights(x, gamma, beta):
+    _check_like(gamma, (x.shape[1],), x.dtype, "gamma", x.device)
+    _check_like(beta, (x.shape[1],), x.dtype, "beta", x.device)
+
+
+def ozk_int8quant_rows(x: torch.Tensor, norm: bool = False, gamma: torch.Tensor | None = None,
+                       beta: torch.Tensor | None = None, eps: float = 1e-5,
+                       out: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+                       stream=None):
+    """(codes int8 [rows][cols], scale fp32 [rows]) of the rows of x, or with norm=True of
+    their layer norm: the left operand of ozk_int8linear."""
+    code = _check_x(x)
+    rows, cols = x.shape
+    _check_norm_weights(x, gamma, beta)
+    _check_like(out, (rows, cols), torch.int8, "out", x.device)
+    _check_like(scale, (rows,), torch.float32, "scale", x.device)
+    with _On(x.device):
+        if out is None:
+            out = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
+        if scale is None:
+            scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+        _call("ozk_int8quant_rows", rows, cols, code, _dev_ptr(x), _ld(x), 1 if norm else 0,
+              _dev_ptr(gamma), _dev_ptr(beta), float(eps), _dev_ptr(out), _ld(out),
+              _dev_ptr(scale), _stream(stream, out, scale))
+    return out, scale
+
+
+def _stats_type(dtype):
+    return torch.float64 if dtype == torch.float64 else torch.float32
+
+
+def ozk_layernorm(x: torch.Tensor, gamma: torch.Tensor | None = None,
+                  beta: torch.Tensor | None = None, eps: float = 1e-5, stats: bool = False,
+                  out: torch.Tensor | None = None, mean: torch.Tensor | None = None,
+                  rstd: torch.Tensor | None = None, stream=None):
+    """Layer norm of the rows of x; with stats=True (y, mean, rstd), the last two (fp32, fp64
+    for a float64 x) for ozk_layernorm_backward.  out may be x."""
+    code = _check_x(x)
+    rows, cols = x.shape
+    _check_norm_weights(x, gamma, beta)
+    _check_like(out, (rows, cols), x.dtype, "out", x.device)
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        _check_like(t, (rows,), _stats_type(x.dtype), name, x.device)
+    with _On(x.device):
+        if out is None:
+            out = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+        if stats:
+            new = lambda: torch.empty(rows, dtype=_stats_type(x.dtype), device=x.device)
+            mean = new() if mean is None else mean
+            rstd = new() if rstd is None else rstd
+        _call("ozk_layernorm", rows, cols, code, _dev_ptr(x), _ld(x), _dev_ptr(gamma),
+              _dev_ptr(beta), float(eps), _dev_ptr(out), _ld(out), _dev_ptr(mean),
+              _dev_ptr(rstd), _stream(stream, out, mean, rstd))
+    return (out, mean, rstd) if stats else out
+
+
+def ozk_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor | None,
+                           mean: torch.Tensor, rstd: torch.Tensor, need_dx: bool = True,
+                           need_weights: bool = True, dx: torch.Tensor | None = None,
+                           dgamma: torch.Tensor | None = None,
+                           dbeta: torch.Tensor | None = None,
+                           workspace: torch.Tensor | None = None, stream=None):
+    """(dx, dgamma, dbeta) of ozk_layernorm from the gradient of its output and the forward's
+    mean and rstd; None where not needed.  dx may be dy or x."""
+    code = _check_x(x)
+    rows, cols = x.shape
+    _check_like(dy, (rows, cols), x.dtype, "dy", x.device)
+    _check_like(gamma, (cols,), x.dtype, "gamma", x.device)
+    _check_like(mean, (rows,), _stats_type(x.dtype), "mean", x.device)
+    _check_like(rstd, (rows,), _stats_type(x.dtype), "rstd", x.device)
+    _check_like(dx, (rows, cols), x.dtype, "dx", x.device)
+    _check_like(dgamma, (cols,), x.dtype, "dgamma", x.device)
+    _check_like(dbeta, (cols,), x.dtype, "dbeta", x.device)
+    _check_workspace(workspace, x.device)
+    with _On(x.device):
+        new = lambda *shape: torch.empty(shape, dtype=x.dtype, device=x.device)
+        dx = (new(rows, cols) if dx is None else dx) if need_dx else None
+        if need_weights:
+            dgamma = new(cols) if dgamma is None else dgamma
+            dbeta = new(cols) if dbeta is None else dbeta
+            if workspace is None:
+                workspace = _workspace(
+                    ozk_layernorm_backward_workspace_size(rows, cols, x.dtype), x.device)
+        else:
+            dgamma = dbeta = None
+        _call("ozk_layernorm_backward", rows, cols, code, _dev_ptr(dy), _ld(dy), _dev_ptr(x),
+              _ld(x), _dev_ptr(gamma), _dev_ptr(mean), _dev_ptr(rstd), _dev_ptr(dx),
+              _ld_opt(dx), _dev_ptr(dgamma), _dev_ptr(dbeta), _dev_ptr(workspace),
+              0 if workspace is None else workspace.numel(),
+              _stream(stream, dx, dgamma, dbeta, workspace))
+    return dx, dgamma, dbeta

@@ -137,6 +137,35 @@ int deconstruct_operands(const double* A, int64_t m, int64_t k, int64_t lda, con
                          kp, n * kp, exps_b, scaling == OZK_SCALING_NORM, s);
 }
 
+// Everything of C = A B before the reconstruction: the residues of the r products (ld n,
+// plane stride m n) and the exponents, in the workspace.
+struct DgemmResidues {
+  const int8_t* residues;
+  const int32_t* exps_a;
+  const int32_t* exps_b;
+};
+int dgemm_residues(int64_t m, int64_t n, int64_t k, const double* A, int64_t lda,
+                   const double* B, int64_t ldb, int r, int scaling, int wa, int wb,
+                   const DgemmLayout& L, void* workspace, hipEvent_t gemm_start,
+                   hipEvent_t gemm_stop, hipStream_t s, DgemmResidues* out) {
+  Carver cv(workspace);
+  int8_t* planes_a = static_cast<int8_t*>(cv.take(L.planes_a));
+  int8_t* planes_b = static_cast<int8_t*>(cv.take(L.planes_b));
+  int8_t* residues = static_cast<int8_t*>(cv.take(L.residues));
+  int32_t* exps_a = static_cast<int32_t*>(cv.take(L.exps_a));
+  int32_t* exps_b = static_cast<int32_t*>(cv.take(L.exps_b));
+  void* scr_a = cv.take(L.scr_a);
+  void* scr_b = cv.take(L.scr_b);
+  const int64_t kp = L.kp;
+  int st;
+  if ((st = deconstruct_operands(A, m, k, lda, B, n, ldb, r, scaling, wa, wb, planes_a,
+                                 planes_b, kp, exps_a, exps_b, scr_a, scr_b, s)))
+    return st;
+  *out = {residues, exps_a, exps_b};
+  return launch_gemm_i8(m, n, kp, r, planes_a, m * kp, planes_b, n * kp, residues, n, m * n,
+                        kEpiResidues, s, gemm_start, gemm_stop);
+}
+
 }  // namespace
 
 extern "C" {
@@ -293,24 +322,13 @@ int ozk_dgemm_ex_timed(int64_t m, int64_t n, int64_t k, const double* A, int64_t
   if (!workspace || workspace_bytes < L.total()) return OZK_EWORKSPACE;
   if (!aligned(workspace, 256)) return OZK_EINVAL;
   if ((size_t)m * n > (size_t)0x7fffffffffffull) return OZK_EUNSUPPORTED;
-  Carver cv(workspace);
-  int8_t* planes_a = static_cast<int8_t*>(cv.take(L.planes_a));
-  int8_t* planes_b = static_cast<int8_t*>(cv.take(L.planes_b));
-  int8_t* residues = static_cast<int8_t*>(cv.take(L.residues));
-  int32_t* exps_a = static_cast<int32_t*>(cv.take(L.exps_a));
-  int32_t* exps_b = static_cast<int32_t*>(cv.take(L.exps_b));
-  void* scr_a = cv.take(L.scr_a);
-  void* scr_b = cv.take(L.scr_b);
   hipStream_t s = as_stream(stream);
-  const int64_t kp = L.kp;
-  if ((st = deconstruct_operands(A, m, k, lda, B, n, ldb, r, scaling, wa, wb, planes_a,
-                                 planes_b, kp, exps_a, exps_b, scr_a, scr_b, s)))
+  DgemmResidues D;
+  if ((st = dgemm_residues(m, n, k, A, lda, B, ldb, r, scaling, wa, wb, L, workspace,
+                           static_cast<hipEvent_t>(gemm_start),
+                           static_cast<hipEvent_t>(gemm_stop), s, &D)))
     return st;
-  if ((st = launch_gemm_i8(m, n, kp, r, planes_a, m * kp, planes_b, n * kp, residues, n, m * n,
-                           kEpiResidues, s, static_cast<hipEvent_t>(gemm_start),
-                           static_cast<hipEvent_t>(gemm_stop))))
-    return st;
-  return launch_crt(m, n, r, residues, 0, n, m * n, exps_a, exps_b, C, ldc, s);
+  return launch_crt(m, n, r, D.residues, 0, n, m * n, D.exps_a, D.exps_b, C, ldc, s);
 }
 
 int ozk_dgemm(int64_t m, int64_t n, int64_t k, const double* A, int64_t lda, const double* B,
@@ -692,6 +710,293 @@ int ozk_spmv_csr(int64_t rows, int64_t cols, int64_t nnz, const int32_t* row_ptr
     return st;
   // y as a 1 x rows matrix: output j scaled by x's exponent plus row j's
   return launch_crt(1, rows, r, res, 0, rows, rows, x_exp, row_exps, y, rows, s);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- emulated DGEMM: epilogue
+namespace {
+
+bool act_ok(int act) { return act >= OZK_ACT_NONE && act <= OZK_ACT_SILU; }
+
+// One product of the gradient: `left` (lines along left_axis) times `right`, inner
+// dimension K, rows x cols outputs.
+struct GradProduct {
+  int64_t rows, cols, K;
+  const double* left;
+  int64_t left_rows, left_cols, ldl;
+  int left_axis;
+  const double* right;
+  int64_t right_rows, right_cols, ldr;
+  int right_axis;
+};
+
+struct GradLayout {
+  int64_t kp;
+  size_t planes_l, planes_r, residues, exps_l, exps_r, scratch;
+  size_t total() const {
+    return align256(planes_l) + align256(planes_r) + align256(residues) + align256(exps_l) +
+           align256(exps_r) + align256(scratch);
+  }
+};
+
+GradLayout grad_layout(const GradProduct& P, int r) {
+  GradLayout L;
+  L.kp = round_up(P.K, 2 * kPlaneK);
+  L.planes_l = (size_t)r * P.rows * L.kp;
+  L.planes_r = (size_t)r * P.cols * L.kp;
+  L.residues = (size_t)r * P.rows * P.cols;
+  L.exps_l = (size_t)P.rows * 4;
+  L.exps_r = (size_t)P.cols * 4;
+  const size_t sl = deconstruct_scratch(P.left_rows, P.left_cols, P.left_axis);
+  const size_t sr = deconstruct_scratch(P.right_rows, P.right_cols, P.right_axis);
+  L.scratch = sl > sr ? sl : sr;   // one operand after the other
+  return L;
+}
+
+// dA = G B^T: rows of G against rows of B; dB = A^T G: columns of A against columns of G.
+GradProduct grad_a(int64_t m, int64_t n, int64_t k, const double* g, int64_t ldg,
+                   const double* B, int64_t ldb) {
+  return {m, k, n, g, m, n, ldg, 0, B, k, n, ldb, 0};
+}
+GradProduct grad_b(int64_t m, int64_t n, int64_t k, const double* A, int64_t lda,
+                   const double* g, int64_t ldg) {
+  return {k, n, m, A, m, k, lda, 1, g, m, n, ldg, 1};
+}
+
+int grad_product(const GradProduct& P, int r, int scaling, double* out, int64_t ldo,
+                 void* workspace, hipStream_t s) {
+  int wa = 0, wb = 0, st;
+  if ((st = scaling_widths(scaling, r, P.K, &wa, &wb))) return st;
+  const GradLayout L = grad_layout(P, r);
+  Carver cv(workspace);
+  int8_t* pl = static_cast<int8_t*>(cv.take(L.planes_l));
+  int8_t* pr = static_cast<int8_t*>(cv.take(L.planes_r));
+  int8_t* res = static_cast<int8_t*>(cv.take(L.residues));
+  int32_t* el = static_cast<int32_t*>(cv.take(L.exps_l));
+  int32_t* er = static_cast<int32_t*>(cv.take(L.exps_r));
+  void* scratch = cv.take(L.scratch);
+  if ((st = deconstruct_impl(P.left, P.left_rows, P.left_cols, P.ldl, P.left_axis, r, scaling, wa,
+                             pl, L.kp, P.rows * L.kp, el, scratch, s)))
+    return st;
+  if ((st = deconstruct_impl(P.right, P.right_rows, P.right_cols, P.ldr, P.right_axis, r,
+                             scaling, wb, pr, L.kp, P.cols * L.kp, er, scratch, s)))
+    return st;
+  if ((st = launch_gemm_i8(P.rows, P.cols, L.kp, r, pl, P.rows * L.kp, pr, P.cols * L.kp, res,
+                           P.cols, P.rows * P.cols, kEpiResidues, s)))
+    return st;
+  return launch_crt(P.rows, P.cols, r, res, 0, P.cols, P.rows * P.cols, el, er, out, ldo, s);
+}
+
+// Workspace of the gradient: G, the chunks' sums of its columns, and the larger of the two
+// products' scratch.
+struct EpilogueGradLayout {
+  size_t g, part, products;
+  size_t total() const { return align256(g) + align256(part) + align256(products); }
+};
+
+EpilogueGradLayout epilogue_grad_layout(int64_t m, int64_t n, int64_t k, int r) {
+  EpilogueGradLayout L;
+  L.g = (size_t)m * n * 8;
+  L.part = (size_t)act_grad_chunks(m > 0 ? m : 1) * n * 8;
+  const size_t a = grad_layout(grad_a(m, n, k, nullptr, n, nullptr, n), r).total();
+  const size_t b = grad_layout(grad_b(m, n, k, nullptr, k, nullptr, n), r).total();
+  L.products = a > b ? a : b;
+  return L;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ozk_dgemm_epilogue(int64_t m, int64_t n, int64_t k, const double* A, int64_t lda,
+                       const double* B, int64_t ldb, const double* bias, int act,
+                       const double* residual, int64_t ldr, double* Z, int64_t ldz, double* C,
+                       int64_t ldc, int r, int scaling, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  if (check_r(r) != OZK_OK || !act_ok(act)) return OZK_EINVAL;
+  if (scaling != OZK_SCALING_MAX && scaling != OZK_SCALING_NORM) return OZK_EINVAL;
+  if (m < 0 || n < 0 || k < 1) return OZK_EINVAL;
+  if (k > OZK_MAX_K) return OZK_ERANGE;
+  const int64_t n1 = n > 0 ? n : 1;
+  if (lda < k || ldb < n1 || ldc < n1 || (residual && ldr < n1) || (Z && ldz < n1))
+    return OZK_EINVAL;
+  int wa = 0, wb = 0;
+  int st = scaling_widths(scaling, r, k, &wa, &wb);
+  if (st != OZK_OK) return st;
+  if (m == 0 || n == 0) return OZK_OK;
+  if (!A || !B || !C) return OZK_EINVAL;
+  const DgemmLayout L = dgemm_layout(m, n, k, r);
+  if (!workspace || workspace_bytes < L.total()) return OZK_EWORKSPACE;
+  if (!aligned(workspace, 256)) return OZK_EINVAL;
+  if ((size_t)m * n > (size_t)0x7fffffffffffull) return OZK_EUNSUPPORTED;
+  hipStream_t s = as_stream(stream);
+  DgemmResidues D;
+  if ((st = dgemm_residues(m, n, k, A, lda, B, ldb, r, scaling, wa, wb, L, workspace, nullptr,
+                           nullptr, s, &D)))
+    return st;
+  const DgemmEpilogue E{bias, residual, ldr, Z, ldz, act};
+  return launch_crt_epilogue(m, n, r, D.residues, n, m * n, D.exps_a, D.exps_b, E, C, ldc, s);
+}
+
+int ozk_dgemm_epilogue_grad_workspace_size(int64_t m, int64_t n, int64_t k, int r,
+                                           size_t* bytes) {
+  if (!bytes || m < 0 || n < 0 || k < 1 || check_r(r) != OZK_OK) return OZK_EINVAL;
+  if (m > OZK_MAX_K || n > OZK_MAX_K || k > OZK_MAX_K) return OZK_ERANGE;
+  *bytes = epilogue_grad_layout(m, n, k, r).total();
+  return OZK_OK;
+}
+
+int ozk_dgemm_epilogue_grad(int64_t m, int64_t n, int64_t k, const double* dC, int64_t lddc,
+                            const double* A, int64_t lda, const double* B, int64_t ldb,
+                            const double* Z, int64_t ldz, int act, double* dA, int64_t ldda,
+                            double* dB, int64_t lddb, double* dbias, int r, int scaling,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  if (check_r(r) != OZK_OK || !act_ok(act)) return OZK_EINVAL;
+  if (scaling != OZK_SCALING_MAX && scaling != OZK_SCALING_NORM) return OZK_EINVAL;
+  if (m < 0 || n < 0 || k < 1) return OZK_EINVAL;
+  if (m > OZK_MAX_K || n > OZK_MAX_K || k > OZK_MAX_K) return OZK_ERANGE;
+  const int64_t n1 = n > 0 ? n : 1;
+  if (lddc < n1 || (act != OZK_ACT_NONE && ldz < n1)) return OZK_EINVAL;
+  if ((dA && (ldda < k || ldb < n1)) || (dB && (lddb < n1 || lda < k))) return OZK_EINVAL;
+  int wa = 0, wb = 0, st;
+  if (m == 0 || n == 0) {   // sums of no terms
+    hipStream_t s = as_stream(stream);
+    if (m > 0 && dA && (st = launch_zero_rows(dA, m, k, ldda, s))) return st;
+    if (n > 0 && dB && (st = launch_zero_rows(dB, k, n, lddb, s))) return st;
+    if (n > 0 && dbias && (st = launch_zero_rows(dbias, 1, n, n, s))) return st;
+    return OZK_OK;
+  }
+  if (dA && (st = scaling_widths(scaling, r, n, &wa, &wb))) return st;
+  if (dB && (st = scaling_widths(scaling, r, m, &wa, &wb))) return st;
+  if (!dA && !dB && !dbias) return OZK_OK;
+  if (!dC || (act != OZK_ACT_NONE && !Z) || (dA && !B) || (dB && !A)) return OZK_EINVAL;
+  const EpilogueGradLayout L = epilogue_grad_layout(m, n, k, r);
+  if (!workspace || workspace_bytes < L.total()) return OZK_EWORKSPACE;
+  if (!aligned(workspace, 256)) return OZK_EINVAL;
+  Carver cv(workspace);
+  double* g = static_cast<double*>(cv.take(L.g));
+  double* part = static_cast<double*>(cv.take(L.part));
+  void* products = cv.take(L.products);
+  hipStream_t s = as_stream(stream);
+  // without an activation G is dC itself
+  const bool own_g = act != OZK_ACT_NONE && (dA || dB);
+  if ((own_g || dbias) &&
+      (st = launch_act_grad(m, n, dC, lddc, Z, ldz, act, own_g ? g : nullptr, part, dbias, s)))
+    return st;
+  const double* gp = own_g ? g : dC;
+  const int64_t ldg = own_g ? n : lddc;
+  if (dA && (st = grad_product(grad_a(m, n, k, gp, ldg, B, ldb), r, scaling, dA, ldda, products,
+                               s)))
+    return st;
+  if (dB && (st = grad_product(grad_b(m, n, k, A, lda, gp, ldg), r, scaling, dB, lddb, products,
+                               s)))
+    return st;
+  return OZK_OK;
+}
+
+// ---------------------------------------------------------------- int8 linear layer
+int ozk_int8linear_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
+  if (!bytes || m < 0 || n < 0 || k < 1) return OZK_EINVAL;
+  if (k > OZK_MAX_K) return OZK_ERANGE;
+  if (m > 0x7fffffffll || n > 0x7fffffffll) return OZK_EUNSUPPORTED;
+  *bytes = int8linear_workspace(m, n, k);
+  return OZK_OK;
+}
+
+int ozk_int8linear(int64_t m, int64_t n, int64_t k, const int8_t* X, int64_t ldx,
+                   const float* scale_x, const int8_t* W, int64_t ldw, const float* scale_w,
+                   const void* bias, int act, const void* residual, int64_t ldr, int type,
+                   void* C, int64_t ldc, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!act_ok(act) || (type != OZK_F32 && type != OZK_F16 && type != OZK_BF16))
+    return OZK_EINVAL;
+  if (m < 0 || n < 0 || k < 1) return OZK_EINVAL;
+  if (k > OZK_MAX_K) return OZK_ERANGE;
+  const int64_t n1 = n > 0 ? n : 1;
+  if (ldx < k || ldw < k || ldc < n1 || (residual && ldr < n1)) return OZK_EINVAL;
+  if (m == 0 || n == 0) return OZK_OK;
+  if (!X || !scale_x || !W || !scale_w || !C) return OZK_EINVAL;
+  const size_t e = type == OZK_F32 ? 4 : 2;
+  if (!aligned(scale_x, 4) || !aligned(scale_w, 4) || !aligned(bias, e) ||
+      !aligned(residual, e) || !aligned(C, e))
+    return OZK_EINVAL;
+  if (m > 0x7fffffffll || n > 0x7fffffffll) return OZK_EUNSUPPORTED;
+  const size_t need = int8linear_workspace(m, n, k);
+  if (need > workspace_bytes || (need > 0 && !workspace)) return OZK_EWORKSPACE;
+  if (need > 0 && !aligned(workspace, 256)) return OZK_EINVAL;
+  return launch_int8linear(m, n, k, X, ldx, scale_x, W, ldw, scale_w, bias, act, residual, ldr,
+                           type, C, ldc, workspace, as_stream(stream));
+}
+
+// ---------------------------------------------------------------- rows: codes, layer norm
+static int check_rows(int64_t rows, int64_t cols, int type) {
+  if (type < OZK_F64 || type > OZK_BF16 || rows < 0 || cols < 1) return OZK_EINVAL;
+  if (rows > 0x7fffffffll || cols > 0x7fffffffll) return OZK_EUNSUPPORTED;
+  return OZK_OK;
+}
+static size_t type_size(int type) { return type == OZK_F64 ? 8 : type == OZK_F32 ? 4 : 2; }
+
+int ozk_int8quant_rows(int64_t rows, int64_t cols, int type, const void* x, int64_t ldx, int norm,
+                       const void* gamma, const void* beta, double eps, int8_t* q, int64_t ldq,
+                       float* scale, void* stream) {
+  int st = check_rows(rows, cols, type);
+  if (st != OZK_OK) return st;
+  if ((norm != 0 && norm != 1) || ldx < cols || ldq < cols) return OZK_EINVAL;
+  if (norm ? !(eps >= 0.0) : (gamma != nullptr || beta != nullptr)) return OZK_EINVAL;
+  if (rows == 0) return OZK_OK;
+  const size_t e = type_size(type);
+  if (!x || !q || !scale || !aligned(x, e) || !aligned(gamma, e) || !aligned(beta, e) ||
+      !aligned(scale, 4))
+    return OZK_EINVAL;
+  return launch_int8quant(rows, cols, type, x, ldx, norm, gamma, beta, eps, q, ldq, scale,
+                          as_stream(stream));
+}
+
+int ozk_layernorm(int64_t rows, int64_t cols, int type, const void* x, int64_t ldx,
+                  const void* gamma, const void* beta, double eps, void* y, int64_t ldy,
+                  void* mean, void* rstd, void* stream) {
+  int st = check_rows(rows, cols, type);
+  if (st != OZK_OK) return st;
+  if (ldx < cols || ldy < cols || !(eps >= 0.0)) return OZK_EINVAL;
+  if (rows == 0) return OZK_OK;
+  const size_t e = type_size(type), a = e > 4 ? e : 4;
+  if (!x || !y || !aligned(x, e) || !aligned(y, e) || !aligned(gamma, e) || !aligned(beta, e) ||
+      !aligned(mean, a) || !aligned(rstd, a))
+    return OZK_EINVAL;
+  return launch_layernorm(rows, cols, type, x, ldx, gamma, beta, eps, y, ldy, mean, rstd,
+                          as_stream(stream));
+}
+
+int ozk_layernorm_backward_workspace_size(int64_t rows, int64_t cols, int type, size_t* bytes) {
+  if (!bytes) return OZK_EINVAL;
+  int st = check_rows(rows, cols, type);
+  if (st != OZK_OK) return st;
+  *bytes = align256((size_t)layernorm_backward_groups(rows) * 2 * cols *
+                    (type == OZK_F64 ? 8 : 4));
+  return OZK_OK;
+}
+
+int ozk_layernorm_backward(int64_t rows, int64_t cols, int type, const void* dy, int64_t lddy,
+                           const void* x, int64_t ldx, const void* gamma, const void* mean,
+                           const void* rstd, void* dx, int64_t lddx, void* dgamma, void* dbeta,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  int st = ozk_layernorm_backward_workspace_size(rows, cols, type, &need);
+  if (st != OZK_OK) return st;
+  if (ldx < cols || lddy < cols || (dx && lddx < cols)) return OZK_EINVAL;
+  const size_t e = type_size(type), a = e > 4 ? e : 4;
+  if (rows > 0 && (!dy || !x || !mean || !rstd)) return OZK_EINVAL;
+  if (!aligned(dy, e) || !aligned(x, e) || !aligned(gamma, e) || !aligned(mean, a) ||
+      !aligned(rstd, a) || !aligned(dx, e) || !aligned(dgamma, e) || !aligned(dbeta, e))
+    return OZK_EINVAL;
+  if (rows == 0) dx = nullptr;   // the sums over no rows are zero
+  if (!dx && !dgamma && !dbeta) return OZK_OK;
+  if (rows > 0 && (dgamma || dbeta)) {
+    if (!workspace || workspace_bytes < need) return OZK_EWORKSPACE;
+    if (!aligned(workspace, 256)) return OZK_EINVAL;
+  }
+  return launch_layernorm_backward(rows, cols, type, dy, lddy, x, ldx, gamma, mean, rstd, dx,
+                                   lddx, dgamma, dbeta, workspace, as_stream(stream));
 }
 
 }  // extern "C"

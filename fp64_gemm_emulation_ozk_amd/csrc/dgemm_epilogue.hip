@@ -1,0 +1,127 @@
+// The emulated fp64 product's epilogue, and what its gradient needs beside two products.
+//
+// Forward: Z = A B + 1 b^T, C = act(Z) + R.  The reconstruction finishes one output per
+// lane in a register, so bias, activation and residual are applied there: C (and Z, if
+// kept for the backward pass) is written once, the product alone never.
+// Backward: G = dC * act'(Z) elementwise, db = column sums of G; dA = G B^T and dB = A^T G
+// are products of the same kind.
+#include "activation.h"
+#include "crt_core.h"
+
+namespace ozk {
+namespace {
+
+// The residual may be C itself: a lane reads its element before it writes it.
+template <int R>
+__global__ __launch_bounds__(256) void crt_epilogue_kernel(
+    int64_t m, int64_t n, const int8_t* __restrict__ res, int64_t ldr, int64_t stride_r,
+    const int32_t* __restrict__ ea, const int32_t* __restrict__ eb, DgemmEpilogue E, double* c,
+    int64_t ldc) {
+  crt_outputs<R, int8_t>(m, n, res, ldr, stride_r, ea, eb, [=](int64_t i, int64_t j, double v) {
+    if (E.bias) v += E.bias[j];
+    if (E.z) E.z[i * E.ldz + j] = v;
+    v = activate(v, E.act);
+    if (E.residual) v += E.residual[i * E.ldr + j];
+    c[i * ldc + j] = v;
+  });
+}
+
+template <int R>
+void launch_r(dim3 grid, hipStream_t s, int64_t m, int64_t n, const int8_t* res, int64_t ldr,
+              int64_t stride_r, const int32_t* ea, const int32_t* eb, const DgemmEpilogue& E,
+              double* c, int64_t ldc) {
+  hipLaunchKernelGGL((crt_epilogue_kernel<R>), grid, dim3(256), 0, s, m, n, res, ldr, stride_r,
+                     ea, eb, E, c, ldc);
+}
+
+// Column c of a chunk of rows per thread: G, and the chunk's sum of G.
+__global__ __launch_bounds__(256) void act_grad_kernel(
+    int64_t m, int64_t n, int64_t chunk, const double* __restrict__ dc, int64_t lddc,
+    const double* __restrict__ z, int64_t ldz, int act, double* __restrict__ g,
+    double* __restrict__ part) {
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (c >= n) return;
+  const int64_t r0 = blockIdx.y * chunk, r1 = r0 + chunk < m ? r0 + chunk : m;
+  double sum = 0;
+#pragma unroll 4
+  for (int64_t i = r0; i < r1; ++i) {
+    double v = dc[i * lddc + c];
+    if (act != OZK_ACT_NONE) v *= activate_slope(z[i * ldz + c], act);
+    if (g) g[i * n + c] = v;
+    sum += v;
+  }
+  if (part) part[blockIdx.y * n + c] = sum;
+}
+
+// out[c] = the chunks' sums of column c, in a fixed order: 16 columns x 16 slices per
+// workgroup, slice s adding chunks s, s + 16, ..., then the slices in order.
+__global__ __launch_bounds__(256) void column_join_kernel(int64_t n, int chunks,
+                                                          const double* __restrict__ part,
+                                                          double* __restrict__ out) {
+  __shared__ double sums[16][17];
+  const int cl = threadIdx.x & 15, slice = threadIdx.x >> 4;
+  const int64_t c = (int64_t)blockIdx.x * 16 + cl;
+  double s = 0;
+  if (c < n)
+    for (int g = slice; g < chunks; g += 16) s += part[(int64_t)g * n + c];
+  sums[slice][cl] = s;
+  __syncthreads();
+  if (slice == 0 && c < n) {
+    for (int w = 1; w < 16; ++w) s += sums[w][cl];
+    out[c] = s;
+  }
+}
+
+__global__ __launch_bounds__(256) void zero_rows_kernel(double* __restrict__ p, int64_t rows,
+                                                        int64_t cols, int64_t ld) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < rows * cols) p[i / cols * ld + i % cols] = 0.0;
+}
+
+}  // namespace
+
+int launch_zero_rows(double* p, int64_t rows, int64_t cols, int64_t ld, hipStream_t s) {
+  hipLaunchKernelGGL(zero_rows_kernel, dim3((unsigned)((rows * cols + 255) / 256)), dim3(256), 0,
+                     s, p, rows, cols, ld);
+  return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
+}
+
+int launch_crt_epilogue(int64_t m, int64_t n, int r, const int8_t* res, int64_t ldr,
+                        int64_t stride_r, const int32_t* ea, const int32_t* eb,
+                        const DgemmEpilogue& E, double* c, int64_t ldc, hipStream_t s) {
+  if (m <= 0 || n <= 0) return OZK_OK;
+  const dim3 grid((unsigned)crt_blocks(m, n));
+  switch (r) {
+#define OZK_R(R)                                                             \
+  case R:                                                                    \
+    launch_r<R>(grid, s, m, n, res, ldr, stride_r, ea, eb, E, c, ldc);       \
+    break
+    OZK_R(1); OZK_R(2); OZK_R(3); OZK_R(4); OZK_R(5); OZK_R(6); OZK_R(7); OZK_R(8); OZK_R(9);
+    OZK_R(10); OZK_R(11); OZK_R(12); OZK_R(13); OZK_R(14); OZK_R(15); OZK_R(16); OZK_R(17);
+    OZK_R(18); OZK_R(19); OZK_R(20);
+#undef OZK_R
+    default: return OZK_EINVAL;
+  }
+  return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
+}
+
+// Rows of a chunk: 16, or as many as leave at most 256 chunks.
+int64_t act_grad_chunks(int64_t m) {
+  const int64_t rows = (m + 255) / 256 > 16 ? (m + 255) / 256 : 16;
+  return (m + rows - 1) / rows;
+}
+
+int launch_act_grad(int64_t m, int64_t n, const double* dc, int64_t lddc, const double* z,
+                    int64_t ldz, int act, double* g, double* part, double* dbias,
+                    hipStream_t s) {
+  const int64_t chunks = act_grad_chunks(m), chunk = (m + chunks - 1) / chunks;
+  hipLaunchKernelGGL(act_grad_kernel, dim3((unsigned)((n + 255) / 256), (unsigned)chunks),
+                     dim3(256), 0, s, m, n, chunk, dc, lddc, z, ldz, act, g,
+                     dbias ? part : nullptr);
+  if (dbias)
+    hipLaunchKernelGGL(column_join_kernel, dim3((unsigned)((n + 15) / 16)), dim3(256), 0, s, n,
+                       (int)chunks, part, dbias);
+  return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
+}
+
+}  // namespace ozk

@@ -1,0 +1,665 @@
+// Layer norm over rows, forward and backward, and rows of int8 codes.
+//
+// With mu = mean(x), rho = (mean((x - mu)^2) + eps)^(-1/2) of a row and xh = (x - mu) rho:
+//   forward   y = xh gamma + beta
+//   backward  g = dy gamma; dx = rho (g - mean(g) - xh mean(g xh));
+//             dgamma = sum over rows of dy xh, dbeta = sum over rows of dy
+//   codes     s = fp32(max |y| / 127), q = rint(y / s) for y = x or the forward's y
+//
+// All of it is bound by HBM: a row is read once into registers (the mean, then the
+// centred sum of squares, are taken from there), one 16-byte load per thread and step.
+// Sums and statistics are fp32 for the types of at most 32 bits and fp64 for fp64; the
+// codes' statistics are fp64 for every type (fp64 arithmetic runs at the fp32 rate here), so
+// that a code depends on the order of the sums only within 1e-13 of a rounding border.
+#include "ozk_internal.h"
+#include "rows.h"
+
+namespace ozk {
+namespace {
+
+// Number of valid elements of the vector that starts at column c.
+template <int N>
+__device__ __forceinline__ int valid(int64_t c, int64_t cols) {
+  const int64_t left = cols - c;
+  return left >= N ? N : (left > 0 ? (int)left : 0);
+}
+
+// ------------------------------------------------------------------ forward
+// kT threads of a row hold it in kV vectors each (vector v of thread t starts at column
+// (v kT + t) N).  kT = 64: four rows per workgroup; else one.
+template <typename T, int kT, int kV>
+__global__ __launch_bounds__(kT < 256 ? 256 : kT) void layernorm_kernel(
+    int64_t rows, int64_t cols, const T* __restrict__ x, int64_t ldx,
+    const T* __restrict__ gamma, const T* __restrict__ beta, typename AccOf<T>::type eps,
+    T* __restrict__ y, int64_t ldy, typename AccOf<T>::type* __restrict__ mean_out,
+    typename AccOf<T>::type* __restrict__ rstd_out) {
+  typedef typename AccOf<T>::type A;
+  constexpr int N = Vec<T>::N;
+  constexpr int kRows = kT < 256 ? 256 / kT : 1;
+  __shared__ A slots[2][kT / 64];
+  const int t = threadIdx.x % kT;
+  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kT;
+  if (kRows > 1 && row >= rows) return;  // whole waves
+  const T* xr = x + row * ldx;
+  A a[kV][N];
+  A sum = 0;
+#pragma unroll
+  for (int v = 0; v < kV; ++v) {
+    load_vec<T, A>(xr, (int64_t)(v * kT + t) * N, cols, a[v]);
+#pragma unroll
+    for (int u = 0; u < N; ++u) sum += a[v][u];
+  }
+  const A inv = (A)1 / (A)cols;
+  const A mean = row_all<kT>(sum, SumOp(), slots[0]) * inv;
+  A sq = 0;
+#pragma unroll
+  for (int v = 0; v < kV; ++v) {
+    const int nv = valid<N>((int64_t)(v * kT + t) * N, cols);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      a[v][u] -= mean;
+      if (u < nv) sq += a[v][u] * a[v][u];
+    }
+  }
+  const A var = row_all<kT>(sq, SumOp(), slots[1]) * inv;
+  const A rstd = (A)1 / sqrt(var + eps);
+  if (t == 0) {
+    if (mean_out) mean_out[row] = mean;
+    if (rstd_out) rstd_out[row] = rstd;
+  }
+  T* yr = y + row * ldy;
+#pragma unroll
+  for (int v = 0; v < kV; ++v) {
+    const int64_t c = (int64_t)(v * kT + t) * N;
+    if (c >= cols) continue;
+    A g[N], b[N];
+    if (gamma) load_vec<T, A>(gamma, c, cols, g);
+    if (beta) load_vec<T, A>(beta, c, cols, b);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      A w = a[v][u] * rstd;
+      if (gamma) w *= g[u];
+      if (beta) w += b[u];
+      a[v][u] = w;
+    }
+    store_vec<T, A>(yr, c, cols, a[v]);
+  }
+}
+
+// Rows too long for registers: three passes over the row (it stays in L2).
+template <typename T>
+__global__ __launch_bounds__(1024) void layernorm_long_kernel(
+    int64_t cols, const T* __restrict__ x, int64_t ldx, const T* __restrict__ gamma,
+    const T* __restrict__ beta, typename AccOf<T>::type eps, T* __restrict__ y, int64_t ldy,
+    typename AccOf<T>::type* __restrict__ mean_out,
+    typename AccOf<T>::type* __restrict__ rstd_out) {
+  typedef typename AccOf<T>::type A;
+  constexpr int N = Vec<T>::N, kT = 1024;
+  __shared__ A slots[2][kT / 64];
+  const int64_t row = blockIdx.x;
+  const T* xr = x + row * ldx;
+  A sum = 0, a[N];
+  for (int64_t c = (int64_t)threadIdx.x * N; c < cols; c += kT * N) {
+    load_vec<T, A>(xr, c, cols, a);
+#pragma unroll
+    for (int u = 0; u < N; ++u) sum += a[u];
+  }
+  const A inv = (A)1 / (A)cols;
+  const A mean = row_all<kT>(sum, SumOp(), slots[0]) * inv;
+  A sq = 0;
+  for (int64_t c = (int64_t)threadIdx.x * N; c < cols; c += kT * N) {
+    load_vec<T, A>(xr, c, cols, a);
+    const int nv = valid<N>(c, cols);
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+      if (u < nv) sq += (a[u] - mean) * (a[u] - mean);
+  }
+  const A var = row_all<kT>(sq, SumOp(), slots[1]) * inv;
+  const A rstd = (A)1 / sqrt(var + eps);
+  if (threadIdx.x == 0) {
+    if (mean_out) mean_out[row] = mean;
+    if (rstd_out) rstd_out[row] = rstd;
+  }
+  T* yr = y + row * ldy;
+  for (int64_t c = (int64_t)threadIdx.x * N; c < cols; c += kT * N) {
+    load_vec<T, A>(xr, c, cols, a);
+    A g[N], b[N];
+    if (gamma) load_vec<T, A>(gamma, c, cols, g);
+    if (beta) load_vec<T, A>(beta, c, cols, b);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      A w = (a[u] - mean) * rstd;
+      if (gamma) w *= g[u];
+      if (beta) w += b[u];
+      a[u] = w;
+    }
+    store_vec<T, A>(yr, c, cols, a);
+  }
+}
+
+// ------------------------------------------------------------------ int8 codes
+// Scale and reciprocal of a row from its largest magnitude.  A row with a value that is not
+// finite, or whose scale is no finite fp32, gets the scale NaN and zero codes; a row of
+// zeros (or of values below the smallest fp32 scale) the scale 0 and zero codes.
+struct CodeScale {
+  float scale;
+  double inv;
+};
+__device__ __forceinline__ CodeScale code_scale(double amax, bool bad) {
+  const float s = (float)(amax / 127.0);
+  if (bad || !(s <= 3.402823466e38f)) return {__builtin_nanf(""), 0.0};
+  return {s, s > 0.0f ? 1.0 / (double)s : 0.0};
+}
+
+// rint(w inv) as a byte: adding 1.5 2^52 rounds to the nearest integer, ties to even, and
+// leaves it in the low word.  A subnormal scale can be off by a third: then the quotient
+// passes 127 and is cut.
+__device__ __forceinline__ int code_of(double w, double inv) {
+  const double p = w * inv;
+  const double c = p > 127.0 ? 127.0 : (p < -127.0 ? -127.0 : p);
+  return (int)(uint32_t)__double_as_longlong(c + kMagic);
+}
+
+template <int N>
+__device__ __forceinline__ void store_codes(int8_t* __restrict__ p, int64_t c, int64_t cols,
+                                            const int (&q)[N]) {
+  if (c + N <= cols) {
+    typedef int8_t V __attribute__((ext_vector_type(N), aligned(1)));
+    V v;
+#pragma unroll
+    for (int u = 0; u < N; ++u) v[u] = (int8_t)q[u];
+    *reinterpret_cast<V*>(p + c) = v;
+  } else {
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+      if (c + u < cols) p[c + u] = (int8_t)q[u];
+  }
+}
+
+// kNorm: y = layer norm of x, else y = x.
+template <typename T, int kT, int kV, bool kNorm>
+__global__ __launch_bounds__(kT < 256 ? 256 : kT) void int8quant_kernel(
+    int64_t rows, int64_t cols, const T* __restrict__ x, int64_t ldx,
+    const T* __restrict__ gamma, const T* __restrict__ beta, double eps,
+    int8_t* __restrict__ q, int64_t ldq, float* __restrict__ scale) {
+  constexpr int N = Vec<T>::N;
+  constexpr int kRows = kT < 256 ? 256 / kT : 1;
+  __shared__ double slots[4][kT / 64];
+  const int t = threadIdx.x % kT;
+  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kT;
+  if (kRows > 1 && row >= rows) return;
+  const T* xr = x + row * ldx;
+  double a[kV][N];
+  double sum = 0;
+#pragma unroll
+  for (int v = 0; v < kV; ++v) {
+    load_vec<T, double>(xr, (int64_t)(v * kT + t) * N, cols, a[v]);
+    if (kNorm) {
+#pragma unroll
+      for (int u = 0; u < N; ++u) sum += a[v][u];
+    }
+  }
+  if constexpr (kNorm) {
+    const double mean = row_all<kT>(sum, SumOp(), slots[0]) / (double)cols;
+    double sq = 0;
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+      const int nv = valid<N>((int64_t)(v * kT + t) * N, cols);
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        a[v][u] -= mean;
+        if (u < nv) sq += a[v][u] * a[v][u];
+      }
+    }
+    const double var = row_all<kT>(sq, SumOp(), slots[1]) / (double)cols;
+    const double rstd = 1.0 / sqrt(var + eps);
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+      const int64_t c = (int64_t)(v * kT + t) * N;
+      double g[N], b[N];
+      if (gamma) load_vec<T, double>(gamma, c, cols, g);
+      if (beta) load_vec<T, double>(beta, c, cols, b);
+      const int nv = valid<N>(c, cols);
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        double w = a[v][u] * rstd;
+        if (gamma) w *= g[u];
+        if (beta) w += b[u];
+        a[v][u] = u < nv ? w : 0.0;
+      }
+    }
+  }
+  double amax = 0;
+  bool bad = false;
+#pragma unroll
+  for (int v = 0; v < kV; ++v)
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const double m = __builtin_fabs(a[v][u]);
+      bad |= !(m <= 1.7976931348623157e308);
+      amax = m > amax ? m : amax;
+    }
+  amax = row_all<kT>(bad ? __builtin_huge_val() : amax, MaxOp(), slots[2]);
+  const CodeScale cs = code_scale(amax, !(amax <= 1.7976931348623157e308));
+  if (t == 0) scale[row] = cs.scale;
+  int8_t* qr = q + row * ldq;
+#pragma unroll
+  for (int v = 0; v < kV; ++v) {
+    const int64_t c = (int64_t)(v * kT + t) * N;
+    if (c >= cols) continue;
+    int codes[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) codes[u] = cs.inv == 0.0 ? 0 : code_of(a[v][u], cs.inv);
+    store_codes<N>(qr, c, cols, codes);
+  }
+}
+
+template <typename T, bool kNorm>
+__global__ __launch_bounds__(1024) void int8quant_long_kernel(
+    int64_t cols, const T* __restrict__ x, int64_t ldx, const T* __restrict__ gamma,
+    const T* __restrict__ beta, double eps, int8_t* __restrict__ q, int64_t ldq,
+    float* __restrict__ scale) {
+  constexpr int N = Vec<T>::N, kT = 1024;
+  __shared__ double slots[3][kT / 64];
+  const int64_t row = blockIdx.x;
+  const T* xr = x + row * ldx;
+  double a[N], mean = 0, rstd = 1;
+  if (kNorm) {
+    double sum = 0;
+    for (int64_t c = (int64_t)threadIdx.x * N; c < cols; c += kT * N) {
+      load_vec<T, double>(xr, c, cols, a);
+#pragma unroll
+      for (int u = 0; u < N; ++u) sum += a[u];
+    }
+    mean = row_all<kT>(sum, SumOp(), slots[0]) / (double)cols;
+    double sq = 0;
+    for (int64_t c = (int64_t)threadIdx.x * N; c < cols; c += kT * N) {
+      load_vec<T, double>(xr, c, cols, a);
+      const int nv = valid<N>(c, cols);
+#pragma unroll
+      for (int u = 0; u < N; ++u)
+        if (u < nv) sq += (a[u] - mean) * (a[u] - mean);
+    }
+    rstd = 1.0 / sqrt(row_all<kT>(sq, SumOp(), slots[1]) / (double)cols + eps);
+  }
+  auto values = [&](int64_t c) {
+    load_vec<T, double>(xr, c, cols, a);
+    if (!kNorm) return;
+    double g[N], b[N];
+    if (gamma) load_vec<T, double>(gamma, c, cols, g);
+    if (beta) load_vec<T, double>(beta, c, cols, b);
+    const int nv = valid<N>(c, cols);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      double w = (a[u] - mean) * rstd;
+      if (gamma) w *= g[u];
+      if (beta) w += b[u];
+      a[u] = u < nv ? w : 0.0;
+    }
+  };
+  double amax = 0;
+  bool bad = false;
+  for (int64_t c = (int64_t)threadIdx.x * N; c < cols; c += kT * N) {
+    values(c);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const double m = __builtin_fabs(a[u]);
+      bad |= !(m <= 1.7976931348623157e308);
+      amax = m > amax ? m : amax;
+    }
+  }
+  amax = row_all<kT>(bad ? __builtin_huge_val() : amax, MaxOp(), slots[2]);
+  const CodeScale cs = code_scale(amax, !(amax <= 1.7976931348623157e308));
+  if (threadIdx.x == 0) scale[row] = cs.scale;
+  for (int64_t c = (int64_t)threadIdx.x * N; c < cols; c += kT * N) {
+    values(c);
+    int codes[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) codes[u] = cs.inv == 0.0 ? 0 : code_of(a[u], cs.inv);
+    store_codes<N>(q + row * ldq, c, cols, codes);
+  }
+}
+
+// ------------------------------------------------------------------ backward
+// Workgroup b of G walks rows b, b + G, ...: dx row by row, and the column sums dy xh and dy
+// of its rows in registers, written to partials [G][2][cols] at the end.
+template <typename T, int kT, int kV>
+__global__ __launch_bounds__(kT) void layernorm_backward_kernel(
+    int64_t rows, int64_t cols, const T* __restrict__ dy, int64_t lddy,
+    const T* __restrict__ x, int64_t ldx, const T* __restrict__ gamma,
+    const typename AccOf<T>::type* __restrict__ mean,
+    const typename AccOf<T>::type* __restrict__ rstd, T* __restrict__ dx, int64_t lddx,
+    typename AccOf<T>::type* __restrict__ part) {
+  typedef typename AccOf<T>::type A;
+  constexpr int N = Vec<T>::N;
+  __shared__ A slots[2][2][kT / 64];
+  const int t = threadIdx.x;
+  A dg[kV][N], db[kV][N];
+#pragma unroll
+  for (int v = 0; v < kV; ++v)
+#pragma unroll
+    for (int u = 0; u < N; ++u) dg[v][u] = db[v][u] = 0;
+  const A inv = (A)1 / (A)cols;
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, flip ^= 1) {
+    const T* xr = x + row * ldx;
+    const T* dyr = dy + row * lddy;
+    const A mu = mean[row], rho = rstd[row];
+    A xh[kV][N], g[kV][N];
+    A s1 = 0, s2 = 0;
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+      const int64_t c = (int64_t)(v * kT + t) * N;
+      A w[N];
+      load_vec<T, A>(xr, c, cols, xh[v]);
+      load_vec<T, A>(dyr, c, cols, g[v]);
+      if (gamma) load_vec<T, A>(gamma, c, cols, w);
+      const int nv = valid<N>(c, cols);
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        xh[v][u] = u < nv ? (xh[v][u] - mu) * rho : (A)0;
+        const A d = g[v][u];
+        dg[v][u] += d * xh[v][u];
+        db[v][u] += d;
+        if (gamma) g[v][u] = d * w[u];
+        s1 += g[v][u] * xh[v][u];
+        s2 += g[v][u];
+      }
+    }
+    // two slot sets in turn: a row's reads of one set end before the barrier of the next
+    // row, which comes before the set is written again
+    s1 = wave_all(s1, SumOp());
+    s2 = wave_all(s2, SumOp());
+    if constexpr (kT > 64) {
+      if ((t & 63) == 0) {
+        slots[flip][0][t >> 6] = s1;
+        slots[flip][1][t >> 6] = s2;
+      }
+      __syncthreads();
+      s1 = slots[flip][0][0];
+      s2 = slots[flip][1][0];
+#pragma unroll
+      for (int w = 1; w < kT / 64; ++w) {
+        s1 += slots[flip][0][w];
+        s2 += slots[flip][1][w];
+      }
+    }
+    const A c1 = s1 * inv, c2 = s2 * inv;
+    if (dx) {
+      T* dxr = dx + row * lddx;
+#pragma unroll
+      for (int v = 0; v < kV; ++v) {
+        const int64_t c = (int64_t)(v * kT + t) * N;
+        if (c >= cols) continue;
+#pragma unroll
+        for (int u = 0; u < N; ++u) g[v][u] = rho * (g[v][u] - c2 - xh[v][u] * c1);
+        store_vec<T, A>(dxr, c, cols, g[v]);
+      }
+    }
+  }
+  if (part) {
+    A* p = part + (int64_t)blockIdx.x * 2 * cols;
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+      const int64_t c = (int64_t)(v * kT + t) * N;
+#pragma unroll
+      for (int u = 0; u < N; ++u)
+        if (c + u < cols) {
+          p[c + u] = dg[v][u];
+          p[cols + c + u] = db[v][u];
+        }
+    }
+  }
+}
+
+// Rows too long for registers: dx from two passes over the row.
+template <typename T>
+__global__ __launch_bounds__(1024) void layernorm_backward_long_kernel(
+    int64_t cols, const T* __restrict__ dy, int64_t lddy, const T* __restrict__ x, int64_t ldx,
+    const T* __restrict__ gamma, const typename AccOf<T>::type* __restrict__ mean,
+    const typename AccOf<T>::type* __restrict__ rstd, T* __restrict__ dx, int64_t lddx) {
+  typedef typename AccOf<T>::type A;
+  constexpr int N = Vec<T>::N, kT = 1024;
+  __shared__ A slots[2][kT / 64];
+  const int64_t row = blockIdx.x;
+  const T* xr = x + row * ldx;
+  const T* dyr = dy + row * lddy;
+  const A mu = mean[row], rho = rstd[row], inv = (A)1 / (A)cols;
+  A a[N], d[N], w[N], s1 = 0, s2 = 0;
+  auto values = [&](int64_t c) {   // a = xh, d = g
+    load_vec<T, A>(xr, c, cols, a);
+    load_vec<T, A>(dyr, c, cols, d);
+    if (gamma) load_vec<T, A>(gamma, c, cols, w);
+    const int nv = valid<N>(c, cols);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      a[u] = u < nv ? (a[u] - mu) * rho : (A)0;
+      if (gamma) d[u] *= w[u];
+    }
+  };
+  for (int64_t c = (int64_t)threadIdx.x * N; c < cols; c += kT * N) {
+    values(c);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      s1 += d[u] * a[u];
+      s2 += d[u];
+    }
+  }
+  const A c1 = row_all<kT>(s1, SumOp(), slots[0]) * inv;
+  const A c2 = row_all<kT>(s2, SumOp(), slots[1]) * inv;
+  for (int64_t c = (int64_t)threadIdx.x * N; c < cols; c += kT * N) {
+    values(c);
+#pragma unroll
+    for (int u = 0; u < N; ++u) a[u] = rho * (d[u] - c2 - a[u] * c1);
+    store_vec<T, A>(dx + row * lddx, c, cols, a);
+  }
+}
+
+// Column sums of the long rows: workgroup (bx, by) of G row groups takes 256 vectors of
+// columns and rows by, by + G, ...
+template <typename T>
+__global__ __launch_bounds__(256) void layernorm_backward_cols_kernel(
+    int64_t rows, int64_t cols, const T* __restrict__ dy, int64_t lddy,
+    const T* __restrict__ x, int64_t ldx, const typename AccOf<T>::type* __restrict__ mean,
+    const typename AccOf<T>::type* __restrict__ rstd, typename AccOf<T>::type* __restrict__ part) {
+  typedef typename AccOf<T>::type A;
+  constexpr int N = Vec<T>::N;
+  const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * N;
+  if (c >= cols) return;
+  A dg[N], db[N], a[N], d[N];
+#pragma unroll
+  for (int u = 0; u < N; ++u) dg[u] = db[u] = 0;
+  for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+    load_vec<T, A>(x + row * ldx, c, cols, a);
+    load_vec<T, A>(dy + row * lddy, c, cols, d);
+    const A mu = mean[row], rho = rstd[row];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      dg[u] += d[u] * ((a[u] - mu) * rho);
+      db[u] += d[u];
+    }
+  }
+  A* p = part + (int64_t)blockIdx.y * 2 * cols;
+#pragma unroll
+  for (int u = 0; u < N; ++u)
+    if (c + u < cols) {
+      p[c + u] = dg[u];
+      p[cols + c + u] = db[u];
+    }
+}
+
+// dgamma and dbeta from the G partials of each column, added in a fixed order: slice s of
+// 16 adds partials s, s + 16, ... in order, then the slices are added in order.  Workgroup:
+// 16 columns (of the 2 cols values) x 16 slices.
+template <typename T>
+__global__ __launch_bounds__(256) void layernorm_join_kernel(
+    int64_t cols, int groups, const typename AccOf<T>::type* __restrict__ part,
+    T* __restrict__ dgamma, T* __restrict__ dbeta) {
+  typedef typename AccOf<T>::type A;
+  __shared__ A sums[16][17];
+  const int cl = threadIdx.x & 15, slice = threadIdx.x >> 4;
+  const int64_t c = (int64_t)blockIdx.x * 16 + cl;
+  A s = 0;
+  if (c < 2 * cols)
+    for (int g = slice; g < groups; g += 16) s += part[(int64_t)g * 2 * cols + c];
+  sums[slice][cl] = s;
+  __syncthreads();
+  if (slice == 0 && c < 2 * cols) {
+    for (int w = 1; w < 16; ++w) s += sums[w][cl];
+    if (c < cols) {
+      if (dgamma) dgamma[c] = (T)s;
+    } else {
+      if (dbeta) dbeta[c - cols] = (T)s;
+    }
+  }
+}
+
+// Threads and vectors per thread for a row of `vecs` 16-byte vectors.
+#define OZK_ROW_SHAPES(GO)         \
+  if (vecs <= 64) GO(64, 1);       \
+  else if (vecs <= 128) GO(64, 2); \
+  else if (vecs <= 256) GO(64, 4); \
+  else if (vecs <= 512) GO(256, 2);  \
+  else if (vecs <= 1024) GO(256, 4); \
+  else if (vecs <= 2048) GO(1024, 2); \
+  else GO(1024, 4)
+constexpr int64_t kRowVecs = 4096;   // vectors a workgroup holds
+
+template <typename T>
+int layernorm_t(int64_t rows, int64_t cols, const void* x, int64_t ldx, const void* gamma,
+                const void* beta, double eps, void* y, int64_t ldy, void* mean, void* rstd,
+                hipStream_t s) {
+  typedef typename AccOf<T>::type A;
+  const int64_t vecs = (cols + Vec<T>::N - 1) / Vec<T>::N;
+  const T *xt = (const T*)x, *gt = (const T*)gamma, *bt = (const T*)beta;
+  if (vecs > kRowVecs) {
+    hipLaunchKernelGGL((layernorm_long_kernel<T>), dim3((unsigned)rows), dim3(1024), 0, s, cols,
+                       xt, ldx, gt, bt, (A)eps, (T*)y, ldy, (A*)mean, (A*)rstd);
+  } else {
+#define OZK_LN(NT, NV)                                                                         \
+  hipLaunchKernelGGL((layernorm_kernel<T, NT, NV>),                                            \
+                     dim3((unsigned)(NT < 256 ? (rows + 3) / 4 : rows)),                       \
+                     dim3(NT < 256 ? 256 : NT), 0, s, rows, cols, xt, ldx, gt, bt, (A)eps,     \
+                     (T*)y, ldy, (A*)mean, (A*)rstd)
+    OZK_ROW_SHAPES(OZK_LN);
+#undef OZK_LN
+  }
+  return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
+}
+
+template <typename T, bool kNorm>
+int int8quant_t(int64_t rows, int64_t cols, const void* x, int64_t ldx, const void* gamma,
+                const void* beta, double eps, int8_t* q, int64_t ldq, float* scale,
+                hipStream_t s) {
+  const int64_t vecs = (cols + Vec<T>::N - 1) / Vec<T>::N;
+  const T *xt = (const T*)x, *gt = (const T*)gamma, *bt = (const T*)beta;
+  if (vecs > kRowVecs) {
+    hipLaunchKernelGGL((int8quant_long_kernel<T, kNorm>), dim3((unsigned)rows), dim3(1024), 0, s,
+                       cols, xt, ldx, gt, bt, eps, q, ldq, scale);
+  } else {
+#define OZK_Q(NT, NV)                                                                          \
+  hipLaunchKernelGGL((int8quant_kernel<T, NT, NV, kNorm>),                                     \
+                     dim3((unsigned)(NT < 256 ? (rows + 3) / 4 : rows)),                       \
+                     dim3(NT < 256 ? 256 : NT), 0, s, rows, cols, xt, ldx, gt, bt, eps, q,     \
+                     ldq, scale)
+    OZK_ROW_SHAPES(OZK_Q);
+#undef OZK_Q
+  }
+  return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
+}
+
+// Vectors a backward workgroup holds per row (its column sums take registers too).
+constexpr int64_t kBackwardVecs = 2048;
+
+template <typename T>
+int layernorm_backward_t(int64_t rows, int64_t cols, const void* dy, int64_t lddy,
+                         const void* x, int64_t ldx, const void* gamma, const void* mean,
+                         const void* rstd, void* dx, int64_t lddx, void* dgamma, void* dbeta,
+                         void* workspace, hipStream_t s) {
+  typedef typename AccOf<T>::type A;
+  const int64_t vecs = (cols + Vec<T>::N - 1) / Vec<T>::N;
+  const int groups = layernorm_backward_groups(rows);
+  A* part = dgamma || dbeta ? (A*)workspace : nullptr;
+  const T *dyt = (const T*)dy, *xt = (const T*)x, *gt = (const T*)gamma;
+  const A *mt = (const A*)mean, *rt = (const A*)rstd;
+  if (rows == 0) {
+    part = nullptr;
+  } else if (vecs > kBackwardVecs) {
+    if (dx)
+      hipLaunchKernelGGL((layernorm_backward_long_kernel<T>), dim3((unsigned)rows), dim3(1024),
+                         0, s, cols, dyt, lddy, xt, ldx, gt, mt, rt, (T*)dx, lddx);
+    if (part)
+      hipLaunchKernelGGL((layernorm_backward_cols_kernel<T>),
+                         dim3((unsigned)((vecs + 255) / 256), (unsigned)groups), dim3(256), 0, s,
+                         rows, cols, dyt, lddy, xt, ldx, mt, rt, part);
+  } else {
+#define OZK_LNB(NT, NV)                                                                       \
+  hipLaunchKernelGGL((layernorm_backward_kernel<T, NT, NV>), dim3((unsigned)groups), dim3(NT), \
+                     0, s, rows, cols, dyt, lddy, xt, ldx, gt, mt, rt, (T*)dx, lddx, part)
+    if (vecs <= 64) OZK_LNB(64, 1);
+    else if (vecs <= 128) OZK_LNB(64, 2);
+    else if (vecs <= 256) OZK_LNB(256, 1);
+    else if (vecs <= 512) OZK_LNB(256, 2);
+    else if (vecs <= 1024) OZK_LNB(1024, 1);
+    else OZK_LNB(1024, 2);
+#undef OZK_LNB
+  }
+  if (dgamma || dbeta)   // zeros where there are no rows
+    hipLaunchKernelGGL((layernorm_join_kernel<T>), dim3((unsigned)((2 * cols + 15) / 16)),
+                       dim3(256), 0, s, cols, groups, part, (T*)dgamma, (T*)dbeta);
+  return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
+}
+
+}  // namespace
+
+// Row groups of the backward pass: two workgroups' worth of rows per CU, each leaving one
+// partial of the column sums.
+int layernorm_backward_groups(int64_t rows) { return (int)(rows < 512 ? rows : 512); }
+
+int launch_layernorm(int64_t rows, int64_t cols, int type, const void* x, int64_t ldx,
+                     const void* gamma, const void* beta, double eps, void* y, int64_t ldy,
+                     void* mean, void* rstd, hipStream_t s) {
+  switch (type) {
+    case OZK_F64:
+      return layernorm_t<double>(rows, cols, x, ldx, gamma, beta, eps, y, ldy, mean, rstd, s);
+    case OZK_F32:
+      return layernorm_t<float>(rows, cols, x, ldx, gamma, beta, eps, y, ldy, mean, rstd, s);
+    case OZK_F16:
+      return layernorm_t<f16_t>(rows, cols, x, ldx, gamma, beta, eps, y, ldy, mean, rstd, s);
+    default:
+      return layernorm_t<bf16_t>(rows, cols, x, ldx, gamma, beta, eps, y, ldy, mean, rstd, s);
+  }
+}
+
+int launch_int8quant(int64_t rows, int64_t cols, int type, const void* x, int64_t ldx, int norm,
+                     const void* gamma, const void* beta, double eps, int8_t* q, int64_t ldq,
+                     float* scale, hipStream_t s) {
+#define OZK_QT(T)                                                                             \
+  return norm ? int8quant_t<T, true>(rows, cols, x, ldx, gamma, beta, eps, q, ldq, scale, s)  \
+              : int8quant_t<T, false>(rows, cols, x, ldx, gamma, beta, eps, q, ldq, scale, s)
+  switch (type) {
+    case OZK_F64: OZK_QT(double);
+    case OZK_F32: OZK_QT(float);
+    case OZK_F16: OZK_QT(f16_t);
+    default: OZK_QT(bf16_t);
+  }
+#undef OZK_QT
+}
+
+int launch_layernorm_backward(int64_t rows, int64_t cols, int type, const void* dy, int64_t lddy,
+                              const void* x, int64_t ldx, const void* gamma, const void* mean,
+                              const void* rstd, void* dx, int64_t lddx, void* dgamma, void* dbeta,
+                              void* workspace, hipStream_t s) {
+#define OZK_BT(T)                                                                            \
+  return layernorm_backward_t<T>(rows, cols, dy, lddy, x, ldx, gamma, mean, rstd, dx, lddx,  \
+                                 dgamma, dbeta, workspace, s)
+  switch (type) {
+    case OZK_F64: OZK_BT(double);
+    case OZK_F32: OZK_BT(float);
+    case OZK_F16: OZK_BT(f16_t);
+    default: OZK_BT(bf16_t);
+  }
+#undef OZK_BT
+}
+
+}  // namespace ozk

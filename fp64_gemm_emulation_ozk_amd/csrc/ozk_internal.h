@@ -166,4 +166,49 @@ int launch_crt(int64_t m, int64_t n, int r, const void* res, int res_is_i32, int
                int64_t stride_r, const int32_t* ea, const int32_t* eb, double* c, int64_t ldc,
                hipStream_t s);
 
+// The fp64 product with its epilogue: bias [n], residual and the kept pre-activations z
+// (each null where absent) of launch_crt's outputs, residues in int8.
+struct DgemmEpilogue {
+  const double* bias;
+  const double* residual;
+  int64_t ldr;
+  double* z;
+  int64_t ldz;
+  int act;
+};
+int launch_crt_epilogue(int64_t m, int64_t n, int r, const int8_t* res, int64_t ldr,
+                        int64_t stride_r, const int32_t* ea, const int32_t* eb,
+                        const DgemmEpilogue& E, double* c, int64_t ldc, hipStream_t s);
+// Its gradient's elementwise part: g (m x n, ld n, or null) = dc * act'(z), dbias (or null) =
+// column sums of g through part, act_grad_chunks(m) x n sums.
+int64_t act_grad_chunks(int64_t m);
+int launch_act_grad(int64_t m, int64_t n, const double* dc, int64_t lddc, const double* z,
+                    int64_t ldz, int act, double* g, double* part, double* dbias,
+                    hipStream_t s);
+
+// p[i * ld + j] = 0 for i < rows, j < cols.
+int launch_zero_rows(double* p, int64_t rows, int64_t cols, int64_t ld, hipStream_t s);
+
+// int8 linear layer (int8linear.hip); workspace: int8linear_workspace(m, n, k) bytes.
+size_t int8linear_workspace(int64_t m, int64_t n, int64_t k);
+int launch_int8linear(int64_t m, int64_t n, int64_t k, const int8_t* x, int64_t ldx,
+                      const float* sx, const int8_t* w, int64_t ldw, const float* sw,
+                      const void* bias, int act, const void* residual, int64_t ldr, int type,
+                      void* c, int64_t ldc, void* workspace, hipStream_t s);
+
+// Rows of int8 codes and layer norm (layernorm.hip); gamma, beta, mean, rstd, dx, dgamma and
+// dbeta may each be null where ozk.h says so.  The backward pass leaves
+// layernorm_backward_groups(rows) partial column sums of 2 cols values in workspace.
+int launch_int8quant(int64_t rows, int64_t cols, int type, const void* x, int64_t ldx, int norm,
+                     const void* gamma, const void* beta, double eps, int8_t* q, int64_t ldq,
+                     float* scale, hipStream_t s);
+int launch_layernorm(int64_t rows, int64_t cols, int type, const void* x, int64_t ldx,
+                     const void* gamma, const void* beta, double eps, void* y, int64_t ldy,
+                     void* mean, void* rstd, hipStream_t s);
+int layernorm_backward_groups(int64_t rows);
+int launch_layernorm_backward(int64_t rows, int64_t cols, int type, const void* dy, int64_t lddy,
+                              const void* x, int64_t ldx, const void* gamma, const void* mean,
+                              const void* rstd, void* dx, int64_t lddx, void* dgamma, void* dbeta,
+                              void* workspace, hipStream_t s);
+
 }  // namespace ozk

@@ -60,6 +60,17 @@ extern "C" {
 #define OZK_SCALING_MAX 0     /* scaling rule: per-line max (default of every entry point) */
 #define OZK_SCALING_NORM 1    /* scaling rule: per-line 2-norm (Cauchy-Schwarz), *_ex only */
 
+#define OZK_ACT_NONE 0        /* activations of the products' epilogues, act(z) = */
+#define OZK_ACT_RELU 1        /*   max(z, 0) (slope 0 at 0) */
+#define OZK_ACT_GELU 2        /*   z Phi(z), Phi the normal distribution function */
+#define OZK_ACT_GELU_TANH 3   /*   z (1 + tanh((2/pi)^(1/2) (z + 0.044715 z^3))) / 2 */
+#define OZK_ACT_SILU 4        /*   z / (1 + exp(-z)) */
+
+#define OZK_F64 0             /* element types of the row operators and the int8 layer */
+#define OZK_F32 1
+#define OZK_F16 2
+#define OZK_BF16 3
+
 #define OZK_MAX_MODULI 20
 #define OZK_MAX_K 131071      /* |residue product| <= 2^14: int32 sums stay exact */
 #define OZK_PLANE_K 64        /* residue and limb planes pad K to a multiple of this */
@@ -185,6 +196,38 @@ int ozk_dgemm(int64_t m, int64_t n, int64_t k, const double* A, int64_t lda,
 int ozk_dgemm_ex(int64_t m, int64_t n, int64_t k, const double* A, int64_t lda,
                  const double* B, int64_t ldb, double* C, int64_t ldc, int r, int scaling,
                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- emulated DGEMM: epilogue
+ * A linear layer in emulated fp64 (no counterpart in the pages; the product is that of
+ * ozk_dgemm_ex):
+ *     Z = A B + 1 bias^T,   C = act(Z) + residual
+ * bias (n entries) and residual (m x n, ldr >= n) may be NULL; act is an OZK_ACT_* value.
+ * Z, if not NULL, receives the pre-activations the gradient needs (ldz >= n).  The product
+ * is rounded once (as ozk_dgemm_ex), then the bias is added, the activation taken and the
+ * residual added, one fp64 rounding or fp64 function each, in the registers of the
+ * reconstruction.  residual may be C itself; otherwise outputs overlap no input.  Other
+ * arguments, the errors and the workspace (ozk_dgemm_workspace_size) are those of
+ * ozk_dgemm_ex; OZK_EINVAL for an unknown act. */
+int ozk_dgemm_epilogue(int64_t m, int64_t n, int64_t k, const double* A, int64_t lda,
+                       const double* B, int64_t ldb, const double* bias, int act,
+                       const double* residual, int64_t ldr, double* Z, int64_t ldz, double* C,
+                       int64_t ldc, int r, int scaling, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/* Its gradient: from dC (m x n), A, B and Z (ignored for OZK_ACT_NONE, may be NULL then)
+ *     G = dC * act'(Z),   dA = G B^T,   dB = A^T G,   dbias = column sums of G
+ * (the residual's gradient is dC).  dA (m x k), dB (k x n) and dbias (n entries) may each be
+ * NULL and are then not computed (A is needed for dB, B for dA).  Both products are emulated
+ * with r moduli like ozk_dgemm_ex, inner dimensions n and m; dbias is summed in fp64 in a
+ * fixed order.  m, n and k at most OZK_MAX_K.  m = 0 or n = 0 gives zero gradients.  The
+ * workspace (256-byte aligned, ozk_dgemm_epilogue_grad_workspace_size bytes) serves any
+ * choice of outputs.  No output overlaps an input. */
+int ozk_dgemm_epilogue_grad_workspace_size(int64_t m, int64_t n, int64_t k, int r, size_t* bytes);
+int ozk_dgemm_epilogue_grad(int64_t m, int64_t n, int64_t k, const double* dC, int64_t lddc,
+                            const double* A, int64_t lda, const double* B, int64_t ldb,
+                            const double* Z, int64_t ldz, int act, double* dA, int64_t ldda,
+                            double* dB, int64_t lddb, double* dbias, int r, int scaling,
+                            void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------- emulated DGEMV
  * Y = A X for A m x k and X k x nrhs (1 <= nrhs <= 32): the memory-bound GEMV and
@@ -339,6 +382,57 @@ int ozk_int4int8gemm_fp4awe_workspace_size(int64_t m, int64_t n, int64_t k, size
 int ozk_int4int8gemm_fp4awe(int64_t m, int64_t n, int64_t k, const int8_t* A, int64_t lda,
                             const int8_t* B, int64_t ldb, int32_t* C, int64_t ldc,
                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- int8 linear layer
+ * A linear layer on int8 codes (no counterpart in the pages):
+ *     C[i][j] = act(scale_x[i] scale_w[j] sum_h X[i][h] W[j][h] + bias[j]) + residual[i][j]
+ * X m x k and W n x k int8, both with K contiguous (W holds one row per output: its rows are
+ * the columns of the B of ozk_int8gemm_*), scale_x (m) and scale_w (n) fp32.  bias (n) and
+ * residual (m x n, ldr >= n) may be NULL and have the type of C: OZK_F32, OZK_F16 or
+ * OZK_BF16.  The sum is exact in int32 (1 <= k <= OZK_MAX_K); what follows is fp32, rounded
+ * once to C's type.  A scale that is NaN gives NaN in the outputs it touches.  residual may
+ * be C itself; otherwise C overlaps no input.  Any leading dimensions ldx, ldw >= k and any
+ * byte alignment of X and W; the other pointers are aligned to their elements. */
+int ozk_int8linear_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes);
+int ozk_int8linear(int64_t m, int64_t n, int64_t k, const int8_t* X, int64_t ldx,
+                   const float* scale_x, const int8_t* W, int64_t ldw, const float* scale_w,
+                   const void* bias, int act, const void* residual, int64_t ldr, int type,
+                   void* C, int64_t ldc, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- rows: int8 codes, layer norm
+ * x is rows x cols (ldx >= cols, cols >= 1) of `type`, an OZK_F* value; gamma and beta (cols
+ * entries of that type, or NULL: ones and zeros) scale and shift the normalised row
+ *     y = (x - mu) rho gamma + beta,  mu = mean(x),  rho = (mean((x - mu)^2) + eps)^(-1/2)
+ * with eps >= 0.  Pointers are aligned to their elements.  rows and cols below 2^31
+ * (OZK_EUNSUPPORTED beyond).  Only the cols entries of each row are written.
+ *
+ * ozk_int8quant_rows: the left operand of ozk_int8linear.  q[i][j] = rint(y[i][j] / scale[i])
+ * (ties to even, |q| <= 127) and scale[i] = fp32(max_j |y[i][j]| / 127), with y = x (norm = 0;
+ * gamma and beta must be NULL, eps is ignored) or the layer norm of x (norm = 1).  All of it
+ * in fp64 until the codes and the scale are rounded.  A row of zeros has scale 0 and zero
+ * codes; a row whose y has an Inf or NaN, or whose scale is no finite fp32, has scale NaN
+ * and zero codes.
+ *
+ * ozk_layernorm: y (ldy >= cols, may be x itself with ldy = ldx) and, where not NULL, mean
+ * and rstd (rows entries, fp64 for OZK_F64, else fp32) for the backward pass.
+ *
+ * ozk_layernorm_backward: with xh = (x - mean) rstd, g = dy gamma,
+ *     dx = rstd (g - mean(g) - xh mean(g xh)),  dgamma = sum_i dy xh,  dbeta = sum_i dy
+ * each where its pointer is not NULL; dgamma and dbeta are of `type`, rounded once from sums
+ * in fp32 (fp64 for OZK_F64) that are joined in a fixed order.  dx may be dy or x itself
+ * (with that leading dimension).  rows = 0 gives dgamma = dbeta = 0.  The workspace (256-byte
+ * aligned) is needed for dgamma or dbeta. */
+int ozk_int8quant_rows(int64_t rows, int64_t cols, int type, const void* x, int64_t ldx, int norm,
+                       const void* gamma, const void* beta, double eps, int8_t* q, int64_t ldq,
+                       float* scale, void* stream);
+int ozk_layernorm(int64_t rows, int64_t cols, int type, const void* x, int64_t ldx,
+                  const void* gamma, const void* beta, double eps, void* y, int64_t ldy,
+                  void* mean, void* rstd, void* stream);
+int ozk_layernorm_backward_workspace_size(int64_t rows, int64_t cols, int type, size_t* bytes);
+int ozk_layernorm_backward(int64_t rows, int64_t cols, int type, const void* dy, int64_t lddy,
+                           const void* x, int64_t ldx, const void* gamma, const void* mean,
+                           const void* rstd, void* dx, int64_t lddx, void* dgamma, void* dbeta,
+                           void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------- measurement support
  * ozk_dgemm_ex_timed: ozk_dgemm_ex that also has the launch of the r residue products
