@@ -328,7 +328,9 @@ LINEAR = [(1, 1, 1), (1, 16, 64), (1, 700, 1000), (2, 33, 129), (7, 4100, 257), 
           (17, 130, 1001), (31, 65, 128), (33, 1000, 300), (48, 272, 2048), (64, 128, 128),
           (65, 129, 256), (100, 515, 383), (128, 256, 512), (130, 300, 1024), (200, 96, 5000),
           (256, 256, 256), (300, 520, 384), (513, 257, 640), (1000, 1030, 130), (3, 48, 30000),
-          (128, 128, 16384), (700, 2050, 1024)]
+          (128, 128, 16384), (700, 2050, 1024),
+          # enough tiles of 256 x 256 for every compute unit: K whole, ending in a step, odd
+          (3000, 4500, 272), (2900, 4600, 384), (3000, 4500, 131)]
 
 
 @pytest.mark.parametrize("m,n,k", LINEAR)
