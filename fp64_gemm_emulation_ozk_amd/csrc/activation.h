@@ -70,6 +70,19 @@ __device__ __forceinline__ float activate(float z, int act) {
   }
 }
 
+// activate of N values: the choice of the function stands outside their loop.
+template <int N>
+__device__ __forceinline__ void activate_all(float (&z)[N], int act) {
+  auto each = [&](int a) {
+#pragma unroll
+    for (int u = 0; u < N; ++u) z[u] = activate(z[u], a);
+  };
+  if (act == OZK_ACT_RELU) each(OZK_ACT_RELU);
+  else if (act == OZK_ACT_GELU) each(OZK_ACT_GELU);
+  else if (act == OZK_ACT_GELU_TANH) each(OZK_ACT_GELU_TANH);
+  else if (act == OZK_ACT_SILU) each(OZK_ACT_SILU);
+}
+
 // d activate / dz.  p (1 - p) is an exact 0 where the logistic function has settled; there
 // the slope is p, also where the factor beside it would overflow.
 __device__ __forceinline__ double activate_slope(double z, int act) {

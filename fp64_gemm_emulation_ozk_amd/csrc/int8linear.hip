@@ -33,6 +33,15 @@ __device__ __forceinline__ float pre_activation(int sum, float s, float t, float
   return __builtin_fmaf((float)sum * s, t, b);
 }
 
+// One output.
+template <typename O>
+__device__ __forceinline__ void put1(const Epilogue<O>& E, int64_t row, int64_t col, int sum) {
+  float z = pre_activation(sum, E.sx[row], E.sw[col], E.bias ? (float)E.bias[col] : 0.0f);
+  z = activate(z, E.act);
+  if (E.residual) z += (float)E.residual[row * E.ldr + col];
+  E.c[row * E.ldc + col] = (O)z;
+}
+
 // Four consecutive outputs of one row from their int32 sums.
 template <typename O>
 __device__ __forceinline__ void put4(const Epilogue<O>& E, int64_t row, int64_t col,
@@ -46,56 +55,33 @@ __device__ __forceinline__ void put4(const Epilogue<O>& E, int64_t row, int64_t 
     V b, r, o;
     if (E.bias) b = *reinterpret_cast<const V*>(E.bias + col);
     if (E.residual) r = *reinterpret_cast<const V*>(E.residual + row * E.ldr + col);
+    float z[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      z[u] = pre_activation(acc[u], s, t[u], E.bias ? (float)b[u] : 0.0f);
+    activate_all(z, E.act);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      float z = pre_activation(acc[u], s, t[u], E.bias ? (float)b[u] : 0.0f);
-      z = activate(z, E.act);
-      if (E.residual) z += (float)r[u];
-      o[u] = (O)z;
+      if (E.residual) z[u] += (float)r[u];
+      o[u] = (O)z[u];
     }
     *reinterpret_cast<V*>(E.c + row * E.ldc + col) = o;
     return;
   }
-#pragma unroll
+#pragma unroll 1
   for (int u = 0; u < 4; ++u) {
     const int64_t j = col + u;
-    if (j >= E.n) continue;
-    float z = pre_activation(acc[u], s, E.sw[j], E.bias ? (float)E.bias[j] : 0.0f);
-    z = activate(z, E.act);
-    if (E.residual) z += (float)E.residual[row * E.ldr + j];
-    E.c[row * E.ldc + j] = (O)z;
+    if (j >= E.n) break;
+    put1(E, row, j, u == 0 ? acc[0] : (u == 1 ? acc[1] : acc[2]));
   }
 }
 
-// Eight consecutive outputs of one row: one 16-byte access where a type has two bytes.
+// The outputs from col to the row's end, fewer than eight, from staged sums.
 template <typename O>
-__device__ __forceinline__ void put8(const Epilogue<O>& E, int64_t row, int64_t col,
-                                     const v4i& lo, const v4i& hi) {
-  typedef O V __attribute__((ext_vector_type(8), aligned(sizeof(O))));
-  typedef float F __attribute__((ext_vector_type(8), aligned(4)));
-  if (row >= E.m || col >= E.n) return;
-  if (col + 8 > E.n) {
-    put4(E, row, col, lo);
-    put4(E, row, col + 4, hi);
-    return;
-  }
-  const float s = E.sx[row];
-  const F t = *reinterpret_cast<const F*>(E.sw + col);
-  V b, r, o;
-  if (E.bias) b = *reinterpret_cast<const V*>(E.bias + col);
-  if (E.residual) r = *reinterpret_cast<const V*>(E.residual + row * E.ldr + col);
-  float z[8];
-#pragma unroll
-  for (int u = 0; u < 8; ++u)
-    z[u] = pre_activation(u < 4 ? lo[u & 3] : hi[u & 3], s, t[u], E.bias ? (float)b[u] : 0.0f);
-#pragma unroll
-  for (int u = 0; u < 8; ++u) z[u] = activate(z[u], E.act);
-#pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    if (E.residual) z[u] += (float)r[u];
-    o[u] = (O)z[u];
-  }
-  *reinterpret_cast<V*>(E.c + row * E.ldc + col) = o;
+__device__ __forceinline__ void put_ragged(const Epilogue<O>& E, int64_t row, int64_t col,
+                                        const int32_t* sums) {
+#pragma unroll 1
+  for (int u = 0; col + u < E.n; ++u) put1(E, row, col + u, sums[u]);
 }
 
 // Bytes h .. h + 15 of a row of which `left` bytes are left from p on, zero past them, at any
@@ -253,10 +239,11 @@ constexpr int kStepK = 128;   // K bytes of a step: whole cache lines of every r
 constexpr int kXcds = 8;
 
 // Shape of a workgroup tile: kBM x kBN outputs by kWR x kWC waves, each wave TI x TJ blocks
-// of 16 x 16, operands in a ring of kS stages of one K step.
-template <int kBM, int kBN, int kWR, int kWC, int kS>
+// of 16 x 16, operands in a ring of two stages of one K step.
+template <int kBM, int kBN, int kWR, int kWC>
 struct Tile {
-  static constexpr int BM = kBM, BN = kBN, WR = kWR, WC = kWC, S = kS;
+  static constexpr int BM = kBM, BN = kBN, WR = kWR, WC = kWC;
+  static constexpr int S = 2;   // stages of the ring
   static constexpr int NW = WR * WC;
   static constexpr int WM = BM / WR, WN = BN / WC;
   static constexpr int TI = WM / 16, TJ = WN / 16;
@@ -269,17 +256,16 @@ struct Tile {
                                                                                      : TI / 4);
   static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "loads of A and B are whole");
   static_assert(TI % kPhase == 0 && kPhase * 16 * kPitch * 4 * NW <= S * kStage, "staging fits");
-  static_assert(kLoads <= TI * TJ, "a load after each MFMA of a half at most");
 };
 
 // X W^T over the K steps [t0, t1) of a tile: operand tiles go through LDS (direct loads where
 // rows are 16-byte aligned and k is a multiple of 16; else through registers, zero past k).
 // An LDS row is 128 bytes, its eight 16-byte chunks XORed with (row >> 1) & 7 so that the 16
 // lanes of a fragment read (rows r .. r + 15, one logical chunk) cover all 64 banks.
-// Per step every wave runs two halves of TI x TJ MFMAs (16 x 16 x 64); the fragments of the
-// next half are read between the MFMAs of the current one.  Between the halves the wave waits
-// for its loads of step t + 1 and its reads, and the barrier makes step t + 1 complete and
-// step t fully read; the second half issues the loads of step t + kS into step t's stage.
+// Per step every wave runs quarters of 2 x TJ blocks; before the last one it waits for its
+// loads of step t + 1 and for its reads of step t (the last quarter's operands are in
+// registers by then), so one barrier a step makes step t + 1 complete and step t's stage free
+// for step t + 2, whose loads have three quarters of a step to land.
 template <typename O, typename TL, bool kDirect>
 __global__ __launch_bounds__(64 * TL::NW) void int8linear_tile_kernel(
     int64_t k, const int8_t* __restrict__ x, int64_t ldx, const int8_t* __restrict__ w,
@@ -338,7 +324,7 @@ __global__ __launch_bounds__(64 * TL::NW) void int8linear_tile_kernel(
     const bool is_w = wave + NW * q >= BM / 8;
     const int8_t* base = (is_w ? base_w : base_x) + (int64_t)t * kStepK;
     if constexpr (kDirect) {
-      // a chunk past k re-reads the row's last one; the fragments of X are zeroed there
+      // a chunk past k re-reads the row's last one (clear_tail)
       const int64_t rest = left(t) - 16;
       const uint32_t c = chunk16 < rest ? chunk16 : (uint32_t)rest;
       dma16_sbase(voff[q] + c, (uint64_t)base,
@@ -365,40 +351,70 @@ __global__ __launch_bounds__(64 * TL::NW) void int8linear_tile_kernel(
   const int frow = lane & 15, fchunk = lane >> 4, sw = frow >> 1;
   const int off0 = ((0 + fchunk) ^ sw) << 4, off1 = ((4 + fchunk) ^ sw) << 4;
   const int arow = (wr * TL::WM + frow) * kStepK, brow = (BM + wc * TL::WN + frow) * kStepK;
-  v4i fa[2][TI], fb[2][TJ];
-  auto read = [&](int h, int t, int idx) {   // fragment idx of half h of step t
-    const int8_t* st = lds + (t % S) * TL::kStage + (h ? off1 : off0);
-    if (idx < TI) {
-      v4i v = *reinterpret_cast<const v4i*>(st + arow + idx * 16 * kStepK);
-      if (kDirect && left(t) < kStepK)   // uniform
-        v = 64 * h + 16 * fchunk < left(t) ? v : v4i{0, 0, 0, 0};
-      fa[h][idx] = v;
-    } else {
-      fb[h][idx - TI] = *reinterpret_cast<const v4i*>(st + brow + (idx - TI) * 16 * kStepK);
-    }
+  v4i fa[2][2][2], fb[2][TJ];   // fa[set][K half][row block of a quarter], fb[K half][block]
+  auto read_a = [&](int set, const int8_t* st, int kh, int rb, int ii) {
+    fa[set][kh][ii] =
+        *reinterpret_cast<const v4i*>(st + arow + (kh ? off1 : off0) + rb * 16 * kStepK);
   };
-  auto wait_loads = [&](int younger) {   // this wave's loads but the youngest `younger` steps
-    if constexpr (kDirect) {
-      if (S > 2 && younger >= S - 2)
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L * (S - 2)) : "memory");
-      else
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  auto read_b = [&](const int8_t* st, int kh, int j) {
+    fb[kh][j] = *reinterpret_cast<const v4i*>(st + brow + (kh ? off1 : off0) + j * 16 * kStepK);
+  };
+  auto stage = [&](int t) { return lds + (t % S) * TL::kStage; };
+  // The chunks of X past k in the row's last, short step (whole chunks: k is a multiple of
+  // 16) are made zero in LDS, all waves together; what W holds there then does not count.
+  auto clear_tail = [&](int t) {
+    if (!kDirect || t >= nk || left(t) >= kStepK) return;
+    const int first = (int)left(t) / 16;
+    for (int i = threadIdx.x; i < BM * 8; i += 64 * NW) {
+      const int row = i >> 3, c = i & 7;
+      if (c >= first)
+        *reinterpret_cast<v4i*>(stage(t) + row * kStepK + ((c ^ ((row >> 1) & 7)) << 4)) =
+            v4i{0, 0, 0, 0};
     }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    wg_barrier();
+  };
+  // Quarter q (row blocks 2q and 2q + 1): MFMA idx is row block 2q + idx / (2 TJ), column block
+  // (idx / 2) % TJ, K half idx % 2, a block's two halves back to back.  Its first four MFMAs
+  // are followed by the reads of the next quarter's A fragments into the other set (the last
+  // quarter's: row blocks 0 and 1 of stage `next`); the last quarter also replaces each B
+  // fragment after its last use and issues the loads of step `tl`, if there is one.
+  constexpr int NQ = TI / 2, kQuarter = 4 * TJ;
+  static_assert(NQ % 2 == 0 && L <= kQuarter, "sets alternate; loads fit a quarter");
+  auto quarter = [&](int q, const int8_t* st, const int8_t* next, int tl) {
+    const int as = q & 1;
+    const bool is_last = q == NQ - 1;
+#pragma unroll
+    for (int idx = 0; idx < kQuarter; ++idx) {
+      const int ii = idx / (2 * TJ), j = (idx >> 1) % TJ, kh = idx & 1;
+      acc[2 * q + ii][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[kh][j], fa[as][kh][ii],
+                                                                 acc[2 * q + ii][j], 0, 0, 0);
+      if (idx < 4) {
+        if (!is_last) read_a(as ^ 1, st, idx & 1, 2 * (q + 1) + (idx >> 1), idx >> 1);
+        else read_a(as ^ 1, next, idx & 1, idx >> 1, idx >> 1);
+      }
+      if (is_last && ii == 1) read_b(next, kh, j);
+      if (is_last && (idx * L) / kQuarter != ((idx + 1) * L) / kQuarter && tl < nk)
+        load(tl, (idx * L) / kQuarter);
+      __builtin_amdgcn_sched_barrier(0);
+      // the wave that reaches the second half of a quarter first is preferred, so the two
+      // waves of a SIMD run apart
+      if (idx == kQuarter / 2 - 1) __builtin_amdgcn_s_setprio(1);
+    }
+    __builtin_amdgcn_s_setprio(0);
   };
 
   if constexpr (kDirect) {
 #pragma unroll
-    for (int t = 0; t < S; ++t)
-      if (t < nk)
+    for (int q = 0; q < L; ++q) load(0, q);
+    if (nk > 1) {
 #pragma unroll
-        for (int q = 0; q < L; ++q) load(t, q);
-    // step 0 has landed when at most the other S - 1 steps' loads are under way
-    if (nk >= S)
-      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L * (S - 1)) : "memory");
-    else
+      for (int q = 0; q < L; ++q) load(1, q);
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L) : "memory");
+    } else {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
   } else {
-    // steps 0 and 1 go in, step 2 waits in registers
 #pragma unroll
     for (int t = 0; t < 2; ++t)
       if (t < nk) {
@@ -406,37 +422,33 @@ __global__ __launch_bounds__(64 * TL::NW) void int8linear_tile_kernel(
         for (int q = 0; q < L; ++q) load(t, q);
         put_staged(t);
       }
-    static_assert(kDirect || S == 2, "register staging runs two stages");
   }
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   wg_barrier();
+  clear_tail(0);
 #pragma unroll
-  for (int idx = 0; idx < TI + TJ; ++idx) read(0, 0, idx);
+  for (int idx = 0; idx < 4; ++idx) read_a(0, lds, idx & 1, idx >> 1, idx >> 1);
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) {
+    read_b(lds, 0, j);
+    read_b(lds, 1, j);
+  }
   for (int t = 0; t < nk; ++t) {
     __builtin_amdgcn_sched_barrier(0);
+    const int8_t* st = stage(t);
     // step t + 1 waits in registers since the last step (steps 0 and 1 are in place)
     if (!kDirect && t > 0 && t + 1 < nk) put_staged(t + 1);
 #pragma unroll
-    for (int idx = 0; idx < TI * TJ; ++idx) {
-      const int i = idx / TJ, j = idx % TJ;
-      acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[0][j], fa[0][i], acc[i][j], 0, 0, 0);
-      if (idx < TI + TJ) read(1, t, idx);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    wait_loads(nk - 2 - t);
+    for (int q = 0; q < NQ - 1; ++q) quarter(q, st, st, nk);
+    // this wave's loads of step t + 1 have landed and it has read all of step t; past the
+    // barrier that holds for every wave
+    if (kDirect) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     wg_barrier();
+    clear_tail(t + 1);
     __builtin_amdgcn_sched_barrier(0);
-    const bool more = t + 1 < nk;
-    const int tl = t + (kDirect ? S : 2);
-#pragma unroll
-    for (int idx = 0; idx < TI * TJ; ++idx) {
-      const int i = idx / TJ, j = idx % TJ;
-      acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[1][j], fa[1][i], acc[i][j], 0, 0, 0);
-      if (idx < TI + TJ && more) read(0, t + 1, idx);
-      if (idx < L && tl < nk) load(tl, idx);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+    // after the last step: a harmless re-read of it
+    quarter(NQ - 1, st, t + 1 < nk ? stage(t + 1) : st, t + 2);
   }
 
   // lane l of block (i, j): row 16 i + l % 16, columns 16 j + 4 (l / 16) .. + 3
@@ -451,11 +463,43 @@ __global__ __launch_bounds__(64 * TL::NW) void int8linear_tile_kernel(
     return;
   }
   // Staged through this wave's part of the ring so that eight lanes finish one row of 64
-  // columns, eight consecutive outputs each, and the code of the epilogue stands once.
-  wg_barrier();   // every wave is past its last read
+  // columns, eight consecutive outputs each.  The rows' scales and residuals are asked for
+  // four groups of rows ahead: an output's own work is short, the latency of its operands is
+  // not.  The loop over the groups of a phase is kept a loop: written out, the epilogue does
+  // not fit the instruction cache (4096 x 16384 x 4096 with gelu and residual: 1.2 ms).
+  typedef O V8 __attribute__((ext_vector_type(8), aligned(sizeof(O))));
+  typedef float F8 __attribute__((ext_vector_type(8), aligned(4)));
+  constexpr int kLanes = TL::WN / 8, kRows = 64 / kLanes;        // lanes of a row, rows at once
+  constexpr int kIters = TL::kPhase * 16 / kRows, kPhases = TI / TL::kPhase, kAhead = 4;
+  const int lrow = lane / kLanes, lcol = 8 * (lane % kLanes);
+  const int64_t col = wcol0 + lcol;
+  const bool whole = col + 8 <= E.n;
+  float t[8], b[8], s[kAhead];
+  V8 res[kAhead];
+  auto ahead = [&](int slot, int64_t row) {
+    if (row >= E.m) return;
+    s[slot] = E.sx[row];
+    if (E.residual && whole)
+      res[slot] = *reinterpret_cast<const V8*>(E.residual + row * E.ldr + col);
+  };
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) ahead(u, wrow0 + u * kRows + lrow);
+#pragma unroll
+  for (int u = 0; u < 8; ++u) t[u] = b[u] = 0.0f;
+  if (whole) {
+    const F8 tv = *reinterpret_cast<const F8*>(E.sw + col);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) t[u] = tv[u];
+    if (E.bias) {
+      const V8 bv = *reinterpret_cast<const V8*>(E.bias + col);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) b[u] = (float)bv[u];
+    }
+  }
+  wg_barrier();   // every wave is past its last read of the ring
   int32_t* mine = reinterpret_cast<int32_t*>(lds) + wave * (TL::kPhase * 16 * TL::kPitch);
 #pragma unroll
-  for (int ph = 0; ph < TI / TL::kPhase; ++ph) {
+  for (int ph = 0; ph < kPhases; ++ph) {
 #pragma unroll
     for (int i = 0; i < TL::kPhase; ++i)
 #pragma unroll
@@ -463,13 +507,37 @@ __global__ __launch_bounds__(64 * TL::NW) void int8linear_tile_kernel(
         *reinterpret_cast<v4i*>(mine + (16 * i + frow) * TL::kPitch + 16 * j + 4 * fchunk) =
             acc[ph * TL::kPhase + i][j];
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    constexpr int kLanes = TL::WN / 8;   // lanes of a row
 #pragma unroll 1
-    for (int r = lane / kLanes; r < TL::kPhase * 16; r += 64 / kLanes) {
-      const int c = 8 * (lane % kLanes);
-      const v4i lo = *reinterpret_cast<const v4i*>(mine + r * TL::kPitch + c);
-      const v4i hi = *reinterpret_cast<const v4i*>(mine + r * TL::kPitch + c + 4);
-      put8(E, wrow0 + ph * TL::kPhase * 16 + r, wcol0 + c, lo, hi);
+    for (int it = 0; it < kIters; ++it) {
+      const int64_t row = wrow0 + (ph * kIters + it) * kRows + lrow;
+      const int32_t* from = mine + (it * kRows + lrow) * TL::kPitch + lcol;
+      const v4i lo = *reinterpret_cast<const v4i*>(from);
+      const v4i hi = *reinterpret_cast<const v4i*>(from + 4);
+      const float s0 = s[0];
+      const V8 r0 = res[0];
+#pragma unroll
+      for (int u = 0; u + 1 < kAhead; ++u) {
+        s[u] = s[u + 1];
+        res[u] = res[u + 1];
+      }
+      if ((ph * kIters + it + kAhead) < kPhases * kIters) ahead(kAhead - 1, row + kAhead * kRows);
+      if (row >= E.m) continue;
+      if (!whole) {
+        put_ragged(E, row, col, from);
+        continue;
+      }
+      float z[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        z[u] = pre_activation(u < 4 ? lo[u & 3] : hi[u & 3], s0, t[u], b[u]);
+      activate_all(z, E.act);
+      V8 o;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (E.residual) z[u] += (float)r0[u];
+        o[u] = (O)z[u];
+      }
+      *reinterpret_cast<V8*>(E.c + row * E.ldc + col) = o;
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
@@ -497,8 +565,8 @@ __global__ __launch_bounds__(256) void int8linear_join_kernel(Epilogue<O> E, int
   put4(E, row, col, s);
 }
 
-typedef Tile<256, 256, 2, 4, 2> TileLarge;
-typedef Tile<128, 128, 2, 2, 2> TileMid;
+typedef Tile<256, 256, 2, 4> TileLarge;
+typedef Tile<128, 128, 2, 2> TileMid;
 
 // How a product is run.  few: the kernel for few rows, mt x nt blocks of 16 x 16 a workgroup;
 // else tiles of one shape.  K is split over `splits` workgroups where there are fewer tiles
