@@ -108,7 +108,7 @@ _SIGNATURES = {
     "ozk_dgemm_epilogue_grad": (_int, [_i64, _i64, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr,
                                        _i64, _int, _ptr, _i64, _ptr, _i64, _ptr, _int, _int, _ptr,
                                        _size, _ptr]),
-    "ozk_int8linear_workspace_size": (_int, [_i64, _i64, _i64, _ptr]),
+    "ozk_int8linear_workspace_size": (_int, [_i64, _i64, _i64, _int, _ptr]),
     "ozk_int8linear": (_int, [_i64, _i64, _i64, _ptr, _i64, _ptr, _ptr, _i64, _ptr, _ptr, _int,
                               _ptr, _i64, _int, _ptr, _i64, _ptr, _size, _ptr]),
     "ozk_int8quant_rows": (_int, [_i64, _i64, _int, _ptr, _i64, _int, _ptr, _ptr, _f64, _ptr,
@@ -699,8 +699,10 @@ def ozk_dgemm_epilogue_grad_workspace_size(m: int, n: int, k: int, r: int) -> in
     return _size_query("ozk_dgemm_epilogue_grad_workspace_size", m, n, k, r)
 
 
-def ozk_int8linear_workspace_size(m: int, n: int, k: int) -> int:
-    return _size_query("ozk_int8linear_workspace_size", m, n, k)
+def ozk_int8linear_workspace_size(m: int, n: int, k: int, aligned: bool = False) -> int:
+    """aligned: X and W at multiples of 16 bytes, k and both leading dimensions multiples of
+    16 and the latter below 2^24."""
+    return _size_query("ozk_int8linear_workspace_size", m, n, k, 1 if aligned else 0)
 
 
 def ozk_layernorm_backward_workspace_size(rows: int, cols: int, dtype) -> int:
@@ -809,7 +811,9 @@ def ozk_int8linear(x: torch.Tensor, scale_x: torch.Tensor, w: torch.Tensor,
     with _On(x.device):
         if out is None:
             out = torch.empty((m, n), dtype=dtype, device=x.device)
-        ws_bytes = ozk_int8linear_workspace_size(m, n, k)
+        aligned = ((x.data_ptr() | w.data_ptr() | _ld(x) | _ld(w) | k) & 15 == 0
+                   and max(_ld(x), _ld(w)) < 1 << 24)
+        ws_bytes = ozk_int8linear_workspace_size(m, n, k, aligned)
         if workspace is None and ws_bytes > 0:
             workspace = _workspace(ws_bytes, x.device)
         _call("ozk_int8linear", m, n, k, _dev_ptr(x), _ld(x), _dev_ptr(scale_x), _dev_ptr(w),

@@ -33,6 +33,9 @@ DEVICE_FLAGS = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang
 # (cross-lane swaps, conversions): results in VGPRs save a copy out of the AGPRs each.
 EXTRA_FLAGS = {"crt.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                "dgemm_epilogue.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+               # without it the accumulators of the smaller tiles are copied between AGPRs and
+               # VGPRs around every MFMA
+               "int8linear.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                # the 6-product encoding table is searched at compile time
                "fp4awe.hip": ["-fconstexpr-steps=16777216"],
                "fp4awe4.hip": ["-fconstexpr-steps=16777216"]}

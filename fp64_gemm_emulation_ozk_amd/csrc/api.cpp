@@ -896,11 +896,11 @@ int ozk_dgemm_epilogue_grad(int64_t m, int64_t n, int64_t k, const double* dC, i
 }
 
 // ---------------------------------------------------------------- int8 linear layer
-int ozk_int8linear_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
-  if (!bytes || m < 0 || n < 0 || k < 1) return OZK_EINVAL;
+int ozk_int8linear_workspace_size(int64_t m, int64_t n, int64_t k, int aligned, size_t* bytes) {
+  if (!bytes || m < 0 || n < 0 || k < 1 || (aligned != 0 && aligned != 1)) return OZK_EINVAL;
   if (k > OZK_MAX_K) return OZK_ERANGE;
   if (m > 0x7fffffffll || n > 0x7fffffffll) return OZK_EUNSUPPORTED;
-  *bytes = int8linear_workspace(m, n, k);
+  *bytes = int8linear_workspace(m, n, k, aligned != 0);
   return OZK_OK;
 }
 
@@ -921,7 +921,7 @@ int ozk_int8linear(int64_t m, int64_t n, int64_t k, const int8_t* X, int64_t ldx
       !aligned(residual, e) || !aligned(C, e))
     return OZK_EINVAL;
   if (m > 0x7fffffffll || n > 0x7fffffffll) return OZK_EUNSUPPORTED;
-  const size_t need = int8linear_workspace(m, n, k);
+  const size_t need = int8linear_workspace(m, n, k, int8linear_aligned(X, ldx, W, ldw, k));
   if (need > workspace_bytes || (need > 0 && !workspace)) return OZK_EWORKSPACE;
   if (need > 0 && !aligned(workspace, 256)) return OZK_EINVAL;
   return launch_int8linear(m, n, k, X, ldx, scale_x, W, ldw, scale_w, bias, act, residual, ldr,

@@ -1,8 +1,6 @@
 // int8 linear layer: C = act(s t^T * (X W^T) + 1 b^T) + R, X m x k and W n x k int8 with K
 // contiguous in both, s and t fp32 scales of their rows.  The int8 product is exact in
 // int32 (k <= OZK_MAX_K); everything after it is fp32, rounded once to the output's type.
-#include <type_traits>
-
 #include "activation.h"
 #include "lds_dma.h"
 #include "ozk_internal.h"
@@ -84,36 +82,37 @@ __device__ __forceinline__ void put_ragged(const Epilogue<O>& E, int64_t row, in
   for (int u = 0; col + u < E.n; ++u) put1(E, row, col + u, sums[u]);
 }
 
-// Bytes h .. h + 15 of a row of which `left` bytes are left from p on, zero past them, at any
-// alignment.  The last bytes come from the 16 that end the row, shifted down; a row shorter
-// than that (`shorter`) is read byte by byte.
-__device__ __forceinline__ v4i load16(const int8_t* __restrict__ p, int64_t h, int64_t left,
-                                      bool shorter) {
-  if (h + 16 <= left) return *reinterpret_cast<const v4i_bytes*>(p + h);
-  uint64_t lo = 0, hi = 0;
-  if (h < left) {
-    if (!shorter) {
-      const v4i v = *reinterpret_cast<const v4i_bytes*>(p + left - 16);
-      lo = (uint64_t)(uint32_t)v[0] | (uint64_t)(uint32_t)v[1] << 32;
-      hi = (uint64_t)(uint32_t)v[2] | (uint64_t)(uint32_t)v[3] << 32;
-      const int bits = 8 * (int)(h + 16 - left);   // 8 .. 120
-      if (bits >= 64) {
-        lo = hi >> (bits - 64);
-        hi = 0;
-      } else {
-        lo = lo >> bits | hi << (64 - bits);
-        hi >>= bits;
-      }
-    } else {
-#pragma unroll 1
-      for (int u = (int)(left - h) - 1; u >= 0; --u) {
-        hi = hi << 8 | lo >> 56;
-        lo = lo << 8 | (uint8_t)p[h + u];
-      }
-    }
+// Bytes h .. h + 15 of a row of k, zero past k, at any alignment, in two steps so that many
+// loads can be on their way: the 16 bytes at h or, where those leave the row, its last 16;
+// and the shift that moves what lies past k out.  k >= 16.
+__device__ __forceinline__ v4i load16(const int8_t* __restrict__ p, int64_t h, int64_t k) {
+  return *reinterpret_cast<const v4i_bytes*>(p + (h + 16 <= k ? h : k - 16));
+}
+__device__ __forceinline__ v4i shift16(const v4i& v, int64_t h, int64_t k) {
+  const int64_t over = h + 16 - k;   // bytes past k
+  if (over <= 0) return v;
+  if (over >= 16) return v4i{0, 0, 0, 0};
+  uint64_t lo = (uint64_t)(uint32_t)v[0] | (uint64_t)(uint32_t)v[1] << 32;
+  uint64_t hi = (uint64_t)(uint32_t)v[2] | (uint64_t)(uint32_t)v[3] << 32;
+  const int bits = 8 * (int)over;   // 8 .. 120
+  if (bits >= 64) {
+    lo = hi >> (bits - 64);
+    hi = 0;
+  } else {
+    lo = lo >> bits | hi << (64 - bits);
+    hi >>= bits;
   }
   return v4i{(int)(uint32_t)lo, (int)(uint32_t)(lo >> 32), (int)(uint32_t)hi,
              (int)(uint32_t)(hi >> 32)};
+}
+
+// The bytes of a row of fewer than 16.
+__device__ __forceinline__ v4i load_short(const int8_t* __restrict__ p, int64_t h, int64_t k) {
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int u = 0; u < 15; ++u)
+    if (h + u < k) w[u >> 2] |= (uint32_t)(uint8_t)p[h + u] << (8 * (u & 3));
+  return v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
 }
 
 // Four int32 partial sums of an m x n product.
@@ -129,11 +128,10 @@ __device__ __forceinline__ void put_part(int32_t* __restrict__ p, int64_t row, i
     if (col + u < n) p[row * n + col + u] = acc[u];
 }
 
-// Few rows: workgroup = 16 kMT rows x 16 kNT columns of C, its kWaves waves taking the K
-// steps of 128 bytes in turn (of the workgroup's split of K).  Operands go from global
-// memory to the matrix core's registers directly: lane l of a fragment holds row l % 16 and
-// 16 bytes of K.  Whole steps run kDeep at a time, all their loads issued first: what bounds
-// the kernel is the stream of W, so bytes in flight count.
+// Few rows at any alignment: workgroup = 16 kMT rows x 16 kNT columns of C, its kWaves waves
+// taking the K steps of 128 bytes in turn (of the workgroup's split of K).  Operands go from
+// global memory to the matrix core's registers directly: lane l of a fragment holds row
+// l % 16 and 16 bytes of K.  Whole steps run kDeep at a time, all their loads issued first.
 template <typename O, int kMT, int kNT, int kWaves, int kDeep>
 __global__ __launch_bounds__(64 * kWaves) void int8linear_few_kernel(
     int64_t k, const int8_t* __restrict__ x, int64_t ldx, const int8_t* __restrict__ w,
@@ -141,21 +139,19 @@ __global__ __launch_bounds__(64 * kWaves) void int8linear_few_kernel(
   __shared__ v4i sums[kWaves][kMT * kNT][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t tiles_n = (E.n + 16 * kNT - 1) / (16 * kNT);
   const int split = blockIdx.x % splits;
-  const int64_t id = blockIdx.x / splits;
-  const int64_t col0 = id % tiles_n * (16 * kNT), row0 = id / tiles_n * (16 * kMT);
+  const int64_t col0 = (int64_t)(blockIdx.x / splits) * (16 * kNT), lo = 16 * (lane >> 4);
   const int8_t* wp[kNT];
 #pragma unroll
   for (int j = 0; j < kNT; ++j) {
     const int64_t r = col0 + 16 * j + (lane & 15);
-    wp[j] = w + (r < E.n ? r : E.n - 1) * ldw + 16 * (lane >> 4);
+    wp[j] = w + (r < E.n ? r : E.n - 1) * ldw;
   }
   const int8_t* xp[kMT];
 #pragma unroll
   for (int i = 0; i < kMT; ++i) {
-    const int64_t r = row0 + 16 * i + (lane & 15);
-    xp[i] = x + (r < E.m ? r : E.m - 1) * ldx + 16 * (lane >> 4);
+    const int64_t r = 16 * i + (lane & 15);
+    xp[i] = x + (r < E.m ? r : E.m - 1) * ldx;
   }
   v4i acc[kMT][kNT];
 #pragma unroll
@@ -173,7 +169,7 @@ __global__ __launch_bounds__(64 * kWaves) void int8linear_few_kernel(
     for (int d = 0; d < kDeep; ++d)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int64_t at = (t + d * kWaves) * 128 + 64 * h;
+        const int64_t at = (t + d * kWaves) * 128 + 64 * h + lo;
 #pragma unroll
         for (int j = 0; j < kNT; ++j)
           fb[d][h][j] = *reinterpret_cast<const v4i_bytes*>(wp[j] + at);
@@ -194,19 +190,32 @@ __global__ __launch_bounds__(64 * kWaves) void int8linear_few_kernel(
   }
 #pragma unroll 1
   for (; t < t1; t += kWaves) {   // what is left, a short last step among it
+    v4i fb[2][kNT], fa[2][kMT];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int64_t at = t * 128 + 64 * h, lo = 16 * (lane >> 4);
-      v4i b[kNT];
+      const int64_t at = t * 128 + 64 * h + lo;
 #pragma unroll
-      for (int j = 0; j < kNT; ++j) b[j] = load16(wp[j] - lo, at + lo, k, k < 16);
+      for (int j = 0; j < kNT; ++j)
+        fb[h][j] = k < 16 ? load_short(wp[j], at, k) : load16(wp[j], at, k);
 #pragma unroll
-      for (int i = 0; i < kMT; ++i) {
-        const v4i a = load16(xp[i] - lo, at + lo, k, k < 16);
+      for (int i = 0; i < kMT; ++i)
+        fa[h][i] = k < 16 ? load_short(xp[i], at, k) : load16(xp[i], at, k);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t at = t * 128 + 64 * h + lo;
+      if (k >= 16) {
+#pragma unroll
+        for (int j = 0; j < kNT; ++j) fb[h][j] = shift16(fb[h][j], at, k);
+#pragma unroll
+        for (int i = 0; i < kMT; ++i) fa[h][i] = shift16(fa[h][i], at, k);
+      }
+#pragma unroll
+      for (int i = 0; i < kMT; ++i)
 #pragma unroll
         for (int j = 0; j < kNT; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[j], a, acc[i][j], 0, 0, 0);
-      }
+          acc[i][j] =
+              __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[h][j], fa[h][i], acc[i][j], 0, 0, 0);
     }
   }
 #pragma unroll
@@ -218,13 +227,103 @@ __global__ __launch_bounds__(64 * kWaves) void int8linear_few_kernel(
     v4i s = sums[0][b][lane];
 #pragma unroll
     for (int v = 1; v < kWaves; ++v) s += sums[v][b][lane];
-    const int64_t row = row0 + 16 * (b / kNT) + (lane & 15);
+    const int64_t row = 16 * (b / kNT) + (lane & 15);
     const int64_t col = col0 + 16 * (b % kNT) + 4 * (lane >> 4);
     if (part)
       put_part(part + split * E.m * E.n, row, col, E.m, E.n, s);
     else
       put4(E, row, col, s);
   }
+}
+
+// Up to 16 rows, aligned operands (as the tiles'): the same split of the work, but each wave
+// streams its steps through a ring of its own in LDS by direct loads of 8 rows x 128 bytes.
+// Sixteen rows x 64 bytes straight into registers, lane by lane another row, get a quarter of
+// that rate (38 against 152 bytes/ns per CU from L2, 19 against 27 from HBM).  No barriers:
+// a wave waits for its own loads, reads its fragments and refills the slot.  kXR rows of X
+// (8 for up to 8) travel with each step.
+template <typename O, int kXR, int kS>
+__global__ __launch_bounds__(512) void int8linear_stream_kernel(
+    int64_t k, const int8_t* __restrict__ x, int64_t ldx, const int8_t* __restrict__ w,
+    int64_t ldw, Epilogue<O> E, int splits, int32_t* __restrict__ part) {
+  constexpr int kWaves = 8, kSlot = (16 + kXR) * 128, L = kSlot / 1024;
+  __shared__ __attribute__((aligned(1024))) int8_t lds[kWaves * kS * kSlot];
+  static_assert(kWaves * 1024 <= kWaves * kS * kSlot, "the sums fit the ring");
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int split = blockIdx.x % splits;
+  const int64_t col0 = (int64_t)(blockIdx.x / splits) * 16;
+  const int steps = (int)((k + 127) / 128);
+  const int t0 = (int)((int64_t)steps * split / splits) + wave;
+  const int t1 = (int)((int64_t)steps * (split + 1) / splits);
+  const int own = t0 < t1 ? (t1 - t0 + kWaves - 1) / kWaves : 0;   // steps t0 + 8 i
+  // load q: 8 rows of W (q < 2) or X; lane i takes row i / 8, physical chunk i % 8, which
+  // holds logical chunk (i % 8) ^ ((row >> 1) & 7)
+  uint32_t voff[L], chunk[2];
+#pragma unroll
+  for (int q = 0; q < L; ++q) {
+    const bool is_w = q < 2;
+    const int64_t r = 8 * (is_w ? q : q - 2) + (lane >> 3);
+    const int64_t last = is_w ? E.n - 1 - col0 : E.m - 1;
+    voff[q] = (uint32_t)((r < last ? r : last) * (is_w ? ldw : ldx));
+  }
+#pragma unroll
+  for (int q = 0; q < 2; ++q) chunk[q] = 16 * ((lane & 7) ^ ((4 * q + (lane >> 4)) & 7));
+  const uint32_t ring = __builtin_amdgcn_readfirstlane(lds_address(lds) + wave * (kS * kSlot));
+  const int8_t* wbase = w + col0 * ldw;
+  auto load = [&](int i) {
+    const int64_t at = (int64_t)(t0 + kWaves * i) * 128, rest = k - at - 16;
+    const uint32_t slot = ring + (uint32_t)(i % kS) * kSlot;
+#pragma unroll
+    for (int q = 0; q < L; ++q) {
+      const uint32_t c = chunk[q & 1] < rest ? chunk[q & 1] : (uint32_t)rest;
+      dma16_sbase(voff[q] + c, (uint64_t)((q < 2 ? wbase : x) + at), slot + q * 1024);
+    }
+  };
+  const int frow = lane & 15, fchunk = lane >> 4;
+  v4i acc{0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < kS; ++i)
+    if (i < own) load(i);
+  for (int i = 0; i < own; ++i) {
+    const int younger = own - 1 - i;
+    if (younger >= kS - 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L * (kS - 1)) : "memory");
+    else if (kS > 3 && younger == 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L * 2) : "memory");
+    else if (kS > 2 && younger == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const int8_t* slot = lds + wave * (kS * kSlot) + (i % kS) * kSlot;
+    const int xrow = frow & (kXR - 1);
+    v4i fb[2], fa[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      fb[h] = *reinterpret_cast<const v4i*>(slot + frow * 128 +
+                                            (((4 * h + fchunk) ^ ((frow >> 1) & 7)) << 4));
+      fa[h] = *reinterpret_cast<const v4i*>(slot + (16 + xrow) * 128 +
+                                            (((4 * h + fchunk) ^ ((xrow >> 1) & 7)) << 4));
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    if (i + kS < own) load(i + kS);
+    const int64_t left = k - (int64_t)(t0 + kWaves * i) * 128;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (left < 128) fa[h] = 64 * h + 16 * fchunk < left ? fa[h] : v4i{0, 0, 0, 0};
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[h], fa[h], acc, 0, 0, 0);
+    }
+  }
+  // every wave is past its ring: the sums take its first bytes
+  __syncthreads();
+  v4i* sums = reinterpret_cast<v4i*>(lds);
+  sums[wave * 64 + lane] = acc;
+  __syncthreads();
+  if (wave) return;
+#pragma unroll
+  for (int v = 1; v < kWaves; ++v) acc += sums[v * 64 + lane];
+  const int64_t row = frow, col = col0 + 4 * fchunk;
+  if (part)
+    put_part(part + split * E.m * E.n, row, col, E.m, E.n, acc);
+  else
+    put4(E, row, col, acc);
 }
 
 // ------------------------------------------------------------------ tiles
@@ -238,239 +337,167 @@ __device__ __forceinline__ void wg_barrier() {
 constexpr int kStepK = 128;   // K bytes of a step: whole cache lines of every row
 constexpr int kXcds = 8;
 
-// Shape of a workgroup tile: kBM x kBN outputs by kWR x kWC waves, each wave TI x TJ blocks
-// of 16 x 16, operands in a ring of two stages of one K step.
-template <int kBM, int kBN, int kWR, int kWC>
+// Shape of a workgroup tile: kBM x kBN outputs by kWR x kWC waves (times kKG, which split each
+// K step), each wave TI x TJ blocks of 16 x 16, operands in a ring of kS stages of one K step.
+template <int kBM, int kBN, int kWR, int kWC, int kKG, int kS>
 struct Tile {
-  static constexpr int BM = kBM, BN = kBN, WR = kWR, WC = kWC;
-  static constexpr int S = 2;   // stages of the ring
-  static constexpr int NW = WR * WC;
+  static constexpr int BM = kBM, BN = kBN, WR = kWR, WC = kWC, KG = kKG, S = kS;
+  static constexpr int NW = WR * WC * KG;
   static constexpr int WM = BM / WR, WN = BN / WC;
   static constexpr int TI = WM / 16, TJ = WN / 16;
   static constexpr int kStage = (BM + BN) * kStepK;   // bytes
   static constexpr int kLoads = kStage / 1024 / NW;   // 1 KiB (8 rows) per wave and load
   static constexpr int kPitch = WN + 4;               // staged outputs of a wave, in words
-  static constexpr int kPhase = S * kStage / NW / (16 * kPitch * 4) >= TI
-                                    ? TI
-                                    : (S * kStage / NW / (16 * kPitch * 4) >= TI / 2 ? TI / 2
-                                                                                     : TI / 4);
-  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "loads of A and B are whole");
-  static_assert(TI % kPhase == 0 && kPhase * 16 * kPitch * 4 * NW <= S * kStage, "staging fits");
+  // row blocks a wave finishes, and how many of them its share of the ring stages at once
+  static constexpr int kOwn = TI / KG;
+  static constexpr int kFit = S * kStage / NW / (16 * kPitch * 4);
+  static constexpr int kPhase = kFit >= kOwn ? kOwn : (kFit >= kOwn / 2 ? kOwn / 2 : kOwn / 4);
+  static_assert(BM % 16 == 0 && kStage % (1024 * NW) == 0, "loads are whole");
+  static_assert(NW % 2 == 0 && BM % 16 == 0, "one chunk for all loads of a lane");
+  static_assert(kOwn % kPhase == 0 && kPhase * 16 * kPitch * 4 * NW <= S * kStage, "staging fits");
+  static_assert(S >= 2 && S <= 6 && kLoads * (S - 1) <= 63, "the load counter's range");
 };
 
-// X W^T over the K steps [t0, t1) of a tile: operand tiles go through LDS (direct loads where
-// rows are 16-byte aligned and k is a multiple of 16; else through registers, zero past k).
+// A workgroup's tile: which one, its K steps, and its operands' way into the ring.  Rows are
+// 16-byte aligned and k is a multiple of 16 (other operands are laid out so first).
 // An LDS row is 128 bytes, its eight 16-byte chunks XORed with (row >> 1) & 7 so that the 16
 // lanes of a fragment read (rows r .. r + 15, one logical chunk) cover all 64 banks.
-// Per step every wave runs quarters of 2 x TJ blocks; before the last one it waits for its
-// loads of step t + 1 and for its reads of step t (the last quarter's operands are in
-// registers by then), so one barrier a step makes step t + 1 complete and step t's stage free
-// for step t + 2, whose loads have three quarters of a step to land.
-template <typename O, typename TL, bool kDirect>
-__global__ __launch_bounds__(64 * TL::NW) void int8linear_tile_kernel(
-    int64_t k, const int8_t* __restrict__ x, int64_t ldx, const int8_t* __restrict__ w,
-    int64_t ldw, Epilogue<O> E, int tiles_m, int tiles_n, int splits, int group_m,
-    int32_t* __restrict__ part) {
-  constexpr int BM = TL::BM, BN = TL::BN, TI = TL::TI, TJ = TL::TJ, NW = TL::NW, S = TL::S;
-  constexpr int L = TL::kLoads;
-  __shared__ __attribute__((aligned(1024))) int8_t lds[S * TL::kStage];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wr = wave / TL::WC, wc = wave % TL::WC;
+template <typename TL>
+struct Walk {
+  static constexpr int BM = TL::BM, BN = TL::BN, NW = TL::NW, S = TL::S, L = TL::kLoads;
+  int8_t* lds;
+  int wave, lane;
+  int split, t0, nk;       // this block's split of K: steps t0 .. t0 + nk - 1
+  int64_t row0, col0, k;
+  const int8_t* base_x;
+  const int8_t* base_w;
+  uint32_t voff[L];        // row offset from the tile's first row, per load
+  uint32_t chunk16, wave_lds;
 
   // Block -> (split, tile row, tile column).  The hardware deals blocks out round-robin over
   // the 8 XCDs; XCD x takes one contiguous run of the order (split, groups of group_m tile
   // rows, column, row in group), so the tiles in flight on it share panels in its L2.
-  const int total = gridDim.x, per = total / kXcds, extra = total % kXcds;
-  const int xcd = blockIdx.x % kXcds;
-  const int id = xcd * per + (xcd < extra ? xcd : extra) + blockIdx.x / kXcds;
-  const int tiles = tiles_m * tiles_n;
-  const int split = id / tiles, rem = id - split * tiles;
-  const int per_group = group_m * tiles_n;
-  const int first = rem / per_group * group_m;
-  const int gsize = tiles_m - first < group_m ? tiles_m - first : group_m;
-  const int in_group = rem % per_group;
-  const int64_t row0 = (int64_t)(first + in_group % gsize) * BM;
-  const int64_t col0 = (int64_t)(in_group / gsize) * BN;
-  const int steps = (int)((k + kStepK - 1) / kStepK);
-  const int t0 = (int)((int64_t)steps * split / splits);
-  const int t1 = (int)((int64_t)steps * (split + 1) / splits);
-  const int nk = t1 - t0;
-
-  // Load q of this wave: region rg = wave + NW q, rows 8 rg .. 8 rg + 7 of X (then of W);
-  // lane i takes row i / 8 of it, physical chunk i % 8; rows past the matrix re-read its last.
-  const int8_t* base_x = x + row0 * ldx + (int64_t)t0 * kStepK;
-  const int8_t* base_w = w + col0 * ldw + (int64_t)t0 * kStepK;
-  typedef typename std::conditional<kDirect, uint32_t, int64_t>::type Offset;
-  Offset voff[L];   // row offset from the tile's first row
-  // logical K offset of the lane's chunk: the swizzle depends on the region's parity alone,
-  // which is the wave's (NW is even)
-  static_assert(NW % 2 == 0, "one chunk for all loads of a lane");
-  const uint32_t chunk16 = 16 * ((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7));
+  __device__ __forceinline__ Walk(int8_t* ring, int64_t m, int64_t n, int64_t kk,
+                                  const int8_t* x, int64_t ldx, const int8_t* w, int64_t ldw,
+                                  int tiles_m, int tiles_n, int splits, int group_m)
+      : lds(ring), k(kk) {
+    lane = threadIdx.x & 63;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int total = gridDim.x, per = total / kXcds, extra = total % kXcds;
+    const int xcd = blockIdx.x % kXcds;
+    const int id = xcd * per + (xcd < extra ? xcd : extra) + blockIdx.x / kXcds;
+    const int tiles = tiles_m * tiles_n;
+    split = id / tiles;
+    const int rem = id - split * tiles, per_group = group_m * tiles_n;
+    const int first = rem / per_group * group_m;
+    const int gsize = tiles_m - first < group_m ? tiles_m - first : group_m;
+    const int in_group = rem % per_group;
+    row0 = (int64_t)(first + in_group % gsize) * BM;
+    col0 = (int64_t)(in_group / gsize) * BN;
+    const int steps = (int)((k + kStepK - 1) / kStepK);
+    t0 = (int)((int64_t)steps * split / splits);
+    nk = (int)((int64_t)steps * (split + 1) / splits) - t0;
+    base_x = x + row0 * ldx + (int64_t)t0 * kStepK;
+    base_w = w + col0 * ldw + (int64_t)t0 * kStepK;
+    // Load q of this wave: region rg = wave + NW q, rows 8 rg .. 8 rg + 7 of X (then of W);
+    // lane i takes row i / 8 of it, physical chunk i % 8; rows past the matrix re-read its
+    // last.  The swizzle depends on the region's parity alone, which is the wave's.
+    chunk16 = 16 * ((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7));
 #pragma unroll
-  for (int q = 0; q < L; ++q) {
-    const int rg = wave + NW * q;
-    const bool is_w = rg >= BM / 8;
-    const int row = 8 * (is_w ? rg - BM / 8 : rg) + (lane >> 3);
-    const int64_t origin = is_w ? col0 : row0, last = (is_w ? E.n : E.m) - 1;
-    const int64_t gr = origin + row < last ? origin + row : last;
-    voff[q] = (Offset)((gr - origin) * (is_w ? ldw : ldx));
+    for (int q = 0; q < L; ++q) {
+      const int rg = wave + NW * q;
+      const bool is_w = rg >= BM / 8;
+      const int row = 8 * (is_w ? rg - BM / 8 : rg) + (lane >> 3);
+      const int64_t origin = is_w ? col0 : row0, last = (is_w ? n : m) - 1;
+      const int64_t gr = origin + row < last ? origin + row : last;
+      voff[q] = (uint32_t)((gr - origin) * (is_w ? ldw : ldx));
+    }
+    wave_lds = __builtin_amdgcn_readfirstlane(lds_address(lds) + wave * 1024);
   }
-  const uint32_t wave_lds = __builtin_amdgcn_readfirstlane(lds_address(lds) + wave * 1024);
-  v4i staged[kDirect ? 1 : L];
-  // K bytes left from the first byte of step t (of this split) on
-  auto left = [&](int t) { return k - (int64_t)(t0 + t) * kStepK; };
-  auto load = [&](int t, int q) {
+
+  // K bytes left from the first byte of step t on
+  __device__ __forceinline__ int64_t left(int t) const { return k - (int64_t)(t0 + t) * kStepK; }
+  __device__ __forceinline__ const int8_t* stage(int t) const {
+    return lds + (t % S) * TL::kStage;
+  }
+
+  // Load q of step t.  A chunk past k re-reads the row's last one (clear_tail).
+  __device__ __forceinline__ void load(int t, int q) const {
     const bool is_w = wave + NW * q >= BM / 8;
     const int8_t* base = (is_w ? base_w : base_x) + (int64_t)t * kStepK;
-    if constexpr (kDirect) {
-      // a chunk past k re-reads the row's last one (clear_tail)
-      const int64_t rest = left(t) - 16;
-      const uint32_t c = chunk16 < rest ? chunk16 : (uint32_t)rest;
-      dma16_sbase(voff[q] + c, (uint64_t)base,
-                  wave_lds + (uint32_t)(t % S) * TL::kStage + q * (NW * 1024));
-    } else {
-      staged[q] = load16(base + voff[q], chunk16, left(t), k < 16);
-    }
-  };
-  auto put_staged = [&](int t) {
-    if constexpr (!kDirect) {
-#pragma unroll
-      for (int q = 0; q < L; ++q)
-        *reinterpret_cast<v4i*>(lds + (t % S) * TL::kStage + (wave + NW * q) * 1024 +
-                                lane * 16) = staged[q];
-    }
-  };
+    const int64_t rest = left(t) - 16;
+    const uint32_t c = chunk16 < rest ? chunk16 : (uint32_t)rest;
+    dma16_sbase(voff[q] + c, (uint64_t)base,
+                wave_lds + (uint32_t)(t % S) * TL::kStage + q * (NW * 1024));
+  }
 
-  v4i acc[TI][TJ];
-#pragma unroll
-  for (int i = 0; i < TI; ++i)
-#pragma unroll
-    for (int j = 0; j < TJ; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+  // Waits until of this wave's loads at most those of the youngest `younger` steps are under
+  // way (`most`: the number that is asked for on every step but the last ones).
+  template <int kMost>
+  __device__ __forceinline__ void wait_loads(int younger) const {
+    if (younger >= kMost) {
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L * kMost) : "memory");
+      return;
+    }
+    if (kMost > 3 && younger == 3) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L * 3) : "memory");
+    else if (kMost > 2 && younger == 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L * 2) : "memory");
+    else if (kMost > 1 && younger == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  }
 
-  const int frow = lane & 15, fchunk = lane >> 4, sw = frow >> 1;
-  const int off0 = ((0 + fchunk) ^ sw) << 4, off1 = ((4 + fchunk) ^ sw) << 4;
-  const int arow = (wr * TL::WM + frow) * kStepK, brow = (BM + wc * TL::WN + frow) * kStepK;
-  v4i fa[2][2][2], fb[2][TJ];   // fa[set][K half][row block of a quarter], fb[K half][block]
-  auto read_a = [&](int set, const int8_t* st, int kh, int rb, int ii) {
-    fa[set][kh][ii] =
-        *reinterpret_cast<const v4i*>(st + arow + (kh ? off1 : off0) + rb * 16 * kStepK);
-  };
-  auto read_b = [&](const int8_t* st, int kh, int j) {
-    fb[kh][j] = *reinterpret_cast<const v4i*>(st + brow + (kh ? off1 : off0) + j * 16 * kStepK);
-  };
-  auto stage = [&](int t) { return lds + (t % S) * TL::kStage; };
+  // The ring's first stages asked for, step 0 in place for every wave.
+  __device__ __forceinline__ void begin() const {
+#pragma unroll
+    for (int t = 0; t < S; ++t)
+      if (t < nk)
+#pragma unroll
+        for (int q = 0; q < L; ++q) load(t, q);
+    wait_loads<S - 1>(nk - 1);
+    wg_barrier();
+    clear_tail(0);
+  }
+
   // The chunks of X past k in the row's last, short step (whole chunks: k is a multiple of
   // 16) are made zero in LDS, all waves together; what W holds there then does not count.
-  auto clear_tail = [&](int t) {
-    if (!kDirect || t >= nk || left(t) >= kStepK) return;
+  __device__ __forceinline__ void clear_tail(int t) const {
+    if (t >= nk || left(t) >= kStepK) return;
     const int first = (int)left(t) / 16;
     for (int i = threadIdx.x; i < BM * 8; i += 64 * NW) {
       const int row = i >> 3, c = i & 7;
       if (c >= first)
-        *reinterpret_cast<v4i*>(stage(t) + row * kStepK + ((c ^ ((row >> 1) & 7)) << 4)) =
-            v4i{0, 0, 0, 0};
+        *reinterpret_cast<v4i*>(lds + (t % S) * TL::kStage + row * kStepK +
+                                ((c ^ ((row >> 1) & 7)) << 4)) = v4i{0, 0, 0, 0};
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     wg_barrier();
-  };
-  // Quarter q (row blocks 2q and 2q + 1): MFMA idx is row block 2q + idx / (2 TJ), column block
-  // (idx / 2) % TJ, K half idx % 2, a block's two halves back to back.  Its first four MFMAs
-  // are followed by the reads of the next quarter's A fragments into the other set (the last
-  // quarter's: row blocks 0 and 1 of stage `next`); the last quarter also replaces each B
-  // fragment after its last use and issues the loads of step `tl`, if there is one.
-  constexpr int NQ = TI / 2, kQuarter = 4 * TJ;
-  static_assert(NQ % 2 == 0 && L <= kQuarter, "sets alternate; loads fit a quarter");
-  auto quarter = [&](int q, const int8_t* st, const int8_t* next, int tl) {
-    const int as = q & 1;
-    const bool is_last = q == NQ - 1;
-#pragma unroll
-    for (int idx = 0; idx < kQuarter; ++idx) {
-      const int ii = idx / (2 * TJ), j = (idx >> 1) % TJ, kh = idx & 1;
-      acc[2 * q + ii][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[kh][j], fa[as][kh][ii],
-                                                                 acc[2 * q + ii][j], 0, 0, 0);
-      if (idx < 4) {
-        if (!is_last) read_a(as ^ 1, st, idx & 1, 2 * (q + 1) + (idx >> 1), idx >> 1);
-        else read_a(as ^ 1, next, idx & 1, idx >> 1, idx >> 1);
-      }
-      if (is_last && ii == 1) read_b(next, kh, j);
-      if (is_last && (idx * L) / kQuarter != ((idx + 1) * L) / kQuarter && tl < nk)
-        load(tl, (idx * L) / kQuarter);
-      __builtin_amdgcn_sched_barrier(0);
-      // the wave that reaches the second half of a quarter first is preferred, so the two
-      // waves of a SIMD run apart
-      if (idx == kQuarter / 2 - 1) __builtin_amdgcn_s_setprio(1);
-    }
-    __builtin_amdgcn_s_setprio(0);
-  };
+  }
+};
 
-  if constexpr (kDirect) {
-#pragma unroll
-    for (int q = 0; q < L; ++q) load(0, q);
-    if (nk > 1) {
-#pragma unroll
-      for (int q = 0; q < L; ++q) load(1, q);
-      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L) : "memory");
-    } else {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    }
-  } else {
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-      if (t < nk) {
-#pragma unroll
-        for (int q = 0; q < L; ++q) load(t, q);
-        put_staged(t);
-      }
-  }
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  wg_barrier();
-  clear_tail(0);
-#pragma unroll
-  for (int idx = 0; idx < 4; ++idx) read_a(0, lds, idx & 1, idx >> 1, idx >> 1);
-#pragma unroll
-  for (int j = 0; j < TJ; ++j) {
-    read_b(lds, 0, j);
-    read_b(lds, 1, j);
-  }
-  for (int t = 0; t < nk; ++t) {
-    __builtin_amdgcn_sched_barrier(0);
-    const int8_t* st = stage(t);
-    // step t + 1 waits in registers since the last step (steps 0 and 1 are in place)
-    if (!kDirect && t > 0 && t + 1 < nk) put_staged(t + 1);
-#pragma unroll
-    for (int q = 0; q < NQ - 1; ++q) quarter(q, st, st, nk);
-    // this wave's loads of step t + 1 have landed and it has read all of step t; past the
-    // barrier that holds for every wave
-    if (kDirect) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    wg_barrier();
-    clear_tail(t + 1);
-    __builtin_amdgcn_sched_barrier(0);
-    // after the last step: a harmless re-read of it
-    quarter(NQ - 1, st, t + 1 < nk ? stage(t + 1) : st, t + 2);
-  }
-
-  // lane l of block (i, j): row 16 i + l % 16, columns 16 j + 4 (l / 16) .. + 3
-  const int64_t wrow0 = row0 + wr * TL::WM, wcol0 = col0 + wc * TL::WN;
+// The outputs of a wave's NI x TJ blocks (lane l of block (i, j): row 16 i + l % 16, columns
+// 16 j + 4 (l / 16) .. + 3), or their partial sums.  The blocks are staged through this wave's
+// part `mine` of the ring so that eight lanes finish one row of 64 columns, eight consecutive
+// outputs each.  The rows' scales and residuals are asked for four groups of rows ahead: an
+// output's own work is short, the latency of its operands is not.  The loop over the groups
+// of a phase is kept a loop: written out, the epilogue does not fit the instruction cache
+// (4096 x 16384 x 4096 with gelu and residual took 1.23 ms so, 0.29 as a loop).
+template <typename TL, typename O, int NI>
+__device__ __forceinline__ void put_tile(const Epilogue<O>& E, const v4i (&acc)[NI][TL::TJ],
+                                         int64_t wrow0, int64_t wcol0, int lane, int32_t* mine,
+                                         int32_t* __restrict__ part) {
+  constexpr int TJ = TL::TJ;
+  const int frow = lane & 15, fchunk = lane >> 4;
   if (part) {
-    int32_t* p = part + (int64_t)split * E.m * E.n;
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
       for (int j = 0; j < TJ; ++j)
-        put_part(p, wrow0 + 16 * i + frow, wcol0 + 16 * j + 4 * fchunk, E.m, E.n, acc[i][j]);
+        put_part(part, wrow0 + 16 * i + frow, wcol0 + 16 * j + 4 * fchunk, E.m, E.n, acc[i][j]);
     return;
   }
-  // Staged through this wave's part of the ring so that eight lanes finish one row of 64
-  // columns, eight consecutive outputs each.  The rows' scales and residuals are asked for
-  // four groups of rows ahead: an output's own work is short, the latency of its operands is
-  // not.  The loop over the groups of a phase is kept a loop: written out, the epilogue does
-  // not fit the instruction cache (4096 x 16384 x 4096 with gelu and residual: 1.2 ms).
   typedef O V8 __attribute__((ext_vector_type(8), aligned(sizeof(O))));
   typedef float F8 __attribute__((ext_vector_type(8), aligned(4)));
   constexpr int kLanes = TL::WN / 8, kRows = 64 / kLanes;        // lanes of a row, rows at once
-  constexpr int kIters = TL::kPhase * 16 / kRows, kPhases = TI / TL::kPhase, kAhead = 4;
+  constexpr int kIters = TL::kPhase * 16 / kRows, kPhases = NI / TL::kPhase, kAhead = 4;
   const int lrow = lane / kLanes, lcol = 8 * (lane % kLanes);
   const int64_t col = wcol0 + lcol;
   const bool whole = col + 8 <= E.n;
@@ -483,7 +510,8 @@ __global__ __launch_bounds__(64 * TL::NW) void int8linear_tile_kernel(
       res[slot] = *reinterpret_cast<const V8*>(E.residual + row * E.ldr + col);
   };
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u) ahead(u, wrow0 + u * kRows + lrow);
+  for (int u = 0; u < kAhead; ++u)
+    if (u < kIters * kPhases) ahead(u, wrow0 + u * kRows + lrow);
 #pragma unroll
   for (int u = 0; u < 8; ++u) t[u] = b[u] = 0.0f;
   if (whole) {
@@ -496,8 +524,6 @@ __global__ __launch_bounds__(64 * TL::NW) void int8linear_tile_kernel(
       for (int u = 0; u < 8; ++u) b[u] = (float)bv[u];
     }
   }
-  wg_barrier();   // every wave is past its last read of the ring
-  int32_t* mine = reinterpret_cast<int32_t*>(lds) + wave * (TL::kPhase * 16 * TL::kPitch);
 #pragma unroll
   for (int ph = 0; ph < kPhases; ++ph) {
 #pragma unroll
@@ -543,6 +569,205 @@ __global__ __launch_bounds__(64 * TL::NW) void int8linear_tile_kernel(
   }
 }
 
+// The large tile, whose K steps are long: per step every wave runs quarters of 2 x TJ blocks;
+// before the last one it waits for its loads of step t + 1 and for its reads of step t (the
+// last quarter's operands are in registers by then), so one barrier a step makes step t + 1
+// complete and step t's stage free for step t + S, whose loads have S - 1 steps to land less
+// a quarter.  Two stages are enough.
+template <typename O, typename TL>
+__global__ __launch_bounds__(64 * TL::NW) void int8linear_tile_kernel(
+    int64_t k, const int8_t* __restrict__ x, int64_t ldx, const int8_t* __restrict__ w,
+    int64_t ldw, Epilogue<O> E, int tiles_m, int tiles_n, int splits, int group_m,
+    int32_t* __restrict__ part) {
+  constexpr int BM = TL::BM, TI = TL::TI, TJ = TL::TJ, S = TL::S, L = TL::kLoads;
+  static_assert(TL::KG == 1, "one wave for both K halves");
+  __shared__ __attribute__((aligned(1024))) int8_t lds[S * TL::kStage];
+  const Walk<TL> W(lds, E.m, E.n, k, x, ldx, w, ldw, tiles_m, tiles_n, splits, group_m);
+  const int wr = W.wave / TL::WC, wc = W.wave % TL::WC, nk = W.nk;
+
+  v4i acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+
+  const int frow = W.lane & 15, fchunk = W.lane >> 4, sw = frow >> 1;
+  const int off0 = ((0 + fchunk) ^ sw) << 4, off1 = ((4 + fchunk) ^ sw) << 4;
+  const int arow = (wr * TL::WM + frow) * kStepK, brow = (BM + wc * TL::WN + frow) * kStepK;
+  v4i fa[2][2][2], fb[2][TJ];   // fa[set][K half][row block of a quarter], fb[K half][block]
+  auto read_a = [&](int set, const int8_t* st, int kh, int rb, int ii) {
+    fa[set][kh][ii] =
+        *reinterpret_cast<const v4i*>(st + arow + (kh ? off1 : off0) + rb * 16 * kStepK);
+  };
+  auto read_b = [&](const int8_t* st, int kh, int j) {
+    fb[kh][j] = *reinterpret_cast<const v4i*>(st + brow + (kh ? off1 : off0) + j * 16 * kStepK);
+  };
+  // Quarter q (row blocks 2q and 2q + 1): MFMA idx is row block 2q + idx / (2 TJ), column block
+  // (idx / 2) % TJ, K half idx % 2, a block's two halves back to back.  Its first four MFMAs
+  // are followed by the reads of the next quarter's A fragments into the other set (the last
+  // quarter's: row blocks 0 and 1 of stage `next`); the last quarter also replaces each B
+  // fragment after its last use and issues the loads of step `tl`, if there is one.
+  constexpr int NQ = TI / 2, kQuarter = 4 * TJ;
+  static_assert(NQ % 2 == 0 && L <= kQuarter, "sets alternate; loads fit a quarter");
+  auto quarter = [&](int q, const int8_t* st, const int8_t* next, int tl) {
+    const int as = q & 1;
+    const bool is_last = q == NQ - 1;
+#pragma unroll
+    for (int idx = 0; idx < kQuarter; ++idx) {
+      const int ii = idx / (2 * TJ), j = (idx >> 1) % TJ, kh = idx & 1;
+      acc[2 * q + ii][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[kh][j], fa[as][kh][ii],
+                                                                 acc[2 * q + ii][j], 0, 0, 0);
+      if (idx < 4) {
+        if (!is_last) read_a(as ^ 1, st, idx & 1, 2 * (q + 1) + (idx >> 1), idx >> 1);
+        else read_a(as ^ 1, next, idx & 1, idx >> 1, idx >> 1);
+      }
+      if (is_last && ii == 1) read_b(next, kh, j);
+      if (is_last && (idx * L) / kQuarter != ((idx + 1) * L) / kQuarter && tl < nk)
+        W.load(tl, (idx * L) / kQuarter);
+      __builtin_amdgcn_sched_barrier(0);
+      // the wave that reaches the second half of a quarter first is preferred, so the two
+      // waves of a SIMD run apart
+      if (idx == kQuarter / 2 - 1) __builtin_amdgcn_s_setprio(1);
+    }
+    __builtin_amdgcn_s_setprio(0);
+  };
+
+  W.begin();
+#pragma unroll
+  for (int idx = 0; idx < 4; ++idx) read_a(0, lds, idx & 1, idx >> 1, idx >> 1);
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) {
+    read_b(lds, 0, j);
+    read_b(lds, 1, j);
+  }
+  for (int t = 0; t < nk; ++t) {
+    __builtin_amdgcn_sched_barrier(0);
+    const int8_t* st = W.stage(t);
+#pragma unroll
+    for (int q = 0; q < NQ - 1; ++q) quarter(q, st, st, nk);
+    // this wave's loads of step t + 1 have landed and it has read all of step t; past the
+    // barrier that holds for every wave
+    W.template wait_loads<S - 2>(nk - 2 - t);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    wg_barrier();
+    W.clear_tail(t + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    // after the last step: a harmless re-read of it
+    quarter(NQ - 1, st, t + 1 < nk ? W.stage(t + 1) : st, t + S);
+  }
+  wg_barrier();   // every wave is past its last read of the ring
+  put_tile<TL, O, TI>(E, acc, W.row0 + wr * TL::WM, W.col0 + wc * TL::WN, W.lane,
+                      reinterpret_cast<int32_t*>(lds) + W.wave * (TL::kPhase * 16 * TL::kPitch),
+                      part ? part + (int64_t)W.split * E.m * E.n : nullptr);
+}
+
+// The smaller tiles, whose K steps take a fraction of a load's latency: as many stages as
+// LDS holds, and per step one barrier, one set of fragment reads and one run of MFMAs.  A
+// pair of waves shares the outputs of a wave and splits each step's K bytes, 64 for either
+// (two waves per SIMD cover each other's reads); the sums of both meet in LDS at the end.
+// Behind the barrier of step t the wave reads step t + 1 and asks for step t + S while step
+// t's MFMAs run from registers.
+template <typename O, typename TL>
+__global__ __launch_bounds__(64 * TL::NW) void int8linear_small_kernel(
+    int64_t k, const int8_t* __restrict__ x, int64_t ldx, const int8_t* __restrict__ w,
+    int64_t ldw, Epilogue<O> E, int tiles_m, int tiles_n, int splits, int group_m,
+    int32_t* __restrict__ part) {
+  constexpr int BM = TL::BM, TI = TL::TI, TJ = TL::TJ, S = TL::S, L = TL::kLoads;
+  static_assert(TL::KG == 2 && TI % 2 == 0 && L <= TI * TJ, "pairs of waves");
+  __shared__ __attribute__((aligned(1024))) int8_t lds[S * TL::kStage];
+  const Walk<TL> W(lds, E.m, E.n, k, x, ldx, w, ldw, tiles_m, tiles_n, splits, group_m);
+  const int kh = W.wave / (TL::WR * TL::WC), wt = W.wave % (TL::WR * TL::WC);
+  const int wr = wt / TL::WC, wc = wt % TL::WC, nk = W.nk;
+
+  v4i acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+
+  const int frow = W.lane & 15, fchunk = W.lane >> 4, sw = frow >> 1;
+  const int off = ((4 * kh + fchunk) ^ sw) << 4;
+  const int arow = (wr * TL::WM + frow) * kStepK + off;
+  const int brow = (BM + wc * TL::WN + frow) * kStepK + off;
+  v4i fa[2][TI], fb[2][TJ];
+  auto read = [&](int set, int t) {
+    const int8_t* st = W.stage(t);
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+      fb[set][j] = *reinterpret_cast<const v4i*>(st + brow + j * 16 * kStepK);
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+      fa[set][i] = *reinterpret_cast<const v4i*>(st + arow + i * 16 * kStepK);
+  };
+  auto step = [&](int set, int t) {
+    W.template wait_loads<S - 2>(nk - 2 - t);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    wg_barrier();
+    W.clear_tail(t + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    if (t + 1 < nk) read(set ^ 1, t + 1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int idx = 0; idx < TI * TJ; ++idx) {
+      const int i = idx / TJ, j = idx % TJ;
+      acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[set][j], fa[set][i], acc[i][j], 0, 0, 0);
+      if (idx < L && t + S < nk) W.load(t + S, idx);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  W.begin();
+  read(0, 0);
+  int t = 0;
+  for (; t + 1 < nk; t += 2) {
+    step(0, t);
+    step(1, t + 1);
+  }
+  if (t < nk) step(0, t);
+
+  // Wave kh of a pair finishes row blocks kh TI / 2 ..: the other half goes to its partner.
+  wg_barrier();   // every wave is past its last read of the ring
+  constexpr int H = TI / 2;
+  v4i* boxes = reinterpret_cast<v4i*>(lds);   // [wave][H][TJ][lane]
+  static_assert(TL::NW * H * TJ * 1024 <= S * TL::kStage, "halves fit the ring");
+  v4i own[H][TJ];
+#pragma unroll
+  for (int i = 0; i < H; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      boxes[((W.wave * H + i) * TJ + j) * 64 + W.lane] = kh ? acc[i][j] : acc[H + i][j];
+      own[i][j] = kh ? acc[H + i][j] : acc[i][j];
+    }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  wg_barrier();
+  const int partner = wt + (kh ? 0 : TL::WR * TL::WC);
+#pragma unroll
+  for (int i = 0; i < H; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) own[i][j] += boxes[((partner * H + i) * TJ + j) * 64 + W.lane];
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  wg_barrier();
+  put_tile<TL, O, H>(E, own, W.row0 + wr * TL::WM + kh * 16 * H, W.col0 + wc * TL::WN, W.lane,
+                     reinterpret_cast<int32_t*>(lds) + W.wave * (TL::kPhase * 16 * TL::kPitch),
+                     part ? part + (int64_t)W.split * E.m * E.n : nullptr);
+}
+
+// Rows of k bytes at any alignment laid out with leading dimension kp (a multiple of 16),
+// zeros from k on: both operands in one launch, 16 bytes a thread.
+__global__ __launch_bounds__(256) void int8linear_layout_kernel(
+    int64_t m, int64_t n, int64_t k, int64_t kp, const int8_t* __restrict__ x, int64_t ldx,
+    int8_t* __restrict__ xo, const int8_t* __restrict__ w, int64_t ldw,
+    int8_t* __restrict__ wo) {
+  const int64_t chunks = kp / 16, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  int64_t row = id / chunks;
+  const int64_t h = id % chunks * 16;
+  if (row >= m + n) return;
+  const bool is_w = row >= m;
+  row -= is_w ? m : 0;
+  const int8_t* p = is_w ? w + row * ldw : x + row * ldx;
+  const v4i v = k < 16 ? load_short(p, h, k) : shift16(load16(p, h, k), h, k);
+  *reinterpret_cast<v4i*>((is_w ? wo : xo) + row * kp + h) = v;
+}
+
 // The outputs of a product whose K was split: the partial sums added, then the epilogue.
 template <typename O>
 __global__ __launch_bounds__(256) void int8linear_join_kernel(Epilogue<O> E, int splits,
@@ -565,57 +790,84 @@ __global__ __launch_bounds__(256) void int8linear_join_kernel(Epilogue<O> E, int
   put4(E, row, col, s);
 }
 
-typedef Tile<256, 256, 2, 4> TileLarge;
-typedef Tile<128, 128, 2, 2> TileMid;
+typedef Tile<256, 256, 2, 4, 1, 2> TileLarge;
+typedef Tile<128, 128, 2, 2, 2, 4> TileMid;
+typedef Tile<64, 128, 1, 4, 2, 6> TileSmall;
 
-// How a product is run.  few: the kernel for few rows, mt x nt blocks of 16 x 16 a workgroup;
-// else tiles of one shape.  K is split over `splits` workgroups where there are fewer tiles
-// than the compute units take.
+// How a product is run: by the kernels for few rows (a workgroup takes all rows) or by tiles
+// of one shape; K is split over `splits` workgroups where there are fewer tiles than the
+// compute units take.
+enum Shape { kStream, kFew, kSmall, kMid, kLarge };
 struct Plan {
-  bool few, large;
-  int mt, nt;
+  Shape shape;
   int64_t tiles_m, tiles_n;
   int splits;
 };
 
-Plan plan_of(int64_t m, int64_t n, int64_t k) {
-  Plan p{};
+// Up to 16 rows: the stream kernel; unaligned, up to 64 rows, the few kernel (37 x 4100 x 1001:
+// 7.5 us, against 13.8 with the operands laid out for a tile).  More rows: the tile shape and
+// split of the least estimated time, in microseconds, of rounds of 256 workgroups that each
+// cost `fixed` and `step` per K step.  Measured, one round of 4096 K values: small 22.7, mid
+// 29, large 61 (512, 1024, 4096 x 4096 outputs), and 5.3, 7.1, 9.6 for 128.  A split costs the
+// launch of the join and the partial sums' way out and back (5 TB/s).
+Plan plan_of(int64_t m, int64_t n, int64_t k, bool aligned) {
   const int64_t steps = (k + kStepK - 1) / kStepK;
-  p.few = m <= 64;
-  if (p.few) {
-    p.mt = m <= 16 ? 1 : (m <= 32 ? 2 : 4);
-    p.nt = m <= 16 ? 1 : 2;
-    p.tiles_m = 1;
-    p.tiles_n = (n + 16 * p.nt - 1) / (16 * p.nt);
-    // a workgroup's eight waves take two batches of steps at least
+  if (m <= (aligned ? 16 : 64)) {
+    const int64_t bn = m <= 16 ? 16 : 32;
+    Plan p{aligned ? kStream : kFew, 1, (n + bn - 1) / bn, 1};
+    // a workgroup's eight waves take eight steps each at least
     const int64_t s = 256 / p.tiles_n, most = steps / 64;
     p.splits = (int)(s < most ? s : most);
     if (p.splits < 1) p.splits = 1;
     return p;
   }
-  p.large = (m + 255) / 256 * ((n + 255) / 256) >= 192;
-  const int64_t b = p.large ? 256 : 128;
-  p.tiles_m = (m + b - 1) / b;
-  p.tiles_n = (n + b - 1) / b;
-  p.splits = 1;
-  const int64_t tiles = p.tiles_m * p.tiles_n;
-  if (!p.large) {
-    int64_t s = 512 / tiles;
-    const int64_t most = steps / 8;
-    s = s < most ? s : most;
-    p.splits = s < 1 ? 1 : (s > 16 ? 16 : (int)s);
+  struct Cost {
+    Shape shape;
+    int64_t bm, bn;
+    double fixed, step;
+  };
+  const Cost costs[] = {{kSmall, 64, 128, 4.8, 0.55}, {kMid, 128, 128, 6.3, 0.72},
+                        {kLarge, 256, 256, 8.2, 1.65}};
+  Plan best{};
+  double least = 0;
+  for (const Cost& c : costs) {
+    const int64_t tm = (m + c.bm - 1) / c.bm, tn = (n + c.bn - 1) / c.bn, tiles = tm * tn;
+    for (int64_t sp = 1; sp <= 16 && (sp == 1 || (tiles * sp <= 256 && steps / sp >= 4)); ++sp) {
+      const double rounds = (double)((tiles * sp + 255) / 256);
+      double t = rounds * (c.fixed + c.step * (double)((steps + sp - 1) / sp));
+      if (sp > 1) t += 3.0 + (double)sp * (double)m * (double)n * 8.0 / 5e6;
+      if (least == 0 || t < least) {
+        least = t;
+        best = {c.shape, tm, tn, (int)sp};
+      }
+    }
   }
-  return p;
+  return best;
 }
 
-template <typename O, typename TL, bool kDirect>
+size_t partial_bytes(const Plan& p, int64_t m, int64_t n) {
+  return p.splits > 1 ? align256((size_t)p.splits * m * n * 4) : 0;
+}
+
+// What the tiles' direct loads take: 16-byte aligned rows, whole chunks of K, and a lane's
+// offset within a tile in 32 bits.
+bool rows_aligned(const int8_t* x, int64_t ldx, const int8_t* w, int64_t ldw, int64_t k) {
+  return (((uintptr_t)x | (uintptr_t)w | (uint64_t)ldx | (uint64_t)ldw | (uint64_t)k) & 15) == 0 &&
+         ldx < (1 << 24) && ldw < (1 << 24);
+}
+
+template <typename O, typename TL>
 void launch_tiles(const Plan& p, int64_t k, const int8_t* x, int64_t ldx, const int8_t* w,
                   int64_t ldw, const Epilogue<O>& E, int32_t* part, hipStream_t s) {
   const int group_m = 8;
-  hipLaunchKernelGGL((int8linear_tile_kernel<O, TL, kDirect>),
-                     dim3((unsigned)(p.tiles_m * p.tiles_n * p.splits)), dim3(64 * TL::NW), 0, s,
-                     k, x, ldx, w, ldw, E, (int)p.tiles_m, (int)p.tiles_n, p.splits, group_m,
-                     p.splits > 1 ? part : nullptr);
+  const dim3 grid((unsigned)(p.tiles_m * p.tiles_n * p.splits)), block(64 * TL::NW);
+  int32_t* const sums = p.splits > 1 ? part : nullptr;
+  if constexpr (TL::KG == 1)
+    hipLaunchKernelGGL((int8linear_tile_kernel<O, TL>), grid, block, 0, s, k, x, ldx, w, ldw, E,
+                       (int)p.tiles_m, (int)p.tiles_n, p.splits, group_m, sums);
+  else
+    hipLaunchKernelGGL((int8linear_small_kernel<O, TL>), grid, block, 0, s, k, x, ldx, w, ldw, E,
+                       (int)p.tiles_m, (int)p.tiles_n, p.splits, group_m, sums);
 }
 
 template <typename O>
@@ -624,32 +876,37 @@ int int8linear_t(int64_t m, int64_t n, int64_t k, const int8_t* x, int64_t ldx, 
                  const void* residual, int64_t ldr, void* c, int64_t ldc, void* workspace,
                  hipStream_t s) {
   const Epilogue<O> E{m, n, sx, sw, (const O*)bias, (const O*)residual, ldr, (O*)c, ldc, act};
-  const Plan p = plan_of(m, n, k);
+  const bool aligned = rows_aligned(x, ldx, w, ldw, k);
+  const Plan p = plan_of(m, n, k, aligned);
   int32_t* part = static_cast<int32_t*>(workspace);
   if (p.tiles_m * p.tiles_n * p.splits > 0x7fffffff) return OZK_EUNSUPPORTED;
-  // direct loads: 16-byte aligned rows and K; a lane's offset within a tile in 32 bits
-  const bool direct = (((uintptr_t)x | (uintptr_t)w | (uint64_t)ldx | (uint64_t)ldw |
-                        (uint64_t)k) & 15) == 0 && ldx < (1 << 24) && ldw < (1 << 24);
-  if (p.few) {
-#define OZK_FEW(MT, NT, DEEP)                                                                  \
-  hipLaunchKernelGGL((int8linear_few_kernel<O, MT, NT, 8, DEEP>),                              \
-                     dim3((unsigned)(p.tiles_n * p.splits)), dim3(512), 0, s, k, x, ldx, w, ldw, \
-                     E, p.splits, p.splits > 1 ? part : nullptr)
-    if (p.mt == 1) OZK_FEW(1, 1, 4);
-    else if (p.mt == 2) OZK_FEW(2, 2, 2);
-    else OZK_FEW(4, 2, 1);
+  if (p.shape == kStream || p.shape == kFew) {
+    const dim3 grid((unsigned)(p.tiles_n * p.splits)), block(512);
+    int32_t* const sums = p.splits > 1 ? part : nullptr;
+#define OZK_FEW(KERNEL) \
+  hipLaunchKernelGGL(KERNEL, grid, block, 0, s, k, x, ldx, w, ldw, E, p.splits, sums)
+    if (p.shape == kStream && m <= 8) OZK_FEW((int8linear_stream_kernel<O, 8, 3>));
+    else if (p.shape == kStream) OZK_FEW((int8linear_stream_kernel<O, 16, 4>));
+    else if (m <= 16) OZK_FEW((int8linear_few_kernel<O, 1, 1, 8, 4>));
+    else if (m <= 32) OZK_FEW((int8linear_few_kernel<O, 2, 2, 8, 2>));
+    else OZK_FEW((int8linear_few_kernel<O, 4, 2, 8, 1>));
 #undef OZK_FEW
-  } else if (!direct) {
-    Plan q = p;
-    if (p.large) {
-      q.tiles_m = (m + 127) / 128;
-      q.tiles_n = (n + 127) / 128;
-    }
-    launch_tiles<O, TileMid, false>(q, k, x, ldx, w, ldw, E, part, s);
-  } else if (p.large) {
-    launch_tiles<O, TileLarge, true>(p, k, x, ldx, w, ldw, E, part, s);
   } else {
-    launch_tiles<O, TileMid, true>(p, k, x, ldx, w, ldw, E, part, s);
+    if (!aligned) {
+      const int64_t kp = round_up(k, 16);
+      int8_t* xo = static_cast<int8_t*>(workspace) + partial_bytes(p, m, n);
+      int8_t* wo = xo + align256((size_t)m * kp);
+      const int64_t blocks = ((m + n) * (kp / 16) + 255) / 256;
+      if (blocks > 0x7fffffff) return OZK_EUNSUPPORTED;
+      hipLaunchKernelGGL(int8linear_layout_kernel, dim3((unsigned)blocks), dim3(256), 0, s, m, n,
+                         k, kp, x, ldx, xo, w, ldw, wo);
+      x = xo;
+      w = wo;
+      ldx = ldw = k = kp;
+    }
+    if (p.shape == kLarge) launch_tiles<O, TileLarge>(p, k, x, ldx, w, ldw, E, part, s);
+    else if (p.shape == kMid) launch_tiles<O, TileMid>(p, k, x, ldx, w, ldw, E, part, s);
+    else launch_tiles<O, TileSmall>(p, k, x, ldx, w, ldw, E, part, s);
   }
   if (p.splits > 1)
     hipLaunchKernelGGL((int8linear_join_kernel<O>),
@@ -660,10 +917,19 @@ int int8linear_t(int64_t m, int64_t n, int64_t k, const int8_t* x, int64_t ldx, 
 
 }  // namespace
 
-size_t int8linear_workspace(int64_t m, int64_t n, int64_t k) {
+bool int8linear_aligned(const int8_t* x, int64_t ldx, const int8_t* w, int64_t ldw, int64_t k) {
+  return rows_aligned(x, ldx, w, ldw, k);
+}
+
+size_t int8linear_workspace(int64_t m, int64_t n, int64_t k, bool aligned) {
   if (m <= 0 || n <= 0) return 0;
-  const Plan p = plan_of(m, n, k);
-  return p.splits > 1 ? (size_t)p.splits * m * n * 4 : 0;
+  const Plan p = plan_of(m, n, k, aligned);
+  size_t bytes = partial_bytes(p, m, n);
+  if (p.shape >= kSmall && !aligned) {
+    const int64_t kp = round_up(k, 16);
+    bytes += align256((size_t)m * kp) + align256((size_t)n * kp);
+  }
+  return bytes;
 }
 
 int launch_int8linear(int64_t m, int64_t n, int64_t k, const int8_t* x, int64_t ldx,

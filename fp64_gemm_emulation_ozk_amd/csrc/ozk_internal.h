@@ -189,8 +189,10 @@ int launch_act_grad(int64_t m, int64_t n, const double* dc, int64_t lddc, const 
 // p[i * ld + j] = 0 for i < rows, j < cols.
 int launch_zero_rows(double* p, int64_t rows, int64_t cols, int64_t ld, hipStream_t s);
 
-// int8 linear layer (int8linear.hip); workspace: int8linear_workspace(m, n, k) bytes.
-size_t int8linear_workspace(int64_t m, int64_t n, int64_t k);
+// int8 linear layer (int8linear.hip); workspace: int8linear_workspace(m, n, k, aligned) bytes,
+// aligned: int8linear_aligned of the operands.
+bool int8linear_aligned(const int8_t* x, int64_t ldx, const int8_t* w, int64_t ldw, int64_t k);
+size_t int8linear_workspace(int64_t m, int64_t n, int64_t k, bool aligned);
 int launch_int8linear(int64_t m, int64_t n, int64_t k, const int8_t* x, int64_t ldx,
                       const float* sx, const int8_t* w, int64_t ldw, const float* sw,
                       const void* bias, int act, const void* residual, int64_t ldr, int type,

@@ -392,8 +392,12 @@ int ozk_int4int8gemm_fp4awe(int64_t m, int64_t n, int64_t k, const int8_t* A, in
  * OZK_BF16.  The sum is exact in int32 (1 <= k <= OZK_MAX_K); what follows is fp32, rounded
  * once to C's type.  A scale that is NaN gives NaN in the outputs it touches.  residual may
  * be C itself; otherwise C overlaps no input.  Any leading dimensions ldx, ldw >= k and any
- * byte alignment of X and W; the other pointers are aligned to their elements. */
-int ozk_int8linear_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes);
+ * byte alignment of X and W; the other pointers are aligned to their elements.  The workspace
+ * (256-byte aligned) holds partial sums where K is split over workgroups and, for more than
+ * a few rows, X and W with aligned rows unless they have them: aligned = 1 in the query
+ * stands for X and W at multiples of 16 bytes with ldx, ldw and k multiples of 16 and ldx,
+ * ldw < 2^24 (0: anything).  The query may return 0; workspace may be NULL then. */
+int ozk_int8linear_workspace_size(int64_t m, int64_t n, int64_t k, int aligned, size_t* bytes);
 int ozk_int8linear(int64_t m, int64_t n, int64_t k, const int8_t* X, int64_t ldx,
                    const float* scale_x, const int8_t* W, int64_t ldw, const float* scale_w,
                    const void* bias, int act, const void* residual, int64_t ldr, int type,

@@ -82,13 +82,25 @@ def test_int8linear_refusals(lib):
     assert call(k=131072, ldx=131072, ldw=131072) == ERANGE
     assert call(m=1 << 31) == EUNSUPPORTED
     assert call(m=0) == OK and call(n=0) == OK
-    # a shape whose K is split over workgroups needs its partial sums
-    need = ozk.ozk_int8linear_workspace_size(1, 16, 131071)
-    if need:
-        big = dict(m=1, n=16, k=131071, ldx=131071, ldw=131071, ldc=16, ldr=16)
-        assert call(**big) == EWORKSPACE
+    # a shape whose K is split over workgroups needs its partial sums, unaligned operands of
+    # more than a few rows an aligned copy; a call is held to what its own operands need
+    for m, n, k, aligned in ((1, 16, 131071, False), (100, 100, 100, False),
+                             (100, 100, 8192, True)):
+        need = ozk.ozk_int8linear_workspace_size(m, n, k, aligned)
+        assert need > 0
+        big = dict(m=m, n=n, k=k, ldx=k, ldw=k, ldc=n, ldr=n)
+        assert call(**big) == EWORKSPACE and call(**big, wsb=need - 1) == EWORKSPACE
         assert call(**big, wsb=need, ws=None) == EWORKSPACE
         assert call(**big, wsb=need, ws=ODD) == EINVAL
+        if aligned:
+            assert ozk.ozk_int8linear_workspace_size(m, n, k, False) >= need + (m + n) * k
+            assert call(**big, wsb=need, X=ctypes.c_void_p(0x1008)) == EWORKSPACE
+    assert ozk.ozk_int8linear_workspace_size(100, 4096, 128, True) == 0   # one K step
+    out = ctypes.c_size_t()
+    size = lib.ozk_int8linear_workspace_size
+    assert size(4, 4, 0, 0, ctypes.byref(out)) == EINVAL and size(4, 4, 4, 0, None) == EINVAL
+    assert size(4, 4, 4, 2, ctypes.byref(out)) == EINVAL
+    assert size(4, 4, 131072, 0, ctypes.byref(out)) == ERANGE
 
 
 @pytest.mark.parametrize("kind", [0, 1, 2, 3])

@@ -37,9 +37,10 @@ def tiny(dtype):
 def assert_near(got, want, tol, what):
     err = np.abs(got - want)
     bad = ~(err <= tol)
-    assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.size} off, worst "
-                           f"{np.nanmax(err / np.maximum(tol, 1e-300)):.3g} of the tolerance "
-                           f"at {np.argwhere(bad)[0].tolist()}")
+    if bad.any():
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.size} off, worst "
+                             f"{np.nanmax(err / np.maximum(tol, 1e-300)):.3g} of the tolerance "
+                             f"at {np.argwhere(bad)[0].tolist()}")
 
 
 def padded(x, pad, offset=0):
