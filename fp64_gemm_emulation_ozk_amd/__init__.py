@@ -33,7 +33,8 @@ __all__ = [
     "ozk_int8gemm_fp4limb_workspace_size", "ozk_deconstruct_workspace_size",
     "OZK_ACT_NONE", "OZK_ACT_RELU", "OZK_ACT_GELU", "OZK_ACT_GELU_TANH", "OZK_ACT_SILU",
     "OZK_F64", "OZK_F32", "OZK_F16", "OZK_BF16",
-    "ozk_dgemm_epilogue", "ozk_dgemm_epilogue_grad", "ozk_dgemm_epilogue_grad_workspace_size",
+    "ozk_dgemm_epilogue", "ozk_dgemm_epilogue_workspace_size", "ozk_dgemm_epilogue_grad",
+    "ozk_dgemm_epilogue_grad_workspace_size",
     "ozk_int8linear", "ozk_int8linear_workspace_size",
     "ozk_int8quant_rows", "ozk_layernorm", "ozk_layernorm_backward",
     "ozk_layernorm_backward_workspace_size",
@@ -104,6 +105,7 @@ _SIGNATURES = {
                                        _size, _ptr]),
     "ozk_dgemm_epilogue": (_int, [_i64, _i64, _i64, _ptr, _i64, _ptr, _i64, _ptr, _int, _ptr,
                                   _i64, _ptr, _i64, _ptr, _i64, _int, _int, _ptr, _size, _ptr]),
+    "ozk_dgemm_epilogue_workspace_size": (_int, [_i64, _i64, _i64, _int, _ptr]),
     "ozk_dgemm_epilogue_grad_workspace_size": (_int, [_i64, _i64, _i64, _int, _ptr]),
     "ozk_dgemm_epilogue_grad": (_int, [_i64, _i64, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr,
                                        _i64, _int, _ptr, _i64, _ptr, _i64, _ptr, _int, _int, _ptr,
@@ -695,6 +697,10 @@ class _On:
             self._guard.__exit__(*exc)
 
 
+def ozk_dgemm_epilogue_workspace_size(m: int, n: int, k: int, r: int) -> int:
+    return _size_query("ozk_dgemm_epilogue_workspace_size", m, n, k, r)
+
+
 def ozk_dgemm_epilogue_grad_workspace_size(m: int, n: int, k: int, r: int) -> int:
     return _size_query("ozk_dgemm_epilogue_grad_workspace_size", m, n, k, r)
 
@@ -740,7 +746,7 @@ def ozk_dgemm_epilogue(a: torch.Tensor, b: torch.Tensor, r: int,
         if out is None:
             out = torch.empty((m, n), dtype=torch.float64, device=a.device)
         if workspace is None:
-            workspace = _workspace(ozk_dgemm_workspace_size(m, n, k, r), a.device)
+            workspace = _workspace(ozk_dgemm_epilogue_workspace_size(m, n, k, r), a.device)
         _call("ozk_dgemm_epilogue", m, n, k, _dev_ptr(a), _ld(a), _dev_ptr(b), _ld(b),
               _dev_ptr(bias), _act(act), _dev_ptr(residual), _ld_opt(residual),
               _dev_ptr(preact), _ld_opt(preact), _dev_ptr(out), _ld(out), r, _scaling(scaling),

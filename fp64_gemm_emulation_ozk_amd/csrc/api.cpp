@@ -137,35 +137,6 @@ int deconstruct_operands(const double* A, int64_t m, int64_t k, int64_t lda, con
                          kp, n * kp, exps_b, scaling == OZK_SCALING_NORM, s);
 }
 
-// Everything of C = A B before the reconstruction: the residues of the r products (ld n,
-// plane stride m n) and the exponents, in the workspace.
-struct DgemmResidues {
-  const int8_t* residues;
-  const int32_t* exps_a;
-  const int32_t* exps_b;
-};
-int dgemm_residues(int64_t m, int64_t n, int64_t k, const double* A, int64_t lda,
-                   const double* B, int64_t ldb, int r, int scaling, int wa, int wb,
-                   const DgemmLayout& L, void* workspace, hipEvent_t gemm_start,
-                   hipEvent_t gemm_stop, hipStream_t s, DgemmResidues* out) {
-  Carver cv(workspace);
-  int8_t* planes_a = static_cast<int8_t*>(cv.take(L.planes_a));
-  int8_t* planes_b = static_cast<int8_t*>(cv.take(L.planes_b));
-  int8_t* residues = static_cast<int8_t*>(cv.take(L.residues));
-  int32_t* exps_a = static_cast<int32_t*>(cv.take(L.exps_a));
-  int32_t* exps_b = static_cast<int32_t*>(cv.take(L.exps_b));
-  void* scr_a = cv.take(L.scr_a);
-  void* scr_b = cv.take(L.scr_b);
-  const int64_t kp = L.kp;
-  int st;
-  if ((st = deconstruct_operands(A, m, k, lda, B, n, ldb, r, scaling, wa, wb, planes_a,
-                                 planes_b, kp, exps_a, exps_b, scr_a, scr_b, s)))
-    return st;
-  *out = {residues, exps_a, exps_b};
-  return launch_gemm_i8(m, n, kp, r, planes_a, m * kp, planes_b, n * kp, residues, n, m * n,
-                        kEpiResidues, s, gemm_start, gemm_stop);
-}
-
 }  // namespace
 
 extern "C" {
@@ -322,13 +293,24 @@ int ozk_dgemm_ex_timed(int64_t m, int64_t n, int64_t k, const double* A, int64_t
   if (!workspace || workspace_bytes < L.total()) return OZK_EWORKSPACE;
   if (!aligned(workspace, 256)) return OZK_EINVAL;
   if ((size_t)m * n > (size_t)0x7fffffffffffull) return OZK_EUNSUPPORTED;
+  Carver cv(workspace);
+  int8_t* planes_a = static_cast<int8_t*>(cv.take(L.planes_a));
+  int8_t* planes_b = static_cast<int8_t*>(cv.take(L.planes_b));
+  int8_t* residues = static_cast<int8_t*>(cv.take(L.residues));
+  int32_t* exps_a = static_cast<int32_t*>(cv.take(L.exps_a));
+  int32_t* exps_b = static_cast<int32_t*>(cv.take(L.exps_b));
+  void* scr_a = cv.take(L.scr_a);
+  void* scr_b = cv.take(L.scr_b);
   hipStream_t s = as_stream(stream);
-  DgemmResidues D;
-  if ((st = dgemm_residues(m, n, k, A, lda, B, ldb, r, scaling, wa, wb, L, workspace,
-                           static_cast<hipEvent_t>(gemm_start),
-                           static_cast<hipEvent_t>(gemm_stop), s, &D)))
+  const int64_t kp = L.kp;
+  if ((st = deconstruct_operands(A, m, k, lda, B, n, ldb, r, scaling, wa, wb, planes_a,
+                                 planes_b, kp, exps_a, exps_b, scr_a, scr_b, s)))
     return st;
-  return launch_crt(m, n, r, D.residues, 0, n, m * n, D.exps_a, D.exps_b, C, ldc, s);
+  if ((st = launch_gemm_i8(m, n, kp, r, planes_a, m * kp, planes_b, n * kp, residues, n, m * n,
+                           kEpiResidues, s, static_cast<hipEvent_t>(gemm_start),
+                           static_cast<hipEvent_t>(gemm_stop))))
+    return st;
+  return launch_crt(m, n, r, residues, 0, n, m * n, exps_a, exps_b, C, ldc, s);
 }
 
 int ozk_dgemm(int64_t m, int64_t n, int64_t k, const double* A, int64_t lda, const double* B,
@@ -719,9 +701,9 @@ namespace {
 
 bool act_ok(int act) { return act >= OZK_ACT_NONE && act <= OZK_ACT_SILU; }
 
-// One product of the gradient: `left` (lines along left_axis) times `right`, inner
-// dimension K, rows x cols outputs.
-struct GradProduct {
+// A product of the epilogue's or the gradient's: `left` (its lines along left_axis) times
+// `right`, inner dimension K, rows x cols outputs.
+struct Product {
   int64_t rows, cols, K;
   const double* left;
   int64_t left_rows, left_cols, ldl;
@@ -731,61 +713,79 @@ struct GradProduct {
   int right_axis;
 };
 
-struct GradLayout {
-  int64_t kp;
-  size_t planes_l, planes_r, residues, exps_l, exps_r, scratch;
+// Workspace of a product.  The rows of residues are padded to 64 so that every store of the
+// modular products and every load of the reconstruction is a whole vector (1500 x 2050 x
+// 1001: 133.6 -> RES us a product); the padding's columns are products with whatever lines
+// follow the right planes, which therefore end in as many lines more.
+struct ProductLayout {
+  int64_t kp, np;
+  size_t planes_l, planes_r, residues, exps_l, exps_r, scr_l, scr_r;
   size_t total() const {
     return align256(planes_l) + align256(planes_r) + align256(residues) + align256(exps_l) +
-           align256(exps_r) + align256(scratch);
+           align256(exps_r) + align256(scr_l) + align256(scr_r);
   }
 };
 
-GradLayout grad_layout(const GradProduct& P, int r) {
-  GradLayout L;
+ProductLayout product_layout(const Product& P, int r) {
+  ProductLayout L;
   L.kp = round_up(P.K, 2 * kPlaneK);
+  L.np = round_up(P.cols, 64);
   L.planes_l = (size_t)r * P.rows * L.kp;
-  L.planes_r = (size_t)r * P.cols * L.kp;
-  L.residues = (size_t)r * P.rows * P.cols;
+  L.planes_r = ((size_t)r * P.cols + (L.np - P.cols)) * L.kp;
+  L.residues = (size_t)r * P.rows * L.np;
   L.exps_l = (size_t)P.rows * 4;
   L.exps_r = (size_t)P.cols * 4;
-  const size_t sl = deconstruct_scratch(P.left_rows, P.left_cols, P.left_axis);
-  const size_t sr = deconstruct_scratch(P.right_rows, P.right_cols, P.right_axis);
-  L.scratch = sl > sr ? sl : sr;   // one operand after the other
+  L.scr_l = deconstruct_scratch(P.left_rows, P.left_cols, P.left_axis);
+  L.scr_r = deconstruct_scratch(P.right_rows, P.right_cols, P.right_axis);
   return L;
 }
 
-// dA = G B^T: rows of G against rows of B; dB = A^T G: columns of A against columns of G.
-GradProduct grad_a(int64_t m, int64_t n, int64_t k, const double* g, int64_t ldg,
-                   const double* B, int64_t ldb) {
-  return {m, k, n, g, m, n, ldg, 0, B, k, n, ldb, 0};
-}
-GradProduct grad_b(int64_t m, int64_t n, int64_t k, const double* A, int64_t lda,
-                   const double* g, int64_t ldg) {
-  return {k, n, m, A, m, k, lda, 1, g, m, n, ldg, 1};
-}
-
-int grad_product(const GradProduct& P, int r, int scaling, double* out, int64_t ldo,
-                 void* workspace, hipStream_t s) {
-  int wa = 0, wb = 0, st;
-  if ((st = scaling_widths(scaling, r, P.K, &wa, &wb))) return st;
-  const GradLayout L = grad_layout(P, r);
+// The product in emulated fp64, then E.
+int run_product(const Product& P, int r, int scaling, const DgemmEpilogue& E, double* out,
+                int64_t ldo, void* workspace, hipStream_t s) {
+  int wl = 0, wr = 0, st;
+  if ((st = scaling_widths(scaling, r, P.K, &wl, &wr))) return st;
+  const ProductLayout L = product_layout(P, r);
   Carver cv(workspace);
   int8_t* pl = static_cast<int8_t*>(cv.take(L.planes_l));
   int8_t* pr = static_cast<int8_t*>(cv.take(L.planes_r));
   int8_t* res = static_cast<int8_t*>(cv.take(L.residues));
   int32_t* el = static_cast<int32_t*>(cv.take(L.exps_l));
   int32_t* er = static_cast<int32_t*>(cv.take(L.exps_r));
-  void* scratch = cv.take(L.scratch);
-  if ((st = deconstruct_impl(P.left, P.left_rows, P.left_cols, P.ldl, P.left_axis, r, scaling, wa,
-                             pl, L.kp, P.rows * L.kp, el, scratch, s)))
+  void* scr_l = cv.take(L.scr_l);
+  void* scr_r = cv.take(L.scr_r);
+  const int64_t sl = P.rows * L.kp, sr = P.cols * L.kp;   // plane strides
+  if (P.left_axis == 0 && P.right_axis == 1) {
+    st = deconstruct_operands(P.left, P.rows, P.K, P.ldl, P.right, P.cols, P.ldr, r, scaling, wl,
+                              wr, pl, pr, L.kp, el, er, scr_l, scr_r, s);
+  } else {
+    st = deconstruct_impl(P.left, P.left_rows, P.left_cols, P.ldl, P.left_axis, r, scaling, wl,
+                          pl, L.kp, sl, el, scr_l, s);
+    if (st == OZK_OK)
+      st = deconstruct_impl(P.right, P.right_rows, P.right_cols, P.ldr, P.right_axis, r, scaling,
+                            wr, pr, L.kp, sr, er, scr_r, s);
+  }
+  if (st != OZK_OK) return st;
+  if ((st = launch_gemm_i8(P.rows, L.np, L.kp, r, pl, sl, pr, sr, res, L.np, P.rows * L.np,
+                           kEpiResidues, s)))
     return st;
-  if ((st = deconstruct_impl(P.right, P.right_rows, P.right_cols, P.ldr, P.right_axis, r,
-                             scaling, wb, pr, L.kp, P.cols * L.kp, er, scratch, s)))
-    return st;
-  if ((st = launch_gemm_i8(P.rows, P.cols, L.kp, r, pl, P.rows * L.kp, pr, P.cols * L.kp, res,
-                           P.cols, P.rows * P.cols, kEpiResidues, s)))
-    return st;
-  return launch_crt(P.rows, P.cols, r, res, 0, P.cols, P.rows * P.cols, el, er, out, ldo, s);
+  return launch_crt_epilogue(P.rows, P.cols, r, res, L.np, P.rows * L.np, el, er, E, out, ldo, s);
+}
+
+// C = A B: rows of A against columns of B.
+Product forward_product(int64_t m, int64_t n, int64_t k, const double* A, int64_t lda,
+                        const double* B, int64_t ldb) {
+  return {m, n, k, A, m, k, lda, 0, B, k, n, ldb, 1};
+}
+
+// dA = G B^T: rows of G against rows of B; dB = A^T G: columns of A against columns of G.
+Product grad_a(int64_t m, int64_t n, int64_t k, const double* g, int64_t ldg,
+                   const double* B, int64_t ldb) {
+  return {m, k, n, g, m, n, ldg, 0, B, k, n, ldb, 0};
+}
+Product grad_b(int64_t m, int64_t n, int64_t k, const double* A, int64_t lda,
+                   const double* g, int64_t ldg) {
+  return {k, n, m, A, m, k, lda, 1, g, m, n, ldg, 1};
 }
 
 // Workspace of the gradient: G, the chunks' sums of its columns, and the larger of the two
@@ -799,8 +799,8 @@ EpilogueGradLayout epilogue_grad_layout(int64_t m, int64_t n, int64_t k, int r) 
   EpilogueGradLayout L;
   L.g = (size_t)m * n * 8;
   L.part = (size_t)act_grad_chunks(m > 0 ? m : 1) * n * 8;
-  const size_t a = grad_layout(grad_a(m, n, k, nullptr, n, nullptr, n), r).total();
-  const size_t b = grad_layout(grad_b(m, n, k, nullptr, k, nullptr, n), r).total();
+  const size_t a = product_layout(grad_a(m, n, k, nullptr, n, nullptr, n), r).total();
+  const size_t b = product_layout(grad_b(m, n, k, nullptr, k, nullptr, n), r).total();
   L.products = a > b ? a : b;
   return L;
 }
@@ -808,6 +808,13 @@ EpilogueGradLayout epilogue_grad_layout(int64_t m, int64_t n, int64_t k, int r) 
 }  // namespace
 
 extern "C" {
+
+int ozk_dgemm_epilogue_workspace_size(int64_t m, int64_t n, int64_t k, int r, size_t* bytes) {
+  if (!bytes || m < 0 || n < 0 || k < 1 || check_r(r) != OZK_OK) return OZK_EINVAL;
+  if (k > OZK_MAX_K) return OZK_ERANGE;
+  *bytes = product_layout(forward_product(m, n, k, nullptr, k, nullptr, n), r).total();
+  return OZK_OK;
+}
 
 int ozk_dgemm_epilogue(int64_t m, int64_t n, int64_t k, const double* A, int64_t lda,
                        const double* B, int64_t ldb, const double* bias, int act,
@@ -826,17 +833,12 @@ int ozk_dgemm_epilogue(int64_t m, int64_t n, int64_t k, const double* A, int64_t
   if (st != OZK_OK) return st;
   if (m == 0 || n == 0) return OZK_OK;
   if (!A || !B || !C) return OZK_EINVAL;
-  const DgemmLayout L = dgemm_layout(m, n, k, r);
-  if (!workspace || workspace_bytes < L.total()) return OZK_EWORKSPACE;
+  const Product P = forward_product(m, n, k, A, lda, B, ldb);
+  if (!workspace || workspace_bytes < product_layout(P, r).total()) return OZK_EWORKSPACE;
   if (!aligned(workspace, 256)) return OZK_EINVAL;
   if ((size_t)m * n > (size_t)0x7fffffffffffull) return OZK_EUNSUPPORTED;
-  hipStream_t s = as_stream(stream);
-  DgemmResidues D;
-  if ((st = dgemm_residues(m, n, k, A, lda, B, ldb, r, scaling, wa, wb, L, workspace, nullptr,
-                           nullptr, s, &D)))
-    return st;
-  const DgemmEpilogue E{bias, residual, ldr, Z, ldz, act};
-  return launch_crt_epilogue(m, n, r, D.residues, n, m * n, D.exps_a, D.exps_b, E, C, ldc, s);
+  return run_product(P, r, scaling, {bias, residual, ldr, Z, ldz, act}, C, ldc, workspace,
+                     as_stream(stream));
 }
 
 int ozk_dgemm_epilogue_grad_workspace_size(int64_t m, int64_t n, int64_t k, int r,
@@ -886,11 +888,12 @@ int ozk_dgemm_epilogue_grad(int64_t m, int64_t n, int64_t k, const double* dC, i
     return st;
   const double* gp = own_g ? g : dC;
   const int64_t ldg = own_g ? n : lddc;
-  if (dA && (st = grad_product(grad_a(m, n, k, gp, ldg, B, ldb), r, scaling, dA, ldda, products,
-                               s)))
+  const DgemmEpilogue none{nullptr, nullptr, 0, nullptr, 0, OZK_ACT_NONE};
+  if (dA && (st = run_product(grad_a(m, n, k, gp, ldg, B, ldb), r, scaling, none, dA, ldda,
+                              products, s)))
     return st;
-  if (dB && (st = grad_product(grad_b(m, n, k, A, lda, gp, ldg), r, scaling, dB, lddb, products,
-                               s)))
+  if (dB && (st = run_product(grad_b(m, n, k, A, lda, gp, ldg), r, scaling, none, dB, lddb,
+                              products, s)))
     return st;
   return OZK_OK;
 }

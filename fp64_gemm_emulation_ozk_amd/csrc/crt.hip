@@ -5,14 +5,23 @@
 namespace ozk {
 namespace {
 
+struct Store {
+  double* c;
+  int64_t ldc;
+  struct Nothing {};
+  __device__ __forceinline__ Nothing ask(int64_t, int64_t) const { return {}; }
+  __device__ __forceinline__ void operator()(int64_t i, int64_t j, double v, Nothing) const {
+    c[i * ldc + j] = v;
+  }
+};
+
 template <int R, typename T>
 __global__ __launch_bounds__(256) void crt_kernel(int64_t m, int64_t n, const T* __restrict__ res,
                                                   int64_t ldr, int64_t stride_r,
                                                   const int32_t* __restrict__ ea,
                                                   const int32_t* __restrict__ eb,
                                                   double* __restrict__ c, int64_t ldc) {
-  crt_outputs<R, T>(m, n, res, ldr, stride_r, ea, eb,
-                    [=](int64_t i, int64_t j, double v) { c[i * ldc + j] = v; });
+  crt_outputs<R, T>(m, n, n, res, ldr, stride_r, ea, eb, Store{c, ldc});
 }
 
 template <int R>

@@ -391,12 +391,15 @@ __device__ __forceinline__ void transpose_words(const WordLoads<R>& raw, uint32_
 }
 
 // Persistent waves: each takes groups of 64 consecutive outputs of one row, lane i
-// finishing output j0 + i; consecutive waves take consecutive groups.  put(i, j, value)
-// takes each output (i, j), j < n, once.
-// Columns past n read as residue 0 and are not put.
+// finishing output j0 + i; consecutive waves take consecutive groups.  put takes each output
+// (i, j), j < n, once: put.ask(i, j) is called before its value is computed (to load what goes
+// with it), put(i, j, value, asked) after.
+// Columns past n read as residue 0 (or, where a row has nl > n residues, as what stands
+// there) and are not put.
 template <int R, typename T, typename Put>
-__device__ __forceinline__ void crt_outputs(int64_t m, int64_t n, const T* __restrict__ res,
-                                            int64_t ldr, int64_t stride_r,
+__device__ __forceinline__ void crt_outputs(int64_t m, int64_t n, int64_t nl,
+                                            const T* __restrict__ res, int64_t ldr,
+                                            int64_t stride_r,
                                             const int32_t* __restrict__ ea,
                                             const int32_t* __restrict__ eb, Put put) {
   using S = CrtShape<R>;
@@ -417,8 +420,10 @@ __device__ __forceinline__ void crt_outputs(int64_t m, int64_t n, const T* __res
 
   // A group covers outputs j0 .. j0+63 of row i; (i, j0) are wave-uniform and advance
   // without divisions.
-  auto word_path = [&](int64_t j0) { return words && j0 + 64 <= n; };
+  auto word_path = [&](int64_t j0) { return words && j0 + 64 <= nl; };
   auto finish_group = [&](int64_t i, int64_t j0, const v4i& b1v, const v4i& b2v) {
+    const int64_t j = j0 + lane;
+    const auto asked = put.ask(i, j < n ? j : n - 1);
     const v16i zero = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
     const v16i d1 = __builtin_amdgcn_mfma_i32_32x32x32_i8(a_op, b1v, zero, 0, 0, 0);
     const v16i d2 = __builtin_amdgcn_mfma_i32_32x32x32_i8(a_op, b2v, zero, 0, 0, 0);
@@ -448,11 +453,10 @@ __device__ __forceinline__ void crt_outputs(int64_t m, int64_t n, const T* __res
       const int v = (pos != 4 && b + 1 < S::kNE) ? sum[b] + 256 * sum[b + 1] : sum[b];
       x[b / 5] = __builtin_fma((double)v, (double)(1ll << (8 * pos)), x[b / 5]);
     }
-    const int64_t j = j0 + lane;
     if (j < n) {
       const int32_t e_i = ea[i], f_j = eb[j];
       const bool nan = e_i == INT32_MIN || f_j == INT32_MIN;
-      put(i, j, finish<S::kL, S::kBigTop>(x, e_i + f_j, nan));
+      put(i, j, finish<S::kL, S::kBigTop>(x, e_i + f_j, nan), asked);
     }
   };
   // Position (row, group within the row) of a group, advanced by `waves` groups.

@@ -11,27 +11,58 @@
 namespace ozk {
 namespace {
 
+// Which activations a kernel holds.  Each set is its own kernel because of the registers:
+// with erfc in it all ran three waves per SIMD, against six without any.
+enum ActSet { kSimple, kExp, kErfc };   // none, relu; gelu_tanh, silu; gelu
+inline ActSet act_set(int act) {
+  return act == OZK_ACT_GELU ? kErfc
+                             : (act == OZK_ACT_GELU_TANH || act == OZK_ACT_SILU ? kExp : kSimple);
+}
+
 // The residual may be C itself: a lane reads its element before it writes it.
-template <int R>
+template <ActSet kSet>
+struct Finish {
+  DgemmEpilogue E;
+  double* c;
+  int64_t ldc;
+  struct Asked {
+    double bias, residual;
+  };
+  __device__ __forceinline__ Asked ask(int64_t i, int64_t j) const {
+    return {E.bias ? E.bias[j] : 0.0, E.residual ? E.residual[i * E.ldr + j] : 0.0};
+  }
+  __device__ __forceinline__ void operator()(int64_t i, int64_t j, double v,
+                                             const Asked& a) const {
+    if (E.bias) v += a.bias;
+    if (E.z) E.z[i * E.ldz + j] = v;
+    if (kSet == kErfc) v = activate(v, OZK_ACT_GELU);
+    else if (kSet == kExp) v = activate(v, E.act == OZK_ACT_SILU ? OZK_ACT_SILU : OZK_ACT_GELU_TANH);
+    else if (E.act == OZK_ACT_RELU) v = activate(v, OZK_ACT_RELU);
+    if (E.residual) v += a.residual;
+    c[i * ldc + j] = v;
+  }
+};
+
+template <int R, ActSet kSet>
 __global__ __launch_bounds__(256) void crt_epilogue_kernel(
     int64_t m, int64_t n, const int8_t* __restrict__ res, int64_t ldr, int64_t stride_r,
     const int32_t* __restrict__ ea, const int32_t* __restrict__ eb, DgemmEpilogue E, double* c,
     int64_t ldc) {
-  crt_outputs<R, int8_t>(m, n, res, ldr, stride_r, ea, eb, [=](int64_t i, int64_t j, double v) {
-    if (E.bias) v += E.bias[j];
-    if (E.z) E.z[i * E.ldz + j] = v;
-    v = activate(v, E.act);
-    if (E.residual) v += E.residual[i * E.ldr + j];
-    c[i * ldc + j] = v;
-  });
+  crt_outputs<R, int8_t>(m, n, ldr, res, ldr, stride_r, ea, eb, Finish<kSet>{E, c, ldc});
 }
 
 template <int R>
 void launch_r(dim3 grid, hipStream_t s, int64_t m, int64_t n, const int8_t* res, int64_t ldr,
               int64_t stride_r, const int32_t* ea, const int32_t* eb, const DgemmEpilogue& E,
               double* c, int64_t ldc) {
-  hipLaunchKernelGGL((crt_epilogue_kernel<R>), grid, dim3(256), 0, s, m, n, res, ldr, stride_r,
-                     ea, eb, E, c, ldc);
+#define OZK_SET(SET)                                                                           \
+  hipLaunchKernelGGL((crt_epilogue_kernel<R, SET>), grid, dim3(256), 0, s, m, n, res, ldr,     \
+                     stride_r, ea, eb, E, c, ldc)
+  const ActSet set = act_set(E.act);
+  if (set == kErfc) OZK_SET(kErfc);
+  else if (set == kExp) OZK_SET(kExp);
+  else OZK_SET(kSimple);
+#undef OZK_SET
 }
 
 // Column c of a chunk of rows per thread: G, and the chunk's sum of G.

@@ -167,7 +167,8 @@ int launch_crt(int64_t m, int64_t n, int r, const void* res, int res_is_i32, int
                hipStream_t s);
 
 // The fp64 product with its epilogue: bias [n], residual and the kept pre-activations z
-// (each null where absent) of launch_crt's outputs, residues in int8.
+// (each null where absent) of launch_crt's outputs, residues in int8, rows of ldr >= n of
+// them, all of which may be read.
 struct DgemmEpilogue {
   const double* bias;
   const double* residual;

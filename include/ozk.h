@@ -206,8 +206,9 @@ int ozk_dgemm_ex(int64_t m, int64_t n, int64_t k, const double* A, int64_t lda,
  * is rounded once (as ozk_dgemm_ex), then the bias is added, the activation taken and the
  * residual added, one fp64 rounding or fp64 function each, in the registers of the
  * reconstruction.  residual may be C itself; otherwise outputs overlap no input.  Other
- * arguments, the errors and the workspace (ozk_dgemm_workspace_size) are those of
- * ozk_dgemm_ex; OZK_EINVAL for an unknown act. */
+ * arguments and the errors are those of ozk_dgemm_ex, with OZK_EINVAL for an unknown act; the
+ * workspace (256-byte aligned) takes ozk_dgemm_epilogue_workspace_size bytes. */
+int ozk_dgemm_epilogue_workspace_size(int64_t m, int64_t n, int64_t k, int r, size_t* bytes);
 int ozk_dgemm_epilogue(int64_t m, int64_t n, int64_t k, const double* A, int64_t lda,
                        const double* B, int64_t ldb, const double* bias, int act,
                        const double* residual, int64_t ldr, double* Z, int64_t ldz, double* C,

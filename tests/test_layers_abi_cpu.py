@@ -42,6 +42,12 @@ def test_dgemm_epilogue_refusals(lib):
     assert call(r=2, k=1 << 16, lda=1 << 16) == ERANGE          # no bit budget
     assert call(ws=None, wsb=0) == EWORKSPACE and call(wsb=16) == EWORKSPACE
     assert call(m=0, ws=None, wsb=0) == OK and call(n=0, ws=None, wsb=0) == OK
+    out = ctypes.c_size_t()
+    size = lib.ozk_dgemm_epilogue_workspace_size
+    assert size(4, 4, 4, 14, None) == EINVAL and size(4, 4, 0, 14, ctypes.byref(out)) == EINVAL
+    assert size(4, 4, 131072, 14, ctypes.byref(out)) == ERANGE
+    assert size(4, 4, 4, 14, ctypes.byref(out)) == OK
+    assert call(wsb=out.value - 1) == EWORKSPACE
     # absent operands ask for nothing of their leading dimensions
     assert call(R=None, ldr=0, Z=None, ldz=0, wsb=16) == EWORKSPACE
 
