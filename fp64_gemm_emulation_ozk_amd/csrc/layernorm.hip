@@ -29,9 +29,8 @@ __device__ __forceinline__ int valid(int64_t c, int64_t cols) {
 // (v kT + t) N).  kT = 64: four rows per workgroup; else one.
 template <typename T, int kT, int kV>
 __global__ __launch_bounds__(kT < 256 ? 256 : kT) void layernorm_kernel(
-    int64_t rows, int64_t cols, const T* __restrict__ x, int64_t ldx,
-    const T* __restrict__ gamma, const T* __restrict__ beta, typename AccOf<T>::type eps,
-    T* __restrict__ y, int64_t ldy, typename AccOf<T>::type* __restrict__ mean_out,
+    int64_t rows, int64_t cols, const T* x, int64_t ldx,
+    const T* __restrict__ gamma, const T* __restrict__ beta, typename AccOf<T>::type eps, T* y, int64_t ldy, typename AccOf<T>::type* __restrict__ mean_out,
     typename AccOf<T>::type* __restrict__ rstd_out) {
   typedef typename AccOf<T>::type A;
   constexpr int N = Vec<T>::N;
@@ -89,8 +88,8 @@ __global__ __launch_bounds__(kT < 256 ? 256 : kT) void layernorm_kernel(
 // Rows too long for registers: three passes over the row (it stays in L2).
 template <typename T>
 __global__ __launch_bounds__(1024) void layernorm_long_kernel(
-    int64_t cols, const T* __restrict__ x, int64_t ldx, const T* __restrict__ gamma,
-    const T* __restrict__ beta, typename AccOf<T>::type eps, T* __restrict__ y, int64_t ldy,
+    int64_t cols, const T* x, int64_t ldx, const T* __restrict__ gamma,
+    const T* __restrict__ beta, typename AccOf<T>::type eps, T* y, int64_t ldy,
     typename AccOf<T>::type* __restrict__ mean_out,
     typename AccOf<T>::type* __restrict__ rstd_out) {
   typedef typename AccOf<T>::type A;
@@ -176,24 +175,21 @@ __device__ __forceinline__ void store_codes(int8_t* __restrict__ p, int64_t c, i
   }
 }
 
-// kNorm: y = layer norm of x, else y = x.
-template <typename T, int kT, int kV, bool kNorm>
-__global__ __launch_bounds__(kT < 256 ? 256 : kT) void int8quant_kernel(
-    int64_t rows, int64_t cols, const T* __restrict__ x, int64_t ldx,
-    const T* __restrict__ gamma, const T* __restrict__ beta, double eps,
+// kNorm: y = layer norm of x, else y = x.  fp64 x: everything in fp64.
+template <int kT, int kV, bool kNorm>
+__device__ __forceinline__ void int8quant_row_f64(
+    int64_t row, int64_t cols, const double* __restrict__ x, int64_t ldx,
+    const double* __restrict__ gamma, const double* __restrict__ beta, double eps,
     int8_t* __restrict__ q, int64_t ldq, float* __restrict__ scale) {
-  constexpr int N = Vec<T>::N;
-  constexpr int kRows = kT < 256 ? 256 / kT : 1;
-  __shared__ double slots[4][kT / 64];
+  constexpr int N = Vec<double>::N;
+  __shared__ double slots[3][kT / 64];
   const int t = threadIdx.x % kT;
-  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kT;
-  if (kRows > 1 && row >= rows) return;
-  const T* xr = x + row * ldx;
+  const double* xr = x + row * ldx;
   double a[kV][N];
   double sum = 0;
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
-    load_vec<T, double>(xr, (int64_t)(v * kT + t) * N, cols, a[v]);
+    load_vec<double, double>(xr, (int64_t)(v * kT + t) * N, cols, a[v]);
     if (kNorm) {
 #pragma unroll
       for (int u = 0; u < N; ++u) sum += a[v][u];
@@ -217,8 +213,8 @@ __global__ __launch_bounds__(kT < 256 ? 256 : kT) void int8quant_kernel(
     for (int v = 0; v < kV; ++v) {
       const int64_t c = (int64_t)(v * kT + t) * N;
       double g[N], b[N];
-      if (gamma) load_vec<T, double>(gamma, c, cols, g);
-      if (beta) load_vec<T, double>(beta, c, cols, b);
+      if (gamma) load_vec<double, double>(gamma, c, cols, g);
+      if (beta) load_vec<double, double>(beta, c, cols, b);
       const int nv = valid<N>(c, cols);
 #pragma unroll
       for (int u = 0; u < N; ++u) {
@@ -252,6 +248,189 @@ __global__ __launch_bounds__(kT < 256 ? 256 : kT) void int8quant_kernel(
     for (int u = 0; u < N; ++u) codes[u] = cs.inv == 0.0 ? 0 : code_of(a[v][u], cs.inv);
     store_codes<N>(qr, c, cols, codes);
   }
+}
+
+// x of at most 32 bits: the same codes and scale, most of the work in fp32.  The row's sums are
+// fp64 (of x - c and its square, c the row's first value; again about the mean where c lies
+// far from it).  y and y / s are formed in fp32 beside a bound e of their error; where that
+// bound leaves the largest magnitude or a code's rounding open (about one value in five
+// thousand), the value is formed in fp64.  A row whose magnitudes are out of the bound's
+// reach (below 1e-30, above 1e37, not finite) takes fp64 throughout.
+// All in fp64, 4096 x 8192 bf16 with the norm took 69.5 us, 4096 x 16384 without 61.1.
+template <typename T, int kT, int kV, bool kNorm>
+__device__ __forceinline__ void int8quant_row(
+    int64_t row, int64_t cols, const T* __restrict__ x, int64_t ldx,
+    const T* __restrict__ gamma, const T* __restrict__ beta, double eps,
+    int8_t* __restrict__ q, int64_t ldq, float* __restrict__ scale) {
+  constexpr int N = Vec<T>::N, kW = kT / 64;
+  __shared__ double sums[kNorm ? 3 : 1][kW];
+  __shared__ float tops[3][kW];
+  const int t = threadIdx.x % kT;
+  const T* xr = x + row * ldx;
+  typename Vec<T>::type raw[kV];
+#pragma unroll
+  for (int v = 0; v < kV; ++v) raw[v] = ask_vec<T>(xr, (int64_t)(v * kT + t) * N, cols);
+
+  double mean = 0.0, rstd = 1.0;
+  if constexpr (kNorm) {
+    const double c0 = (double)xr[0], rows_inv = 1.0 / (double)cols;
+    double s1 = 0, s2 = 0;
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+      const int nv = valid<N>((int64_t)(v * kT + t) * N, cols);
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        const double d = u < nv ? (double)raw[v][u] - c0 : 0.0;
+        s1 += d;
+        s2 = __builtin_fma(d, d, s2);
+      }
+    }
+    s1 = wave_all(s1, SumOp());
+    s2 = wave_all(s2, SumOp());
+    if constexpr (kT > 64) {
+      if ((threadIdx.x & 63) == 0) {
+        sums[0][threadIdx.x >> 6] = s1;
+        sums[1][threadIdx.x >> 6] = s2;
+      }
+      __syncthreads();
+      s1 = sums[0][0];
+      s2 = sums[1][0];
+#pragma unroll
+      for (int w = 1; w < kW; ++w) {
+        s1 += sums[0][w];
+        s2 += sums[1][w];
+      }
+    }
+    const double off = s1 * rows_inv;
+    mean = c0 + off;
+    double var = s2 * rows_inv - off * off;
+    // the difference keeps 2^-53 (1 + off^2 / var) of var (uniform over the row)
+    if (!(off * off <= 64.0 * var)) {
+      double sq = 0;
+#pragma unroll 1
+      for (int64_t c = t; c < cols; c += kT) {
+        const double d = (double)xr[c] - mean;
+        sq = __builtin_fma(d, d, sq);
+      }
+      var = row_all<kT>(sq, SumOp(), sums[2]) * rows_inv;
+    }
+    rstd = 1.0 / sqrt(var + eps);
+  }
+  // y of column c in fp64
+  auto exact = [&](int64_t c) {
+    double y = (double)xr[c];
+    if (kNorm) {
+      y = (y - mean) * rstd;
+      if (gamma) y *= (double)gamma[c];
+      if (beta) y += (double)beta[c];
+    }
+    return y;
+  };
+  // Values that stand open are marked in a word per lane and taken up one by one: their code
+  // stands once, and no fp64 value lives in registers beside the row.
+  static_assert(kV * N <= 32, "one bit per value");
+  auto column = [&](int bit) { return (int64_t)(bit / N * kT + t) * N + bit % N; };
+  const float mean_hi = (float)mean, mean_lo = (float)(mean - (double)mean_hi);
+  const float rstd32 = (float)rstd;
+  float y[kV][N];
+  uint32_t top_y = 0, top_b = 0;   // magnitudes as bits: a NaN is above everything
+#pragma unroll
+  for (int v = 0; v < kV; ++v) {
+    const int64_t c = (int64_t)(v * kT + t) * N;
+    float g[N], b[N];
+    if (kNorm && gamma) load_vec<T, float>(gamma, c, cols, g);
+    if (kNorm && beta) load_vec<T, float>(beta, c, cols, b);
+    const int nv = valid<N>(c, cols);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      float w = (float)raw[v][u];
+      if (kNorm) {
+        w = ((w - mean_hi) - mean_lo) * rstd32;
+        if (gamma) w *= g[u];
+        if (beta) {
+          w += b[u];
+          const uint32_t m = __float_as_uint(b[u]) & 0x7fffffffu;
+          top_b = m > top_b ? m : top_b;
+        }
+        if (u >= nv) w = 0.0f;
+      }
+      y[v][u] = w;
+      const uint32_t m = __float_as_uint(w) & 0x7fffffffu;
+      top_y = m > top_y ? m : top_y;
+    }
+  }
+  // as floats the order of bits is that of the magnitudes, infinities included; a NaN is
+  // passed on as one
+  const float big = __builtin_huge_valf();
+  auto top = [&](uint32_t bits, float* slot) {
+    return row_all<kT>(bits > 0x7f800000u ? big : __uint_as_float(bits), MaxOp(), slot);
+  };
+  const float ymax = top(top_y, tops[0]);
+  const float bmax = kNorm && beta ? top(top_b, tops[1]) : 0.0f;
+  // fp32 y is off by at most 8 roundings of |y - b| + |y| <= 2 |y| + |b| (x is exact)
+  const float e = kNorm ? 8.0f * 5.97e-8f * (2.0f * ymax + bmax) : 0.0f;
+  const bool hard = !(ymax >= 1e-30f && ymax <= 1e37f && bmax <= 1e37f);
+  double amax = (double)ymax;
+  bool bad = false;
+  if (kNorm || hard) {
+    double m64 = 0;
+    uint32_t open = 0;
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+      const int nv = valid<N>((int64_t)(v * kT + t) * N, cols);
+#pragma unroll
+      for (int u = 0; u < N; ++u)
+        if (u < nv && (hard || __builtin_fabsf(y[v][u]) >= ymax - 2.0f * e))
+          open |= 1u << (v * N + u);
+    }
+#pragma unroll 1
+    for (; open; open &= open - 1) {
+      const double m = __builtin_fabs(exact(column(__builtin_ctz(open))));
+      bad |= !(m <= 1.7976931348623157e308);
+      m64 = m > m64 ? m : m64;
+    }
+    amax = row_all<kT>(bad ? __builtin_huge_val() : m64, MaxOp(), sums[0]);
+  }
+  const CodeScale cs = code_scale(amax, !(amax <= 1.7976931348623157e308));
+  if (t == 0) scale[row] = cs.scale;
+  const float inv32 = (float)cs.inv;
+  // of a quotient of at most 127: y's error, and roundings of the reciprocal and the product
+  const float near = hard ? 1.0f : e * inv32 + 4.0f * 127.0f * 5.97e-8f;
+  int8_t* qr = q + row * ldq;
+  uint32_t open = 0;
+#pragma unroll
+  for (int v = 0; v < kV; ++v) {
+    const int64_t c = (int64_t)(v * kT + t) * N;
+    if (c >= cols) continue;
+    const int nv = valid<N>(c, cols);
+    int codes[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const float p = y[v][u] * inv32, r = __builtin_rintf(p);
+      codes[u] = (int)r;
+      if (u < nv && !(__builtin_fabsf(p - r) <= 0.5f - near)) open |= 1u << (v * N + u);
+    }
+    store_codes<N>(qr, c, cols, codes);
+  }
+#pragma unroll 1
+  for (; open; open &= open - 1) {
+    const int64_t c = column(__builtin_ctz(open));
+    qr[c] = (int8_t)(cs.inv == 0.0 ? 0 : code_of(exact(c), cs.inv));
+  }
+}
+
+template <typename T, int kT, int kV, bool kNorm>
+__global__ __launch_bounds__(kT < 256 ? 256 : kT) void int8quant_kernel(
+    int64_t rows, int64_t cols, const T* __restrict__ x, int64_t ldx,
+    const T* __restrict__ gamma, const T* __restrict__ beta, double eps,
+    int8_t* __restrict__ q, int64_t ldq, float* __restrict__ scale) {
+  constexpr int kRows = kT < 256 ? 256 / kT : 1;
+  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kT;
+  if (kRows > 1 && row >= rows) return;   // whole waves
+  if constexpr (sizeof(T) == 8)
+    int8quant_row_f64<kT, kV, kNorm>(row, cols, x, ldx, gamma, beta, eps, q, ldq, scale);
+  else
+    int8quant_row<T, kT, kV, kNorm>(row, cols, x, ldx, gamma, beta, eps, q, ldq, scale);
 }
 
 template <typename T, bool kNorm>
@@ -322,50 +501,67 @@ __global__ __launch_bounds__(1024) void int8quant_long_kernel(
 
 // ------------------------------------------------------------------ backward
 // Workgroup b of G walks rows b, b + G, ...: dx row by row, and the column sums dy xh and dy
-// of its rows in registers, written to partials [G][2][cols] at the end.
+// of its rows in registers, written to partials [G][2][cols] at the end.  A row is asked for
+// one row ahead, before the reduction of the row in hand.
 template <typename T, int kT, int kV>
 __global__ __launch_bounds__(kT) void layernorm_backward_kernel(
-    int64_t rows, int64_t cols, const T* __restrict__ dy, int64_t lddy,
-    const T* __restrict__ x, int64_t ldx, const T* __restrict__ gamma,
-    const typename AccOf<T>::type* __restrict__ mean,
-    const typename AccOf<T>::type* __restrict__ rstd, T* __restrict__ dx, int64_t lddx,
+    int64_t rows, int64_t cols, const T* dy, int64_t lddy, const T* x, int64_t ldx,
+    const T* __restrict__ gamma, const typename AccOf<T>::type* __restrict__ mean,
+    const typename AccOf<T>::type* __restrict__ rstd, T* dx, int64_t lddx,
     typename AccOf<T>::type* __restrict__ part) {
   typedef typename AccOf<T>::type A;
+  typedef typename Vec<T>::type V;
   constexpr int N = Vec<T>::N;
   __shared__ A slots[2][2][kT / 64];
   const int t = threadIdx.x;
-  A dg[kV][N], db[kV][N];
+  // gamma stays in registers where a thread of a large workgroup has them
+  constexpr bool kKeep = kT * kV * N < 16384;
+  A dg[kV][N], db[kV][N], w[kKeep ? kV : 1][N];
+  V nx[kV], ny[kV];
+  A nmu = 0, nrho = 0;
+  auto ask = [&](int64_t row) {
+    if (row >= rows) return;
+    nmu = mean[row];
+    nrho = rstd[row];
 #pragma unroll
-  for (int v = 0; v < kV; ++v)
+    for (int v = 0; v < kV; ++v) {
+      const int64_t c = (int64_t)(v * kT + t) * N;
+      nx[v] = ask_vec<T>(x + row * ldx, c, cols);
+      ny[v] = ask_vec<T>(dy + row * lddy, c, cols);
+    }
+  };
+  ask(blockIdx.x);
 #pragma unroll
-    for (int u = 0; u < N; ++u) dg[v][u] = db[v][u] = 0;
+  for (int v = 0; v < kV; ++v) {
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      dg[v][u] = db[v][u] = 0;
+      if (kKeep || v == 0) w[kKeep ? v : 0][u] = 1;
+    }
+    if (kKeep && gamma) load_vec<T, A>(gamma, (int64_t)(v * kT + t) * N, cols, w[kKeep ? v : 0]);
+  }
   const A inv = (A)1 / (A)cols;
   int flip = 0;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, flip ^= 1) {
-    const T* xr = x + row * ldx;
-    const T* dyr = dy + row * lddy;
-    const A mu = mean[row], rho = rstd[row];
+    const A mu = nmu, rho = nrho;
     A xh[kV][N], g[kV][N];
     A s1 = 0, s2 = 0;
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
-      const int64_t c = (int64_t)(v * kT + t) * N;
-      A w[N];
-      load_vec<T, A>(xr, c, cols, xh[v]);
-      load_vec<T, A>(dyr, c, cols, g[v]);
-      if (gamma) load_vec<T, A>(gamma, c, cols, w);
-      const int nv = valid<N>(c, cols);
+      const int nv = valid<N>((int64_t)(v * kT + t) * N, cols);
+      if (!kKeep && gamma) load_vec<T, A>(gamma, (int64_t)(v * kT + t) * N, cols, w[0]);
 #pragma unroll
       for (int u = 0; u < N; ++u) {
-        xh[v][u] = u < nv ? (xh[v][u] - mu) * rho : (A)0;
-        const A d = g[v][u];
+        xh[v][u] = u < nv ? ((A)nx[v][u] - mu) * rho : (A)0;
+        const A d = (A)ny[v][u];
         dg[v][u] += d * xh[v][u];
         db[v][u] += d;
-        if (gamma) g[v][u] = d * w[u];
+        g[v][u] = d * w[kKeep ? v : 0][u];
         s1 += g[v][u] * xh[v][u];
         s2 += g[v][u];
       }
     }
+    ask(row + gridDim.x);
     // two slot sets in turn: a row's reads of one set end before the barrier of the next
     // row, which comes before the set is written again
     s1 = wave_all(s1, SumOp());
@@ -379,9 +575,9 @@ __global__ __launch_bounds__(kT) void layernorm_backward_kernel(
       s1 = slots[flip][0][0];
       s2 = slots[flip][1][0];
 #pragma unroll
-      for (int w = 1; w < kT / 64; ++w) {
-        s1 += slots[flip][0][w];
-        s2 += slots[flip][1][w];
+      for (int wv = 1; wv < kT / 64; ++wv) {
+        s1 += slots[flip][0][wv];
+        s2 += slots[flip][1][wv];
       }
     }
     const A c1 = s1 * inv, c2 = s2 * inv;
@@ -415,9 +611,9 @@ __global__ __launch_bounds__(kT) void layernorm_backward_kernel(
 // Rows too long for registers: dx from two passes over the row.
 template <typename T>
 __global__ __launch_bounds__(1024) void layernorm_backward_long_kernel(
-    int64_t cols, const T* __restrict__ dy, int64_t lddy, const T* __restrict__ x, int64_t ldx,
+    int64_t cols, const T* dy, int64_t lddy, const T* x, int64_t ldx,
     const T* __restrict__ gamma, const typename AccOf<T>::type* __restrict__ mean,
-    const typename AccOf<T>::type* __restrict__ rstd, T* __restrict__ dx, int64_t lddx) {
+    const typename AccOf<T>::type* __restrict__ rstd, T* dx, int64_t lddx) {
   typedef typename AccOf<T>::type A;
   constexpr int N = Vec<T>::N, kT = 1024;
   __shared__ A slots[2][kT / 64];
@@ -500,8 +696,19 @@ __global__ __launch_bounds__(256) void layernorm_join_kernel(
   const int cl = threadIdx.x & 15, slice = threadIdx.x >> 4;
   const int64_t c = (int64_t)blockIdx.x * 16 + cl;
   A s = 0;
-  if (c < 2 * cols)
-    for (int g = slice; g < groups; g += 16) s += part[(int64_t)g * 2 * cols + c];
+  if (c < 2 * cols) {
+    const A* p = part + c;
+    const int64_t ld = 2 * cols;
+    int g = slice;
+    for (; g + 112 < groups; g += 128) {   // eight partials asked for at once
+      A a[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) a[u] = p[(g + 16 * u) * ld];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += a[u];
+    }
+    for (; g < groups; g += 16) s += p[g * ld];
+  }
   sums[slice][cl] = s;
   __syncthreads();
   if (slice == 0 && c < 2 * cols) {

@@ -110,7 +110,7 @@ __device__ __forceinline__ A row_all(A v, F f, A* slot) {
 
 // Elements c .. c + N - 1 of a row of `cols`, zero past its end.
 template <typename T, typename A>
-__device__ __forceinline__ void load_vec(const T* __restrict__ p, int64_t c, int64_t cols,
+__device__ __forceinline__ void load_vec(const T* p, int64_t c, int64_t cols,
                                          A (&a)[Vec<T>::N]) {
   constexpr int N = Vec<T>::N;
   if (c + N <= cols) {
@@ -123,9 +123,22 @@ __device__ __forceinline__ void load_vec(const T* __restrict__ p, int64_t c, int
   }
 }
 
+// The same in two steps, so that a row can be asked for before it is needed: the 16 bytes
+// as they are (past the row's end: zeros), and their values.
+template <typename T>
+__device__ __forceinline__ typename Vec<T>::type ask_vec(const T* p, int64_t c,
+                                                         int64_t cols) {
+  constexpr int N = Vec<T>::N;
+  if (c + N <= cols) return *reinterpret_cast<const typename Vec<T>::type*>(p + c);
+  typename Vec<T>::type v;
+#pragma unroll
+  for (int u = 0; u < N; ++u) v[u] = c + u < cols ? p[c + u] : (T)0.0f;
+  return v;
+}
+
 // The same elements stored, each rounded once to T; nothing past the row's end.
 template <typename T, typename A>
-__device__ __forceinline__ void store_vec(T* __restrict__ p, int64_t c, int64_t cols,
+__device__ __forceinline__ void store_vec(T* p, int64_t c, int64_t cols,
                                           const A (&a)[Vec<T>::N]) {
   constexpr int N = Vec<T>::N;
   if (c + N <= cols) {
