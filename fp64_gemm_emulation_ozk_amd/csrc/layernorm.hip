@@ -264,27 +264,30 @@ __device__ __forceinline__ void int8quant_row(
     int8_t* __restrict__ q, int64_t ldq, float* __restrict__ scale) {
   constexpr int N = Vec<T>::N, kW = kT / 64;
   __shared__ double sums[kNorm ? 3 : 1][kW];
-  __shared__ float tops[3][kW];
+  __shared__ float tops[2][kW];
   const int t = threadIdx.x % kT;
   const T* xr = x + row * ldx;
   typename Vec<T>::type raw[kV];
+  uint32_t in_row = 0;   // a bit per value that lies in the row
 #pragma unroll
-  for (int v = 0; v < kV; ++v) raw[v] = ask_vec<T>(xr, (int64_t)(v * kT + t) * N, cols);
+  for (int v = 0; v < kV; ++v) {
+    const int64_t c = (int64_t)(v * kT + t) * N;
+    raw[v] = ask_vec_first<T>(xr, c, cols);
+    in_row |= ((1u << valid<N>(c, cols)) - 1u) << (v * N);
+  }
 
   double mean = 0.0, rstd = 1.0;
   if constexpr (kNorm) {
     const double c0 = (double)xr[0], rows_inv = 1.0 / (double)cols;
     double s1 = 0, s2 = 0;
 #pragma unroll
-    for (int v = 0; v < kV; ++v) {
-      const int nv = valid<N>((int64_t)(v * kT + t) * N, cols);
+    for (int v = 0; v < kV; ++v)
 #pragma unroll
       for (int u = 0; u < N; ++u) {
-        const double d = u < nv ? (double)raw[v][u] - c0 : 0.0;
+        const double d = (double)raw[v][u] - c0;
         s1 += d;
         s2 = __builtin_fma(d, d, s2);
       }
-    }
     s1 = wave_all(s1, SumOp());
     s2 = wave_all(s2, SumOp());
     if constexpr (kT > 64) {
@@ -337,22 +340,20 @@ __device__ __forceinline__ void int8quant_row(
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
     const int64_t c = (int64_t)(v * kT + t) * N;
-    float g[N], b[N];
-    if (kNorm && gamma) load_vec<T, float>(gamma, c, cols, g);
-    if (kNorm && beta) load_vec<T, float>(beta, c, cols, b);
-    const int nv = valid<N>(c, cols);
+    typename Vec<T>::type g, b;
+    if (kNorm && gamma) g = ask_vec_first<T>(gamma, c, cols);
+    if (kNorm && beta) b = ask_vec_first<T>(beta, c, cols);
 #pragma unroll
     for (int u = 0; u < N; ++u) {
       float w = (float)raw[v][u];
       if (kNorm) {
         w = ((w - mean_hi) - mean_lo) * rstd32;
-        if (gamma) w *= g[u];
+        if (gamma) w *= (float)g[u];
         if (beta) {
-          w += b[u];
-          const uint32_t m = __float_as_uint(b[u]) & 0x7fffffffu;
+          w += (float)b[u];
+          const uint32_t m = __float_as_uint((float)b[u]) & 0x7fffffffu;
           top_b = m > top_b ? m : top_b;
         }
-        if (u >= nv) w = 0.0f;
       }
       y[v][u] = w;
       const uint32_t m = __float_as_uint(w) & 0x7fffffffu;
@@ -361,12 +362,22 @@ __device__ __forceinline__ void int8quant_row(
   }
   // as floats the order of bits is that of the magnitudes, infinities included; a NaN is
   // passed on as one
-  const float big = __builtin_huge_valf();
-  auto top = [&](uint32_t bits, float* slot) {
-    return row_all<kT>(bits > 0x7f800000u ? big : __uint_as_float(bits), MaxOp(), slot);
+  auto top = [](uint32_t bits) {
+    return wave_all(bits > 0x7f800000u ? __builtin_huge_valf() : __uint_as_float(bits), MaxOp());
   };
-  const float ymax = top(top_y, tops[0]);
-  const float bmax = kNorm && beta ? top(top_b, tops[1]) : 0.0f;
+  float ymax = top(top_y), bmax = kNorm && beta ? top(top_b) : 0.0f;
+  if constexpr (kT > 64) {
+    if ((threadIdx.x & 63) == 0) {
+      tops[0][threadIdx.x >> 6] = ymax;
+      tops[1][threadIdx.x >> 6] = bmax;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+      ymax = tops[0][w] > ymax ? tops[0][w] : ymax;
+      bmax = tops[1][w] > bmax ? tops[1][w] : bmax;
+    }
+  }
   // fp32 y is off by at most 8 roundings of |y - b| + |y| <= 2 |y| + |b| (x is exact)
   const float e = kNorm ? 8.0f * 5.97e-8f * (2.0f * ymax + bmax) : 0.0f;
   const bool hard = !(ymax >= 1e-30f && ymax <= 1e37f && bmax <= 1e37f);
@@ -375,14 +386,13 @@ __device__ __forceinline__ void int8quant_row(
   if (kNorm || hard) {
     double m64 = 0;
     uint32_t open = 0;
+    const float least = ymax - 2.0f * e;
 #pragma unroll
-    for (int v = 0; v < kV; ++v) {
-      const int nv = valid<N>((int64_t)(v * kT + t) * N, cols);
+    for (int v = 0; v < kV; ++v)
 #pragma unroll
       for (int u = 0; u < N; ++u)
-        if (u < nv && (hard || __builtin_fabsf(y[v][u]) >= ymax - 2.0f * e))
-          open |= 1u << (v * N + u);
-    }
+        open |= __builtin_fabsf(y[v][u]) >= least ? 1u << (v * N + u) : 0u;
+    open = (hard ? ~0u : open) & in_row;
 #pragma unroll 1
     for (; open; open &= open - 1) {
       const double m = __builtin_fabs(exact(column(__builtin_ctz(open))));
@@ -395,23 +405,22 @@ __device__ __forceinline__ void int8quant_row(
   if (t == 0) scale[row] = cs.scale;
   const float inv32 = (float)cs.inv;
   // of a quotient of at most 127: y's error, and roundings of the reciprocal and the product
-  const float near = hard ? 1.0f : e * inv32 + 4.0f * 127.0f * 5.97e-8f;
+  const float within = hard ? -1.0f : 0.5f - (e * inv32 + 4.0f * 127.0f * 5.97e-8f);
   int8_t* qr = q + row * ldq;
   uint32_t open = 0;
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
-    const int64_t c = (int64_t)(v * kT + t) * N;
-    if (c >= cols) continue;
-    const int nv = valid<N>(c, cols);
     int codes[N];
 #pragma unroll
     for (int u = 0; u < N; ++u) {
       const float p = y[v][u] * inv32, r = __builtin_rintf(p);
       codes[u] = (int)r;
-      if (u < nv && !(__builtin_fabsf(p - r) <= 0.5f - near)) open |= 1u << (v * N + u);
+      open |= __builtin_fabsf(p - r) <= within ? 0u : 1u << (v * N + u);
     }
-    store_codes<N>(qr, c, cols, codes);
+    const int64_t c = (int64_t)(v * kT + t) * N;
+    if (c < cols) store_codes<N>(qr, c, cols, codes);
   }
+  open &= in_row;
 #pragma unroll 1
   for (; open; open &= open - 1) {
     const int64_t c = column(__builtin_ctz(open));
@@ -500,11 +509,12 @@ __global__ __launch_bounds__(1024) void int8quant_long_kernel(
 }
 
 // ------------------------------------------------------------------ backward
-// Workgroup b of G walks rows b, b + G, ...: dx row by row, and the column sums dy xh and dy
-// of its rows in registers, written to partials [G][2][cols] at the end.  A row is asked for
-// one row ahead, before the reduction of the row in hand.
+// Workgroup b of G walks rows b, b + G, ... (four rows at once, one a wave, where a wave
+// holds a row): dx row by row, and the column sums dy xh and dy of its rows in registers,
+// written to partials [G][2][cols] at the end.  A row is asked for one row ahead, before the
+// reduction of the row in hand.
 template <typename T, int kT, int kV>
-__global__ __launch_bounds__(kT) void layernorm_backward_kernel(
+__global__ __launch_bounds__(kT < 256 ? 256 : kT) void layernorm_backward_kernel(
     int64_t rows, int64_t cols, const T* dy, int64_t lddy, const T* x, int64_t ldx,
     const T* __restrict__ gamma, const typename AccOf<T>::type* __restrict__ mean,
     const typename AccOf<T>::type* __restrict__ rstd, T* dx, int64_t lddx,
@@ -512,8 +522,11 @@ __global__ __launch_bounds__(kT) void layernorm_backward_kernel(
   typedef typename AccOf<T>::type A;
   typedef typename Vec<T>::type V;
   constexpr int N = Vec<T>::N;
+  constexpr int kRows = kT < 256 ? 256 / kT : 1;   // rows of a workgroup at once
   __shared__ A slots[2][2][kT / 64];
-  const int t = threadIdx.x;
+  __shared__ A joined[kRows > 1 ? (kRows - 1) * 2 * kV * N * 64 : 1];
+  const int t = threadIdx.x % kT, sub = threadIdx.x / kT;
+  const int64_t stride = (int64_t)gridDim.x * kRows;
   // gamma stays in registers where a thread of a large workgroup has them
   constexpr bool kKeep = kT * kV * N < 16384;
   A dg[kV][N], db[kV][N], w[kKeep ? kV : 1][N];
@@ -530,7 +543,7 @@ __global__ __launch_bounds__(kT) void layernorm_backward_kernel(
       ny[v] = ask_vec<T>(dy + row * lddy, c, cols);
     }
   };
-  ask(blockIdx.x);
+  ask(blockIdx.x * kRows + sub);
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
 #pragma unroll
@@ -542,7 +555,7 @@ __global__ __launch_bounds__(kT) void layernorm_backward_kernel(
   }
   const A inv = (A)1 / (A)cols;
   int flip = 0;
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, flip ^= 1) {
+  for (int64_t row = blockIdx.x * kRows + sub; row < rows; row += stride, flip ^= 1) {
     const A mu = nmu, rho = nrho;
     A xh[kV][N], g[kV][N];
     A s1 = 0, s2 = 0;
@@ -561,7 +574,7 @@ __global__ __launch_bounds__(kT) void layernorm_backward_kernel(
         s2 += g[v][u];
       }
     }
-    ask(row + gridDim.x);
+    ask(row + stride);
     // two slot sets in turn: a row's reads of one set end before the barrier of the next
     // row, which comes before the set is written again
     s1 = wave_all(s1, SumOp());
@@ -593,11 +606,50 @@ __global__ __launch_bounds__(kT) void layernorm_backward_kernel(
       }
     }
   }
-  if (part) {
-    A* p = part + (int64_t)blockIdx.x * 2 * cols;
+  if (!part) return;   // the whole grid
+  if constexpr (kRows > 1) {   // the waves' sums, in order
+    A* mine = joined + (sub - 1) * (2 * kV * N * 64) + t;
+    if (sub) {
 #pragma unroll
-    for (int v = 0; v < kV; ++v) {
-      const int64_t c = (int64_t)(v * kT + t) * N;
+      for (int v = 0; v < kV; ++v)
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+          mine[(v * N + u) * 64] = dg[v][u];
+          mine[((kV + v) * N + u) * 64] = db[v][u];
+        }
+    }
+    __syncthreads();
+    if (sub) return;
+#pragma unroll
+    for (int w = 0; w < kRows - 1; ++w)
+#pragma unroll
+      for (int v = 0; v < kV; ++v)
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+          const A* his = joined + w * (2 * kV * N * 64) + t;
+          dg[v][u] += his[(v * N + u) * 64];
+          db[v][u] += his[((kV + v) * N + u) * 64];
+        }
+  }
+  A* p = part + (int64_t)blockIdx.x * 2 * cols;
+  typedef A S __attribute__((ext_vector_type(16 / sizeof(A)), aligned(sizeof(A))));
+  constexpr int NS = 16 / (int)sizeof(A);   // sums of a 16-byte store
+#pragma unroll
+  for (int v = 0; v < kV; ++v) {
+    const int64_t c = (int64_t)(v * kT + t) * N;
+    if (c + N <= cols) {
+#pragma unroll
+      for (int u = 0; u < N; u += NS) {
+        S a, b;
+#pragma unroll
+        for (int e = 0; e < NS; ++e) {
+          a[e] = dg[v][u + e];
+          b[e] = db[v][u + e];
+        }
+        *reinterpret_cast<S*>(p + c + u) = a;
+        *reinterpret_cast<S*>(p + cols + c + u) = b;
+      }
+    } else {
 #pragma unroll
       for (int u = 0; u < N; ++u)
         if (c + u < cols) {
@@ -722,12 +774,12 @@ __global__ __launch_bounds__(256) void layernorm_join_kernel(
 }
 
 // Threads and vectors per thread for a row of `vecs` 16-byte vectors.
-#define OZK_ROW_SHAPES(GO)         \
-  if (vecs <= 64) GO(64, 1);       \
-  else if (vecs <= 128) GO(64, 2); \
-  else if (vecs <= 256) GO(64, 4); \
-  else if (vecs <= 512) GO(256, 2);  \
-  else if (vecs <= 1024) GO(256, 4); \
+#define OZK_ROW_SHAPES(GO)            \
+  if (vecs <= 64) GO(64, 1);          \
+  else if (vecs <= 128) GO(64, 2);    \
+  else if (vecs <= 256) GO(64, 4);    \
+  else if (vecs <= 512) GO(256, 2);   \
+  else if (vecs <= 1024) GO(256, 4);  \
   else if (vecs <= 2048) GO(1024, 2); \
   else GO(1024, 4)
 constexpr int64_t kRowVecs = 4096;   // vectors a workgroup holds
@@ -754,24 +806,36 @@ int layernorm_t(int64_t rows, int64_t cols, const void* x, int64_t ldx, const vo
   return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
 }
 
+// Threads of a row and values per thread for the codes.  The reductions and the fp64 divisions
+// cost a wave the same whatever it holds, so many rows take up to 32 values per thread (4096 x
+// 8192 with the norm, bf16 / fp32: 42 / 76 us with 16 / 8 values per thread); a few rows leave
+// the chip empty and spread wider (1 x 8192: 6.0 us, 8.0 with 32 values a thread, 7.1 with 8).
 template <typename T, bool kNorm>
 int int8quant_t(int64_t rows, int64_t cols, const void* x, int64_t ldx, const void* gamma,
                 const void* beta, double eps, int8_t* q, int64_t ldq, float* scale,
                 hipStream_t s) {
-  const int64_t vecs = (cols + Vec<T>::N - 1) / Vec<T>::N;
+  constexpr int N = Vec<T>::N;
   const T *xt = (const T*)x, *gt = (const T*)gamma, *bt = (const T*)beta;
-  if (vecs > kRowVecs) {
-    hipLaunchKernelGGL((int8quant_long_kernel<T, kNorm>), dim3((unsigned)rows), dim3(1024), 0, s,
-                       cols, xt, ldx, gt, bt, eps, q, ldq, scale);
-  } else {
-#define OZK_Q(NT, NV)                                                                          \
-  hipLaunchKernelGGL((int8quant_kernel<T, NT, NV, kNorm>),                                     \
+  const bool wide = rows < 256;
+#define OZK_Q(NT, VALUES)                                                                      \
+  hipLaunchKernelGGL((int8quant_kernel<T, NT, VALUES / N, kNorm>),                             \
                      dim3((unsigned)(NT < 256 ? (rows + 3) / 4 : rows)),                       \
                      dim3(NT < 256 ? 256 : NT), 0, s, rows, cols, xt, ldx, gt, bt, eps, q,     \
                      ldq, scale)
-    OZK_ROW_SHAPES(OZK_Q);
+  constexpr int kMost = N == 2 ? 16 : 32;   // fp64 rows: their values' registers
+  if (cols > 1024 * kMost)
+    hipLaunchKernelGGL((int8quant_long_kernel<T, kNorm>), dim3((unsigned)rows), dim3(1024), 0, s,
+                       cols, xt, ldx, gt, bt, eps, q, ldq, scale);
+  else if (cols <= 512) OZK_Q(64, 8);
+  else if (cols <= 2048 && wide) OZK_Q(256, 8);
+  else if (cols <= 8192 && wide) OZK_Q(512, 16);
+  else if (cols <= 1024) OZK_Q(64, 16);
+  else if (cols <= 2048) OZK_Q(64, 32);
+  else if (cols <= 4096) OZK_Q(256, 16);
+  else if (cols <= 8192) OZK_Q(256, 32);
+  else if (cols <= 16384) OZK_Q(1024, 16);
+  else if constexpr (kMost == 32) OZK_Q(1024, 32);
 #undef OZK_Q
-  }
   return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
 }
 
@@ -785,13 +849,16 @@ int layernorm_backward_t(int64_t rows, int64_t cols, const void* dy, int64_t ldd
                          void* workspace, hipStream_t s) {
   typedef typename AccOf<T>::type A;
   const int64_t vecs = (cols + Vec<T>::N - 1) / Vec<T>::N;
-  const int groups = layernorm_backward_groups(rows);
+  const bool in_registers = vecs <= kBackwardVecs;
+  const int rows_once = in_registers ? (vecs <= 128 ? 4 : 1) : 8;
+  int groups = (int)((rows + rows_once - 1) / rows_once);
+  if (groups > layernorm_backward_groups(rows)) groups = layernorm_backward_groups(rows);
   A* part = dgamma || dbeta ? (A*)workspace : nullptr;
   const T *dyt = (const T*)dy, *xt = (const T*)x, *gt = (const T*)gamma;
   const A *mt = (const A*)mean, *rt = (const A*)rstd;
   if (rows == 0) {
     part = nullptr;
-  } else if (vecs > kBackwardVecs) {
+  } else if (!in_registers) {
     if (dx)
       hipLaunchKernelGGL((layernorm_backward_long_kernel<T>), dim3((unsigned)rows), dim3(1024),
                          0, s, cols, dyt, lddy, xt, ldx, gt, mt, rt, (T*)dx, lddx);
@@ -801,8 +868,9 @@ int layernorm_backward_t(int64_t rows, int64_t cols, const void* dy, int64_t ldd
                          rows, cols, dyt, lddy, xt, ldx, mt, rt, part);
   } else {
 #define OZK_LNB(NT, NV)                                                                       \
-  hipLaunchKernelGGL((layernorm_backward_kernel<T, NT, NV>), dim3((unsigned)groups), dim3(NT), \
-                     0, s, rows, cols, dyt, lddy, xt, ldx, gt, mt, rt, (T*)dx, lddx, part)
+  hipLaunchKernelGGL((layernorm_backward_kernel<T, NT, NV>), dim3((unsigned)groups),          \
+                     dim3(NT < 256 ? 256 : NT), 0, s, rows, cols, dyt, lddy, xt, ldx, gt, mt, \
+                     rt, (T*)dx, lddx, part)
     if (vecs <= 64) OZK_LNB(64, 1);
     else if (vecs <= 128) OZK_LNB(64, 2);
     else if (vecs <= 256) OZK_LNB(256, 1);
@@ -819,8 +887,8 @@ int layernorm_backward_t(int64_t rows, int64_t cols, const void* dy, int64_t ldd
 
 }  // namespace
 
-// Row groups of the backward pass: two workgroups' worth of rows per CU, each leaving one
-// partial of the column sums.
+// Row groups of the backward pass at most: two workgroups per CU, each leaving one partial of
+// the column sums.
 int layernorm_backward_groups(int64_t rows) { return (int)(rows < 512 ? rows : 512); }
 
 int launch_layernorm(int64_t rows, int64_t cols, int type, const void* x, int64_t ldx,

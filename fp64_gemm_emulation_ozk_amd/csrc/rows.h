@@ -136,6 +136,19 @@ __device__ __forceinline__ typename Vec<T>::type ask_vec(const T* p, int64_t c,
   return v;
 }
 
+// The same with the row's first element past its end: what stands there then adds nothing to
+// a maximum over the row, nor to sums of differences from that element, and needs no mask.
+template <typename T>
+__device__ __forceinline__ typename Vec<T>::type ask_vec_first(const T* p, int64_t c,
+                                                               int64_t cols) {
+  constexpr int N = Vec<T>::N;
+  if (c + N <= cols) return *reinterpret_cast<const typename Vec<T>::type*>(p + c);
+  typename Vec<T>::type v;
+#pragma unroll
+  for (int u = 0; u < N; ++u) v[u] = p[c + u < cols ? c + u : 0];
+  return v;
+}
+
 // The same elements stored, each rounded once to T; nothing past the row's end.
 template <typename T, typename A>
 __device__ __forceinline__ void store_vec(T* p, int64_t c, int64_t cols,

@@ -262,6 +262,45 @@ def test_int8quant_rows(kind, cols):
         check_codes(q, scale, layers.layernorm(host(x), eps=0.5)[0])
 
 
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("cols", [65, 520, 1030, 2047, 4096, 5000, 8200, 16390])
+def test_int8quant_many_rows(kind, cols):
+    """The shapes that many rows take; among them rows far from their first value's scale
+    (the sums are taken again about the mean), of magnitudes beyond fp32 arithmetic's reach,
+    and with quotients on and beside the borders."""
+    announce(f"int8quant many rows {kind} cols={cols}")
+    dtype, rows = TYPES[kind], 260
+    x, gamma, beta, _ = row_input(rows, cols, dtype, cols + 3)
+    big = 1e30 if kind in ("float64", "float32", "bfloat16") else 6e4
+    x[3, 0] = big                      # the first value alone
+    x[4, :] = 1000.0 + x[4] % 1        # far from zero
+    x[5] *= 2.0 ** -20
+    if kind != "float16":
+        x[6] *= 1e36
+        x[7] *= 1e-36
+    half = torch.arange(cols, dtype=torch.float64) % 255 - 127
+    x[8] = (half / 2 + 0.25).to(dtype)
+    x[9] = half.to(dtype)
+    x[9, 0], x[9, 1:7] = 127, torch.tensor([0.5, 1.5, 2.5, -0.5, -1.5, 126.5]).to(dtype)
+    x[10] = 0
+    x[11, 1] = float("nan")
+    xd = padded(x, 1, 3)
+    q, scale = ozk.ozk_int8quant_rows(xd)
+    check_codes(q, scale, host(x))
+    assert q[9, 1:7].tolist() == [0, 2, 2, 0, -2, 126]
+    with np.errstate(over="ignore", invalid="ignore"):
+        y = layers.layernorm(host(x), host(gamma), host(beta))[0]
+        plain = layers.layernorm(host(x))[0]
+    # row 3's statistics hang on one value: its others differ from the mean by less than fp64
+    # keeps of it, in the reference as well
+    keep = [i for i in range(rows) if i != 3]
+    q, scale = ozk.ozk_int8quant_rows(xd, norm=True, gamma=gamma.to(device()),
+                                      beta=beta.to(device()))
+    check_codes(q[keep], scale[keep], y[keep])
+    q, scale = ozk.ozk_int8quant_rows(xd, norm=True)
+    check_codes(q[keep], scale[keep], plain[keep])
+
+
 def test_int8quant_rows_edges():
     """NaN, Inf, fp64 values past fp32's range, values below every fp32 scale, subnormal
     scales, ties to even; what stands behind a row's end stays."""
