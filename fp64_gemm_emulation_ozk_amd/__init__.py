@@ -11,6 +11,7 @@ library is not built, loading fails with an error.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -653,14 +654,21 @@ def ozk_int4int8gemm_fp4awe(a: torch.Tensor, b: torch.Tensor, out: torch.Tensor 
 def _check_rows(t: torch.Tensor, dtype, name: str):
     """A matrix operand of the layer operators.  Rows that overlap (an expanded or unfolded
     view) have no leading dimension the library takes."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.dim() == 2
+            and t.is_contiguous()):
+        return
     _check(t, dtype, name)
     if t.shape[0] > 1 and t.shape[1] > 0 and t.stride(0) < t.shape[1]:
         raise ValueError(f"{name}'s rows overlap")
 
 
 def _check_like(t: torch.Tensor | None, shape: tuple, dtype, name: str, device):
-    """An operand of the layer operators that may be absent: shape, dtype, device, strides."""
+    """An operand of the layer operators that may be absent: shape, dtype, device, strides.
+    (These calls take a few microseconds on the GPU: what holds is found out at once.)"""
     if t is None:
+        return
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == device and t.is_contiguous()):
         return
     if len(shape) == 2:
         _check_rows(t, dtype, name)
@@ -681,38 +689,60 @@ def _check_workspace(t: torch.Tensor | None, device):
 
 
 class _On:
-    """The calls of a `with` block go to `device`: its current stream (or `stream`), its
-    context.  Switching costs a few microseconds and is left out on the current device."""
+    """The calls of a `with` block go to `device`: its context and its current stream, unless
+    another is given.  Switching costs a few microseconds and is left out on the current
+    device."""
+
+    __slots__ = ("_device", "_guard")
 
     def __init__(self, device):
-        self._guard = (None if device.index == torch.cuda.current_device()
-                       else torch.cuda.device(device))
+        self._device = device
+        self._guard = None
 
     def __enter__(self):
-        if self._guard is not None:
+        if self._device.index != torch.cuda.current_device():
+            self._guard = torch.cuda.device(self._device)
             self._guard.__enter__()
+        return self
 
     def __exit__(self, *exc):
         if self._guard is not None:
             self._guard.__exit__(*exc)
 
+    def stream(self, stream, *tensors):
+        """The handle of `stream`, tensors marked as used there (as _stream), or of the
+        device's current stream."""
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self._device.index)
+        return _stream(stream, *tensors)
+
+
+def _at(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+@functools.lru_cache(maxsize=1024)
+def _layer_size(name: str, *args) -> int:
+    """A workspace query, a function of its arguments alone."""
+    return _size_query(name, *args)
+
 
 def ozk_dgemm_epilogue_workspace_size(m: int, n: int, k: int, r: int) -> int:
-    return _size_query("ozk_dgemm_epilogue_workspace_size", m, n, k, r)
+    return _layer_size("ozk_dgemm_epilogue_workspace_size", m, n, k, r)
 
 
 def ozk_dgemm_epilogue_grad_workspace_size(m: int, n: int, k: int, r: int) -> int:
-    return _size_query("ozk_dgemm_epilogue_grad_workspace_size", m, n, k, r)
+    return _layer_size("ozk_dgemm_epilogue_grad_workspace_size", m, n, k, r)
 
 
 def ozk_int8linear_workspace_size(m: int, n: int, k: int, aligned: bool = False) -> int:
     """aligned: X and W at multiples of 16 bytes, k and both leading dimensions multiples of
     16 and the latter below 2^24."""
-    return _size_query("ozk_int8linear_workspace_size", m, n, k, 1 if aligned else 0)
+    return _layer_size("ozk_int8linear_workspace_size", m, n, k, 1 if aligned else 0)
 
 
 def ozk_layernorm_backward_workspace_size(rows: int, cols: int, dtype) -> int:
-    return _size_query("ozk_layernorm_backward_workspace_size", rows, cols, _type(dtype))
+    return _layer_size("ozk_layernorm_backward_workspace_size", rows, cols, _type(dtype))
 
 
 def _type(dtype) -> int:
@@ -742,15 +772,15 @@ def ozk_dgemm_epilogue(a: torch.Tensor, b: torch.Tensor, r: int,
     for t, name in ((residual, "residual"), (preact, "preact"), (out, "out")):
         _check_like(t, (m, n), torch.float64, name, a.device)
     _check_workspace(workspace, a.device)
-    with _On(a.device):
+    with _On(a.device) as on:
         if out is None:
-            out = torch.empty((m, n), dtype=torch.float64, device=a.device)
+            out = a.new_empty((m, n))
         if workspace is None:
             workspace = _workspace(ozk_dgemm_epilogue_workspace_size(m, n, k, r), a.device)
-        _call("ozk_dgemm_epilogue", m, n, k, _dev_ptr(a), _ld(a), _dev_ptr(b), _ld(b),
-              _dev_ptr(bias), _act(act), _dev_ptr(residual), _ld_opt(residual),
-              _dev_ptr(preact), _ld_opt(preact), _dev_ptr(out), _ld(out), r, _scaling(scaling),
-              _dev_ptr(workspace), workspace.numel(), _stream(stream, out, workspace))
+        _call("ozk_dgemm_epilogue", m, n, k, _at(a), _ld(a), _at(b), _ld(b),
+              _at(bias), _act(act), _at(residual), _ld_opt(residual),
+              _at(preact), _ld_opt(preact), _at(out), _ld(out), r, _scaling(scaling),
+              _at(workspace), workspace.numel(), on.stream(stream, out, workspace))
     return out
 
 
@@ -776,17 +806,17 @@ def ozk_dgemm_epilogue_grad(dc: torch.Tensor, a: torch.Tensor, b: torch.Tensor, 
     _check_like(db, (k, n), torch.float64, "db", dc.device)
     _check_like(dbias, (n,), torch.float64, "dbias", dc.device)
     _check_workspace(workspace, dc.device)
-    with _On(dc.device):
-        new = lambda *shape: torch.empty(shape, dtype=torch.float64, device=dc.device)
+    with _On(dc.device) as on:
+        new = lambda *shape: dc.new_empty(shape)
         da = (new(m, k) if da is None else da) if need_da else None
         db = (new(k, n) if db is None else db) if need_db else None
         dbias = (new(n) if dbias is None else dbias) if need_dbias else None
         if workspace is None:
             workspace = _workspace(ozk_dgemm_epilogue_grad_workspace_size(m, n, k, r), dc.device)
-        _call("ozk_dgemm_epilogue_grad", m, n, k, _dev_ptr(dc), _ld(dc), _dev_ptr(a), _ld(a),
-              _dev_ptr(b), _ld(b), _dev_ptr(preact), _ld_opt(preact), act, _dev_ptr(da),
-              _ld_opt(da), _dev_ptr(db), _ld_opt(db), _dev_ptr(dbias), r, _scaling(scaling),
-              _dev_ptr(workspace), workspace.numel(), _stream(stream, da, db, dbias, workspace))
+        _call("ozk_dgemm_epilogue_grad", m, n, k, _at(dc), _ld(dc), _at(a), _ld(a),
+              _at(b), _ld(b), _at(preact), _ld_opt(preact), act, _at(da),
+              _ld_opt(da), _at(db), _ld_opt(db), _at(dbias), r, _scaling(scaling),
+              _at(workspace), workspace.numel(), on.stream(stream, da, db, dbias, workspace))
     return da, db, dbias
 
 
@@ -814,18 +844,18 @@ def ozk_int8linear(x: torch.Tensor, scale_x: torch.Tensor, w: torch.Tensor,
     _check_like(residual, (m, n), dtype, "residual", x.device)
     _check_like(out, (m, n), dtype, "out", x.device)
     _check_workspace(workspace, x.device)
-    with _On(x.device):
+    with _On(x.device) as on:
         if out is None:
-            out = torch.empty((m, n), dtype=dtype, device=x.device)
+            out = x.new_empty((m, n), dtype=dtype)
         aligned = ((x.data_ptr() | w.data_ptr() | _ld(x) | _ld(w) | k) & 15 == 0
                    and max(_ld(x), _ld(w)) < 1 << 24)
         ws_bytes = ozk_int8linear_workspace_size(m, n, k, aligned)
         if workspace is None and ws_bytes > 0:
             workspace = _workspace(ws_bytes, x.device)
-        _call("ozk_int8linear", m, n, k, _dev_ptr(x), _ld(x), _dev_ptr(scale_x), _dev_ptr(w),
-              _ld(w), _dev_ptr(scale_w), _dev_ptr(bias), _act(act), _dev_ptr(residual),
-              _ld_opt(residual), code, _dev_ptr(out), _ld(out), _dev_ptr(workspace),
-              0 if workspace is None else workspace.numel(), _stream(stream, out, workspace))
+        _call("ozk_int8linear", m, n, k, _at(x), _ld(x), _at(scale_x), _at(w),
+              _ld(w), _at(scale_w), _at(bias), _act(act), _at(residual),
+              _ld_opt(residual), code, _at(out), _ld(out), _at(workspace),
+              0 if workspace is None else workspace.numel(), on.stream(stream, out, workspace))
     return out
 
 
@@ -853,14 +883,14 @@ def ozk_int8quant_rows(x: torch.Tensor, norm: bool = False, gamma: torch.Tensor 
     _check_norm_weights(x, gamma, beta)
     _check_like(out, (rows, cols), torch.int8, "out", x.device)
     _check_like(scale, (rows,), torch.float32, "scale", x.device)
-    with _On(x.device):
+    with _On(x.device) as on:
         if out is None:
-            out = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
+            out = x.new_empty((rows, cols), dtype=torch.int8)
         if scale is None:
-            scale = torch.empty(rows, dtype=torch.float32, device=x.device)
-        _call("ozk_int8quant_rows", rows, cols, code, _dev_ptr(x), _ld(x), 1 if norm else 0,
-              _dev_ptr(gamma), _dev_ptr(beta), float(eps), _dev_ptr(out), _ld(out),
-              _dev_ptr(scale), _stream(stream, out, scale))
+            scale = x.new_empty(rows, dtype=torch.float32)
+        _call("ozk_int8quant_rows", rows, cols, code, _at(x), _ld(x), 1 if norm else 0,
+              _at(gamma), _at(beta), float(eps), _at(out), _ld(out),
+              _at(scale), on.stream(stream, out, scale))
     return out, scale
 
 
@@ -880,16 +910,16 @@ def ozk_layernorm(x: torch.Tensor, gamma: torch.Tensor | None = None,
     _check_like(out, (rows, cols), x.dtype, "out", x.device)
     for t, name in ((mean, "mean"), (rstd, "rstd")):
         _check_like(t, (rows,), _stats_type(x.dtype), name, x.device)
-    with _On(x.device):
+    with _On(x.device) as on:
         if out is None:
-            out = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+            out = x.new_empty((rows, cols))
         if stats:
-            new = lambda: torch.empty(rows, dtype=_stats_type(x.dtype), device=x.device)
+            new = lambda: x.new_empty(rows, dtype=_stats_type(x.dtype))
             mean = new() if mean is None else mean
             rstd = new() if rstd is None else rstd
-        _call("ozk_layernorm", rows, cols, code, _dev_ptr(x), _ld(x), _dev_ptr(gamma),
-              _dev_ptr(beta), float(eps), _dev_ptr(out), _ld(out), _dev_ptr(mean),
-              _dev_ptr(rstd), _stream(stream, out, mean, rstd))
+        _call("ozk_layernorm", rows, cols, code, _at(x), _ld(x), _at(gamma),
+              _at(beta), float(eps), _at(out), _ld(out), _at(mean),
+              _at(rstd), on.stream(stream, out, mean, rstd))
     return (out, mean, rstd) if stats else out
 
 
@@ -911,8 +941,8 @@ def ozk_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tenso
     _check_like(dgamma, (cols,), x.dtype, "dgamma", x.device)
     _check_like(dbeta, (cols,), x.dtype, "dbeta", x.device)
     _check_workspace(workspace, x.device)
-    with _On(x.device):
-        new = lambda *shape: torch.empty(shape, dtype=x.dtype, device=x.device)
+    with _On(x.device) as on:
+        new = lambda *shape: x.new_empty(shape)
         dx = (new(rows, cols) if dx is None else dx) if need_dx else None
         if need_weights:
             dgamma = new(cols) if dgamma is None else dgamma
@@ -922,9 +952,9 @@ def ozk_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tenso
                     ozk_layernorm_backward_workspace_size(rows, cols, x.dtype), x.device)
         else:
             dgamma = dbeta = None
-        _call("ozk_layernorm_backward", rows, cols, code, _dev_ptr(dy), _ld(dy), _dev_ptr(x),
-              _ld(x), _dev_ptr(gamma), _dev_ptr(mean), _dev_ptr(rstd), _dev_ptr(dx),
-              _ld_opt(dx), _dev_ptr(dgamma), _dev_ptr(dbeta), _dev_ptr(workspace),
+        _call("ozk_layernorm_backward", rows, cols, code, _at(dy), _ld(dy), _at(x),
+              _ld(x), _at(gamma), _at(mean), _at(rstd), _at(dx),
+              _ld_opt(dx), _at(dgamma), _at(dbeta), _at(workspace),
               0 if workspace is None else workspace.numel(),
-              _stream(stream, dx, dgamma, dbeta, workspace))
+              on.stream(stream, dx, dgamma, dbeta, workspace))
     return dx, dgamma, dbeta
