@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(PKG_DIR, "libozk.so")
 ARCH = "gfx950"
 DEVICE_SOURCES = ["deconstruct.hip", "gemm_i8.hip", "crt.hip", "gemv.hip", "gemv_digits.hip",
                   "fp4limb.hip", "fp4awe.hip", "fp4awe4.hip", "spmv.hip", "noalloc.hip",
-                  "dgemm_epilogue.hip", "int8linear.hip", "layernorm.hip"]
+                  "dgemm_epilogue.hip", "small_products.hip", "int8linear.hip", "layernorm.hip"]
 HOST_SOURCES = ["rns_host.cpp", "api.cpp"]
 
 COMMON_FLAGS = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",
@@ -36,6 +36,7 @@ EXTRA_FLAGS = {"crt.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                # without it the accumulators of the smaller tiles are copied between AGPRs and
                # VGPRs around every MFMA
                "int8linear.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+               "small_products.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                # the 6-product encoding table is searched at compile time
                "fp4awe.hip": ["-fconstexpr-steps=16777216"],
                "fp4awe4.hip": ["-fconstexpr-steps=16777216"]}

@@ -740,36 +740,87 @@ ProductLayout product_layout(const Product& P, int r) {
   return L;
 }
 
-// The product in emulated fp64, then E.
-int run_product(const Product& P, int r, int scaling, const DgemmEpilogue& E, double* out,
-                int64_t ldo, void* workspace, hipStream_t s) {
-  int wl = 0, wr = 0, st;
-  if ((st = scaling_widths(scaling, r, P.K, &wl, &wr))) return st;
-  const ProductLayout L = product_layout(P, r);
-  Carver cv(workspace);
-  int8_t* pl = static_cast<int8_t*>(cv.take(L.planes_l));
-  int8_t* pr = static_cast<int8_t*>(cv.take(L.planes_r));
-  int8_t* res = static_cast<int8_t*>(cv.take(L.residues));
-  int32_t* el = static_cast<int32_t*>(cv.take(L.exps_l));
-  int32_t* er = static_cast<int32_t*>(cv.take(L.exps_r));
-  void* scr_l = cv.take(L.scr_l);
-  void* scr_r = cv.take(L.scr_r);
-  const int64_t sl = P.rows * L.kp, sr = P.cols * L.kp;   // plane strides
-  if (P.left_axis == 0 && P.right_axis == 1) {
-    st = deconstruct_operands(P.left, P.rows, P.K, P.ldl, P.right, P.cols, P.ldr, r, scaling, wl,
-                              wr, pl, pr, L.kp, el, er, scr_l, scr_r, s);
-  } else {
-    st = deconstruct_impl(P.left, P.left_rows, P.left_cols, P.ldl, P.left_axis, r, scaling, wl,
-                          pl, L.kp, sl, el, scr_l, s);
-    if (st == OZK_OK)
-      st = deconstruct_impl(P.right, P.right_rows, P.right_cols, P.ldr, P.right_axis, r, scaling,
-                            wr, pr, L.kp, sr, er, scr_r, s);
+bool small(const Product& P) {
+  return small_lines(P.rows, P.K) && small_lines(P.cols, P.K);
+}
+
+// A product in its workspace, and what becomes of it.
+struct Job {
+  Product P;
+  DgemmEpilogue E;
+  double* out;
+  int64_t ldo;
+  ProductLayout L;
+  int8_t *pl, *pr, *res;
+  int32_t *el, *er;
+  void *scr_l, *scr_r;
+  void place(Carver& cv, int r) {
+    L = product_layout(P, r);
+    pl = static_cast<int8_t*>(cv.take(L.planes_l));
+    pr = static_cast<int8_t*>(cv.take(L.planes_r));
+    res = static_cast<int8_t*>(cv.take(L.residues));
+    el = static_cast<int32_t*>(cv.take(L.exps_l));
+    er = static_cast<int32_t*>(cv.take(L.exps_r));
+    scr_l = cv.take(L.scr_l);
+    scr_r = cv.take(L.scr_r);
   }
-  if (st != OZK_OK) return st;
-  if ((st = launch_gemm_i8(P.rows, L.np, L.kp, r, pl, sl, pr, sr, res, L.np, P.rows * L.np,
-                           kEpiResidues, s)))
-    return st;
-  return launch_crt_epilogue(P.rows, P.cols, r, res, L.np, P.rows * L.np, el, er, E, out, ldo, s);
+  int reconstruct(int r, hipStream_t s) const {
+    return launch_crt_epilogue(P.rows, P.cols, r, res, L.np, P.rows * L.np, el, er, E, out, ldo,
+                               s);
+  }
+};
+
+// One or two products in emulated fp64, each with its epilogue.  Small ones run together, each
+// in a workspace of its own (in `workspace` one after the other); others one after the other,
+// over the same workspace.
+int run_jobs(Job* jobs, int count, int r, int scaling, void* workspace, hipStream_t s) {
+  int st, wl = 0, wr = 0;
+  bool together = true;
+  for (int i = 0; i < count; ++i) together = together && small(jobs[i].P);
+  if (together) {
+    SmallOperand op[kSmallOperands];
+    PlaneProduct prod[2];
+    int64_t kp[kSmallOperands];
+    Carver cv(workspace);
+    for (int i = 0; i < count; ++i) {
+      Job& J = jobs[i];
+      const Product& P = J.P;
+      if ((st = scaling_widths(scaling, r, P.K, &wl, &wr))) return st;
+      J.place(cv, r);
+      op[2 * i] = {P.left, P.rows, P.K, P.ldl, P.left_axis, wl, 0, J.pl, J.el};
+      op[2 * i + 1] = {P.right, P.cols, P.K, P.ldr, P.right_axis, wr, 0, J.pr, J.er};
+      kp[2 * i] = kp[2 * i + 1] = J.L.kp;
+      prod[i] = {P.rows, P.cols, J.L.np, J.L.kp, J.pl, J.pr, J.res};
+    }
+    if ((st = launch_small_deconstruct(op, 2 * count, r, scaling, kp, s))) return st;
+    if ((st = launch_products(prod, count, r, s))) return st;
+    for (int i = 0; i < count; ++i)
+      if ((st = jobs[i].reconstruct(r, s))) return st;
+    return OZK_OK;
+  }
+  for (int i = 0; i < count; ++i) {
+    Job& J = jobs[i];
+    const Product& P = J.P;
+    if ((st = scaling_widths(scaling, r, P.K, &wl, &wr))) return st;
+    Carver cv(workspace);
+    J.place(cv, r);
+    const int64_t sl = P.rows * J.L.kp, sr = P.cols * J.L.kp;   // plane strides
+    if (P.left_axis == 0 && P.right_axis == 1) {
+      st = deconstruct_operands(P.left, P.rows, P.K, P.ldl, P.right, P.cols, P.ldr, r, scaling,
+                                wl, wr, J.pl, J.pr, J.L.kp, J.el, J.er, J.scr_l, J.scr_r, s);
+    } else {
+      st = deconstruct_impl(P.left, P.left_rows, P.left_cols, P.ldl, P.left_axis, r, scaling, wl,
+                            J.pl, J.L.kp, sl, J.el, J.scr_l, s);
+      if (st == OZK_OK)
+        st = deconstruct_impl(P.right, P.right_rows, P.right_cols, P.ldr, P.right_axis, r,
+                              scaling, wr, J.pr, J.L.kp, sr, J.er, J.scr_r, s);
+    }
+    if (st != OZK_OK) return st;
+    const PlaneProduct prod{P.rows, P.cols, J.L.np, J.L.kp, J.pl, J.pr, J.res};
+    if ((st = launch_products(&prod, 1, r, s))) return st;
+    if ((st = J.reconstruct(r, s))) return st;
+  }
+  return OZK_OK;
 }
 
 // C = A B: rows of A against columns of B.
@@ -788,8 +839,8 @@ Product grad_b(int64_t m, int64_t n, int64_t k, const double* A, int64_t lda,
   return {k, n, m, A, m, k, lda, 1, g, m, n, ldg, 1};
 }
 
-// Workspace of the gradient: G, the chunks' sums of its columns, and the larger of the two
-// products' scratch.
+// Workspace of the gradient: G, the chunks' sums of its columns, and the two products' (side
+// by side where they run together, else the larger one).
 struct EpilogueGradLayout {
   size_t g, part, products;
   size_t total() const { return align256(g) + align256(part) + align256(products); }
@@ -799,9 +850,10 @@ EpilogueGradLayout epilogue_grad_layout(int64_t m, int64_t n, int64_t k, int r) 
   EpilogueGradLayout L;
   L.g = (size_t)m * n * 8;
   L.part = (size_t)act_grad_chunks(m > 0 ? m : 1) * n * 8;
-  const size_t a = product_layout(grad_a(m, n, k, nullptr, n, nullptr, n), r).total();
-  const size_t b = product_layout(grad_b(m, n, k, nullptr, k, nullptr, n), r).total();
-  L.products = a > b ? a : b;
+  const Product pa = grad_a(m, n, k, nullptr, n, nullptr, n);
+  const Product pb = grad_b(m, n, k, nullptr, k, nullptr, n);
+  const size_t a = product_layout(pa, r).total(), b = product_layout(pb, r).total();
+  L.products = small(pa) && small(pb) ? a + b : (a > b ? a : b);
   return L;
 }
 
@@ -837,8 +889,8 @@ int ozk_dgemm_epilogue(int64_t m, int64_t n, int64_t k, const double* A, int64_t
   if (!workspace || workspace_bytes < product_layout(P, r).total()) return OZK_EWORKSPACE;
   if (!aligned(workspace, 256)) return OZK_EINVAL;
   if ((size_t)m * n > (size_t)0x7fffffffffffull) return OZK_EUNSUPPORTED;
-  return run_product(P, r, scaling, {bias, residual, ldr, Z, ldz, act}, C, ldc, workspace,
-                     as_stream(stream));
+  Job job{P, {bias, residual, ldr, Z, ldz, act}, C, ldc};
+  return run_jobs(&job, 1, r, scaling, workspace, as_stream(stream));
 }
 
 int ozk_dgemm_epilogue_grad_workspace_size(int64_t m, int64_t n, int64_t k, int r,
@@ -889,13 +941,11 @@ int ozk_dgemm_epilogue_grad(int64_t m, int64_t n, int64_t k, const double* dC, i
   const double* gp = own_g ? g : dC;
   const int64_t ldg = own_g ? n : lddc;
   const DgemmEpilogue none{nullptr, nullptr, 0, nullptr, 0, OZK_ACT_NONE};
-  if (dA && (st = run_product(grad_a(m, n, k, gp, ldg, B, ldb), r, scaling, none, dA, ldda,
-                              products, s)))
-    return st;
-  if (dB && (st = run_product(grad_b(m, n, k, A, lda, gp, ldg), r, scaling, none, dB, lddb,
-                              products, s)))
-    return st;
-  return OZK_OK;
+  Job jobs[2];
+  int count = 0;
+  if (dA) jobs[count++] = Job{grad_a(m, n, k, gp, ldg, B, ldb), none, dA, ldda};
+  if (dB) jobs[count++] = Job{grad_b(m, n, k, A, lda, gp, ldg), none, dB, lddb};
+  return count ? run_jobs(jobs, count, r, scaling, products, s) : OZK_OK;
 }
 
 // ---------------------------------------------------------------- int8 linear layer

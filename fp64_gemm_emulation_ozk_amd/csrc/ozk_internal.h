@@ -187,6 +187,32 @@ int launch_act_grad(int64_t m, int64_t n, const double* dc, int64_t lddc, const 
                     int64_t ldz, int act, double* g, double* part, double* dbias,
                     hipStream_t s);
 
+// Small products (small_products.hip).  An operand: lines along `axis` (as the
+// deconstruction's), kdim values each, planes of leading dimension kp (a multiple of 128) and
+// stride lines * kp, exponents of either rule with this width.
+constexpr int kSmallOperands = 4;
+struct SmallOperand {
+  const double* x;
+  int64_t lines, kdim, ld;
+  int axis, width;
+  int wide;            // set by the launch
+  int8_t* planes;
+  int32_t* exps;
+};
+// Residues [r][m][np] of left [r][m][kp] times right [r][n][kp], np a multiple of 64.  Columns
+// n .. np - 1 are written with anything; right ends in np - n more lines that may be read.
+// launch_products takes any size, and the kernel of the least estimated time.
+struct PlaneProduct {
+  int64_t m, n, np, kp;
+  const int8_t* left;
+  const int8_t* right;
+  int8_t* res;
+};
+bool small_lines(int64_t lines, int64_t kdim);   // whether an operand is small
+int launch_small_deconstruct(const SmallOperand* op, int count, int r, int scaling,
+                             const int64_t* kp, hipStream_t s);
+int launch_products(const PlaneProduct* P, int count, int r, hipStream_t s);
+
 // p[i * ld + j] = 0 for i < rows, j < cols.
 int launch_zero_rows(double* p, int64_t rows, int64_t cols, int64_t ld, hipStream_t s);
 
