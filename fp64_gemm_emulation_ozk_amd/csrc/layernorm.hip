@@ -859,13 +859,14 @@ int layernorm_backward_t(int64_t rows, int64_t cols, const void* dy, int64_t ldd
   if (rows == 0) {
     part = nullptr;
   } else if (!in_registers) {
-    if (dx)
-      hipLaunchKernelGGL((layernorm_backward_long_kernel<T>), dim3((unsigned)rows), dim3(1024),
-                         0, s, cols, dyt, lddy, xt, ldx, gt, mt, rt, (T*)dx, lddx);
+    // the column sums first: dx may take the place of dy or x
     if (part)
       hipLaunchKernelGGL((layernorm_backward_cols_kernel<T>),
                          dim3((unsigned)((vecs + 255) / 256), (unsigned)groups), dim3(256), 0, s,
                          rows, cols, dyt, lddy, xt, ldx, mt, rt, part);
+    if (dx)
+      hipLaunchKernelGGL((layernorm_backward_long_kernel<T>), dim3((unsigned)rows), dim3(1024),
+                         0, s, cols, dyt, lddy, xt, ldx, gt, mt, rt, (T*)dx, lddx);
   } else {
 #define OZK_LNB(NT, NV)                                                                       \
   hipLaunchKernelGGL((layernorm_backward_kernel<T, NT, NV>), dim3((unsigned)groups),          \

@@ -227,7 +227,7 @@ double rounds_time(const PlaneProduct* P, int count, int r, int64_t bm, int64_t 
 }  // namespace
 
 bool small_lines(int64_t lines, int64_t kdim) {
-  return kdim <= kLineMax && lines * kdim <= (int64_t)1 << 21;
+  return kdim <= kLineMax && lines * kdim <= (int64_t)3 << 20;
 }
 
 int launch_small_deconstruct(const SmallOperand* op, int count, int r, int scaling,

@@ -206,6 +206,24 @@ def test_layernorm_backward_parts():
     assert dx0.shape == (0, 200) and not dg0.any() and not db0.any()
 
 
+@pytest.mark.parametrize("kind,cols", [("float32", 700), ("bfloat16", 16400), ("float32", 40000)])
+def test_layernorm_in_place(kind, cols):
+    """The output over an input, also where a row does not fit registers (the gradient's column
+    sums then read dy and x in a launch of their own)."""
+    announce(f"layernorm in place {kind} cols={cols}")
+    dtype = TYPES[kind]
+    x, gamma, beta, dy = [t.to(device()) for t in row_input(21, cols, dtype, cols + 9)]
+    y, mean, rstd = ozk.ozk_layernorm(x, gamma, beta, stats=True)
+    over = x.clone()
+    assert torch.equal(ozk.ozk_layernorm(over, gamma, beta, out=over), y)
+    want = ozk.ozk_layernorm_backward(dy, x, gamma, mean, rstd)
+    for which in (0, 1):
+        a, b = dy.clone(), x.clone()
+        got = ozk.ozk_layernorm_backward(a, b, gamma, mean, rstd, dx=(a, b)[which])
+        for g, w in zip(got, want):
+            assert torch.equal(g, w)
+
+
 def test_layernorm_edges():
     """A large common offset (two passes: no cancellation), a constant row, rows with NaN and
     Inf beside sound ones, in place, no rows."""
@@ -481,6 +499,45 @@ def test_dgemm_epilogue_equals_dgemm():
     assert inplace is res
     assert torch.equal(apart.view(torch.int64), res.view(torch.int64))
     assert ozk.ozk_dgemm_epilogue(da[:0], db, 14).shape == (0, 200)
+
+
+# inner and outer sizes on both sides of what the kernels for small products take, one and
+# several tiles of each shape, padded and whole rows of residues
+@pytest.mark.parametrize("m,n,k,r", [(130, 65, 2047, 16), (65, 130, 2049, 16), (40, 70, 5000, 14),
+                                     (1500, 2050, 1001, 16), (700, 640, 2500, 15),
+                                     (2048, 1537, 256, 14), (300, 5000, 130, 20), (1, 300, 700, 14),
+                                     (64, 100, 8192, 16)])
+@pytest.mark.parametrize("scaling", ["max", "norm"])
+def test_dgemm_epilogue_bits_of_dgemm(m, n, k, r, scaling):
+    """The product inside the epilogue and both products of its gradient have the bits of
+    ozk_dgemm_ex on the same operands."""
+    announce(f"dgemm epilogue bits m={m} n={n} k={k} r={r} {scaling}")
+    a, b = [to_dev(v) for v in ozk_inputs.gemm_operands(m, n, k, seed=m + n + k, dist="phi",
+                                                        phi=0.5)]
+    rng = np.random.default_rng(n)
+    dc, res = to_dev(rng.standard_normal((m, n))), to_dev(rng.standard_normal((m, n)))
+    got = ozk.ozk_dgemm_epilogue(a, b, r, residual=res, scaling=scaling)
+    assert torch.equal(got, ozk.ozk_dgemm_ex(a, b, r, scaling) + res)
+    da, db, dbias = ozk.ozk_dgemm_epilogue_grad(dc, a, b, r, scaling=scaling)
+    assert torch.equal(da, ozk.ozk_dgemm_ex(dc, to_dev(host(b).T.copy()), r, scaling))
+    assert torch.equal(db, ozk.ozk_dgemm_ex(to_dev(host(a).T.copy()), dc, r, scaling))
+    assert_near(host(dbias), host(dc).sum(0),
+                (m // 16 + 80) * U64 * np.abs(host(dc)).sum(0) + 1e-300, "dbias")
+
+
+def test_dgemm_epilogue_grad_nonfinite():
+    """A line with Inf or NaN spoils the outputs it touches, in the small kernels too."""
+    announce("dgemm epilogue grad nonfinite")
+    rng = np.random.default_rng(5)
+    a, b = rng.standard_normal((70, 40)), rng.standard_normal((40, 90))
+    dc = rng.standard_normal((70, 90))
+    dc[3, 5] = np.inf
+    a[9, 2] = np.nan
+    da, db, dbias = ozk.ozk_dgemm_epilogue_grad(to_dev(dc), to_dev(a), to_dev(b), 16)
+    na, nb = torch.isnan(da), torch.isnan(db)
+    assert na[3].all() and int(na.sum()) == 40
+    assert nb[:, 5].all() and nb[2].all() and int(nb.sum()) == 40 + 90 - 1
+    assert torch.isinf(dbias[5]) and int(torch.isinf(dbias).sum()) == 1
 
 
 def test_dgemm_epilogue_large_arguments():
