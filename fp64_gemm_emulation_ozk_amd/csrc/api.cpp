@@ -805,7 +805,12 @@ int run_jobs(Job* jobs, int count, int r, int scaling, void* workspace, hipStrea
     Carver cv(workspace);
     J.place(cv, r);
     const int64_t sl = P.rows * J.L.kp, sr = P.cols * J.L.kp;   // plane strides
-    if (P.left_axis == 0 && P.right_axis == 1) {
+    if (small(P)) {
+      const SmallOperand op[2] = {{P.left, P.rows, P.K, P.ldl, P.left_axis, wl, 0, J.pl, J.el},
+                                  {P.right, P.cols, P.K, P.ldr, P.right_axis, wr, 0, J.pr, J.er}};
+      const int64_t kp[2] = {J.L.kp, J.L.kp};
+      st = launch_small_deconstruct(op, 2, r, scaling, kp, s);
+    } else if (P.left_axis == 0 && P.right_axis == 1) {
       st = deconstruct_operands(P.left, P.rows, P.K, P.ldl, P.right, P.cols, P.ldr, r, scaling,
                                 wl, wr, J.pl, J.pr, J.L.kp, J.el, J.er, J.scr_l, J.scr_r, s);
     } else {

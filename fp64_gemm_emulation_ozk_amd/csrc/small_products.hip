@@ -14,8 +14,9 @@ namespace {
 
 // ---------------------------------------------------------------- exponents
 // Workgroup: 16 lines, 64 threads each, a line's values (at most 2048) in registers, 32 per
-// thread.  Columns: thread = column j = t % 16, rows t / 16, + 64, ...; rows: four waves take
-// four rows each in turn... the row's 64 lanes hold values lane, lane + 64, ...
+// thread, asked for eight at a time as far as the line goes (from a clamped place past its end:
+// a load under its own guard waits its turn).  Thread t of an operand of columns takes column t % 16 and rows t / 16,
+// + 64, ...; a wave takes a row, values lane, lane + 64, ...
 constexpr int kLineMax = 2048, kHeld = kLineMax / 64;
 
 struct ExpsArgs {
@@ -45,9 +46,19 @@ __global__ __launch_bounds__(1024) void small_exps_kernel(ExpsArgs A) {
   double a[kHeld];
   uint64_t m = 0;
 #pragma unroll
+  for (int u = 0; u < kHeld; ++u) a[u] = 0.0;
+#pragma unroll
+  for (int g = 0; g < kHeld; g += 8)
+    if (64 * g < P.kdim) {   // uniform
+#pragma unroll
+      for (int u = g; u < g + 8; ++u) {
+        const int64_t h = slice + 64 * u;
+        a[u] = x[(h < P.kdim ? h : P.kdim - 1) * sk];
+      }
+    }
+#pragma unroll
   for (int u = 0; u < kHeld; ++u) {
-    const int64_t h = slice + 64 * u;
-    a[u] = h < P.kdim ? x[h * sk] : 0.0;
+    if (slice + 64 * u >= P.kdim) a[u] = 0.0;
     m = max64(m, abs_bits(a[u]));
   }
   tops[slice][j] = m;
@@ -139,8 +150,10 @@ __global__ __launch_bounds__(256) void small_residues_kernel(ResidueArgs A) {
   const double* x = P.x + line * (P.axis ? 1 : P.ld);
   double a[8];
 #pragma unroll
+  for (int u = 0; u < 8; ++u) a[u] = x[(h0 + u < P.kdim ? h0 + u : P.kdim - 1) * sk];
+#pragma unroll
   for (int u = 0; u < 8; ++u)
-    a[u] = h0 + u < P.kdim && e != INT32_MIN ? x[(h0 + u) * sk] : 0.0;
+    if (h0 + u >= P.kdim || e == INT32_MIN) a[u] = 0.0;
   const int l0 = A.K.r * group / A.groups, l1 = A.K.r * (group + 1) / A.groups;
   int8_t* dst = P.planes + line * A.kp[o] + h0;
   const int64_t stride = P.lines * A.kp[o];
