@@ -41,7 +41,8 @@ __device__ __forceinline__ float logistic_times(float z, float v) {
 }
 
 // The same in fp32 for the int8 layer, whose epilogue is bound by these instructions (16 of
-// them for gelu; the library's erfcf and expf took 2.5 times as long at 4096 x 16384).
+// them for gelu; 4096 x 16384 x 4096 with gelu and residual took 403 us with the library's
+// erfcf and expf, 367 with these, the rest of the kernel the same).
 // gelu: with x = |z| / sqrt 2 and t = 1 / (1 + 0.3275911 x),
 //   erfc(x) = (a1 t + a2 t^2 + a3 t^3 + a4 t^4 + a5 t^5) exp(-x^2) + e, |e| <= 1.5e-7
 // (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26), so the result is off

@@ -715,7 +715,7 @@ struct Product {
 
 // Workspace of a product.  The rows of residues are padded to 64 so that every store of the
 // modular products and every load of the reconstruction is a whole vector (1500 x 2050 x
-// 1001: 133.6 -> RES us a product); the padding's columns are products with whatever lines
+// 1001: 133.6 -> 68 us a product); the padding's columns are products with whatever lines
 // follow the right planes, which therefore end in as many lines more.
 struct ProductLayout {
   int64_t kp, np;

@@ -6,8 +6,9 @@
 //             dgamma = sum over rows of dy xh, dbeta = sum over rows of dy
 //   codes     s = fp32(max |y| / 127), q = rint(y / s) for y = x or the forward's y
 //
-// All of it is bound by HBM: a row is read once into registers (the mean, then the
-// centred sum of squares, are taken from there), one 16-byte load per thread and step.
+// Many rows are bound by HBM: a row is read once into registers (the mean, then the centred
+// sum of squares, are taken from there), in 16-byte loads.  Few rows are bound by a launch and
+// one chain of latencies (load, two reductions, store): 8 x 1024 fp32 takes 4.0 us.
 // Sums and statistics are fp32 for the types of at most 32 bits and fp64 for fp64; the
 // codes' statistics are fp64 for every type (fp64 arithmetic runs at the fp32 rate here), so
 // that a code depends on the order of the sums only within 1e-13 of a rounding border.
@@ -26,7 +27,8 @@ __device__ __forceinline__ int valid(int64_t c, int64_t cols) {
 
 // ------------------------------------------------------------------ forward
 // kT threads of a row hold it in kV vectors each (vector v of thread t starts at column
-// (v kT + t) N).  kT = 64: four rows per workgroup; else one.
+// (v kT + t) N).  kT = 64: four rows per workgroup; else one.  16384 x 4096 bf16: 52 us, 268 MB
+// at 5.1 TB/s, 0.94 of a large copy's rate.
 template <typename T, int kT, int kV>
 __global__ __launch_bounds__(kT < 256 ? 256 : kT) void layernorm_kernel(
     int64_t rows, int64_t cols, const T* x, int64_t ldx,
@@ -256,7 +258,9 @@ __device__ __forceinline__ void int8quant_row_f64(
 // bound leaves the largest magnitude or a code's rounding open (about one value in five
 // thousand), the value is formed in fp64.  A row whose magnitudes are out of the bound's
 // reach (below 1e-30, above 1e37, not finite) takes fp64 throughout.
-// All in fp64, 4096 x 8192 bf16 with the norm took 69.5 us, 4096 x 16384 without 61.1.
+// All in fp64, 4096 x 8192 bf16 with the norm took 69.5 us, 4096 x 16384 without 61.1; so they
+// take 38 and 40, the latter 201 MB at 5.05 TB/s (a large copy: 5.5).  With the norm the fp64
+// sums bind as much as the bytes (4096 x 8192 fp32: 57 us, 2.9 TB/s).
 template <typename T, int kT, int kV, bool kNorm>
 __device__ __forceinline__ void int8quant_row(
     int64_t row, int64_t cols, const T* __restrict__ x, int64_t ldx,
@@ -512,7 +516,9 @@ __global__ __launch_bounds__(1024) void int8quant_long_kernel(
 // Workgroup b of G walks rows b, b + G, ... (four rows at once, one a wave, where a wave
 // holds a row): dx row by row, and the column sums dy xh and dy of its rows in registers,
 // written to partials [G][2][cols] at the end.  A row is asked for one row ahead, before the
-// reduction of the row in hand.
+// reduction of the row in hand.  16384 x 4096 bf16: 78 us and 7 for the join of the sums, 403
+// MB at 4.75 TB/s together (the partials are another 34 MB of traffic); 1000 x 1537 fp32: 10
+// and 5 us, where two rows a workgroup and the second launch are the time.
 template <typename T, int kT, int kV>
 __global__ __launch_bounds__(kT < 256 ? 256 : kT) void layernorm_backward_kernel(
     int64_t rows, int64_t cols, const T* dy, int64_t lddy, const T* x, int64_t ldx,
@@ -783,6 +789,8 @@ __global__ __launch_bounds__(256) void layernorm_join_kernel(
   else if (vecs <= 2048) GO(1024, 2); \
   else GO(1024, 4)
 constexpr int64_t kRowVecs = 4096;   // vectors a workgroup holds
+// Rows of a launch: one takes fewer than 2^32 threads, a row up to 1024 of them.
+constexpr int64_t kRowsOnce = 1 << 21;
 
 template <typename T>
 int layernorm_t(int64_t rows, int64_t cols, const void* x, int64_t ldx, const void* gamma,
@@ -791,6 +799,13 @@ int layernorm_t(int64_t rows, int64_t cols, const void* x, int64_t ldx, const vo
   typedef typename AccOf<T>::type A;
   const int64_t vecs = (cols + Vec<T>::N - 1) / Vec<T>::N;
   const T *xt = (const T*)x, *gt = (const T*)gamma, *bt = (const T*)beta;
+  if (rows > kRowsOnce) {
+    const int st = layernorm_t<T>(kRowsOnce, cols, x, ldx, gamma, beta, eps, y, ldy, mean, rstd, s);
+    if (st != OZK_OK) return st;
+    return layernorm_t<T>(rows - kRowsOnce, cols, xt + kRowsOnce * ldx, ldx, gamma, beta, eps,
+                          (T*)y + kRowsOnce * ldy, ldy, mean ? (A*)mean + kRowsOnce : nullptr,
+                          rstd ? (A*)rstd + kRowsOnce : nullptr, s);
+  }
   if (vecs > kRowVecs) {
     hipLaunchKernelGGL((layernorm_long_kernel<T>), dim3((unsigned)rows), dim3(1024), 0, s, cols,
                        xt, ldx, gt, bt, (A)eps, (T*)y, ldy, (A*)mean, (A*)rstd);
@@ -817,6 +832,13 @@ int int8quant_t(int64_t rows, int64_t cols, const void* x, int64_t ldx, const vo
   constexpr int N = Vec<T>::N;
   const T *xt = (const T*)x, *gt = (const T*)gamma, *bt = (const T*)beta;
   const bool wide = rows < 256;
+  if (rows > kRowsOnce) {
+    const int st = int8quant_t<T, kNorm>(kRowsOnce, cols, x, ldx, gamma, beta, eps, q, ldq, scale,
+                                         s);
+    if (st != OZK_OK) return st;
+    return int8quant_t<T, kNorm>(rows - kRowsOnce, cols, xt + kRowsOnce * ldx, ldx, gamma, beta,
+                                 eps, q + kRowsOnce * ldq, ldq, scale + kRowsOnce, s);
+  }
 #define OZK_Q(NT, VALUES)                                                                      \
   hipLaunchKernelGGL((int8quant_kernel<T, NT, VALUES / N, kNorm>),                             \
                      dim3((unsigned)(NT < 256 ? (rows + 3) / 4 : rows)),                       \
@@ -864,9 +886,11 @@ int layernorm_backward_t(int64_t rows, int64_t cols, const void* dy, int64_t ldd
       hipLaunchKernelGGL((layernorm_backward_cols_kernel<T>),
                          dim3((unsigned)((vecs + 255) / 256), (unsigned)groups), dim3(256), 0, s,
                          rows, cols, dyt, lddy, xt, ldx, mt, rt, part);
-    if (dx)
-      hipLaunchKernelGGL((layernorm_backward_long_kernel<T>), dim3((unsigned)rows), dim3(1024),
-                         0, s, cols, dyt, lddy, xt, ldx, gt, mt, rt, (T*)dx, lddx);
+    for (int64_t r0 = 0; dx && r0 < rows; r0 += kRowsOnce)
+      hipLaunchKernelGGL((layernorm_backward_long_kernel<T>),
+                         dim3((unsigned)(rows - r0 < kRowsOnce ? rows - r0 : kRowsOnce)),
+                         dim3(1024), 0, s, cols, dyt + r0 * lddy, lddy, xt + r0 * ldx, ldx, gt,
+                         mt + r0, rt + r0, (T*)dx + r0 * lddx, lddx);
   } else {
 #define OZK_LNB(NT, NV)                                                                       \
   hipLaunchKernelGGL((layernorm_backward_kernel<T, NT, NV>), dim3((unsigned)groups),          \

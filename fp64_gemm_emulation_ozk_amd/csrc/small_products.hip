@@ -5,6 +5,9 @@
 // tile per modulus leaves most of the chip empty.  Here a line's values are read once into the
 // registers of many threads for its exponent, the moduli are spread over workgroups, and the
 // tiles are 64 x 128 or 128 x 128.  The arithmetic per value is the same (residue_math.h).
+// A product of 64^3, r = 14, takes 17.8 us so (exponents 5, residues, products and
+// reconstruction 4 each: four launches, one after the other's results), 29 by the kernels of
+// the large path.
 #include "ozk_internal.h"
 #include "residue_math.h"
 #include "tile_walk.h"
@@ -15,8 +18,9 @@ namespace {
 // ---------------------------------------------------------------- exponents
 // Workgroup: 16 lines, 64 threads each, a line's values (at most 2048) in registers, 32 per
 // thread, asked for eight at a time as far as the line goes (from a clamped place past its end:
-// a load under its own guard waits its turn).  Thread t of an operand of columns takes column t % 16 and rows t / 16,
-// + 64, ...; a wave takes a row, values lane, lane + 64, ...
+// a load under its own guard waits its turn).  Thread t of an operand of columns takes column
+// t % 16 and rows t / 16, + 64, ...; of an operand of rows a wave takes a row, values lane,
+// lane + 64, ...
 constexpr int kLineMax = 2048, kHeld = kLineMax / 64;
 
 struct ExpsArgs {

@@ -109,6 +109,18 @@ def test_int8linear_refusals(lib):
     assert size(4, 4, 131072, 0, ctypes.byref(out)) == ERANGE
 
 
+def test_int8linear_refuses_what_a_launch_cannot_take(lib):
+    """2^32 threads and more, found before any HIP call."""
+    names = "m n k X ldx sx W ldw sw bias act R ldr type C ldc ws wsb stream".split()
+    call = _caller(lib.ozk_int8linear, names, dict(
+        m=4, n=4, k=16, X=FAKE, ldx=16, sx=FAKE, W=FAKE, ldw=16, sw=FAKE, bias=None, act=0, R=None,
+        ldr=0, type=3, C=FAKE, ldc=1 << 31, ws=FAKE, wsb=1 << 62, stream=None))
+    assert call(n=(1 << 27) + 1) == EUNSUPPORTED
+    assert call(k=17, ldx=17, ldw=17, n=(1 << 27) + 1) == EUNSUPPORTED
+    assert call(m=1 << 20, n=1 << 20) == EUNSUPPORTED
+    assert call(m=65, n=1 << 20, k=131071, ldx=131071, ldw=131071) == EUNSUPPORTED
+
+
 @pytest.mark.parametrize("kind", [0, 1, 2, 3])
 def test_row_operator_refusals(lib, kind):
     names = "rows cols type x ldx norm g b eps q ldq scale stream".split()

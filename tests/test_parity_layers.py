@@ -224,6 +224,22 @@ def test_layernorm_in_place(kind, cols):
             assert torch.equal(g, w)
 
 
+def test_rows_of_several_launches():
+    """More rows than one launch takes: the same bits as those rows alone."""
+    announce("rows of several launches")
+    block, gamma, beta, _ = row_input(1027, 8, torch.float16, 11)
+    rows = (1 << 21) + 1030
+    x = block.to(device()).repeat(rows // 1027 + 1, 1)[:rows].contiguous()
+    gm, bt = gamma.to(device()), beta.to(device())
+    y, mean, rstd = ozk.ozk_layernorm(x, gm, bt, stats=True)
+    q, scale = ozk.ozk_int8quant_rows(x, norm=True, gamma=gm, beta=bt)
+    alone = ozk.ozk_layernorm(x[:1027], gm, bt, stats=True)
+    codes = ozk.ozk_int8quant_rows(x[:1027], norm=True, gamma=gm, beta=bt)
+    for got, want in zip((y, mean, rstd, q, scale), alone + codes):
+        want = want.repeat((rows // 1027 + 1,) + (1,) * (want.dim() - 1))[:rows]
+        assert torch.equal(got, want)
+
+
 def test_layernorm_edges():
     """A large common offset (two passes: no cancellation), a constant row, rows with NaN and
     Inf beside sound ones, in place, no rows."""
