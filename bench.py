@@ -117,7 +117,7 @@ COUNTER_KERNELS = {
     "exps_norm": ("exps_norm_kernel", ["deconstruct.hip"]),
     "residues_rows_fused": ("residues_rows_fused_kernel", ["deconstruct.hip"]),
     "residues_cols": ("residues_cols_kernel", ["deconstruct.hip"]),
-    "crt": ("crt_kernel<16", ["crt.hip"]),
+    "crt": ("crt_kernel<16", ["crt.hip", "crt_core.h"]),
 }
 
 

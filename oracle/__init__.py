@@ -29,5 +29,6 @@ Modules:
     fp4awe     weights (1, 29, 37), limb and pairwise-sum planes, 6-product limb GEMM
     fp4awe4    INT4 x INT8 in 4 FP4 products (limb weight 5, planes at four points)
     spmv       emulated CSR sparse matrix-vector product
+    layers     plain 64-bit forms of the layer operators
 """
 from . import rns, ozaki2, reference, fp4limb, fp4awe, spmv  # noqa: F401
