@@ -108,7 +108,7 @@ __global__ __launch_bounds__(1024) void small_exps_kernel(ExpsArgs A) {
 struct ResidueArgs {
   SmallOperand op[kSmallOperands];
   ResidueConsts K;
-  int count, groups;
+  int count, groups, norm;
   int64_t kp[kSmallOperands];
 };
 
@@ -163,6 +163,89 @@ __global__ __launch_bounds__(256) void small_residues_kernel(ResidueArgs A) {
   const int64_t stride = P.lines * A.kp[o];
   if (P.wide) put_residues<true>(a, e == INT32_MIN ? 0 : e, A.K, l0, l1, dst, stride);
   else put_residues<false>(a, e == INT32_MIN ? 0 : e, A.K, l0, l1, dst, stride);
+}
+
+// Lines of at most 128 kSteps values: exponents and residues in one launch.  Workgroup: 16 lines
+// x one group of moduli, the lines' values in the registers that convert them (8 consecutive K
+// values a thread and step of 128).
+template <int kSteps>
+__global__ __launch_bounds__(256) void small_lines_kernel(ResidueArgs A) {
+  __shared__ uint64_t tops[16][17];
+  __shared__ double sums[16][17];
+  int64_t block = blockIdx.x / A.groups;
+  const int group = blockIdx.x % A.groups;
+  int o = 0;
+  for (; o + 1 < A.count; ++o) {
+    const int64_t blocks = (A.op[o].lines + 15) / 16;
+    if (block < blocks) break;
+    block -= blocks;
+  }
+  const SmallOperand& P = A.op[o];
+  const int j = P.axis ? threadIdx.x & 15 : threadIdx.x >> 4;
+  const int kg = P.axis ? threadIdx.x >> 4 : threadIdx.x & 15;
+  const int64_t line = block * 16 + j, at = line < P.lines ? line : P.lines - 1;
+  const int64_t sk = P.axis ? P.ld : 1;
+  const double* x = P.x + at * (P.axis ? 1 : P.ld);
+  double a[kSteps][8];
+#pragma unroll
+  for (int v = 0; v < kSteps; ++v) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) a[v][u] = 0.0;
+    if (128 * v < P.kdim) {   // uniform
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int64_t h = 128 * v + 8 * kg + u;
+        a[v][u] = x[(h < P.kdim ? h : P.kdim - 1) * sk];
+      }
+    }
+  }
+  uint64_t m = 0;
+#pragma unroll
+  for (int v = 0; v < kSteps; ++v)
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (128 * v + 8 * kg + u >= P.kdim) a[v][u] = 0.0;
+      m = max64(m, abs_bits(a[v][u]));
+    }
+  tops[kg][j] = m;
+  __syncthreads();
+#pragma unroll
+  for (int p = 0; p < 16; ++p) m = max64(m, tops[p][j]);
+  int e;
+  if (A.norm) {   // as small_exps_kernel: the sum of (x 2^-T)^2 in a fixed order
+    const int t = line_ilogb(m);
+    double s = 0.0;
+#pragma unroll
+    for (int v = 0; v < kSteps; ++v)
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const double y = __builtin_ldexp(a[v][u], -t);
+        s = __builtin_fma(y, y, s);
+      }
+    sums[kg][j] = s;
+    __syncthreads();
+    s = sums[0][j];
+#pragma unroll
+    for (int p = 1; p < 16; ++p) s += sums[p][j];
+    e = norm_exponent(m, s, P.width);
+  } else {
+    e = line_exponent(m, P.width);
+  }
+  if (line >= P.lines) return;
+  if (group == 0 && kg == 0) P.exps[line] = e;
+  const int l0 = A.K.r * group / A.groups, l1 = A.K.r * (group + 1) / A.groups;
+  const int64_t stride = P.lines * A.kp[o];
+  const bool nothing = e == INT32_MIN;
+#pragma unroll
+  for (int v = 0; v < kSteps; ++v) {
+    if (128 * v >= A.kp[o]) break;
+    if (nothing)
+#pragma unroll
+      for (int u = 0; u < 8; ++u) a[v][u] = 0.0;
+    int8_t* dst = P.planes + line * A.kp[o] + 128 * v + 8 * kg;
+    if (P.wide) put_residues<true>(a[v], nothing ? 0 : e, A.K, l0, l1, dst, stride);
+    else put_residues<false>(a[v], nothing ? 0 : e, A.K, l0, l1, dst, stride);
+  }
 }
 
 // ---------------------------------------------------------------- modular products
@@ -252,8 +335,8 @@ int launch_small_deconstruct(const SmallOperand* op, int count, int r, int scali
   ExpsArgs E;
   ResidueArgs R;
   E.count = R.count = count;
-  E.norm = scaling == OZK_SCALING_NORM;
-  int64_t lines = 0, blocks = 0;
+  E.norm = R.norm = scaling == OZK_SCALING_NORM;
+  int64_t lines = 0, blocks = 0, longest = 0;
   for (int o = 0; o < count; ++o) {
     E.op[o] = R.op[o] = op[o];
     R.kp[o] = kp[o];
@@ -262,7 +345,18 @@ int launch_small_deconstruct(const SmallOperand* op, int count, int r, int scali
     R.K = *K;
     R.op[o].wide = K->wide;
     lines += (op[o].lines + 15) / 16;
+    longest = kp[o] > longest ? kp[o] : longest;
     blocks += (op[o].lines + 15) / 16 * (kp[o] / 128);
+  }
+  if (longest <= 512) {
+    // moduli in up to eight groups, until there are four workgroups a compute unit
+    R.groups = lines >= 1024 ? 1 : (lines >= 512 ? 2 : (lines >= 256 ? 4 : 8));
+    if (R.groups > r) R.groups = 1;
+    const dim3 grid((unsigned)(lines * R.groups));
+    if (longest <= 128) hipLaunchKernelGGL(small_lines_kernel<1>, grid, dim3(256), 0, s, R);
+    else if (longest <= 256) hipLaunchKernelGGL(small_lines_kernel<2>, grid, dim3(256), 0, s, R);
+    else hipLaunchKernelGGL(small_lines_kernel<4>, grid, dim3(256), 0, s, R);
+    return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
   }
   // moduli in up to four groups, until there are eight workgroups a compute unit
   R.groups = blocks >= 2048 ? 1 : (blocks >= 1024 ? 2 : 4);
