@@ -794,9 +794,13 @@ int run_jobs(Job* jobs, int count, int r, int scaling, void* workspace, hipStrea
     }
     if ((st = launch_small_deconstruct(op, 2 * count, r, scaling, kp, s))) return st;
     if ((st = launch_products(prod, count, r, s))) return st;
-    for (int i = 0; i < count; ++i)
-      if ((st = jobs[i].reconstruct(r, s))) return st;
-    return OZK_OK;
+    if (count == 1) return jobs[0].reconstruct(r, s);
+    // two are the gradient's, without an epilogue
+    const int32_t* const ea[2] = {jobs[0].el, jobs[1].el};
+    const int32_t* const eb[2] = {jobs[0].er, jobs[1].er};
+    double* const out[2] = {jobs[0].out, jobs[1].out};
+    const int64_t ldo[2] = {jobs[0].ldo, jobs[1].ldo};
+    return launch_crt_pair(prod, r, ea, eb, out, ldo, s);
   }
   for (int i = 0; i < count; ++i) {
     Job& J = jobs[i];

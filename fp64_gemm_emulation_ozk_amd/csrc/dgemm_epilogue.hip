@@ -53,6 +53,32 @@ __global__ __launch_bounds__(256) void crt_epilogue_kernel(
   crt_outputs<R, int8_t>(m, n, ldr, res, ldr, stride_r, ea, eb, Finish<kSet>{E, c, ldc});
 }
 
+// Two products without an epilogue in one launch: grid.y picks the one.
+struct Plain {
+  int64_t m, n, ldr, stride_r;
+  const int8_t* res;
+  const int32_t *ea, *eb;
+  double* c;
+  int64_t ldc;
+};
+
+struct PlainStore {
+  double* c;
+  int64_t ldc;
+  struct Nothing {};
+  __device__ __forceinline__ Nothing ask(int64_t, int64_t) const { return {}; }
+  __device__ __forceinline__ void operator()(int64_t i, int64_t j, double v, Nothing) const {
+    c[i * ldc + j] = v;
+  }
+};
+
+template <int R>
+__global__ __launch_bounds__(256) void crt_pair_kernel(Plain a, Plain b) {
+  const Plain p = blockIdx.y ? b : a;
+  crt_outputs<R, int8_t>(p.m, p.n, p.ldr, p.res, p.ldr, p.stride_r, p.ea, p.eb,
+                         PlainStore{p.c, p.ldc});
+}
+
 template <int R>
 void launch_r(dim3 grid, hipStream_t s, int64_t m, int64_t n, const int8_t* res, int64_t ldr,
               int64_t stride_r, const int32_t* ea, const int32_t* eb, const DgemmEpilogue& E,
@@ -65,6 +91,40 @@ void launch_r(dim3 grid, hipStream_t s, int64_t m, int64_t n, const int8_t* res,
   else if (set == kExp) OZK_SET(kExp);
   else OZK_SET(kSimple);
 #undef OZK_SET
+}
+
+// A short gradient's G and the whole column sums in one launch: 16 columns x 64 slices of rows per
+// workgroup, slice s taking rows s, s + 64, ..., the slices added in a fixed order.  (A gradient
+// of 167 x 247 x 512 took 39 us with chunks and their join, and two launches of the
+// reconstruction; so 28.)
+constexpr int64_t kShortRows = 1024;
+
+__global__ __launch_bounds__(1024) void act_grad_short_kernel(
+    int64_t m, int64_t n, const double* __restrict__ dc, int64_t lddc,
+    const double* __restrict__ z, int64_t ldz, int act, double* __restrict__ g,
+    double* __restrict__ dbias) {
+  __shared__ double sums[64][17];
+  const int cl = threadIdx.x & 15, slice = threadIdx.x >> 4;
+  const int64_t c = (int64_t)blockIdx.x * 16 + cl;
+  double sum = 0;
+  if (c < n) {
+#pragma unroll 4
+    for (int64_t i = slice; i < m; i += 64) {
+      double v = dc[i * lddc + c];
+      if (act != OZK_ACT_NONE) v *= activate_slope(z[i * ldz + c], act);
+      if (g) g[i * n + c] = v;
+      sum += v;
+    }
+  }
+  sums[slice][cl] = sum;
+  __syncthreads();
+  if (slice < 4) {   // 64 slices to four, to one
+    for (int p = 1; p < 16; ++p) sum += sums[slice + 4 * p][cl];
+    sums[slice][cl] = sum;
+  }
+  __syncthreads();
+  if (slice == 0 && c < n && dbias)
+    dbias[c] = (sums[0][cl] + sums[1][cl]) + (sums[2][cl] + sums[3][cl]);
 }
 
 // Column c of a chunk of rows per thread: G, and the chunk's sum of G.  1500 x 2050 with silu:
@@ -151,6 +211,30 @@ int launch_crt_epilogue(int64_t m, int64_t n, int r, const int8_t* res, int64_t 
   return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
 }
 
+int launch_crt_pair(const PlaneProduct* P, int r, const int32_t* const* ea,
+                    const int32_t* const* eb, double* const* c, const int64_t* ldc, hipStream_t s) {
+  Plain p[2];
+  int64_t blocks = 0;
+  for (int o = 0; o < 2; ++o) {
+    p[o] = {P[o].m, P[o].n, P[o].np, P[o].m * P[o].np, P[o].res, ea[o], eb[o], c[o], ldc[o]};
+    const int64_t own = crt_blocks(P[o].m, P[o].n);
+    blocks = own > blocks ? own : blocks;
+  }
+  const dim3 grid((unsigned)blocks, 2);
+  switch (r) {
+#define OZK_R(R)                                                                          \
+  case R:                                                                                 \
+    hipLaunchKernelGGL((crt_pair_kernel<R>), grid, dim3(256), 0, s, p[0], p[1]);          \
+    break
+    OZK_R(1); OZK_R(2); OZK_R(3); OZK_R(4); OZK_R(5); OZK_R(6); OZK_R(7); OZK_R(8); OZK_R(9);
+    OZK_R(10); OZK_R(11); OZK_R(12); OZK_R(13); OZK_R(14); OZK_R(15); OZK_R(16); OZK_R(17);
+    OZK_R(18); OZK_R(19); OZK_R(20);
+#undef OZK_R
+    default: return OZK_EINVAL;
+  }
+  return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
+}
+
 // Rows of a chunk: 16, or as many as leave at most 256 chunks.
 int64_t act_grad_chunks(int64_t m) {
   const int64_t rows = (m + 255) / 256 > 16 ? (m + 255) / 256 : 16;
@@ -160,6 +244,11 @@ int64_t act_grad_chunks(int64_t m) {
 int launch_act_grad(int64_t m, int64_t n, const double* dc, int64_t lddc, const double* z,
                     int64_t ldz, int act, double* g, double* part, double* dbias,
                     hipStream_t s) {
+  if (m <= kShortRows) {
+    hipLaunchKernelGGL(act_grad_short_kernel, dim3((unsigned)((n + 15) / 16)), dim3(1024), 0, s, m,
+                       n, dc, lddc, z, ldz, act, g, dbias);
+    return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
+  }
   const int64_t chunks = act_grad_chunks(m), chunk = (m + chunks - 1) / chunks;
   hipLaunchKernelGGL(act_grad_kernel, dim3((unsigned)((n + 255) / 256), (unsigned)chunks),
                      dim3(256), 0, s, m, n, chunk, dc, lddc, z, ldz, act, g,

@@ -212,6 +212,9 @@ bool small_lines(int64_t lines, int64_t kdim);   // whether an operand is small
 int launch_small_deconstruct(const SmallOperand* op, int count, int r, int scaling,
                              const int64_t* kp, hipStream_t s);
 int launch_products(const PlaneProduct* P, int count, int r, hipStream_t s);
+// The reconstruction of two of them, without an epilogue, in one launch (r <= 20).
+int launch_crt_pair(const PlaneProduct* P, int r, const int32_t* const* ea,
+                    const int32_t* const* eb, double* const* c, const int64_t* ldc, hipStream_t s);
 
 // p[i * ld + j] = 0 for i < rows, j < cols.
 int launch_zero_rows(double* p, int64_t rows, int64_t cols, int64_t ld, hipStream_t s);

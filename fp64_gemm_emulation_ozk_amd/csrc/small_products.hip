@@ -1,13 +1,12 @@
-// Small products in emulated fp64: the deconstruction of up to four operands in two launches and
-// the modular products of up to two in one.  At these sizes the kernels of the large path
-// (deconstruct.hip, gemm_i8.hip) are a chain of latencies: a thread there converts 8 or 16
-// values for every modulus one after the other, walks 128 rows of a column, and a 256 x 256
-// tile per modulus leaves most of the chip empty.  Here a line's values are read once into the
+// Small products in emulated fp64: the deconstruction of up to four operands in one launch (lines
+// of at most 512 values) or two and the modular products of up to two in one.  At these sizes
+// the kernels of the large path (deconstruct.hip, gemm_i8.hip) are a chain of latencies: a thread
+// there converts 8 or 16 values for every modulus one after the other, walks 128 rows of a
+// column, and a 256 x 256 tile per modulus leaves most of the chip empty.  Here a line's values are read once into the
 // registers of many threads for its exponent, the moduli are spread over workgroups, and the
 // tiles are 64 x 128 or 128 x 128.  The arithmetic per value is the same (residue_math.h).
-// A product of 64^3, r = 14, takes 17.8 us so (exponents 5, residues, products and
-// reconstruction 4 each: four launches, one after the other's results), 29 by the kernels of
-// the large path.
+// A product of 64^3, r = 14, takes 12 us so (three launches, one after the other's results),
+// 18 with exponents and residues in launches of their own, 29 by the kernels of the large path.
 #include "ozk_internal.h"
 #include "residue_math.h"
 #include "tile_walk.h"
@@ -348,6 +347,7 @@ int launch_small_deconstruct(const SmallOperand* op, int count, int r, int scali
     longest = kp[o] > longest ? kp[o] : longest;
     blocks += (op[o].lines + 15) / 16 * (kp[o] / 128);
   }
+  // (with eight steps a thread, 214 registers, 1024^3 took 76 us, by two launches 59)
   if (longest <= 512) {
     // moduli in up to eight groups, until there are four workgroups a compute unit
     R.groups = lines >= 1024 ? 1 : (lines >= 512 ? 2 : (lines >= 256 ? 4 : 8));

@@ -556,6 +556,51 @@ def test_dgemm_epilogue_grad_nonfinite():
     assert torch.isinf(dbias[5]) and int(torch.isinf(dbias).sum()) == 1
 
 
+@pytest.mark.parametrize("k", [1, 127, 128, 129, 255, 256, 257, 511, 512, 513])
+@pytest.mark.parametrize("scaling", ["max", "norm"])
+def test_dgemm_epilogue_line_lengths(k, scaling):
+    """Both sides of the steps that a thread holds of a line; lines of zeros, with an Inf, a NaN,
+    and far magnitudes.  The gradient's products run over n = k and m = k."""
+    announce(f"dgemm epilogue line lengths k={k} {scaling}")
+    rng = np.random.default_rng(k)
+    a, b = rng.standard_normal((37, k)), rng.standard_normal((k, 50))
+    a[3] = 0.0
+    b[:, 5] = 0.0
+    a[7] *= 1e250
+    b[:, 9] *= 1e-250
+    a[11, k - 1], b[k // 2, 13] = np.inf, np.nan
+    same = lambda x, y: np.testing.assert_array_equal(host(x), host(y))
+    ad, bd = padded(torch.from_numpy(a), 1, 1), padded(torch.from_numpy(b), 3)
+    same(ozk.ozk_dgemm_epilogue(ad, bd, 16, scaling=scaling),
+         ozk.ozk_dgemm_ex(ad, bd, 16, scaling=scaling))
+    # dA: dC (37 x k) times rows of B (50 x k); dB: columns of A (k x 37) against dC (k x 50)
+    da, _, _ = ozk.ozk_dgemm_epilogue_grad(ad, to_dev(rng.standard_normal((37, 50))),
+                                           to_dev(b.T), 16, scaling=scaling)
+    same(da, ozk.ozk_dgemm_ex(ad, bd, 16, scaling=scaling))
+    _, db, _ = ozk.ozk_dgemm_epilogue_grad(bd, to_dev(a.T), to_dev(rng.standard_normal((37, 50))),
+                                           16, scaling=scaling)
+    same(db, ozk.ozk_dgemm_ex(ad, bd, 16, scaling=scaling))
+
+
+@pytest.mark.parametrize("m", [1, 15, 64, 65, 1024, 1025, 2500])
+def test_dgemm_epilogue_grad_bias(m):
+    """The bias's gradient alone, and G where all columns are short: m / 16 + 48 roundings of the
+    sum beside 64 of G."""
+    announce(f"dgemm epilogue grad bias m={m}")
+    rng = np.random.default_rng(m)
+    for n, act in ((1, "silu"), (17, "gelu"), (300, "none")):
+        dc, z = rng.standard_normal((m, n)), 2 * rng.standard_normal((m, n))
+        a, b = to_dev(rng.standard_normal((m, 5))), to_dev(rng.standard_normal((5, n)))
+        _, _, dbias = ozk.ozk_dgemm_epilogue_grad(
+            padded(torch.from_numpy(dc), 2), a, b, 14, act=act, need_da=False, need_db=False,
+            preact=padded(torch.from_numpy(z), 1) if act != "none" else None)
+        g = dc * layers.slope(z, act)
+        tol = (64 * U64 * np.abs(dc) * (1 + z * z)).sum(0)
+        assert_near(host(dbias), g.sum(0), tol + (m // 16 + 48) * U64 * np.abs(g).sum(0), "dbias")
+        again = ozk.ozk_dgemm_epilogue_grad(to_dev(dc), a, b, 14, act=act, preact=to_dev(z))
+        assert torch.equal(again[2], dbias)
+
+
 def test_dgemm_epilogue_large_arguments():
     """Pre-activations far out: the activations and slopes settle without NaN."""
     announce("dgemm epilogue large arguments")
