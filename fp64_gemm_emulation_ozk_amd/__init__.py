@@ -216,7 +216,10 @@ def _check(t: torch.Tensor, dtype, name: str, ndim: int = 2):
 
 
 def _ld(t: torch.Tensor) -> int:
-    return max(t.stride(0), t.shape[1], 1) if t.dim() == 2 else t.shape[-1]
+    if t.dim() != 2:
+        return t.shape[-1]
+    ld, cols = t.stride(0), t.size(1)
+    return ld if ld >= cols > 0 else max(ld, cols, 1)
 
 
 def _workspace(nbytes: int, device) -> torch.Tensor:
@@ -667,8 +670,8 @@ def _check_like(t: torch.Tensor | None, shape: tuple, dtype, name: str, device):
     (These calls take a few microseconds on the GPU: what holds is found out at once.)"""
     if t is None:
         return
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.device == device and t.is_contiguous()):
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape
+            and t.get_device() == device.index and t.is_contiguous()):
         return
     if len(shape) == 2:
         _check_rows(t, dtype, name)
@@ -700,7 +703,7 @@ class _On:
         self._guard = None
 
     def __enter__(self):
-        if self._device.index != torch.cuda.current_device():
+        if self._device.index != torch._C._cuda_getDevice():
             self._guard = torch.cuda.device(self._device)
             self._guard.__enter__()
         return self
@@ -868,8 +871,15 @@ def _check_x(x) -> int:
 
 
 def _check_norm_weights(x, gamma, beta):
-    _check_like(gamma, (x.shape[1],), x.dtype, "gamma", x.device)
-    _check_like(beta, (x.shape[1],), x.dtype, "beta", x.device)
+    if gamma is not None or beta is not None:
+        shape, device = x.shape[1:], x.device
+        _check_like(gamma, shape, x.dtype, "gamma", device)
+        _check_like(beta, shape, x.dtype, "beta", device)
+
+
+def _empty(x):
+    """A new tensor of x's shape and type, rows without gaps."""
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
 
 
 def ozk_int8quant_rows(x: torch.Tensor, norm: bool = False, gamma: torch.Tensor | None = None,
@@ -908,11 +918,12 @@ def ozk_layernorm(x: torch.Tensor, gamma: torch.Tensor | None = None,
     rows, cols = x.shape
     _check_norm_weights(x, gamma, beta)
     _check_like(out, (rows, cols), x.dtype, "out", x.device)
-    for t, name in ((mean, "mean"), (rstd, "rstd")):
-        _check_like(t, (rows,), _stats_type(x.dtype), name, x.device)
+    if mean is not None or rstd is not None:
+        for t, name in ((mean, "mean"), (rstd, "rstd")):
+            _check_like(t, (rows,), _stats_type(x.dtype), name, x.device)
     with _On(x.device) as on:
         if out is None:
-            out = x.new_empty((rows, cols))
+            out = _empty(x)
         if stats:
             new = lambda: x.new_empty(rows, dtype=_stats_type(x.dtype))
             mean = new() if mean is None else mean
@@ -942,11 +953,10 @@ def ozk_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tenso
     _check_like(dbeta, (cols,), x.dtype, "dbeta", x.device)
     _check_workspace(workspace, x.device)
     with _On(x.device) as on:
-        new = lambda *shape: x.new_empty(shape)
-        dx = (new(rows, cols) if dx is None else dx) if need_dx else None
+        dx = (_empty(x) if dx is None else dx) if need_dx else None
         if need_weights:
-            dgamma = new(cols) if dgamma is None else dgamma
-            dbeta = new(cols) if dbeta is None else dbeta
+            dgamma = x.new_empty(cols) if dgamma is None else dgamma
+            dbeta = x.new_empty(cols) if dbeta is None else dbeta
             if workspace is None:
                 workspace = _workspace(
                     ozk_layernorm_backward_workspace_size(rows, cols, x.dtype), x.device)
