@@ -128,7 +128,7 @@ __global__ __launch_bounds__(1024) void act_grad_short_kernel(
 }
 
 // Column c of a chunk of rows per thread: G, and the chunk's sum of G.  1500 x 2050 with silu:
-// 22 to 26 us, bound by exp and the divisions in fp64 (74 MB would take 13).
+// 19 us with eight rows' loads together, 22 to 26 with four (74 MB would take 13.5).
 __global__ __launch_bounds__(256) void act_grad_kernel(
     int64_t m, int64_t n, int64_t chunk, const double* __restrict__ dc, int64_t lddc,
     const double* __restrict__ z, int64_t ldz, int act, double* __restrict__ g,
@@ -137,12 +137,21 @@ __global__ __launch_bounds__(256) void act_grad_kernel(
   if (c >= n) return;
   const int64_t r0 = blockIdx.y * chunk, r1 = r0 + chunk < m ? r0 + chunk : m;
   double sum = 0;
-#pragma unroll 4
-  for (int64_t i = r0; i < r1; ++i) {
-    double v = dc[i * lddc + c];
-    if (act != OZK_ACT_NONE) v *= activate_slope(z[i * ldz + c], act);
-    if (g) g[i * n + c] = v;
-    sum += v;
+  for (int64_t i0 = r0; i0 < r1; i0 += 8) {   // eight rows asked for at once
+    double v[8], w[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int64_t i = i0 + u < r1 ? i0 + u : r1 - 1;
+      v[u] = dc[i * lddc + c];
+      w[u] = act != OZK_ACT_NONE ? z[i * ldz + c] : 0.0;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (i0 + u >= r1) break;   // uniform
+      if (act != OZK_ACT_NONE) v[u] *= activate_slope(w[u], act);
+      if (g) g[(i0 + u) * n + c] = v[u];
+      sum += v[u];
+    }
   }
   if (part) part[blockIdx.y * n + c] = sum;
 }
