@@ -739,8 +739,8 @@ def ozk_dgemm_epilogue_grad_workspace_size(m: int, n: int, k: int, r: int) -> in
 
 
 def ozk_int8linear_workspace_size(m: int, n: int, k: int, aligned: bool = False) -> int:
-    """aligned: X and W at multiples of 16 bytes, k and both leading dimensions multiples of
-    16 and the latter below 2^24."""
+    """Enough for any operands of these sizes; aligned: for X and W at multiples of 16 bytes, k
+    and both leading dimensions multiples of 16 and the latter below 2^24."""
     return _layer_size("ozk_int8linear_workspace_size", m, n, k, 1 if aligned else 0)
 
 

@@ -962,7 +962,10 @@ int ozk_int8linear_workspace_size(int64_t m, int64_t n, int64_t k, int aligned, 
   if (!bytes || m < 0 || n < 0 || k < 1 || (aligned != 0 && aligned != 1)) return OZK_EINVAL;
   if (k > OZK_MAX_K) return OZK_ERANGE;
   if (m > 0x7fffffffll || n > 0x7fffffffll) return OZK_EUNSUPPORTED;
-  *bytes = int8linear_workspace(m, n, k, aligned != 0);
+  // operands of a K that allows it may be aligned, and run in another way than unaligned ones
+  const size_t tiled = k % 16 == 0 ? int8linear_workspace(m, n, k, true) : 0;
+  const size_t any = int8linear_workspace(m, n, k, false);
+  *bytes = k % 16 == 0 && (aligned || tiled > any) ? tiled : any;
   return OZK_OK;
 }
 

@@ -397,7 +397,8 @@ int ozk_int4int8gemm_fp4awe(int64_t m, int64_t n, int64_t k, const int8_t* A, in
  * (256-byte aligned) holds partial sums where K is split over workgroups and, for more than
  * a few rows, X and W with aligned rows unless they have them: aligned = 1 in the query
  * stands for X and W at multiples of 16 bytes with ldx, ldw and k multiples of 16 and ldx,
- * ldw < 2^24 (0: anything).  The query may return 0; workspace may be NULL then.
+ * ldw < 2^24; aligned = 0 gives a size that serves any operands of these m, n and k.  The query
+ * may return 0; workspace may be NULL then.
  * OZK_EUNSUPPORTED from m or n = 2^31 on, and where a launch would pass 2^32 threads: from
  * 2^23 of its tiles (64 x 128 outputs and up; 16 columns for few rows) or 2^32 chunks of 16
  * bytes to be laid out with aligned rows. */

@@ -109,6 +109,25 @@ def test_int8linear_refusals(lib):
     assert size(4, 4, 131072, 0, ctypes.byref(out)) == ERANGE
 
 
+@pytest.mark.parametrize("m", [1, 16, 17, 31, 32, 33, 64, 65, 100, 300, 1000])
+def test_int8linear_general_query_serves_aligned_operands(lib, m):
+    """aligned = 0 stands for any operands: its size is enough for those that are aligned, which
+    run in another way (17 to 64 rows most of all)."""
+    names = "m n k X ldx sx W ldw sw bias act R ldr type C ldc ws wsb stream".split()
+    call = _caller(lib.ozk_int8linear, names, dict(
+        m=m, n=4, k=4, X=FAKE, ldx=4, sx=FAKE, W=FAKE, ldw=4, sw=FAKE, bias=None, act=0, R=None,
+        ldr=0, type=3, C=FAKE, ldc=4, ws=None, wsb=0, stream=None))
+    size = ozk.ozk_int8linear_workspace_size
+    for n in (1, 16, 33, 256, 1000, 4096, 8192):
+        for k in (16, 128, 1024, 4096, 16384, 131056):
+            general, tiled = size(m, n, k), size(m, n, k, True)
+            assert general >= tiled, (m, n, k)
+            if tiled:   # it is taken as enough: only the workspace's address is refused
+                assert call(n=n, k=k, ldx=k, ldw=k, ldc=n, ws=ODD, wsb=general) == EINVAL
+            # a K that no operand can be aligned for
+            assert size(m, n, k + 1) == size(m, n, k + 1, True)
+
+
 def test_int8linear_refuses_what_a_launch_cannot_take(lib):
     """2^32 threads and more, found before any HIP call."""
     names = "m n k X ldx sx W ldw sw bias act R ldr type C ldc ws wsb stream".split()
