@@ -744,15 +744,15 @@ __global__ __launch_bounds__(256) void layernorm_backward_cols_kernel(
 
 // dgamma and dbeta from the G partials of each column, added in a fixed order: slice s of
 // 16 adds partials s, s + 16, ... in order, then the slices are added in order.  Workgroup:
-// 16 columns (of the 2 cols values) x 16 slices.
+// 16 columns (of the 2 cols values, from workgroup `first` of all on) x 16 slices.
 template <typename T>
 __global__ __launch_bounds__(256) void layernorm_join_kernel(
-    int64_t cols, int groups, const typename AccOf<T>::type* __restrict__ part,
+    int64_t first, int64_t cols, int groups, const typename AccOf<T>::type* __restrict__ part,
     T* __restrict__ dgamma, T* __restrict__ dbeta) {
   typedef typename AccOf<T>::type A;
   __shared__ A sums[16][17];
   const int cl = threadIdx.x & 15, slice = threadIdx.x >> 4;
-  const int64_t c = (int64_t)blockIdx.x * 16 + cl;
+  const int64_t c = (first + blockIdx.x) * 16 + cl;
   A s = 0;
   if (c < 2 * cols) {
     const A* p = part + c;
@@ -791,6 +791,7 @@ __global__ __launch_bounds__(256) void layernorm_join_kernel(
 constexpr int64_t kRowVecs = 4096;   // vectors a workgroup holds
 // Rows of a launch: one takes fewer than 2^32 threads, a row up to 1024 of them.
 constexpr int64_t kRowsOnce = 1 << 21;
+constexpr int64_t kJoinsOnce = 1 << 23;   // and workgroups of 256 threads
 
 template <typename T>
 int layernorm_t(int64_t rows, int64_t cols, const void* x, int64_t ldx, const void* gamma,
@@ -907,9 +908,12 @@ int layernorm_backward_t(int64_t rows, int64_t cols, const void* dy, int64_t ldd
     else OZK_LNB(1024, 2);
 #undef OZK_LNB
   }
-  if (dgamma || dbeta)   // zeros where there are no rows
-    hipLaunchKernelGGL((layernorm_join_kernel<T>), dim3((unsigned)((2 * cols + 15) / 16)),
-                       dim3(256), 0, s, cols, groups, part, (T*)dgamma, (T*)dbeta);
+  // zeros where there are no rows
+  const int64_t joins = dgamma || dbeta ? (2 * cols + 15) / 16 : 0;
+  for (int64_t b = 0; b < joins; b += kJoinsOnce)
+    hipLaunchKernelGGL((layernorm_join_kernel<T>),
+                       dim3((unsigned)(joins - b < kJoinsOnce ? joins - b : kJoinsOnce)),
+                       dim3(256), 0, s, b, cols, groups, part, (T*)dgamma, (T*)dbeta);
   return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
 }
 

@@ -240,6 +240,20 @@ def test_rows_of_several_launches():
         assert torch.equal(got, want)
 
 
+def test_layernorm_backward_columns_of_several_launches():
+    """2^27 columns and some: their sums are joined by more than one launch.  One row, so each sum
+    is one term: dy itself and dy xh, rounded as torch rounds the same fp32 steps."""
+    cols = (1 << 27) + 5
+    announce(f"layernorm backward cols={cols}")
+    g = torch.Generator(device=device()).manual_seed(8)
+    dy = torch.randn(1, cols, generator=g, device=device())
+    x = torch.randn(1, cols, generator=g, device=device())
+    mean, rstd = torch.tensor([0.25], device=device()), torch.tensor([1.5], device=device())
+    _, dgamma, dbeta = ozk.ozk_layernorm_backward(dy, x, None, mean, rstd, need_dx=False)
+    assert torch.equal(dbeta, dy[0])
+    assert torch.equal(dgamma, (dy * ((x - mean) * rstd))[0])
+
+
 def test_layernorm_edges():
     """A large common offset (two passes: no cancellation), a constant row, rows with NaN and
     Inf beside sound ones, in place, no rows."""
