@@ -7,6 +7,8 @@
 // tiles are 64 x 128 or 128 x 128.  The arithmetic per value is the same (residue_math.h).
 // A product of 64^3, r = 14, takes 12 us so (three launches, one after the other's results),
 // 18 with exponents and residues in launches of their own, 29 by the kernels of the large path.
+#include <math.h>
+
 #include "ozk_internal.h"
 #include "residue_math.h"
 #include "tile_walk.h"
@@ -312,7 +314,10 @@ void launch_small_t(ProductArgs& A, hipStream_t s) {
                      A);
 }
 
-// Rounds of 256 workgroups for tiles of bm x bn, and their time in microseconds.
+// Rounds of 256 workgroups for tiles of bm x bn, and their time in microseconds.  (A launch of a
+// workgroup of 512 threads a tile ends before 2^23 of them: a few rows against 2^26 columns, 16
+// moduli.  gemm_i8.hip's tiles are 256 x 256 and, past one K step, walked by one workgroup a
+// compute unit.)
 double rounds_time(const PlaneProduct* P, int count, int r, int64_t bm, int64_t bn, double fixed,
                    double step) {
   int64_t tiles = 0, steps = 0;
@@ -320,6 +325,7 @@ double rounds_time(const PlaneProduct* P, int count, int r, int64_t bm, int64_t 
     tiles += (P[o].m + bm - 1) / bm * ((P[o].n + bn - 1) / bn) * r;
     steps = P[o].kp / kStepK > steps ? P[o].kp / kStepK : steps;
   }
+  if (bm < 256 && tiles >= 1 << 23) return HUGE_VAL;
   return (double)((tiles + 255) / 256) * (fixed + step * (double)steps);
 }
 

@@ -555,6 +555,22 @@ def test_dgemm_epilogue_bits_of_dgemm(m, n, k, r, scaling):
                 (m // 16 + 80) * U64 * np.abs(host(dc)).sum(0) + 1e-300, "dbias")
 
 
+def test_dgemm_epilogue_columns_past_a_launch():
+    """One row against 2^26 columns, 16 moduli: as many of the smaller tiles as a launch of 512
+    threads a tile cannot take.  Small integers, so every product is exact."""
+    m, n, k, r = 1, 1 << 26, 1, 16
+    announce(f"dgemm epilogue m={m} n={n} k={k} r={r}")
+    need = ozk.ozk_dgemm_epilogue_workspace_size(m, n, k, r) + 32 * n
+    if torch.cuda.mem_get_info()[0] < need:
+        pytest.skip(f"needs {need >> 30} GiB of device memory")
+    b = (torch.arange(n, device=device()) % 1021 - 510).double()[None]
+    a = torch.full((1, 1), 3.0, dtype=torch.float64, device=device())
+    c = ozk.ozk_dgemm_epilogue(a, b, r, act="relu")
+    assert torch.equal(c, (3 * b).clamp(min=0))
+    del c
+    torch.cuda.empty_cache()   # the workspace's 137 GB
+
+
 def test_dgemm_epilogue_grad_nonfinite():
     """A line with Inf or NaN spoils the outputs it touches, in the small kernels too."""
     announce("dgemm epilogue grad nonfinite")
