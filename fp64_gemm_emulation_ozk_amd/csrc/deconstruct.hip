@@ -473,6 +473,10 @@ int launch_fused(const double* x, int64_t rows, int64_t cols, int64_t ldx,
 
 }  // namespace
 
+// Rows of a launch whose grid has them along y.
+constexpr int64_t kGridRows = 65535;
+static unsigned grid_rows(int64_t left) { return (unsigned)(left < kGridRows ? left : kGridRows); }
+
 int launch_fill_u64(uint64_t* p, int64_t n, uint64_t v, hipStream_t s) {
   if (n <= 0) return OZK_OK;
   hipLaunchKernelGGL(fill_u64_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, p,
@@ -484,9 +488,11 @@ int launch_absmax(const double* x, int64_t rows, int64_t cols, int64_t ldx, int 
                   uint64_t* maxbits, hipStream_t s) {
   if (rows <= 0 || cols <= 0) return OZK_OK;
   if (axis == 0) {
-    if (rows > 65535) return OZK_EUNSUPPORTED;
-    dim3 grid((unsigned)((cols + 2047) / 2048), (unsigned)rows);
-    hipLaunchKernelGGL(absmax_rows_kernel, grid, dim3(256), 0, s, x, cols, ldx, maxbits);
+    for (int64_t r0 = 0; r0 < rows; r0 += kGridRows) {
+      dim3 grid((unsigned)((cols + 2047) / 2048), grid_rows(rows - r0));
+      hipLaunchKernelGGL(absmax_rows_kernel, grid, dim3(256), 0, s, x + r0 * ldx, cols, ldx,
+                         maxbits + r0);
+    }
   } else {
     dim3 grid((unsigned)((cols + 255) / 256), (unsigned)((rows + 63) / 64));
     hipLaunchKernelGGL(absmax_cols_kernel, grid, dim3(256), 0, s, x, rows, cols, ldx, maxbits);
@@ -502,7 +508,15 @@ int launch_residues(const double* x, int64_t rows, int64_t cols, int64_t ldx, in
   const bool wide = K.wide != 0;
   if (axis == 0) {
     if (rows <= 0) return OZK_OK;
-    if (rows > 65535) return OZK_EUNSUPPORTED;
+    if (rows > kGridRows) {
+      for (int64_t r0 = 0; r0 < rows; r0 += kGridRows) {
+        const int st = launch_residues(x + r0 * ldx, grid_rows(rows - r0), cols, ldx, 0, r, p_bits,
+                                       maxbits ? maxbits + r0 : nullptr, planes + r0 * ldp, ldp,
+                                       plane_stride, exps + r0, given_exps, s);
+        if (st != OZK_OK) return st;
+      }
+      return OZK_OK;
+    }
     dim3 grid((unsigned)((ldp + 2047) / 2048), (unsigned)rows);
     const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (ldx & 1) == 0;
 #define OZK_ROWS(W, V, G)                                                                     \
@@ -584,9 +598,10 @@ int launch_norm_exps(const double* x, int64_t rows, int64_t cols, int64_t ldx, i
   const int64_t chunks = norm_chunks(rows, cols, axis);
   if (chunks > 0) {
     if (axis == 0) {
-      if (rows > 65535) return OZK_EUNSUPPORTED;
-      hipLaunchKernelGGL(norm_partials_rows_kernel, dim3((unsigned)chunks, (unsigned)rows),
-                         dim3(256), 0, s, x, cols, ldx, pmax, ps);
+      for (int64_t r0 = 0; r0 < rows; r0 += kGridRows)
+        hipLaunchKernelGGL(norm_partials_rows_kernel,
+                           dim3((unsigned)chunks, grid_rows(rows - r0)), dim3(256), 0, s,
+                           x + r0 * ldx, cols, ldx, pmax + r0 * chunks, ps + r0 * chunks);
     } else {
       hipLaunchKernelGGL(norm_partials_cols_kernel,
                          dim3((unsigned)((cols + 255) / 256), (unsigned)chunks), dim3(256), 0, s,

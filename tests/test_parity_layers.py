@@ -571,6 +571,28 @@ def test_dgemm_epilogue_columns_past_a_launch():
     torch.cuda.empty_cache()   # the workspace's 137 GB
 
 
+@pytest.mark.parametrize("scaling", ["max", "norm"])
+def test_dgemm_epilogue_grad_many_long_rows(scaling):
+    """More than 65535 rows of dC, each past the 32768 values that a workgroup holds: the rows of
+    dA are those of a few rows alone, bit for bit."""
+    m, n, k, r = 65600, 32800, 2, 8
+    announce(f"dgemm epilogue grad m={m} n={n} k={k} r={r} {scaling}")
+    need = ozk.ozk_dgemm_epilogue_grad_workspace_size(m, n, k, r) + 10 * m * n
+    if torch.cuda.mem_get_info()[0] < need:
+        pytest.skip(f"needs {need >> 30} GiB of device memory")
+    g = torch.Generator(device=device()).manual_seed(3)
+    dc = torch.randn(m, n, generator=g, device=device(), dtype=torch.float64)
+    b = torch.randn(k, n, generator=g, device=device(), dtype=torch.float64)
+    a = torch.zeros(m, k, device=device(), dtype=torch.float64)
+    grad = lambda lo, hi: ozk.ozk_dgemm_epilogue_grad(
+        dc[lo:hi], a[lo:hi], b, r, scaling=scaling, need_db=False, need_dbias=False)[0]
+    da = grad(0, m)
+    for lo, hi in ((0, 70), (65500, 65600)):
+        assert torch.equal(da[lo:hi], grad(lo, hi))
+    del dc, da
+    torch.cuda.empty_cache()
+
+
 def test_dgemm_epilogue_grad_nonfinite():
     """A line with Inf or NaN spoils the outputs it touches, in the small kernels too."""
     announce("dgemm epilogue grad nonfinite")
