@@ -183,6 +183,49 @@ def test_layernorm_backward_many_rows(rows, cols):
     assert_near(host(first[2]), want[2], (d + 2) * U32 * np.abs(host(dy)).sum(0), "dbeta")
 
 
+# every shape of workgroup with more rows than it has at once: 64, 256 and 1024 threads, one and
+# two vectors each, gamma kept in registers and read again for each row
+@pytest.mark.parametrize("kind,rows,cols", [
+    ("float32", 2600, 130), ("float32", 2500, 400), ("float32", 1100, 1000),
+    ("float32", 1100, 2048), ("float32", 600, 4000), ("float32", 600, 7001),
+    ("bfloat16", 2200, 300), ("bfloat16", 1030, 4096), ("bfloat16", 600, 16384),
+    ("float16", 600, 8200), ("float64", 2100, 65), ("float64", 600, 2000), ("float64", 520, 4096)])
+def test_layernorm_backward_rows_in_turn(kind, rows, cols):
+    """Rows that a workgroup takes one after the other: dx of every row, also over dy and x while
+    the next row is on its way."""
+    announce(f"layernorm backward rows in turn {kind} rows={rows} cols={cols}")
+    dtype = TYPES[kind]
+    u = U64 if kind == "float64" else U32
+    stat = torch.float64 if kind == "float64" else torch.float32
+    x, gamma, _, dy = row_input(rows, cols, dtype, rows + cols)
+    _, m, r = layers.layernorm(host(x))
+    dyd, xd, gd, md, rd = [t.to(device()) for t in (dy, x, gamma, torch.from_numpy(m).to(stat),
+                                                    torch.from_numpy(r).to(stat))]
+    got = ozk.ozk_layernorm_backward(dyd, xd, gd, md, rd)
+    hx, hdy, hg, hm, hr = host(x), host(dy), host(gamma), host(md), host(rd)
+    want = layers.layernorm_backward(hdy, hx, hg, hm, hr)
+    xh = (hx - hm[:, None]) * hr[:, None]
+    g = hdy * hg
+    c1, c2 = (g * xh).mean(1), g.mean(1)
+    # as in test_layernorm_backward
+    e1 = (depth(cols) + 6) * u * np.abs(g * xh).mean(1)
+    e2 = (depth(cols) + 4) * u * np.abs(g).mean(1)
+    ex = hr[:, None] * (e2[:, None] + np.abs(xh) * e1[:, None]
+                        + 6 * u * (np.abs(g) + np.abs(c2)[:, None]
+                                   + np.abs(xh * c1[:, None]))) * 1.01
+    assert_near(host(got[0]), want[0], ex + half_step(dtype) * (np.abs(want[0]) + ex)
+                + tiny(dtype), "dx")
+    d = rows // 64 + 64   # rows of a group in order, groups of a slice, slices
+    for out, w, t, what in ((got[1], want[1], hdy * xh, "dgamma"), (got[2], want[2], hdy, "dbeta")):
+        e = (d + 4) * u * np.abs(t).sum(0)
+        assert_near(host(out), w, e + half_step(dtype) * (np.abs(w) + e) + tiny(dtype), what)
+    for which in (0, 1):
+        a, b = dyd.clone(), xd.clone()
+        over = ozk.ozk_layernorm_backward(a, b, gd, md, rd, dx=(a, b)[which])
+        for o, w in zip(over, got):
+            assert torch.equal(o, w)
+
+
 def test_layernorm_backward_parts():
     """dx alone needs no workspace; dgamma and dbeta alone leave dx; in place over dy and x;
     no rows give zero sums."""
