@@ -761,6 +761,32 @@ def test_dgemm_epilogue_grad_activations(m, n, k, name):
     assert_near(host(dbias), g.sum(0), eg.sum(0) + 400 * U64 * np.abs(g).sum(0), "dbias")
 
 
+@pytest.mark.parametrize("name", layers.ACTS)
+@pytest.mark.parametrize("m,n,k", [(1025, 130, 20), (1500, 300, 33), (4200, 70, 9)])
+def test_dgemm_epilogue_grad_long_activations(m, n, k, name):
+    """More rows than the short kernel of G takes: G goes into both products.  Chunks of 16 rows,
+    the last of one or of twelve, and of 17; padded dC and Z.  Bounds as above."""
+    announce(f"dgemm epilogue grad long {name} m={m} n={n} k={k}")
+    rng = np.random.default_rng(m + n)
+    a, b = rng.standard_normal((m, k)), rng.standard_normal((k, n))
+    dc, z = rng.standard_normal((m, n)), 2 * rng.standard_normal((m, n))
+    da, db, dbias = ozk.ozk_dgemm_epilogue_grad(
+        padded(torch.from_numpy(dc), 3), to_dev(a), to_dev(b), 16,
+        preact=padded(torch.from_numpy(z), 1), act=name)
+    g = dc * layers.slope(z, name)
+    eg = 64 * U64 * np.abs(dc) * (1 + z * z)
+
+    def tol(left, right, eleft, eright):
+        inner = left.shape[1]
+        scaled = inner * 2.0 ** -44 * np.abs(left).max(1)[:, None] * np.abs(right).max(0)
+        return (eleft @ np.abs(right) + np.abs(left) @ eright
+                + 2 * inner * U64 * (np.abs(left) @ np.abs(right)) + scaled)
+
+    assert_near(host(da), g @ b.T, tol(g, b.T, eg, np.zeros_like(b.T)), "dA")
+    assert_near(host(db), a.T @ g, tol(a.T, g, np.zeros_like(a.T), eg), "dB")
+    assert_near(host(dbias), g.sum(0), eg.sum(0) + (m // 16 + 80) * U64 * np.abs(g).sum(0), "dbias")
+
+
 def test_dgemm_epilogue_grad_is_the_difference_quotient():
     """The gradient of sum(dC * C) for C = gelu(A B + bias), against central differences of
     the library's own forward: h = 2^-16 leaves h^2 |f'''| / 6 (|f'''| below 400 at these
