@@ -14,6 +14,8 @@ struct ActConst {
   static constexpr A kTanhScale = (A)1.59576912160573071175;    // 2 (2 / pi)^(1/2)
   static constexpr A kTanhCubic = (A)0.044715;
   static constexpr A kLog2e = (A)1.44269504088896340736;
+  static constexpr A kLog2eLow = (A)(1.44269504088896340736 - (double)kLog2e);
+  static constexpr A kLn2 = (A)0.69314718055994530942;
 };
 
 // gelu z Phi(z) with Phi(z) = erfc(-z / sqrt 2) / 2 (no cancellation in the lower tail);
@@ -35,48 +37,107 @@ __device__ __forceinline__ double activate(double z, int act) {
   }
 }
 
-// z / (1 + exp(-v)): one exp2 and one reciprocal of the hardware, each within one ulp.
+// The same for the int8 layer, whose epilogue is bound by these instructions, in two forms: for
+// outputs of 16 bits, and (kFull) for fp32 outputs, off by a few units of fp32 (u = 2^-24).
+// 4096 x 16384 x 4096 with gelu and residual: 299 us in bf16, 358 in fp32 (347 there with the
+// shorter form; without an activation 342).
+//
+// z / (1 + exp(-v)), v of z's sign.  For 16 bits one exp2 and one reciprocal of the hardware,
+// each within 2 u; the exponent's rounding adds |v| u.  kFull: with s = exp(-|v|) <= 1 it is
+// z / (1 + s), or z s / (1 + s) below zero; what the product |v| log2 e rounds off goes into s
+// by its first-order term, and the reciprocal takes one Newton step.
+template <bool kFull>
 __device__ __forceinline__ float logistic_times(float z, float v) {
-  return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * ActConst<float>::kLog2e));
+  typedef ActConst<float> K;
+  if constexpr (!kFull)
+    return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * K::kLog2e));
+  const float a = __builtin_fabsf(v), hi = -K::kLog2e * a;
+  const float lo = __builtin_fmaf(-K::kLog2eLow, a, __builtin_fmaf(-K::kLog2e, a, -hi));
+  float s = __builtin_amdgcn_exp2f(hi);
+  s = __builtin_fmaf(s, lo * K::kLn2, s);
+  s = a < 128.0f ? s : 0.0f;   // there lo is large or infinite and s 0
+  const float d = 1.0f + s;
+  float r = __builtin_amdgcn_rcpf(d);
+  r = __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+  return (v < 0.0f ? z * s : z) * r;
 }
 
-// The same in fp32 for the int8 layer, whose epilogue is bound by these instructions (16 of
-// them for gelu; 4096 x 16384 x 4096 with gelu and residual took 403 us with the library's
-// erfcf and expf, 367 with these, the rest of the kernel the same).
-// gelu: with x = |z| / sqrt 2 and t = 1 / (1 + 0.3275911 x),
-//   erfc(x) = (a1 t + a2 t^2 + a3 t^3 + a4 t^4 + a5 t^5) exp(-x^2) + e, |e| <= 1.5e-7
-// (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26), so the result is off
-// by at most 0.75e-7 |z| beside its roundings: about one unit of fp32 in |z|.
-__device__ __forceinline__ float activate(float z, int act) {
+// z Phi(z).  The tail Phi(-|z|) = t P(t) exp(-z^2 / 2) with t = 1 / (1 + q |z|): P is fitted to
+// the scaled tail with the least relative error over |z| <= 13.3 (where the tail leaves fp32), so
+// that the result keeps its leading digits however small it is; above zero Phi = 1 - tail.
+// 16 bits: seven terms, off by 7.5e-7 relative, and exp2's argument by up to 1e-5 at the tail's
+// end: 2^-16, a thirtieth of fp16's rounding.  kFull: eight terms for |z| >= 1 (1.5e-8), what z^2 and
+// its product with log2 e / 2 round off as above, one Newton step; below, where 1 - tail would
+// magnify the tail's error, Phi = 1 / 2 + z M(z^2), M of six terms (7e-10).  Eight units of u at
+// most in all, in a model of these steps.
+template <bool kFull>
+__device__ __forceinline__ float gelu_times(float z) {
+  typedef ActConst<float> K;
+  if constexpr (!kFull) {
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.36f, __builtin_fabsf(z), 1.0f));
+    float p = __builtin_fmaf(0.04746443033f, t, -0.1811617911f);
+    p = __builtin_fmaf(p, t, 0.1828561127f);
+    p = __builtin_fmaf(p, t, 0.02523851208f);
+    p = __builtin_fmaf(p, t, 0.1401986182f);
+    p = __builtin_fmaf(p, t, 0.1416846828f);
+    p = __builtin_fmaf(p, t, 0.1437192857f);
+    const float tail = p * t * __builtin_amdgcn_exp2f(-0.5f * K::kLog2e * z * z);
+    return z * (z < 0.0f ? tail : 1.0f - tail);
+  }
+  const float y = z * z;
+  float m = __builtin_fmaf(-7.654212823e-06f, y, 1.134863851e-04f);
+  m = __builtin_fmaf(m, y, -1.186329988e-03f);
+  m = __builtin_fmaf(m, y, 9.973322973e-03f);
+  m = __builtin_fmaf(m, y, -6.649035960e-02f);
+  m = __builtin_fmaf(m, y, 3.989422917e-01f);
+  const float a = __builtin_fminf(__builtin_fabsf(z), 16.0f);
+  const float d = __builtin_fmaf(0.24f, a, 1.0f);
+  float t = __builtin_amdgcn_rcpf(d);
+  t = __builtin_fmaf(__builtin_fmaf(-d, t, 1.0f), t, t);
+  float p = __builtin_fmaf(-0.05917223543f, t, 0.1761606038f);
+  p = __builtin_fmaf(p, t, -0.1021098420f);
+  p = __builtin_fmaf(p, t, 0.1485771835f);
+  p = __builtin_fmaf(p, t, 0.04906247184f);
+  p = __builtin_fmaf(p, t, 0.09672495723f);
+  p = __builtin_fmaf(p, t, 0.09496610612f);
+  p = __builtin_fmaf(p, t, 0.09578620642f);
+  constexpr float kHalf = -0.5f * K::kLog2e, kHalfLow = -0.5f * K::kLog2eLow;
+  const float sq = a * a, rest = __builtin_fmaf(a, a, -sq), hi = kHalf * sq;
+  float lo = __builtin_fmaf(kHalfLow, sq, __builtin_fmaf(kHalf, sq, -hi));
+  lo = __builtin_fmaf(kHalf, rest, lo);
+  float e = __builtin_amdgcn_exp2f(hi);
+  e = __builtin_fmaf(e, lo * K::kLn2, e);
+  const float tail = p * t * e;
+  const float phi = __builtin_fabsf(z) < 1.0f ? __builtin_fmaf(m, z, 0.5f)
+                                              : (z < 0.0f ? tail : 1.0f - tail);
+  return z * phi;
+}
+
+// Results of the last three below 2^-119 may come as zero.
+template <bool kFull>
+__device__ __forceinline__ float activate32(float z, int act) {
   typedef ActConst<float> K;
   switch (act) {
     case OZK_ACT_RELU:
       return z < 0.0f ? 0.0f : z;
-    case OZK_ACT_GELU: {
-      const float x = __builtin_fabsf(z) * K::kRsqrt2;
-      const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.0f));
-      float p = __builtin_fmaf(1.061405429f, t, -1.453152027f);
-      p = __builtin_fmaf(p, t, 1.421413741f);
-      p = __builtin_fmaf(p, t, -0.284496736f);
-      p = __builtin_fmaf(p, t, 0.254829592f);
-      const float half_tail = 0.5f * (p * t) * __builtin_amdgcn_exp2f(-K::kLog2e * x * x);
-      return z * (z < 0.0f ? half_tail : 1.0f - half_tail);
-    }
+    case OZK_ACT_GELU:
+      return gelu_times<kFull>(z);
     case OZK_ACT_GELU_TANH:
-      return logistic_times(z, K::kTanhScale * __builtin_fmaf(K::kTanhCubic * z * z, z, z));
+      return logistic_times<kFull>(z,
+                                   K::kTanhScale * __builtin_fmaf(K::kTanhCubic * z * z, z, z));
     case OZK_ACT_SILU:
-      return logistic_times(z, z);
+      return logistic_times<kFull>(z, z);
     default:
       return z;
   }
 }
 
-// activate of N values: the choice of the function stands outside their loop.
-template <int N>
+// activate32 of N values: the choice of the function stands outside their loop.
+template <bool kFull, int N>
 __device__ __forceinline__ void activate_all(float (&z)[N], int act) {
   auto each = [&](int a) {
 #pragma unroll
-    for (int u = 0; u < N; ++u) z[u] = activate(z[u], a);
+    for (int u = 0; u < N; ++u) z[u] = activate32<kFull>(z[u], a);
   };
   if (act == OZK_ACT_RELU) each(OZK_ACT_RELU);
   else if (act == OZK_ACT_GELU) each(OZK_ACT_GELU);

@@ -34,7 +34,7 @@ __device__ __forceinline__ float pre_activation(int sum, float s, float t, float
 template <typename O>
 __device__ __forceinline__ void put1(const Epilogue<O>& E, int64_t row, int64_t col, int sum) {
   float z = pre_activation(sum, E.sx[row], E.sw[col], E.bias ? (float)E.bias[col] : 0.0f);
-  z = activate(z, E.act);
+  z = activate32<sizeof(O) == 4>(z, E.act);
   if (E.residual) z += (float)E.residual[row * E.ldr + col];
   E.c[row * E.ldc + col] = (O)z;
 }
@@ -56,7 +56,7 @@ __device__ __forceinline__ void put4(const Epilogue<O>& E, int64_t row, int64_t 
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       z[u] = pre_activation(acc[u], s, t[u], E.bias ? (float)b[u] : 0.0f);
-    activate_all(z, E.act);
+    activate_all<sizeof(O) == 4>(z, E.act);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       if (E.residual) z[u] += (float)r[u];
@@ -423,7 +423,7 @@ __device__ __forceinline__ void put_tile(const Epilogue<O>& E, const v4i (&acc)[
 #pragma unroll
       for (int u = 0; u < 8; ++u)
         z[u] = pre_activation(u < 4 ? lo[u & 3] : hi[u & 3], s0, t[u], b[u]);
-      activate_all(z, E.act);
+      activate_all<sizeof(O) == 4>(z, E.act);
       V8 o;
 #pragma unroll
       for (int u = 0; u < 8; ++u) {

@@ -391,7 +391,9 @@ int ozk_int4int8gemm_fp4awe(int64_t m, int64_t n, int64_t k, const int8_t* A, in
  * the columns of the B of ozk_int8gemm_*), scale_x (m) and scale_w (n) fp32.  bias (n) and
  * residual (m x n, ldr >= n) may be NULL and have the type of C: OZK_F32, OZK_F16 or
  * OZK_BF16.  The sum is exact in int32 (1 <= k <= OZK_MAX_K); what follows is fp32, rounded
- * once to C's type.  A scale that is NaN gives NaN in the outputs it touches.  residual may
+ * once to C's type.  Relative to its result an activation is off by at most 12 units of 2^-24
+ * for an fp32 C (gelu_tanh: 6 |v| more, v its logistic function's argument), 2^-16 or 8 |v| + 12
+ * units for 16 bits; results below 2^-119 may come as zero.  A scale that is NaN gives NaN in the outputs it touches.  residual may
  * be C itself; otherwise C overlaps no input.  Any leading dimensions ldx, ldw >= k and any
  * byte alignment of X and W; the other pointers are aligned to their elements.  The workspace
  * (256-byte aligned) holds partial sums where K is split over workgroups and, for more than

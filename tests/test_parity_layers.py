@@ -482,6 +482,49 @@ def test_int8linear(m, n, k, kind):
         assert (buf[:, n:] == 3.0).all()
 
 
+@pytest.mark.parametrize("name", layers.ACTS[1:])
+@pytest.mark.parametrize("kind", ["float32", "float16", "bfloat16"])
+def test_int8linear_activation_digits(kind, name):
+    """The activations of z = bias (zero codes), relative to the result however small it is.  In
+    units of 2^-24, for fp32: gelu and silu 12 (exp2 within two, its argument's remainder, the
+    reciprocal, the polynomial two or three, three or four products and the fit's quarter);
+    gelu_tanh's exponent v is rounded six times before, 6 |v| more.  16-bit types: 2^-16 from the
+    shorter fit and exp2's argument (gelu), 8 |v| and 12 from v and exp2's argument (the others).
+    Results below 2^-119 may come as zero."""
+    announce(f"int8linear activation digits {kind} {name}")
+    dtype = TYPES[kind]
+    z = np.concatenate([np.linspace(-13.5, 13.5, 5001), -np.exp(np.linspace(-30, 4.4, 900)),
+                        np.exp(np.linspace(-30, 4.4, 900)), [0.0, 1.0, -1.0, 1e4, -1e4, 6e4]])
+    z = torch.from_numpy(z).to(dtype)
+    hz = host(z)
+    n = hz.size
+    for m in (1, 20, 130):   # rows of two kernels for few rows, one of tiles
+        x = torch.zeros((m, 32), dtype=torch.int8, device=device())
+        w = torch.ones((n, 32), dtype=torch.int8, device=device())
+        got = host(ozk.ozk_int8linear(x, torch.ones(m, device=device()), w,
+                                      torch.ones(n, device=device()), bias=z.to(device()),
+                                      act=name, dtype=dtype))
+        assert (got == got[0]).all()
+        want = layers.act(hz, name)
+        v = np.minimum(2 * np.sqrt(2 / np.pi) * np.abs(hz + 0.044715 * hz ** 3), 100)
+        v = v if name == "gelu_tanh" else np.minimum(np.abs(hz), 100)
+        if name == "relu":
+            rel = 0
+        elif kind == "float32":
+            rel = (12 + (6 * v if name == "gelu_tanh" else 0)) * U32
+        else:
+            rel = 2.0 ** -16 if name == "gelu" else (12 + 8 * v) * U32
+        err = rel * np.abs(want) + 2.0 ** -119
+        assert_near(got[0], want, err + half_step(dtype) * (np.abs(want) + err) + tiny(dtype),
+                    f"{name} m={m}")
+    far = torch.tensor([float("inf"), float("nan"), 3e38, -3e38], dtype=torch.float32).to(dtype)
+    got = ozk.ozk_int8linear(x, torch.ones(m, device=device()), w[:4],
+                             torch.ones(4, device=device()), bias=far.to(device()), act=name,
+                             dtype=dtype)[0].double().cpu()
+    assert got[0] == np.inf and torch.isnan(got[1]) and got[2] == far[2].double()
+    assert got[3] == 0 or kind == "float16"   # (there -3e38 is -Inf: the formula's Inf times 0)
+
+
 @pytest.mark.parametrize("m", [1, 20, 130])
 def test_int8linear_longest_k(m):
     """K = 131071 of (-128)(-128): every sum is 2147467264, the largest that int32 must hold."""
