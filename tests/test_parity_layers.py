@@ -392,6 +392,61 @@ def test_int8quant_many_rows(kind, cols):
     check_codes(q[keep], scale[keep], plain[keep])
 
 
+@pytest.mark.parametrize("kind", ["float16", "bfloat16", "float32"])
+@pytest.mark.parametrize("cols", [500, 2000, 16384, 20000])
+def test_int8quant_padded_rows(kind, cols):
+    """Rows of zeros and, under the norm, of one value (with beta, without, with a beta of zeros),
+    beside others: scale and codes as the definition has them."""
+    announce(f"int8quant padded rows {kind} cols={cols}")
+    dtype, rows = TYPES[kind], 300
+    x, gamma, beta, _ = row_input(rows, cols, dtype, cols)
+    x[::3] = 0
+    x[1::3] = 3.3
+    xd, gd, bd = x.to(device()), gamma.to(device()), beta.to(device())
+    q, scale = ozk.ozk_int8quant_rows(xd)
+    check_codes(q, scale, host(x))
+    assert not q[::3].any() and not scale[::3].any()
+    zeros = torch.zeros_like(bd)
+    for g, b in ((None, None), (gd, None), (gd, zeros), (gd, bd)):
+        q, scale = ozk.ozk_int8quant_rows(xd, norm=True, gamma=g, beta=b)
+        # (x - mean of one value is 0 exactly; a 64-bit mean may be a rounding off)
+        y = layers.layernorm(host(x), None if g is None else host(g),
+                             None if b is None else host(b))[0]
+        y[::3] = y[1::3] = 0 if b is None else host(b)
+        check_codes(q, scale, y)
+    # without statistics that are finite, or with a weight that is not, no row is plain
+    q, scale = ozk.ozk_int8quant_rows(xd, norm=True, eps=0.0)
+    assert torch.isnan(scale[::3]).all() and torch.isnan(scale[1::3]).all() and not q[::3].any()
+    gd[cols - 1] = float("inf")
+    assert torch.isnan(ozk.ozk_int8quant_rows(xd, norm=True, gamma=gd)[1]).all()
+
+
+def test_int8quant_zero_rows_take_no_longer():
+    """A batch that is half padding costs no more than one without: the least of five times of ten
+    calls each, with half as much again for the clock (twice as much was the fault)."""
+    announce("int8quant zero rows' time")
+    x = torch.randn(4096, 16384, device=device()).bfloat16()
+    half = x.clone()
+    half[::2] = 0
+    q = torch.empty(x.shape, dtype=torch.int8, device=device())
+    s = torch.empty(4096, device=device())
+
+    def least(x):
+        times = []
+        for _ in range(5):
+            e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            e0.record()
+            for _ in range(10):
+                ozk.ozk_int8quant_rows(x, out=q, scale=s)
+            e1.record()
+            e1.synchronize()
+            times.append(e0.elapsed_time(e1))
+        return min(times)
+
+    least(x)
+    assert least(half) < 1.5 * least(x)
+
+
 def test_int8quant_rows_edges():
     """NaN, Inf, fp64 values past fp32's range, values below every fp32 scale, subnormal
     scales, ties to even; what stands behind a row's end stays."""
