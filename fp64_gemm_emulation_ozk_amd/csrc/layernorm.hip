@@ -26,6 +26,38 @@ __device__ __forceinline__ int valid(int64_t c, int64_t cols) {
 }
 
 // ------------------------------------------------------------------ forward
+// The mean and rstd of a row from the first sum's `mean` and the sums s1 of d = x - mean and s2
+// of d^2: the mean is off by some roundings of the sum, which d shows without them where the row
+// lies far from zero (x - mean is exact there), so that y = (d - off) rstd.  A constant row
+// 12345.6 fp32 had y up to 0.7 from the first mean alone.
+template <typename A>
+struct RowStats {
+  A mean, off, rstd;
+};
+template <int kT, typename A>
+__device__ __forceinline__ RowStats<A> row_stats(A mean, A s1, A s2, A inv, A eps,
+                                                 A (*slots)[kT / 64]) {
+  s1 = wave_all(s1, SumOp());
+  s2 = wave_all(s2, SumOp());
+  if constexpr (kT > 64) {
+    if ((threadIdx.x & 63) == 0) {
+      slots[0][threadIdx.x >> 6] = s1;
+      slots[1][threadIdx.x >> 6] = s2;
+    }
+    __syncthreads();
+    s1 = slots[0][0];
+    s2 = slots[1][0];
+#pragma unroll
+    for (int w = 1; w < kT / 64; ++w) {
+      s1 += slots[0][w];
+      s2 += slots[1][w];
+    }
+  }
+  const A off = s1 * inv, var = s2 * inv - off * off;
+  // (a constant row's difference may fall below zero; a NaN stays one)
+  return {mean + off, off, (A)1 / sqrt((var < 0 ? (A)0 : var) + eps)};
+}
+
 // kT threads of a row hold it in kV vectors each (vector v of thread t starts at column
 // (v kT + t) N).  kT = 64: four rows per workgroup; else one.  16384 x 4096 bf16: 52 us, 268 MB
 // at 5.1 TB/s, 0.94 of a large copy's rate.
@@ -37,7 +69,7 @@ __global__ __launch_bounds__(kT < 256 ? 256 : kT) void layernorm_kernel(
   typedef typename AccOf<T>::type A;
   constexpr int N = Vec<T>::N;
   constexpr int kRows = kT < 256 ? 256 / kT : 1;
-  __shared__ A slots[2][kT / 64];
+  __shared__ A slots[3][kT / 64];
   const int t = threadIdx.x % kT;
   const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kT;
   if (kRows > 1 && row >= rows) return;  // whole waves
@@ -52,21 +84,23 @@ __global__ __launch_bounds__(kT < 256 ? 256 : kT) void layernorm_kernel(
   }
   const A inv = (A)1 / (A)cols;
   const A mean = row_all<kT>(sum, SumOp(), slots[0]) * inv;
-  A sq = 0;
+  A s1 = 0, s2 = 0;
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
     const int nv = valid<N>((int64_t)(v * kT + t) * N, cols);
 #pragma unroll
     for (int u = 0; u < N; ++u) {
       a[v][u] -= mean;
-      if (u < nv) sq += a[v][u] * a[v][u];
+      if (u < nv) {
+        s1 += a[v][u];
+        s2 += a[v][u] * a[v][u];
+      }
     }
   }
-  const A var = row_all<kT>(sq, SumOp(), slots[1]) * inv;
-  const A rstd = (A)1 / sqrt(var + eps);
+  const RowStats<A> S = row_stats<kT>(mean, s1, s2, inv, eps, slots + 1);
   if (t == 0) {
-    if (mean_out) mean_out[row] = mean;
-    if (rstd_out) rstd_out[row] = rstd;
+    if (mean_out) mean_out[row] = S.mean;
+    if (rstd_out) rstd_out[row] = S.rstd;
   }
   T* yr = y + row * ldy;
 #pragma unroll
@@ -78,7 +112,7 @@ __global__ __launch_bounds__(kT < 256 ? 256 : kT) void layernorm_kernel(
     if (beta) load_vec<T, A>(beta, c, cols, b);
 #pragma unroll
     for (int u = 0; u < N; ++u) {
-      A w = a[v][u] * rstd;
+      A w = (a[v][u] - S.off) * S.rstd;
       if (gamma) w *= g[u];
       if (beta) w += b[u];
       a[v][u] = w;
@@ -96,7 +130,7 @@ __global__ __launch_bounds__(1024) void layernorm_long_kernel(
     typename AccOf<T>::type* __restrict__ rstd_out) {
   typedef typename AccOf<T>::type A;
   constexpr int N = Vec<T>::N, kT = 1024;
-  __shared__ A slots[2][kT / 64];
+  __shared__ A slots[3][kT / 64];
   const int64_t row = blockIdx.x;
   const T* xr = x + row * ldx;
   A sum = 0, a[N];
@@ -107,19 +141,22 @@ __global__ __launch_bounds__(1024) void layernorm_long_kernel(
   }
   const A inv = (A)1 / (A)cols;
   const A mean = row_all<kT>(sum, SumOp(), slots[0]) * inv;
-  A sq = 0;
+  A s1 = 0, s2 = 0;
   for (int64_t c = (int64_t)threadIdx.x * N; c < cols; c += kT * N) {
     load_vec<T, A>(xr, c, cols, a);
     const int nv = valid<N>(c, cols);
 #pragma unroll
     for (int u = 0; u < N; ++u)
-      if (u < nv) sq += (a[u] - mean) * (a[u] - mean);
+      if (u < nv) {
+        const A d = a[u] - mean;
+        s1 += d;
+        s2 += d * d;
+      }
   }
-  const A var = row_all<kT>(sq, SumOp(), slots[1]) * inv;
-  const A rstd = (A)1 / sqrt(var + eps);
+  const RowStats<A> S = row_stats<kT>(mean, s1, s2, inv, eps, slots + 1);
   if (threadIdx.x == 0) {
-    if (mean_out) mean_out[row] = mean;
-    if (rstd_out) rstd_out[row] = rstd;
+    if (mean_out) mean_out[row] = S.mean;
+    if (rstd_out) rstd_out[row] = S.rstd;
   }
   T* yr = y + row * ldy;
   for (int64_t c = (int64_t)threadIdx.x * N; c < cols; c += kT * N) {
@@ -129,7 +166,7 @@ __global__ __launch_bounds__(1024) void layernorm_long_kernel(
     if (beta) load_vec<T, A>(beta, c, cols, b);
 #pragma unroll
     for (int u = 0; u < N; ++u) {
-      A w = (a[u] - mean) * rstd;
+      A w = ((a[u] - mean) - S.off) * S.rstd;
       if (gamma) w *= g[u];
       if (beta) w += b[u];
       a[u] = w;

@@ -297,6 +297,42 @@ def test_layernorm_backward_columns_of_several_launches():
     assert torch.equal(dgamma, (dy * ((x - mean) * rstd))[0])
 
 
+@pytest.mark.parametrize("kind", ["float32", "bfloat16"])
+@pytest.mark.parametrize("cols", [1, 5, 130, 777, 1537, 4096, 5000, 20001, 40000])
+def test_layernorm_far_from_zero(kind, cols):
+    """Rows of one value: y is zero.  Rows about a far value: the mean of a sum in fp32 is off by
+    e = (depth + 2) u |value|, x - mean is exact (Sterbenz), and the sum of those differences,
+    each at most |dev| + e, gives the rest of the mean within (depth + 4) u of their mean."""
+    announce(f"layernorm far from zero {kind} cols={cols}")
+    dtype = TYPES[kind]
+    values = (0.1, 3.3, -1000.1, 12345.6)
+    d = depth(cols)
+    flat = torch.tensor(values).to(dtype)[:, None].repeat(1, cols)
+    y, mean, rstd = ozk.ozk_layernorm(flat.to(device()), stats=True)
+    # what is left of the mean, (d + 4) u e, over sqrt(eps); the mean is the value itself but for
+    # one rounding, the variance e^2 (d + 6) u at most
+    e = (d + 2) * U32 * np.abs(host(flat))
+    left = (d + 4) * U32 * e / np.sqrt(1e-5)
+    assert_near(host(y), np.zeros(flat.shape), left * (1 + half_step(dtype)) + tiny(dtype), "flat")
+    assert_near(host(mean), host(flat)[:, 0], U32 * np.abs(host(flat)[:, 0]), "mean")
+    if cols < 100:
+        return
+    g = torch.Generator().manual_seed(cols)
+    x = (torch.randn(4, cols, generator=g) + torch.tensor(values)[:, None]).to(dtype)
+    y, mean, rstd = ozk.ozk_layernorm(x.to(device()), stats=True)
+    wy, wm, wr = layers.layernorm(host(x))
+    dev = np.abs(host(x) - wm[:, None])
+    e = (d + 2) * U32 * np.abs(host(x)).mean(1)
+    each = dev + e[:, None]
+    e_dev = (d + 4) * U32 * each.mean(1)[:, None] + 2 * U32 * each
+    r_rel = 0.75 * ((2 * dev * e_dev + e_dev ** 2).mean(1) + (d + 6) * U32 * (each ** 2).mean(1)) \
+        * wr ** 2 + 4 * U32
+    ey = 1.01 * wr[:, None] * (e_dev + dev * r_rel[:, None]) + 4 * U32 * np.abs(wy)
+    assert_near(host(y), wy, ey + half_step(dtype) * (np.abs(wy) + ey) + tiny(dtype), "y")
+    assert_near(host(mean), wm, e_dev.max(1) + U32 * np.abs(wm), "mean")
+    assert_near(host(rstd), wr, wr * (r_rel + U32), "rstd")
+
+
 def test_layernorm_edges():
     """A large common offset (two passes: no cancellation), a constant row, rows with NaN and
     Inf beside sound ones, in place, no rows."""
