@@ -741,7 +741,8 @@ ProductLayout product_layout(const Product& P, int r) {
 }
 
 bool small(const Product& P) {
-  return small_lines(P.rows, P.K) && small_lines(P.cols, P.K);
+  return small_operands(P.rows > P.cols ? P.rows : P.cols, P.K,
+                        P.left_axis == 1 && P.right_axis == 1);
 }
 
 // A product in its workspace, and what becomes of it.

@@ -208,7 +208,9 @@ struct PlaneProduct {
   const int8_t* right;
   int8_t* res;
 };
-bool small_lines(int64_t lines, int64_t kdim);   // whether an operand is small
+// Whether a product's operands are small: at most `lines` lines of kdim values each; columns:
+// both operands' lines are columns.
+bool small_operands(int64_t lines, int64_t kdim, bool columns);
 int launch_small_deconstruct(const SmallOperand* op, int count, int r, int scaling,
                              const int64_t* kp, hipStream_t s);
 int launch_products(const PlaneProduct* P, int count, int r, hipStream_t s);

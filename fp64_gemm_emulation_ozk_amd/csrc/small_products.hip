@@ -331,8 +331,25 @@ double rounds_time(const PlaneProduct* P, int count, int r, int64_t bm, int64_t 
 
 }  // namespace
 
-bool small_lines(int64_t lines, int64_t kdim) {
-  return kdim <= kLineMax && lines * kdim <= (int64_t)3 << 20;
+// Lines of at most 2048 values, and 2^21 values in the larger operand; 2^25 where its lines have at
+// most 256 values, 2^23 where both operands' lines are columns.  Whole calls with one operand of
+// so many values and 64 lines of the other, r = 16, norm rule, by these kernels and by the large
+// path's, microseconds:
+//   values               2^20         2^21         2^22         2^23
+//   rows of 2048      36.1 / 37.1  38.6 / 35.7  49.7 / 43.9  90.2 / 74.3
+//   rows of 1000      32.9 / 34.9  44.8 / 43.1  68.1 / 59.9   109 / 93.9
+//   columns of 1000   32.4 / 39.2  47.3 / 48.7  74.2 / 67.0   123 / 107    (rows beside them)
+//   rows of 200       39.4 / 48.9  62.8 / 78.9   103 / 134    184 / 241     (2^25: 661 / 999)
+//   columns of 200    38.9 / 46.9  59.0 / 64.2  95.2 / 98.1   191 / 182     (2^25: 746 / 697)
+//   both columns, 2048 36.5 / 62.1 41.9 / 65.2  54.2 / 72.8  98.1 / 114
+//   both columns, 1000 32.7 / 62.4 48.3 / 71.5  75.6 / 89.1   124 / 132
+// (rows of the large path take one launch that keeps a row in a workgroup's registers, whatever
+// its length; two operands of columns take three launches each there.)  Over 600 such cases of
+// lines of 200 to 2048 values, either rule and 2^19 to 2^23.5 values, the choice costs 0.8 % on
+// average, 18 % at worst.
+bool small_operands(int64_t lines, int64_t kdim, bool columns) {
+  const int64_t most = (int64_t)1 << (kdim <= 256 ? 25 : (columns ? 23 : 21));
+  return kdim <= kLineMax && lines * kdim <= most;
 }
 
 int launch_small_deconstruct(const SmallOperand* op, int count, int r, int scaling,
@@ -383,7 +400,11 @@ int launch_products(const PlaneProduct* P, int count, int r, hipStream_t s) {
     A.inv[l] = l < r ? C->inv[l] : 1.0;
   }
   for (int o = 0; o < count; ++o) A.P[o] = P[o];
-  // one round: fixed + step per 128 K values (see the int8 layer's plan, without the launch)
+  // One round: fixed + step per 128 K values (the int8 layer's measured rounds, without the launch).
+  // Whole calls, r = 16, by the small, mid and large tiles: 256^3 13.6, 15.0, 16.4; 512^3 28.7,
+  // 25.5, 28.5; 768^3 55.8, 49.4, 39.8; 60 x 60 x 8192 60.6, 66.2, 106; 384 x 384 x 8192 107, 82.3,
+  // 124; 1024^3 86.2, 67.7, 51.0.  Over 26 shapes of 64 to 16384 the choice costs 0.8 % on average,
+  // 12 % at worst (300 x 1000 x 300: mid 30.2, large 26.9).
   const double small = rounds_time(P, count, r, 64, 128, 2.5, 0.55);
   const double mid = rounds_time(P, count, r, 128, 128, 3.8, 0.72);
   double large = 0;   // gemm_i8.hip, one launch a product

@@ -732,6 +732,33 @@ def test_dgemm_epilogue_bits_of_dgemm(m, n, k, r, scaling):
                 (m // 16 + 80) * U64 * np.abs(host(dc)).sum(0) + 1e-300, "dbias")
 
 
+@pytest.mark.parametrize("m,n,k", [(2090, 70, 1000), (2100, 70, 1000), (70, 2090, 1000),
+                                   (70, 2100, 1000), (130000, 40, 256), (132000, 40, 256),
+                                   (40, 130000, 256), (40, 132000, 256)])
+def test_dgemm_epilogue_where_operands_stop_being_small(m, n, k):
+    """2^21 values, or 2^25 in lines of 256: the bits of ozk_dgemm_ex on either side."""
+    announce(f"dgemm epilogue small or not m={m} n={n} k={k}")
+    g = torch.Generator(device=device()).manual_seed(m + n)
+    a = torch.randn(m, k, generator=g, device=device(), dtype=torch.float64)
+    b = torch.randn(k, n, generator=g, device=device(), dtype=torch.float64)
+    for scaling in ("max", "norm"):
+        assert torch.equal(ozk.ozk_dgemm_epilogue(a, b, 14, scaling=scaling),
+                           ozk.ozk_dgemm_ex(a, b, 14, scaling))
+
+
+@pytest.mark.parametrize("n", [4100, 4200])
+def test_dgemm_epilogue_grad_where_columns_stop_being_small(n):
+    """2^23 values in columns of 2040, and G's rows past any small line: both products' bits."""
+    m, k = 2040, 70
+    announce(f"dgemm epilogue grad small or not n={n}")
+    g = torch.Generator(device=device()).manual_seed(n)
+    new = lambda *s: torch.randn(*s, generator=g, device=device(), dtype=torch.float64)
+    dc, a, b = new(m, n), new(m, k), new(k, n)
+    da, db, _ = ozk.ozk_dgemm_epilogue_grad(dc, a, b, 14)
+    assert torch.equal(da, ozk.ozk_dgemm_ex(dc, b.t().contiguous(), 14))
+    assert torch.equal(db, ozk.ozk_dgemm_ex(a.t().contiguous(), dc, 14))
+
+
 def test_dgemm_epilogue_columns_past_a_launch():
     """One row against 2^26 columns, 16 moduli: as many of the smaller tiles as a launch of 512
     threads a tile cannot take.  Small integers, so every product is exact."""
