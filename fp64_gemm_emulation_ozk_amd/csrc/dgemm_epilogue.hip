@@ -96,7 +96,11 @@ void launch_r(dim3 grid, hipStream_t s, int64_t m, int64_t n, const int8_t* res,
 // A short gradient's G and the whole column sums in one launch: 16 columns x 64 slices of rows per
 // workgroup, slice s taking rows s, s + 64, ..., the slices added in a fixed order.  (A gradient
 // of 167 x 247 x 512 took 39 us with chunks and their join, and two launches of the
-// reconstruction; so 28.)
+// reconstruction; so 28.)  The sums alone, silu, this launch / chunks and their join, us:
+//   rows            256         768         1024        1536        2048
+//   256 columns    5.6 / 9.4  10.1 / 10.1  12.7 / 11.0  17.3 / 11.5  21.8 / 10.4
+//   4096 columns   6.2 / 10.3 12.8 / 15.7  15.7 / 20.1  21.4 / 26.2  28.5 / 31.5
+// (few columns leave compute units idle here; 1024 stands between where either is the faster).
 constexpr int64_t kShortRows = 1024;
 
 __global__ __launch_bounds__(1024) void act_grad_short_kernel(

@@ -831,7 +831,17 @@ __global__ __launch_bounds__(256) void layernorm_join_kernel(
   }
 }
 
-// Threads and vectors per thread for a row of `vecs` 16-byte vectors.
+// Threads and vectors per thread for a row of `vecs` 16-byte vectors: of the shapes that hold the
+// row, the one with the fewest threads and vectors (a reduction across waves, and every idle
+// lane, costs a row the same whatever it holds).  8192 rows of bf16, us:
+//   vecs   64x1  64x2  64x4  256x1  256x2  256x4  1024x1  1024x2
+//     64    7.6   8.5  10.5   13.4   17.2
+//    128         10.9  12.4   15.4   18.5   27.1    44.0
+//    256               18.2   18.7   21.1   29.4    45.7    61.4
+//    512                             27.0   35.3    51.2    63.3
+//   1024                                    51.0    60.9    71.4
+// With 8 rows all are within a microsecond of each other (256 vectors: 6.5 with 64x4, 5.1 with
+// 256x2).  512x2 and 512x4 were no better but for 1024 vectors (46.5).
 #define OZK_ROW_SHAPES(GO)            \
   if (vecs <= 64) GO(64, 1);          \
   else if (vecs <= 128) GO(64, 2);    \
@@ -914,7 +924,9 @@ int int8quant_t(int64_t rows, int64_t cols, const void* x, int64_t ldx, const vo
   return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
 }
 
-// Vectors a backward workgroup holds per row (its column sums take registers too).
+// Vectors a backward workgroup holds per row (its column sums take registers too, so a thread
+// holds two at most: 8192 rows of bf16 with 512 vectors take 43 us with 256x2, 54 with 1024x1, 105
+// with 256x4; with 160 vectors 34 with 256x1, 30 with 64x4, with 256 26 and 28).
 constexpr int64_t kBackwardVecs = 2048;
 
 template <typename T>
