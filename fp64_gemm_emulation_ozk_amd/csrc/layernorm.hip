@@ -305,7 +305,7 @@ __device__ __forceinline__ void int8quant_row(
     int8_t* __restrict__ q, int64_t ldq, float* __restrict__ scale) {
   constexpr int N = Vec<T>::N, kW = kT / 64;
   __shared__ double sums[kNorm ? 3 : 1][kW];
-  __shared__ float tops[2][kW];
+  __shared__ uint32_t tops[kNorm ? 2 : 1][kW];
   const int t = threadIdx.x % kT;
   const T* xr = x + row * ldx;
   typename Vec<T>::type raw[kV];
@@ -408,25 +408,29 @@ __device__ __forceinline__ void int8quant_row(
   auto top = [](uint32_t bits) {
     return wave_all(bits > 0x7f800000u ? __builtin_huge_valf() : __uint_as_float(bits), MaxOp());
   };
-  float ymax = top(top_y), bmax = kNorm && beta ? top(top_b) : 0.0f;
+  uint32_t ybits = __float_as_uint(top(top_y));
+  uint32_t bbits = kNorm && beta ? __float_as_uint(top(top_b)) : 0u;
   if constexpr (kT > 64) {
     if ((threadIdx.x & 63) == 0) {
-      tops[0][threadIdx.x >> 6] = ymax;
-      tops[1][threadIdx.x >> 6] = bmax;
+      tops[0][threadIdx.x >> 6] = ybits;
+      if (kNorm) tops[1][threadIdx.x >> 6] = bbits;
     }
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kW; ++w) {
-      ymax = tops[0][w] > ymax ? tops[0][w] : ymax;
-      bmax = tops[1][w] > bmax ? tops[1][w] : bmax;
+      ybits = tops[0][w] > ybits ? tops[0][w] : ybits;
+      if (kNorm) bbits = tops[1][w] > bbits ? tops[1][w] : bbits;
     }
   }
+  // uniform over the row, so over the wave
+  ybits = __builtin_amdgcn_readfirstlane(ybits);
+  const float ymax = __uint_as_float(ybits), bmax = __uint_as_float(bbits);
   // fp32 y is off by at most 8 roundings of |y - b| + |y| <= 2 |y| + |b| (x is exact)
   const float e = kNorm ? 8.0f * 5.97e-8f * (2.0f * ymax + bmax) : 0.0f;
   // A row of zeros (a padded token; a constant one after the norm without beta) is not open: 4096
   // x 16384 bf16 takes 27 us where all rows are such, 44 where none is (119 with each of their
   // values formed in fp64, 176 after the norm and now 65).
-  const bool zero = ymax == 0.0f && level;
+  const bool zero = ybits == 0 && level;
   const bool hard = !zero && !(ymax >= 1e-30f && ymax <= 1e37f && bmax <= 1e37f);
   double amax = (double)ymax;
   bool bad = false;
