@@ -28,12 +28,18 @@ __device__ __forceinline__ int valid(int64_t c, int64_t cols) {
 // ------------------------------------------------------------------ forward
 // The mean and rstd of a row from the first sum's `mean` and the sums s1 of d = x - mean and s2
 // of d^2: the mean is off by some roundings of the sum, which d shows without them where the row
-// lies far from zero (x - mean is exact there), so that y = (d - off) rstd.  A constant row
-// 12345.6 fp32 had y up to 0.7 from the first mean alone.
+// lies far from zero (x - mean is exact there): y = d rstd + shift.  A constant row 12345.6 fp32
+// had y up to 0.7 from the first mean alone.
 template <typename A>
 struct RowStats {
-  A mean, off, rstd;
+  A mean, rstd, shift;
 };
+__device__ __forceinline__ float fma_of(float a, float b, float c) {
+  return __builtin_fmaf(a, b, c);
+}
+__device__ __forceinline__ double fma_of(double a, double b, double c) {
+  return __builtin_fma(a, b, c);
+}
 template <int kT, typename A>
 __device__ __forceinline__ RowStats<A> row_stats(A mean, A s1, A s2, A inv, A eps,
                                                  A (*slots)[kT / 64]) {
@@ -55,12 +61,13 @@ __device__ __forceinline__ RowStats<A> row_stats(A mean, A s1, A s2, A inv, A ep
   }
   const A off = s1 * inv, var = s2 * inv - off * off;
   // (a constant row's difference may fall below zero; a NaN stays one)
-  return {mean + off, off, (A)1 / sqrt((var < 0 ? (A)0 : var) + eps)};
+  const A rstd = (A)1 / sqrt((var < 0 ? (A)0 : var) + eps);
+  return {mean + off, rstd, -off * rstd};
 }
 
 // kT threads of a row hold it in kV vectors each (vector v of thread t starts at column
-// (v kT + t) N).  kT = 64: four rows per workgroup; else one.  16384 x 4096 bf16: 52 us, 268 MB
-// at 5.1 TB/s, 0.94 of a large copy's rate.
+// (v kT + t) N).  kT = 64: four rows per workgroup; else one.  16384 x 4096 bf16: 51 us, 268 MB
+// at 5.26 TB/s, 0.96 of a large copy's rate.
 template <typename T, int kT, int kV>
 __global__ __launch_bounds__(kT < 256 ? 256 : kT) void layernorm_kernel(
     int64_t rows, int64_t cols, const T* x, int64_t ldx,
@@ -90,11 +97,9 @@ __global__ __launch_bounds__(kT < 256 ? 256 : kT) void layernorm_kernel(
     const int nv = valid<N>((int64_t)(v * kT + t) * N, cols);
 #pragma unroll
     for (int u = 0; u < N; ++u) {
-      a[v][u] -= mean;
-      if (u < nv) {
-        s1 += a[v][u];
-        s2 += a[v][u] * a[v][u];
-      }
+      a[v][u] = u < nv ? a[v][u] - mean : (A)0;
+      s1 += a[v][u];
+      s2 = fma_of(a[v][u], a[v][u], s2);
     }
   }
   const RowStats<A> S = row_stats<kT>(mean, s1, s2, inv, eps, slots + 1);
@@ -111,11 +116,16 @@ __global__ __launch_bounds__(kT < 256 ? 256 : kT) void layernorm_kernel(
     if (gamma) load_vec<T, A>(gamma, c, cols, g);
     if (beta) load_vec<T, A>(beta, c, cols, b);
 #pragma unroll
-    for (int u = 0; u < N; ++u) {
-      A w = (a[v][u] - S.off) * S.rstd;
-      if (gamma) w *= g[u];
-      if (beta) w += b[u];
-      a[v][u] = w;
+    for (int u = 0; u < N; ++u) a[v][u] = fma_of(a[v][u], S.rstd, S.shift);
+    if (gamma && beta) {
+#pragma unroll
+      for (int u = 0; u < N; ++u) a[v][u] = fma_of(a[v][u], g[u], b[u]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        if (gamma) a[v][u] *= g[u];
+        if (beta) a[v][u] += b[u];
+      }
     }
     store_vec<T, A>(yr, c, cols, a[v]);
   }
@@ -150,7 +160,7 @@ __global__ __launch_bounds__(1024) void layernorm_long_kernel(
       if (u < nv) {
         const A d = a[u] - mean;
         s1 += d;
-        s2 += d * d;
+        s2 = fma_of(d, d, s2);
       }
   }
   const RowStats<A> S = row_stats<kT>(mean, s1, s2, inv, eps, slots + 1);
@@ -166,7 +176,7 @@ __global__ __launch_bounds__(1024) void layernorm_long_kernel(
     if (beta) load_vec<T, A>(beta, c, cols, b);
 #pragma unroll
     for (int u = 0; u < N; ++u) {
-      A w = ((a[u] - mean) - S.off) * S.rstd;
+      A w = fma_of(a[u] - mean, S.rstd, S.shift);
       if (gamma) w *= g[u];
       if (beta) w += b[u];
       a[u] = w;
