@@ -8,7 +8,7 @@
 //
 // Many rows are bound by HBM: a row is read once into registers (the mean, then the centred
 // sum of squares, are taken from there), in 16-byte loads.  Few rows are bound by a launch and
-// one chain of latencies (load, two reductions, store): 8 x 1024 fp32 takes 4.0 us.
+// one chain of latencies (load, two reductions, store): 8 x 1024 fp32 takes 3.9 us.
 // Sums and statistics are fp32 for the types of at most 32 bits and fp64 for fp64; the
 // codes' statistics are fp64 for every type (fp64 arithmetic runs at the fp32 rate here), so
 // that a code depends on the order of the sums only within 1e-13 of a rounding border.
@@ -306,8 +306,9 @@ __device__ __forceinline__ void int8quant_row_f64(
 // thousand), the value is formed in fp64.  A row whose magnitudes are out of the bound's
 // reach (below 1e-30, above 1e37, not finite) takes fp64 throughout.
 // All in fp64, 4096 x 8192 bf16 with the norm took 69.5 us, 4096 x 16384 without 61.1; so they
-// take 38 and 40, the latter 201 MB at 5.05 TB/s (a large copy: 5.5).  With the norm the fp64
-// sums bind as much as the bytes (4096 x 8192 fp32: 57 us, 2.9 TB/s).
+// take 37 and 36, the latter 201 MB at a large copy's rate.  With the norm the vector instructions
+// bind, 42 a value (16 without), five of them fp64: they issue in 0.8 of the cycles in bf16, in 0.65
+// in fp32 (4096 x 8192 fp32: 56 us, 3.0 TB/s).
 template <typename T, int kT, int kV, bool kNorm>
 __device__ __forceinline__ void int8quant_row(
     int64_t row, int64_t cols, const T* __restrict__ x, int64_t ldx,

@@ -205,7 +205,9 @@ int ozk_dgemm_ex(int64_t m, int64_t n, int64_t k, const double* A, int64_t lda,
  * Z, if not NULL, receives the pre-activations the gradient needs (ldz >= n).  The product
  * is rounded once (as ozk_dgemm_ex), then the bias is added, the activation taken and the
  * residual added, one fp64 rounding or fp64 function each, in the registers of the
- * reconstruction.  residual may be C itself; otherwise outputs overlap no input.  Other
+ * reconstruction.  (With neither activation nor residual a native fp64 product is the faster up to
+ * about 1024^3, as for ozk_dgemm: an emulated one is at least three launches.)  residual may be
+ * C itself; otherwise outputs overlap no input.  Other
  * arguments and the errors are those of ozk_dgemm_ex, with OZK_EINVAL for an unknown act; the
  * workspace (256-byte aligned) takes ozk_dgemm_epilogue_workspace_size bytes. */
 int ozk_dgemm_epilogue_workspace_size(int64_t m, int64_t n, int64_t k, int r, size_t* bytes);
