@@ -459,6 +459,14 @@ template <bool kWide, int kNT, int kG>
 int launch_fused(const double* x, int64_t rows, int64_t cols, int64_t ldx,
                  const ResidueConsts& K, int norm, int width, int8_t* planes, int64_t ldp,
                  int64_t plane_stride, int32_t* exps, hipStream_t s) {
+  constexpr int64_t kOnce = 1 << 21;   // rows of a launch of fewer than 2^32 threads
+  if (rows > kOnce) {
+    const int st = launch_fused<kWide, kNT, kG>(x, kOnce, cols, ldx, K, norm, width, planes, ldp,
+                                                plane_stride, exps, s);
+    if (st != OZK_OK) return st;
+    return launch_fused<kWide, kNT, kG>(x + kOnce * ldx, rows - kOnce, cols, ldx, K, norm, width,
+                                        planes + kOnce * ldp, ldp, plane_stride, exps + kOnce, s);
+  }
   const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (ldx & 1) == 0;
 #define OZK_FUSED_LAUNCH(V, N)                                                              \
   hipLaunchKernelGGL((residues_rows_fused_kernel<kWide, V, kNT, kG, N>), dim3((unsigned)rows), \
@@ -563,7 +571,7 @@ int launch_deconstruct_pair(const double* a, int64_t m, int64_t k, int64_t lda, 
   p.gx_b = (n + 31) / 32;
   p.blocks_b = p.gx_b * ((kp + 127) / 128);
   const int64_t blocks = m + p.blocks_b;
-  if (blocks > 0x7fffffff) return OZK_EUNSUPPORTED;
+  if (blocks >= 1 << 24) return OZK_EUNSUPPORTED;   // 2^32 threads
   const bool vec = (reinterpret_cast<uintptr_t>(a) & 15) == 0 && (lda & 1) == 0;
   const bool norm = scaling == OZK_SCALING_NORM;
   const int g = k <= 2048 ? 1 : (k <= 4096 ? 2 : 4);

@@ -775,6 +775,23 @@ def test_dgemm_epilogue_columns_past_a_launch():
     torch.cuda.empty_cache()   # the workspace's 137 GB
 
 
+def test_dgemm_epilogue_rows_past_a_launch():
+    """2^24 rows and some, a workgroup a row: deconstructed by more than one launch."""
+    m, n, k, r = (1 << 24) + 5, 2, 3, 14
+    announce(f"dgemm epilogue m={m} n={n} k={k} r={r}")
+    need = ozk.ozk_dgemm_epilogue_workspace_size(m, n, k, r) + 64 * m
+    if torch.cuda.mem_get_info()[0] < need:
+        pytest.skip(f"needs {need >> 30} GiB of device memory")
+    i = torch.arange(m, device=device())
+    a = torch.stack([i % 1021 - 510, i % 7, -(i % 64)], 1).double()   # exact products and sums
+    b = torch.tensor([[3.0, -1.0], [100.0, 7.0], [5.0, 0.5]], device=device(), dtype=torch.float64)
+    want = (a[:, :, None] * b[None]).sum(1)
+    assert torch.equal(ozk.ozk_dgemm_epilogue(a, b, r), want)
+    assert torch.equal(ozk.ozk_dgemm_ex(a, b, r), want)
+    del a, want, i
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("scaling", ["max", "norm"])
 def test_dgemm_epilogue_grad_many_long_rows(scaling):
     """More than 65535 rows of dC, each past the 32768 values that a workgroup holds: the rows of
