@@ -39,6 +39,12 @@ __all__ = [
     "ozk_int8linear", "ozk_int8linear_workspace_size",
     "ozk_int8quant_rows", "ozk_layernorm", "ozk_layernorm_backward",
     "ozk_layernorm_backward_workspace_size",
+    "ozk_dgemm_gated", "ozk_dgemm_gated_workspace_size", "ozk_dgemm_gated_grad",
+    "ozk_dgemm_gated_grad_workspace_size",
+    "ozk_mxfp4_line_bytes", "ozk_mxfp4_scale_bytes", "ozk_mxfp4_quant", "ozk_mxfp4_values",
+    "ozk_mxfp4_linear", "ozk_mxfp4_linear_workspace_size",
+    "ozk_mxfp4_gated", "ozk_mxfp4_gated_workspace_size",
+    "ozk_clip_norm", "ozk_clip_norm_workspace_size",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libozk.so")
@@ -116,6 +122,25 @@ _SIGNATURES = {
                               _ptr, _i64, _int, _ptr, _i64, _ptr, _size, _ptr]),
     "ozk_int8quant_rows": (_int, [_i64, _i64, _int, _ptr, _i64, _int, _ptr, _ptr, _f64, _ptr,
                                   _i64, _ptr, _ptr]),
+    "ozk_dgemm_gated_workspace_size": (_int, [_i64, _i64, _i64, _int, _ptr]),
+    "ozk_dgemm_gated": (_int, [_i64, _i64, _i64, _ptr, _i64, _ptr, _i64, _ptr, _int, _ptr, _i64,
+                               _ptr, _i64, _int, _int, _ptr, _size, _ptr]),
+    "ozk_dgemm_gated_grad_workspace_size": (_int, [_i64, _i64, _i64, _int, _ptr]),
+    "ozk_dgemm_gated_grad": (_int, [_i64, _i64, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr,
+                                    _i64, _int, _ptr, _i64, _ptr, _i64, _ptr, _int, _int, _ptr,
+                                    _size, _ptr]),
+    "ozk_mxfp4_line_bytes": (_i64, [_i64]),
+    "ozk_mxfp4_scale_bytes": (_i64, [_i64]),
+    "ozk_mxfp4_quant": (_int, [_i64, _i64, _int, _ptr, _i64, _int, _ptr, _i64, _ptr, _i64, _ptr]),
+    "ozk_mxfp4_values": (_int, [_i64, _i64, _ptr, _i64, _ptr, _i64, _int, _ptr, _i64, _ptr]),
+    "ozk_mxfp4_linear_workspace_size": (_int, [_i64, _i64, _i64, _ptr]),
+    "ozk_mxfp4_linear": (_int, [_i64, _i64, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64,
+                                _ptr, _int, _ptr, _i64, _int, _ptr, _i64, _ptr, _size, _ptr]),
+    "ozk_mxfp4_gated_workspace_size": (_int, [_i64, _i64, _i64, _ptr]),
+    "ozk_mxfp4_gated": (_int, [_i64, _i64, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64,
+                               _ptr, _int, _int, _ptr, _i64, _ptr, _size, _ptr]),
+    "ozk_clip_norm_workspace_size": (_int, [_i64, _ptr]),
+    "ozk_clip_norm": (_int, [_i64, _ptr, _ptr, _ptr, _ptr, _f64, _ptr, _ptr, _size, _ptr]),
     "ozk_layernorm": (_int, [_i64, _i64, _int, _ptr, _i64, _ptr, _ptr, _f64, _ptr, _i64, _ptr,
                              _ptr, _ptr]),
     "ozk_layernorm_backward_workspace_size": (_int, [_i64, _i64, _int, _ptr]),
@@ -968,3 +993,268 @@ def ozk_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tenso
               0 if workspace is None else workspace.numel(),
               on.stream(stream, dx, dgamma, dbeta, workspace))
     return dx, dgamma, dbeta
+
+
+# ------------------------------------------------------------ a gated feed-forward block
+def ozk_dgemm_gated_workspace_size(m: int, n: int, k: int, r: int) -> int:
+    return _layer_size("ozk_dgemm_gated_workspace_size", m, n, k, r)
+
+
+def ozk_dgemm_gated_grad_workspace_size(m: int, n: int, k: int, r: int) -> int:
+    return _layer_size("ozk_dgemm_gated_grad_workspace_size", m, n, k, r)
+
+
+def _check_halves(count: int, name: str) -> int:
+    """n of a matrix of 2 n columns or lines."""
+    if count % 2:
+        raise ValueError(f"{name} must hold two projections of one size, got {count}")
+    return count // 2
+
+
+def ozk_dgemm_gated(a: torch.Tensor, b: torch.Tensor, r: int, bias: torch.Tensor | None = None,
+                    act="silu", scaling="max", preact: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """Emulated fp64 C = act(Z[:, :n]) * Z[:, n:], Z = A B + bias for B k x 2 n (the gate's
+    projection, then the other); preact (m x 2 n) receives Z for the gradient."""
+    _check_rows(a, torch.float64, "A")
+    _check(b, torch.float64, "B")
+    _check_like(b, (a.shape[1], b.shape[-1]), torch.float64, "B", a.device)
+    m, k = a.shape
+    n = _check_halves(b.shape[1], "B's columns")
+    _check_like(bias, (2 * n,), torch.float64, "bias", a.device)
+    _check_like(preact, (m, 2 * n), torch.float64, "preact", a.device)
+    _check_like(out, (m, n), torch.float64, "out", a.device)
+    _check_workspace(workspace, a.device)
+    with _On(a.device) as on:
+        if out is None:
+            out = a.new_empty((m, n))
+        if workspace is None:
+            workspace = _workspace(ozk_dgemm_gated_workspace_size(m, n, k, r), a.device)
+        _call("ozk_dgemm_gated", m, n, k, _at(a), _ld(a), _at(b), _ld(b), _at(bias), _act(act),
+              _at(preact), _ld_opt(preact), _at(out), _ld(out), r, _scaling(scaling),
+              _at(workspace), workspace.numel(), on.stream(stream, out, workspace))
+    return out
+
+
+def ozk_dgemm_gated_grad(dc: torch.Tensor, a: torch.Tensor, b: torch.Tensor, r: int,
+                         preact: torch.Tensor, act="silu", scaling="max", need_da: bool = True,
+                         need_db: bool = True, need_dbias: bool = True,
+                         da: torch.Tensor | None = None, db: torch.Tensor | None = None,
+                         dbias: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None, stream=None):
+    """(dA, dB, dbias) of ozk_dgemm_gated from the gradient of its output; None where not
+    needed.  preact as the forward wrote it."""
+    act = _act(act)
+    _check_rows(dc, torch.float64, "dC")
+    _check(a, torch.float64, "A")
+    m, n = dc.shape
+    _check_like(a, (m, a.shape[-1]), torch.float64, "A", dc.device)
+    k = a.shape[1]
+    _check_like(b, (k, 2 * n), torch.float64, "B", dc.device)
+    if preact is None:
+        raise ValueError("preact is needed for the gradient")
+    _check_like(preact, (m, 2 * n), torch.float64, "preact", dc.device)
+    _check_like(da, (m, k), torch.float64, "da", dc.device)
+    _check_like(db, (k, 2 * n), torch.float64, "db", dc.device)
+    _check_like(dbias, (2 * n,), torch.float64, "dbias", dc.device)
+    _check_workspace(workspace, dc.device)
+    with _On(dc.device) as on:
+        new = lambda *shape: dc.new_empty(shape)
+        da = (new(m, k) if da is None else da) if need_da else None
+        db = (new(k, 2 * n) if db is None else db) if need_db else None
+        dbias = (new(2 * n) if dbias is None else dbias) if need_dbias else None
+        if workspace is None:
+            workspace = _workspace(ozk_dgemm_gated_grad_workspace_size(m, n, k, r), dc.device)
+        _call("ozk_dgemm_gated_grad", m, n, k, _at(dc), _ld(dc), _at(a), _ld(a), _at(b), _ld(b),
+              _at(preact), _ld_opt(preact), act, _at(da), _ld_opt(da), _at(db), _ld_opt(db),
+              _at(dbias), r, _scaling(scaling), _at(workspace), workspace.numel(),
+              on.stream(stream, da, db, dbias, workspace))
+    return da, db, dbias
+
+
+# ------------------------------------------------------------ microscaled 4-bit codes
+def ozk_mxfp4_line_bytes(k: int) -> int:
+    """Bytes of codes of a line of k values, two a byte, in whole steps of 256 values."""
+    return (k + 255) // 256 * 128
+
+
+def ozk_mxfp4_scale_bytes(k: int) -> int:
+    """Scales of a line of k values, one for 32, in whole steps of 256 values."""
+    return (k + 255) // 256 * 8
+
+
+def ozk_mxfp4_linear_workspace_size(m: int, n: int, k: int) -> int:
+    return _layer_size("ozk_mxfp4_linear_workspace_size", m, n, k)
+
+
+def ozk_mxfp4_gated_workspace_size(m: int, n: int, k: int) -> int:
+    return _layer_size("ozk_mxfp4_gated_workspace_size", m, n, k)
+
+
+def ozk_mxfp4_quant(x: torch.Tensor, axis: int = 0, codes: torch.Tensor | None = None,
+                    scales: torch.Tensor | None = None, stream=None):
+    """(codes uint8 [lines][ozk_mxfp4_line_bytes(k)], scales uint8 [lines][
+    ozk_mxfp4_scale_bytes(k)]) in MX FP4 of the rows of x (axis 0, k = cols) or of its columns
+    (axis 1, k = rows): operands of ozk_mxfp4_linear and ozk_mxfp4_gated."""
+    kind = _check_x(x)
+    if axis not in (0, 1):
+        raise ValueError("axis must be 0 or 1")
+    rows, cols = x.shape
+    lines, k = (cols, rows) if axis else (rows, cols)
+    lb, sb = ozk_mxfp4_line_bytes(k), ozk_mxfp4_scale_bytes(k)
+    _check_like(codes, (lines, lb), torch.uint8, "codes", x.device)
+    _check_like(scales, (lines, sb), torch.uint8, "scales", x.device)
+    with _On(x.device) as on:
+        if codes is None:
+            codes = x.new_empty((lines, lb), dtype=torch.uint8)
+        if scales is None:
+            scales = x.new_empty((lines, sb), dtype=torch.uint8)
+        _call("ozk_mxfp4_quant", rows, cols, kind, _at(x), _ld(x), axis, _at(codes),
+              _line_ld(codes, lb), _at(scales), _line_ld(scales, sb),
+              on.stream(stream, codes, scales))
+    return codes, scales
+
+
+def _line_ld(t: torch.Tensor, width: int) -> int:
+    """Leading dimension of lines; a single one may have any stride."""
+    return _ld(t) if t.shape[0] > 1 else width
+
+
+def _check_lines(codes, scales, name: str, device=None):
+    """Lines of codes and their scales, whole steps of both: (lines, values of a line)."""
+    _check_rows(codes, torch.uint8, name)
+    lines, lb = codes.shape
+    if lb % 128 or lb == 0:
+        raise ValueError(f"{name} must hold whole steps of 128 bytes a line, got {lb}")
+    if device is not None and codes.device != device:
+        raise ValueError(f"{name} is on {codes.device}, expected {device}")
+    if scales is None:
+        raise ValueError(f"{name}'s scales are missing")
+    _check_like(scales, (lines, lb // 16), torch.uint8, f"{name}'s scales", codes.device)
+    return lines, 2 * lb
+
+
+def ozk_mxfp4_values(codes: torch.Tensor, scales: torch.Tensor, k: int | None = None,
+                     dtype=torch.float32, out: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """The values [lines][k] of lines in MX FP4, in `dtype` (the type of `out` where that is
+    given); k defaults to all that the lines hold."""
+    if out is not None:
+        dtype = out.dtype
+    kind = _type(dtype)
+    lines, most = _check_lines(codes, scales, "codes")
+    k = most if k is None else k
+    if not most - 256 < k <= most:
+        raise ValueError(f"lines of {most} values do not hold {k}")
+    _check_like(out, (lines, k), dtype, "out", codes.device)
+    with _On(codes.device) as on:
+        if out is None:
+            out = codes.new_empty((lines, k), dtype=dtype)
+        _call("ozk_mxfp4_values", lines, k, _at(codes), _line_ld(codes, most // 2), _at(scales),
+              _line_ld(scales, most // 32), kind, _at(out), _line_ld(out, k),
+              on.stream(stream, out))
+    return out
+
+
+def _mx_product(name, size, gated, x, scale_x, w, scale_w, bias, act, residual, dtype, out,
+                workspace, stream):
+    if out is not None:
+        dtype = out.dtype
+    kind = _type(dtype)
+    if kind == OZK_F64:
+        raise TypeError("the output is float32, float16 or bfloat16")
+    m, k = _check_lines(x, scale_x, "X")
+    wide, kw = _check_lines(w, scale_w, "W", x.device)
+    if k != kw:
+        raise ValueError(f"X's lines hold {k} values, W's {kw}")
+    n = _check_halves(wide, "W's lines") if gated else wide
+    _check_like(bias, (wide,), dtype, "bias", x.device)
+    _check_like(residual, (m, n), dtype, "residual", x.device)
+    _check_like(out, (m, n), dtype, "out", x.device)
+    _check_workspace(workspace, x.device)
+    with _On(x.device) as on:
+        if out is None:
+            out = x.new_empty((m, n), dtype=dtype)
+        ws_bytes = size(m, n, k)
+        if workspace is None and ws_bytes > 0:
+            workspace = _workspace(ws_bytes, x.device)
+        rest = () if gated else (_at(residual), _ld_opt(residual))
+        _call(name, m, n, k, _at(x), _line_ld(x, k // 2), _at(scale_x), _line_ld(scale_x, k // 32),
+              _at(w), _line_ld(w, k // 2), _at(scale_w), _line_ld(scale_w, k // 32), _at(bias),
+              _act(act), *rest, kind, _at(out), _ld(out), _at(workspace),
+              0 if workspace is None else workspace.numel(), on.stream(stream, out, workspace))
+    return out
+
+
+def ozk_mxfp4_linear(x: torch.Tensor, scale_x: torch.Tensor, w: torch.Tensor,
+                     scale_w: torch.Tensor, bias: torch.Tensor | None = None, act="none",
+                     residual: torch.Tensor | None = None, dtype=torch.bfloat16,
+                     out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """C = act(X W^T + bias) + residual for m lines X and n lines W in MX FP4 (as
+    ozk_mxfp4_quant gives them); C, bias and residual in `dtype` (float32, float16 or bfloat16;
+    the type of `out` where that is given).  residual may be out."""
+    return _mx_product("ozk_mxfp4_linear", ozk_mxfp4_linear_workspace_size, False, x, scale_x, w,
+                       scale_w, bias, act, residual, dtype, out, workspace, stream)
+
+
+def ozk_mxfp4_gated(x: torch.Tensor, scale_x: torch.Tensor, w: torch.Tensor,
+                    scale_w: torch.Tensor, bias: torch.Tensor | None = None, act="silu",
+                    dtype=torch.bfloat16, out: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """C = act(X Wg^T + bias[:n]) * (X Wu^T + bias[n:]) for W = [Wg; Wu] of 2 n lines, in MX
+    FP4 as ozk_mxfp4_linear's operands."""
+    return _mx_product("ozk_mxfp4_gated", ozk_mxfp4_gated_workspace_size, True, x, scale_x, w,
+                       scale_w, bias, act, None, dtype, out, workspace, stream)
+
+
+# ------------------------------------------------------------ clipping to a norm
+def ozk_clip_norm_workspace_size(count: int) -> int:
+    return _layer_size("ozk_clip_norm_workspace_size", count)
+
+
+def ozk_clip_norm(tensors, max_norm: float, out=None, norm: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None):
+    """(N, outputs): the 2-norm N of all values of a list of contiguous tensors (float64,
+    float32, float16 or bfloat16, any shapes, one device) as a float64 tensor of no dimensions,
+    and the tensors times min(1, max_norm / N): in place, or in the tensors of `out`."""
+    tensors = list(tensors)
+    outs = tensors if out is None else list(out)
+    if not tensors:
+        raise ValueError("no tensors to clip")
+    if len(outs) != len(tensors):
+        raise ValueError(f"{len(tensors)} tensors, but {len(outs)} outputs")
+    first = tensors[0]
+    if not isinstance(first, torch.Tensor):
+        raise TypeError("tensors must be CUDA/HIP tensors")
+    index = first.get_device() if first.is_cuda else None
+    kinds = []
+    for group in ((tensors,) if outs is tensors else (tensors, outs)):
+        for t in group:
+            if not isinstance(t, torch.Tensor) or not t.is_cuda:
+                raise TypeError("tensors must be CUDA/HIP tensors")
+            if t.get_device() != index:
+                raise ValueError(f"a tensor is on {t.device}, expected {first.device}")
+            if not t.is_contiguous():
+                raise ValueError("tensors must be contiguous")
+    for t, o in zip(tensors, outs):
+        if o is not t and (o.dtype is not t.dtype or o.shape != t.shape):
+            raise ValueError(f"an output is {o.dtype} {tuple(o.shape)}, its tensor {t.dtype} "
+                             f"{tuple(t.shape)}")
+        kinds.append(_type(t.dtype))
+    _check_like(norm, (), torch.float64, "norm", first.device)
+    _check_workspace(workspace, first.device)
+    n = len(tensors)
+    xs = (_ptr * n)(*[t.data_ptr() for t in tensors])
+    ys = xs if outs is tensors else (_ptr * n)(*[t.data_ptr() for t in outs])
+    sizes = (_i64 * n)(*[t.numel() for t in tensors])
+    types = (_int * n)(*kinds)
+    with _On(first.device) as on:
+        if norm is None:
+            norm = first.new_empty((), dtype=torch.float64)
+        if workspace is None:
+            workspace = _workspace(ozk_clip_norm_workspace_size(n), first.device)
+        _call("ozk_clip_norm", n, xs, ys, sizes, types, float(max_norm), _at(norm),
+              _at(workspace), workspace.numel(), on.stream(stream, norm, workspace))
+    return norm, outs

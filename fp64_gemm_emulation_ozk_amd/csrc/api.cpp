@@ -2,6 +2,9 @@
 // workspace carving, and the stream-ordered launch sequence of each operation.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <new>
+
 #include "ozk_internal.h"
 
 using namespace ozk;
@@ -711,6 +714,7 @@ struct Product {
   const double* right;
   int64_t right_rows, right_cols, ldr;
   int right_axis;
+  int64_t least_np = 0;   // a row of residues holds as many at least
 };
 
 // Workspace of a product.  The rows of residues are padded to 64 so that every store of the
@@ -730,6 +734,7 @@ ProductLayout product_layout(const Product& P, int r) {
   ProductLayout L;
   L.kp = round_up(P.K, 2 * kPlaneK);
   L.np = round_up(P.cols, 64);
+  if (L.np < P.least_np) L.np = P.least_np;
   L.planes_l = (size_t)r * P.rows * L.kp;
   L.planes_r = ((size_t)r * P.cols + (L.np - P.cols)) * L.kp;
   L.residues = (size_t)r * P.rows * L.np;
@@ -751,10 +756,11 @@ struct Job {
   DgemmEpilogue E;
   double* out;
   int64_t ldo;
-  ProductLayout L;
-  int8_t *pl, *pr, *res;
-  int32_t *el, *er;
-  void *scr_l, *scr_r;
+  bool gated = false;   // out: P.cols / 2 columns
+  ProductLayout L{};
+  int8_t *pl = nullptr, *pr = nullptr, *res = nullptr;
+  int32_t *el = nullptr, *er = nullptr;
+  void *scr_l = nullptr, *scr_r = nullptr;
   void place(Carver& cv, int r) {
     L = product_layout(P, r);
     pl = static_cast<int8_t*>(cv.take(L.planes_l));
@@ -766,6 +772,9 @@ struct Job {
     scr_r = cv.take(L.scr_r);
   }
   int reconstruct(int r, hipStream_t s) const {
+    if (gated)
+      return launch_crt_gated(P.rows, P.cols / 2, r, res, L.np, P.rows * L.np, el, er, E, out, ldo,
+                              s);
     return launch_crt_epilogue(P.rows, P.cols, r, res, L.np, P.rows * L.np, el, er, E, out, ldo,
                                s);
   }
@@ -837,6 +846,15 @@ int run_jobs(Job* jobs, int count, int r, int scaling, void* workspace, hipStrea
 Product forward_product(int64_t m, int64_t n, int64_t k, const double* A, int64_t lda,
                         const double* B, int64_t ldb) {
   return {m, n, k, A, m, k, lda, 0, B, k, n, ldb, 1};
+}
+
+// The same for both projections of a gated block, B k x 2 n: the reconstruction reads whole groups
+// of 64 residues from column 0 and from column n on.
+Product gated_product(int64_t m, int64_t n, int64_t k, const double* A, int64_t lda,
+                      const double* B, int64_t ldb) {
+  Product P = forward_product(m, 2 * n, k, A, lda, B, ldb);
+  P.least_np = 2 * round_up(n, 64);
+  return P;
 }
 
 // dA = G B^T: rows of G against rows of B; dB = A^T G: columns of A against columns of G.
@@ -958,6 +976,86 @@ int ozk_dgemm_epilogue_grad(int64_t m, int64_t n, int64_t k, const double* dC, i
   return count ? run_jobs(jobs, count, r, scaling, products, s) : OZK_OK;
 }
 
+// ---------------------------------------------------------------- gated block in emulated fp64
+int ozk_dgemm_gated_workspace_size(int64_t m, int64_t n, int64_t k, int r, size_t* bytes) {
+  if (!bytes || m < 0 || n < 0 || k < 1 || check_r(r) != OZK_OK) return OZK_EINVAL;
+  if (k > OZK_MAX_K) return OZK_ERANGE;
+  if (n > (int64_t)1 << 40) return OZK_EUNSUPPORTED;
+  *bytes = product_layout(gated_product(m, n, k, nullptr, k, nullptr, 2 * n), r).total();
+  return OZK_OK;
+}
+
+int ozk_dgemm_gated(int64_t m, int64_t n, int64_t k, const double* A, int64_t lda, const double* B,
+                    int64_t ldb, const double* bias, int act, double* Z, int64_t ldz, double* C,
+                    int64_t ldc, int r, int scaling, void* workspace, size_t workspace_bytes,
+                    void* stream) {
+  if (check_r(r) != OZK_OK || !act_ok(act)) return OZK_EINVAL;
+  if (scaling != OZK_SCALING_MAX && scaling != OZK_SCALING_NORM) return OZK_EINVAL;
+  if (m < 0 || n < 0 || k < 1) return OZK_EINVAL;
+  if (k > OZK_MAX_K) return OZK_ERANGE;
+  if (n > (int64_t)1 << 40) return OZK_EUNSUPPORTED;
+  const int64_t n1 = n > 0 ? n : 1;
+  if (lda < k || ldb < 2 * n1 || ldc < n1 || (Z && ldz < 2 * n1)) return OZK_EINVAL;
+  int wa = 0, wb = 0;
+  int st = scaling_widths(scaling, r, k, &wa, &wb);
+  if (st != OZK_OK) return st;
+  if (m == 0 || n == 0) return OZK_OK;
+  if (!A || !B || !C) return OZK_EINVAL;
+  const Product P = gated_product(m, n, k, A, lda, B, ldb);
+  if (!workspace || workspace_bytes < product_layout(P, r).total()) return OZK_EWORKSPACE;
+  if (!aligned(workspace, 256)) return OZK_EINVAL;
+  if ((size_t)m * n > (size_t)0x3fffffffffffull) return OZK_EUNSUPPORTED;
+  Job job{P, {bias, nullptr, 0, Z, ldz, act}, C, ldc, true};
+  return run_jobs(&job, 1, r, scaling, workspace, as_stream(stream));
+}
+
+int ozk_dgemm_gated_grad_workspace_size(int64_t m, int64_t n, int64_t k, int r, size_t* bytes) {
+  if (n > OZK_MAX_K / 2) return bytes && m >= 0 && k >= 1 && check_r(r) == OZK_OK ? OZK_ERANGE
+                                                                                  : OZK_EINVAL;
+  return ozk_dgemm_epilogue_grad_workspace_size(m, 2 * n, k, r, bytes);
+}
+
+int ozk_dgemm_gated_grad(int64_t m, int64_t n, int64_t k, const double* dC, int64_t lddc,
+                         const double* A, int64_t lda, const double* B, int64_t ldb,
+                         const double* Z, int64_t ldz, int act, double* dA, int64_t ldda,
+                         double* dB, int64_t lddb, double* dbias, int r, int scaling,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  if (check_r(r) != OZK_OK || !act_ok(act)) return OZK_EINVAL;
+  if (scaling != OZK_SCALING_MAX && scaling != OZK_SCALING_NORM) return OZK_EINVAL;
+  if (m < 0 || n < 0 || k < 1) return OZK_EINVAL;
+  if (m > OZK_MAX_K || n > OZK_MAX_K / 2 || k > OZK_MAX_K) return OZK_ERANGE;
+  const int64_t n1 = n > 0 ? n : 1, w = 2 * n;
+  if (lddc < n1 || ldz < 2 * n1) return OZK_EINVAL;
+  if ((dA && (ldda < k || ldb < 2 * n1)) || (dB && (lddb < 2 * n1 || lda < k))) return OZK_EINVAL;
+  int wa = 0, wb = 0, st;
+  hipStream_t s = as_stream(stream);
+  if (m == 0 || n == 0) {   // sums of no terms
+    if (m > 0 && dA && (st = launch_zero_rows(dA, m, k, ldda, s))) return st;
+    if (n > 0 && dB && (st = launch_zero_rows(dB, k, w, lddb, s))) return st;
+    if (n > 0 && dbias && (st = launch_zero_rows(dbias, 1, w, w, s))) return st;
+    return OZK_OK;
+  }
+  if (dA && (st = scaling_widths(scaling, r, w, &wa, &wb))) return st;
+  if (dB && (st = scaling_widths(scaling, r, m, &wa, &wb))) return st;
+  if (!dA && !dB && !dbias) return OZK_OK;
+  if (!dC || !Z || (dA && !B) || (dB && !A)) return OZK_EINVAL;
+  const EpilogueGradLayout L = epilogue_grad_layout(m, w, k, r);
+  if (!workspace || workspace_bytes < L.total()) return OZK_EWORKSPACE;
+  if (!aligned(workspace, 256)) return OZK_EINVAL;
+  Carver cv(workspace);
+  double* g = static_cast<double*>(cv.take(L.g));
+  double* part = static_cast<double*>(cv.take(L.part));
+  void* products = cv.take(L.products);
+  if ((st = launch_gate_grad(m, n, dC, lddc, Z, ldz, act, dA || dB ? g : nullptr, part, dbias, s)))
+    return st;
+  const DgemmEpilogue none{nullptr, nullptr, 0, nullptr, 0, OZK_ACT_NONE};
+  Job jobs[2];
+  int count = 0;
+  if (dA) jobs[count++] = Job{grad_a(m, w, k, g, w, B, ldb), none, dA, ldda};
+  if (dB) jobs[count++] = Job{grad_b(m, w, k, A, lda, g, w), none, dB, lddb};
+  return count ? run_jobs(jobs, count, r, scaling, products, s) : OZK_OK;
+}
+
 // ---------------------------------------------------------------- int8 linear layer
 int ozk_int8linear_workspace_size(int64_t m, int64_t n, int64_t k, int aligned, size_t* bytes) {
   if (!bytes || m < 0 || n < 0 || k < 1 || (aligned != 0 && aligned != 1)) return OZK_EINVAL;
@@ -1063,6 +1161,177 @@ int ozk_layernorm_backward(int64_t rows, int64_t cols, int type, const void* dy,
   }
   return launch_layernorm_backward(rows, cols, type, dy, lddy, x, ldx, gamma, mean, rstd, dx,
                                    lddx, dgamma, dbeta, workspace, as_stream(stream));
+}
+
+// ---------------------------------------------------------------- MX FP4
+int64_t ozk_mxfp4_line_bytes(int64_t k) { return k > 0 ? (k + 255) / 256 * 128 : 0; }
+int64_t ozk_mxfp4_scale_bytes(int64_t k) { return k > 0 ? (k + 255) / 256 * 8 : 0; }
+
+// Lines of codes and scales over k values as the kernels read and write them.
+static bool lines_ok(int64_t k, const void* codes, int64_t ldq, const void* scales, int64_t lds) {
+  return codes && scales && aligned(codes, 16) && aligned(scales, 8) && ldq % 16 == 0 &&
+         lds % 8 == 0 && ldq >= ozk_mxfp4_line_bytes(k) && lds >= ozk_mxfp4_scale_bytes(k);
+}
+
+int ozk_mxfp4_quant(int64_t rows, int64_t cols, int type, const void* x, int64_t ldx, int axis,
+                    uint8_t* codes, int64_t ldq, uint8_t* scales, int64_t lds, void* stream) {
+  if (type < OZK_F64 || type > OZK_BF16 || (axis != 0 && axis != 1)) return OZK_EINVAL;
+  if (rows < 0 || cols < 0 || (axis ? rows : cols) < 1 || ldx < (cols > 0 ? cols : 1))
+    return OZK_EINVAL;
+  if (rows > 0x7fffffffll || cols > 0x7fffffffll) return OZK_EUNSUPPORTED;
+  if (rows == 0 || cols == 0) return OZK_OK;
+  if (!x || !aligned(x, type_size(type)) || !lines_ok(axis ? rows : cols, codes, ldq, scales, lds))
+    return OZK_EINVAL;
+  return launch_mxfp4_quant(rows, cols, type, x, ldx, axis, codes, ldq, scales, lds,
+                            as_stream(stream));
+}
+
+int ozk_mxfp4_values(int64_t lines, int64_t k, const uint8_t* codes, int64_t ldq,
+                     const uint8_t* scales, int64_t lds, int type, void* out, int64_t ldo,
+                     void* stream) {
+  if (type < OZK_F64 || type > OZK_BF16 || lines < 0 || k < 1 || ldo < k) return OZK_EINVAL;
+  if (lines > 0x7fffffffll || k > 0x7fffffffll) return OZK_EUNSUPPORTED;
+  if (lines == 0) return OZK_OK;
+  if (!out || !aligned(out, type_size(type)) || !lines_ok(k, codes, ldq, scales, lds))
+    return OZK_EINVAL;
+  return launch_mxfp4_values(lines, k, codes, ldq, scales, lds, type, out, ldo, as_stream(stream));
+}
+
+// The checks of both products that depend on sizes alone.
+static int check_mx(int64_t m, int64_t n, int64_t k) {
+  if (m < 0 || n < 0 || k < 1) return OZK_EINVAL;
+  if (k > OZK_MX_MAX_K) return OZK_ERANGE;
+  if (m > 0x7fffffffll || n > 0x3fffffffll) return OZK_EUNSUPPORTED;
+  return OZK_OK;
+}
+
+static int mx_workspace(int64_t m, int64_t n, int64_t k, bool gated, size_t* bytes) {
+  if (!bytes) return OZK_EINVAL;
+  const int st = check_mx(m, n, k);
+  if (st == OZK_OK) *bytes = m > 0 && n > 0 ? mxfp4_linear_workspace(m, n, k, gated) : 0;
+  return st;
+}
+
+static int mx_product(int64_t m, int64_t n, int64_t k, const uint8_t* X, int64_t ldx,
+                      const uint8_t* scale_x, int64_t ldsx, const uint8_t* W, int64_t ldw,
+                      const uint8_t* scale_w, int64_t ldsw, bool gated, const void* bias, int act,
+                      const void* residual, int64_t ldr, int type, void* C, int64_t ldc,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  if (!act_ok(act) || (type != OZK_F32 && type != OZK_F16 && type != OZK_BF16)) return OZK_EINVAL;
+  const int st = check_mx(m, n, k);
+  if (st != OZK_OK) return st;
+  const int64_t n1 = n > 0 ? n : 1;
+  if (ldc < n1 || (residual && ldr < n1)) return OZK_EINVAL;
+  if (m == 0 || n == 0) return OZK_OK;
+  const size_t e = type == OZK_F32 ? 4 : 2;
+  if (!lines_ok(k, X, ldx, scale_x, ldsx) || !lines_ok(k, W, ldw, scale_w, ldsw) || !C ||
+      !aligned(bias, e) || !aligned(residual, e) || !aligned(C, e))
+    return OZK_EINVAL;
+  // a lane's offset within a tile is 32 bits
+  const int64_t far = 1 << 24;
+  if (ldx >= far || ldw >= far || ldsx >= far || ldsw >= far) return OZK_EUNSUPPORTED;
+  const size_t need = mxfp4_linear_workspace(m, n, k, gated);
+  if (need > workspace_bytes || (need > 0 && !workspace)) return OZK_EWORKSPACE;
+  if (need > 0 && !aligned(workspace, 256)) return OZK_EINVAL;
+  return launch_mxfp4_linear(m, n, k, X, ldx, scale_x, ldsx, W, ldw, scale_w, ldsw, gated, bias,
+                             act, residual, ldr, type, C, ldc, workspace, as_stream(stream));
+}
+
+int ozk_mxfp4_linear_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
+  return mx_workspace(m, n, k, false, bytes);
+}
+
+int ozk_mxfp4_linear(int64_t m, int64_t n, int64_t k, const uint8_t* X, int64_t ldx,
+                     const uint8_t* scale_x, int64_t ldsx, const uint8_t* W, int64_t ldw,
+                     const uint8_t* scale_w, int64_t ldsw, const void* bias, int act,
+                     const void* residual, int64_t ldr, int type, void* C, int64_t ldc,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  return mx_product(m, n, k, X, ldx, scale_x, ldsx, W, ldw, scale_w, ldsw, false, bias, act,
+                    residual, ldr, type, C, ldc, workspace, workspace_bytes, stream);
+}
+
+int ozk_mxfp4_gated_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
+  return mx_workspace(m, n, k, true, bytes);
+}
+
+int ozk_mxfp4_gated(int64_t m, int64_t n, int64_t k, const uint8_t* X, int64_t ldx,
+                    const uint8_t* scale_x, int64_t ldsx, const uint8_t* W, int64_t ldw,
+                    const uint8_t* scale_w, int64_t ldsw, const void* bias, int act, int type,
+                    void* C, int64_t ldc, void* workspace, size_t workspace_bytes, void* stream) {
+  return mx_product(m, n, k, X, ldx, scale_x, ldsx, W, ldw, scale_w, ldsw, true, bias, act, nullptr,
+                    0, type, C, ldc, workspace, workspace_bytes, stream);
+}
+
+// ---------------------------------------------------------------- clipping
+int ozk_clip_norm_workspace_size(int64_t count, size_t* bytes) {
+  if (!bytes || count < 0) return OZK_EINVAL;
+  if (count > 0x7fffff) return OZK_EUNSUPPORTED;
+  *bytes = clip_norm_workspace(count);
+  return OZK_OK;
+}
+
+namespace {
+struct Span {
+  uintptr_t from, to;
+  int64_t tensor;
+  bool operator<(const Span& o) const { return from < o.from; }
+};
+
+// Whether an output overlaps another, or an input other than the one it is.
+bool clip_overlaps(int64_t count, const void* const* x, void* const* out, const int64_t* sizes,
+                   const int* types, Span* spans) {
+  int64_t n = 0;
+  for (int64_t i = 0; i < count; ++i)
+    if (sizes[i] > 0) {
+      const uintptr_t p = reinterpret_cast<uintptr_t>(out[i]);
+      spans[n++] = {p, p + sizes[i] * type_size(types[i]), i};
+    }
+  std::sort(spans, spans + n);
+  for (int64_t i = 1; i < n; ++i)
+    if (spans[i].from < spans[i - 1].to) return true;
+  for (int64_t i = 0; i < count; ++i) {
+    if (sizes[i] == 0) continue;
+    const uintptr_t p = reinterpret_cast<uintptr_t>(x[i]), e = p + sizes[i] * type_size(types[i]);
+    // the first output that ends past p (they are in order and apart)
+    const Span* s = std::lower_bound(spans, spans + n, p,
+                                     [](const Span& a, uintptr_t v) { return a.to <= v; });
+    for (; s < spans + n && s->from < e; ++s)
+      if (s->tensor != i || s->from != p) return true;
+  }
+  return false;
+}
+}  // namespace
+
+int ozk_clip_norm(int64_t count, const void* const* x, void* const* out, const int64_t* sizes,
+                  const int* types, double max_norm, double* norm, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  if (count < 0 || !(max_norm >= 0.0) || !norm || !aligned(norm, 8)) return OZK_EINVAL;
+  if (count > 0x7fffff) return OZK_EUNSUPPORTED;
+  if (count > 0 && (!x || !out || !sizes || !types)) return OZK_EINVAL;
+  int64_t bytes = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (types[i] < OZK_F64 || types[i] > OZK_BF16 || sizes[i] < 0) return OZK_EINVAL;
+    if (sizes[i] == 0) continue;
+    const size_t e = type_size(types[i]);
+    if (!x[i] || !out[i] || !aligned(x[i], e) || !aligned(out[i], e)) return OZK_EINVAL;
+    // chunks are counted in 32 bits
+    if (sizes[i] > ((int64_t)1 << 44) / (int64_t)e) return OZK_EUNSUPPORTED;
+    bytes += sizes[i] * e + 32768;
+    if (bytes > (int64_t)1 << 45) return OZK_EUNSUPPORTED;
+  }
+  const size_t need = clip_norm_workspace(count);
+  if (need > workspace_bytes || (need > 0 && !workspace)) return OZK_EWORKSPACE;
+  if (need > 0 && !aligned(workspace, 256)) return OZK_EINVAL;
+  if (count > 0) {
+    Span few[64];
+    Span* spans = count <= 64 ? few : new (std::nothrow) Span[count];
+    if (!spans) return OZK_EUNSUPPORTED;
+    const bool bad = clip_overlaps(count, x, out, sizes, types, spans);
+    if (spans != few) delete[] spans;
+    if (bad) return OZK_EINVAL;
+  }
+  return launch_clip_norm(count, x, out, sizes, types, max_norm, norm, workspace,
+                          as_stream(stream));
 }
 
 }  // extern "C"

@@ -355,7 +355,9 @@ struct WordLoads {
   uint32_t w[2][kND];
 };
 
-template <int R>
+typedef uint32_t word_any __attribute__((aligned(1)));   // a word at any address
+
+template <int R, typename Word = uint32_t>
 __device__ __forceinline__ void load_words(const int8_t* __restrict__ src, int64_t stride_r,
                                            int half, int t, int u, WordLoads<R>& raw) {
   using S = CrtShape<R>;
@@ -367,7 +369,7 @@ __device__ __forceinline__ void load_words(const int8_t* __restrict__ src, int64
       const int l0 = half * S::kH + slot;
       const bool ok = slot < S::kH && l0 < R;
       const int l = ok ? l0 : R - 1;
-      const uint32_t x = *reinterpret_cast<const uint32_t*>(src + l * stride_r + 32 * k + 4 * t);
+      const uint32_t x = *reinterpret_cast<const Word*>(src + l * stride_r + 32 * k + 4 * t);
       raw.w[k][d] = ok ? x : 0u;
     }
 }
@@ -388,6 +390,41 @@ __device__ __forceinline__ void transpose_words(const WordLoads<R>& raw, uint32_
     }
   b1v = v4i{(int)w[0][0], (int)w[0][1], (int)w[0][2], (int)w[0][3]};
   b2v = v4i{(int)w[1][0], (int)w[1][1], (int)w[1][2], (int)w[1][3]};
+}
+
+// The limbs of 64 outputs' integers X, lane i those of output i, from their B operands.
+template <int R>
+__device__ __forceinline__ void lift_limbs(const v4i& a_op, const v4i& b1v, const v4i& b2v,
+                                           const double (&m_limb)[4], double (&x)[4]) {
+  using S = CrtShape<R>;
+  const v16i zero = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+  const v16i d1 = __builtin_amdgcn_mfma_i32_32x32x32_i8(a_op, b1v, zero, 0, 0, 0);
+  const v16i d2 = __builtin_amdgcn_mfma_i32_32x32x32_i8(a_op, b2v, zero, 0, 0, 0);
+  int sum[S::kRows];
+#pragma unroll
+  for (int v = 0; v < S::kSwaps; ++v) {
+    const auto sw = __builtin_amdgcn_permlane32_swap((unsigned)d1[v], (unsigned)d2[v], false,
+                                                     false);
+    const int row_a = 8 * (v / 4) + v % 4;      // rows of the first register
+    if (row_a < S::kRows) sum[row_a] = (int)sw[0];
+    if (row_a + 4 < S::kRows) sum[row_a + 4] = (int)sw[1];
+  }
+  // q from the F rows, then X in 2^40 limbs.
+  // Adjacent digit sums are first combined in int32 (|S_b + 256 S_b+1| < 2^27), which
+  // halves the conversions to fp64.
+  const int f01 = sum[S::kNE] + 256 * sum[S::kNE + 1];
+  const int f23 = sum[S::kNE + 2] + 256 * sum[S::kNE + 3];
+  const double tq = __builtin_fma((double)f23, 0x1p16, (double)f01);
+  const double q = __builtin_rint(tq * 0x1p-24);
+#pragma unroll
+  for (int p = 0; p < 4; ++p) x[p] = p < S::kL ? -q * m_limb[p] : 0.0;   // |q| < 2^11.4: exact
+#pragma unroll
+  for (int b = 0; b < S::kNE; ++b) {
+    const int pos = b % 5;           // digit position inside its 2^40 limb
+    if (pos == 1 || pos == 3) continue;  // folded into the digit below
+    const int v = (pos != 4 && b + 1 < S::kNE) ? sum[b] + 256 * sum[b + 1] : sum[b];
+    x[b / 5] = __builtin_fma((double)v, (double)(1ll << (8 * pos)), x[b / 5]);
+  }
 }
 
 // Persistent waves: each takes groups of 64 consecutive outputs of one row, lane i
@@ -424,35 +461,8 @@ __device__ __forceinline__ void crt_outputs(int64_t m, int64_t n, int64_t nl,
   auto finish_group = [&](int64_t i, int64_t j0, const v4i& b1v, const v4i& b2v) {
     const int64_t j = j0 + lane;
     const auto asked = put.ask(i, j < n ? j : n - 1);
-    const v16i zero = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-    const v16i d1 = __builtin_amdgcn_mfma_i32_32x32x32_i8(a_op, b1v, zero, 0, 0, 0);
-    const v16i d2 = __builtin_amdgcn_mfma_i32_32x32x32_i8(a_op, b2v, zero, 0, 0, 0);
-    int sum[S::kRows];
-#pragma unroll
-    for (int v = 0; v < S::kSwaps; ++v) {
-      const auto sw = __builtin_amdgcn_permlane32_swap((unsigned)d1[v], (unsigned)d2[v], false,
-                                                       false);
-      const int row_a = 8 * (v / 4) + v % 4;      // rows of the first register
-      if (row_a < S::kRows) sum[row_a] = (int)sw[0];
-      if (row_a + 4 < S::kRows) sum[row_a + 4] = (int)sw[1];
-    }
-    // q from the F rows, then X in 2^40 limbs.
-    // Adjacent digit sums are first combined in int32 (|S_b + 256 S_b+1| < 2^27), which
-    // halves the conversions to fp64.
-    const int f01 = sum[S::kNE] + 256 * sum[S::kNE + 1];
-    const int f23 = sum[S::kNE + 2] + 256 * sum[S::kNE + 3];
-    const double tq = __builtin_fma((double)f23, 0x1p16, (double)f01);
-    const double q = __builtin_rint(tq * 0x1p-24);
-    double x[4] = {0.0, 0.0, 0.0, 0.0};
-#pragma unroll
-    for (int p = 0; p < S::kL; ++p) x[p] = -q * m_limb[p];   // |q| < 2^11.4: exact
-#pragma unroll
-    for (int b = 0; b < S::kNE; ++b) {
-      const int pos = b % 5;           // digit position inside its 2^40 limb
-      if (pos == 1 || pos == 3) continue;  // folded into the digit below
-      const int v = (pos != 4 && b + 1 < S::kNE) ? sum[b] + 256 * sum[b + 1] : sum[b];
-      x[b / 5] = __builtin_fma((double)v, (double)(1ll << (8 * pos)), x[b / 5]);
-    }
+    double x[4];
+    lift_limbs<R>(a_op, b1v, b2v, m_limb, x);
     if (j < n) {
       const int32_t e_i = ea[i], f_j = eb[j];
       const bool nan = e_i == INT32_MIN || f_j == INT32_MIN;

@@ -254,6 +254,11 @@ int64_t act_grad_chunks(int64_t m) {
   return (m + rows - 1) / rows;
 }
 
+void launch_column_join(int64_t n, int chunks, const double* part, double* out, hipStream_t s) {
+  hipLaunchKernelGGL(column_join_kernel, dim3((unsigned)((n + 15) / 16)), dim3(256), 0, s, n,
+                     chunks, part, out);
+}
+
 int launch_act_grad(int64_t m, int64_t n, const double* dc, int64_t lddc, const double* z,
                     int64_t ldz, int act, double* g, double* part, double* dbias,
                     hipStream_t s) {
@@ -266,9 +271,7 @@ int launch_act_grad(int64_t m, int64_t n, const double* dc, int64_t lddc, const 
   hipLaunchKernelGGL(act_grad_kernel, dim3((unsigned)((n + 255) / 256), (unsigned)chunks),
                      dim3(256), 0, s, m, n, chunk, dc, lddc, z, ldz, act, g,
                      dbias ? part : nullptr);
-  if (dbias)
-    hipLaunchKernelGGL(column_join_kernel, dim3((unsigned)((n + 15) / 16)), dim3(256), 0, s, n,
-                       (int)chunks, part, dbias);
+  if (dbias) launch_column_join(n, (int)chunks, part, dbias, s);
   return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
 }
 

@@ -1,0 +1,388 @@
+// Lines in microscaled 4-bit floating point (OCP MX FP4: e2m1 codes, an e8m0 scale for every 32
+// values along K), written from a matrix's rows or columns and read back.
+//
+// A block's scale is 2^E, E = floor(log2 max |x|) - 2 held to [-127, 127], stored as E + 127: only
+// the exponent field of the largest magnitude is needed, which a maximum over the magnitudes' bits
+// finds.  A code is RNE(x 2^-E) on {0, 0.5, 1, 1.5, 2, 3, 4, 6}, 6 beyond, which gfx950's
+// conversions to FP4 compute with the scale as their operand.
+#include "ozk_internal.h"
+#include "rows.h"
+
+namespace ozk {
+namespace {
+
+typedef bf16_t v2bf __attribute__((ext_vector_type(2)));
+typedef f16_t v2h __attribute__((ext_vector_type(2)));
+
+constexpr uint32_t kNoScale = 255;   // NaN: a block with Inf or NaN, or past 2^127
+
+// Bits of |x| that compare as the magnitudes do (of a double: the word with its exponent).
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+__device__ __forceinline__ uint32_t magnitude(bf16_t x) {
+  return __builtin_bit_cast(uint16_t, x) & 0x7fffu;
+}
+__device__ __forceinline__ uint32_t magnitude(f16_t x) {
+  return __builtin_bit_cast(uint16_t, x) & 0x7fffu;
+}
+__device__ __forceinline__ uint32_t magnitude(double x) {
+  return (uint32_t)((uint64_t)__double_as_longlong(x) >> 32) & 0x7fffffffu;
+}
+
+// The scale byte of a block from its largest magnitude.  A subnormal fp32 maximum has E below
+// -127 in any case; a subnormal fp16 one is a normal fp32 value.
+template <typename T>
+__device__ __forceinline__ uint32_t scale_of(uint32_t most) {
+  if constexpr (sizeof(T) == 8) {
+    const int e = (int)(most >> 20) - 898;   // 1023 + 2 - 127
+    return e < 0 ? 0u : (e > 254 ? kNoScale : (uint32_t)e);
+  } else {
+    uint32_t field;
+    if constexpr (__is_same(T, f16_t))
+      field = __float_as_uint((float)__builtin_bit_cast(f16_t, (uint16_t)most)) >> 23;
+    else
+      field = most >> (sizeof(T) == 4 ? 23 : 7);
+    return field == 255 ? kNoScale : (field > 2 ? field - 2 : 0u);
+  }
+}
+
+// What the conversions take as 2^E: a float of that value (2^-127 is a subnormal one).
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  return __uint_as_float(byte ? byte << 23 : 0x00400000u);
+}
+
+// A double as a float that rounds to the same code: |x| 2^(20 - E) cut to an integer below 2^23,
+// its last bit set where something was cut off (no code's border lies between), so scale 2^20.
+__device__ __forceinline__ float short_of(double x, int e) {
+  const double v = __builtin_ldexp(__builtin_fabs(x), 20 - e);
+  uint32_t i = (uint32_t)v;
+  i |= (double)i != v ? 1u : 0u;
+  const float f = (float)i;
+  return (uint64_t)__double_as_longlong(x) >> 63 ? -f : f;
+}
+
+// Byte kB of `codes` becomes the codes of a (low nibble) and b.
+template <int kB, typename T>
+__device__ __forceinline__ uint32_t put_pair(uint32_t codes, T a, T b, uint32_t byte) {
+  if constexpr (sizeof(T) == 8) {
+    const int e = (int)byte - 127;
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, short_of(a, e), short_of(b, e), 0x1p20f,
+                                                    kB);
+  } else {
+    const float s = scale_value(byte);
+    if constexpr (sizeof(T) == 4)
+      return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, a, b, s, kB);
+    else if constexpr (__is_same(T, bf16_t))
+      return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(codes, v2bf{a, b}, s, kB);
+    else
+      return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(codes, v2h{a, b}, s, kB);
+  }
+}
+
+// Eight codes; those of a block without a scale are 0.
+template <typename T>
+__device__ __forceinline__ uint32_t put_eight(const T (&v)[8], uint32_t byte) {
+  uint32_t c = put_pair<0>(0u, v[0], v[1], byte);
+  c = put_pair<1>(c, v[2], v[3], byte);
+  c = put_pair<2>(c, v[4], v[5], byte);
+  c = put_pair<3>(c, v[6], v[7], byte);
+  return byte == kNoScale ? 0u : c;
+}
+
+// Values c .. c + 7 of a row, zero past its end.
+template <typename T>
+__device__ __forceinline__ void load_eight(const T* p, int64_t c, int64_t cols, T (&v)[8]) {
+  constexpr int N = Vec<T>::N;
+  if (c + 8 <= cols) {
+#pragma unroll
+    for (int q = 0; q < 8 / N; ++q) {
+      const typename Vec<T>::type w =
+          *reinterpret_cast<const typename Vec<T>::type*>(p + c + q * N);
+#pragma unroll
+      for (int u = 0; u < N; ++u) v[q * N + u] = w[u];
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = c + u < cols ? p[c + u] : (T)0.0f;
+  }
+}
+
+// A half wave's place: unit u (256 values of a line) of a matrix of `steps` units a line.
+struct Unit {
+  uint32_t line, step;
+  __device__ __forceinline__ Unit(uint32_t u, uint32_t steps)
+      : line(u / steps), step(u - line * steps) {}
+  __device__ __forceinline__ void two_on(uint32_t steps) {
+    step += 2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (step >= steps) {
+        step -= steps;
+        ++line;
+      }
+  }
+};
+
+constexpr int kUnits = 8;   // units of a wave, two at a time
+
+// Rows: lane l of a half wave takes values 8 l .. 8 l + 7 of its unit, four lanes a block.
+template <typename T>
+__global__ __launch_bounds__(256) void mxfp4_rows_kernel(uint32_t rows, int64_t cols,
+                                                         uint32_t steps, const T* __restrict__ x,
+                                                         int64_t ldx, uint8_t* __restrict__ codes,
+                                                         int64_t ldq, uint8_t* __restrict__ scales,
+                                                         int64_t lds) {
+  const int lane = threadIdx.x & 63, sub = lane & 31;
+  const uint32_t wave = blockIdx.x * 4 + (threadIdx.x >> 6);
+  Unit at(wave * kUnits + (lane >> 5), steps);
+  T v[kUnits / 2][8];
+  Unit first = at;
+#pragma unroll
+  for (int i = 0; i < kUnits / 2; ++i) {
+    if (at.line < rows)
+      load_eight(x + (int64_t)at.line * ldx, (int64_t)at.step * 256 + 8 * sub, cols, v[i]);
+    at.two_on(steps);
+  }
+  at = first;
+#pragma unroll
+  for (int i = 0; i < kUnits / 2; ++i) {
+    uint32_t most = 0;
+    if (at.line < rows) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const uint32_t a = magnitude(v[i][u]);
+        most = a > most ? a : most;
+      }
+    }
+    uint32_t o = dpp_mov<0xb1>(most);
+    most = o > most ? o : most;
+    o = dpp_mov<0x4e>(most);
+    most = o > most ? o : most;
+    const uint32_t byte = scale_of<T>(most);
+    if (at.line < rows) {
+      *reinterpret_cast<uint32_t*>(codes + (int64_t)at.line * ldq + (int64_t)at.step * 128 +
+                                   4 * sub) = put_eight(v[i], byte);
+      if ((sub & 3) == 0)
+        scales[(int64_t)at.line * lds + (int64_t)at.step * 8 + (sub >> 2)] = (uint8_t)byte;
+    }
+    at.two_on(steps);
+  }
+}
+
+// Columns: a workgroup takes 256 rows x 64 kC columns, wave w its rows 32 w .. 32 w + 31, which
+// are one block of each of a lane's kC columns (two of 16 bits: a row's load is 256 bytes).  The
+// codes meet in LDS, so that a line's 128 bytes leave in one store of eight lanes; a line's eight
+// chunks are XORed with the line's number there, for the banks.
+template <typename T, int kC>
+__global__ __launch_bounds__(512) void mxfp4_cols_kernel(int64_t rows, int64_t cols,
+                                                         uint32_t tiles,
+                                                         const T* __restrict__ x, int64_t ldx,
+                                                         uint8_t* __restrict__ codes, int64_t ldq,
+                                                         uint8_t* __restrict__ scales, int64_t lds) {
+  typedef T V __attribute__((ext_vector_type(kC), aligned(sizeof(T))));
+  constexpr int kLines = 64 * kC;
+  __shared__ uint4 box[kLines * 8];
+  __shared__ uint8_t sbox[kLines][8];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const uint32_t id = blockIdx.x, step = id / tiles;
+  const int64_t col0 = (int64_t)(id - step * tiles) * kLines, row0 = (int64_t)step * 256 + 32 * w;
+  const int64_t c = col0 + kC * lane;
+  const bool whole = c + kC <= cols;
+  T v[kC][32];
+#pragma unroll
+  for (int r = 0; r < 32; ++r) {
+#pragma unroll
+    for (int u = 0; u < kC; ++u) v[u][r] = (T)0.0f;
+    if (row0 + r < rows) {
+      const T* p = x + (row0 + r) * ldx + c;
+      if constexpr (kC == 1) {
+        if (whole) v[0][r] = *p;
+      } else {
+        if (whole) {
+          const V q = *reinterpret_cast<const V*>(p);
+#pragma unroll
+          for (int u = 0; u < kC; ++u) v[u][r] = q[u];
+        } else if (c < cols) {
+          v[0][r] = *p;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kC; ++u) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+      const uint32_t a = magnitude(v[u][r]);
+      most = a > most ? a : most;
+    }
+    const uint32_t byte = scale_of<T>(most);
+    uint32_t q[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      T part[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) part[r] = v[u][8 * e + r];
+      q[e] = put_eight(part, byte);
+    }
+    const int line = kC * lane + u;
+    box[line * 8 + (w ^ (line & 7))] = uint4{q[0], q[1], q[2], q[3]};
+    sbox[line][w] = (uint8_t)byte;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kC; ++i) {
+    const int line = 64 * i + (threadIdx.x >> 3), slot = threadIdx.x & 7;
+    if (col0 + line < cols)
+      *reinterpret_cast<uint4*>(codes + (col0 + line) * ldq + (int64_t)step * 128 +
+                                16 * (slot ^ (line & 7))) = box[line * 8 + slot];
+  }
+  if (threadIdx.x < kLines && col0 + threadIdx.x < cols)
+    *reinterpret_cast<uint2*>(scales + (col0 + threadIdx.x) * lds + (int64_t)step * 8) =
+        *reinterpret_cast<const uint2*>(sbox[threadIdx.x]);
+}
+
+// Eight values of the dword `c` of codes, NaN without a scale.  fp32 holds them but for the largest
+// (6 x 2^127 is Inf there), fp64 all of them.
+template <typename A>
+__device__ __forceinline__ void take_eight(uint32_t c, uint32_t byte, A (&v)[8]) {
+  const float s = sizeof(A) == 8 ? 1.0f : scale_value(byte);
+  const auto a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0);
+  const auto b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1);
+  const auto d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2);
+  const auto e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3);
+  const float w[8] = {a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    v[u] = byte == kNoScale ? __builtin_nanf("") : w[u];
+    if constexpr (sizeof(A) == 8)
+      v[u] *= __longlong_as_double((long long)(byte + 896) << 52);   // 2^(byte - 127)
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void mxfp4_values_kernel(uint32_t lines, int64_t k,
+                                                           uint32_t steps,
+                                                           const uint8_t* __restrict__ codes,
+                                                           int64_t ldq,
+                                                           const uint8_t* __restrict__ scales,
+                                                           int64_t lds, T* __restrict__ out,
+                                                           int64_t ldo) {
+  const int lane = threadIdx.x & 63, sub = lane & 31;
+  const uint32_t wave = blockIdx.x * 4 + (threadIdx.x >> 6);
+  Unit at(wave * kUnits + (lane >> 5), steps);
+  uint32_t c[kUnits / 2], s[kUnits / 2];
+  Unit first = at;
+#pragma unroll
+  for (int i = 0; i < kUnits / 2; ++i) {
+    if (at.line < lines) {
+      c[i] = *reinterpret_cast<const uint32_t*>(codes + (int64_t)at.line * ldq +
+                                                (int64_t)at.step * 128 + 4 * sub);
+      s[i] = scales[(int64_t)at.line * lds + (int64_t)at.step * 8 + (sub >> 2)];
+    }
+    at.two_on(steps);
+  }
+  at = first;
+  constexpr int N = Vec<T>::N;
+#pragma unroll
+  for (int i = 0; i < kUnits / 2; ++i) {
+    if (at.line < lines) {
+      typename AccOf<T>::type v[8];
+      take_eight(c[i], s[i], v);
+      const int64_t h = (int64_t)at.step * 256 + 8 * sub;
+#pragma unroll
+      for (int q = 0; q < 8 / N; ++q) {
+        typename AccOf<T>::type part[N];
+#pragma unroll
+        for (int u = 0; u < N; ++u) part[u] = v[q * N + u];
+        store_vec(out + (int64_t)at.line * ldo, h + q * N, k, part);
+      }
+    }
+    at.two_on(steps);
+  }
+}
+
+// Lines of a launch: fewer than 2^32 threads, units in 32 bits.
+int64_t lines_at_once(int64_t steps) {
+  const int64_t most = (int64_t)1 << 26;
+  return steps < most ? most / steps : 1;
+}
+
+inline unsigned unit_blocks(int64_t lines, int64_t steps) {
+  return (unsigned)((lines * steps + 4 * kUnits - 1) / (4 * kUnits));
+}
+
+template <typename T>
+int quant_t(int64_t rows, int64_t cols, const T* x, int64_t ldx, int axis, uint8_t* codes,
+            int64_t ldq, uint8_t* scales, int64_t lds, hipStream_t s) {
+  const int64_t k = axis ? rows : cols, steps = (k + 255) / 256;
+  if (axis == 0) {
+    const int64_t most = lines_at_once(steps);
+    for (int64_t r = 0; r < rows; r += most) {
+      const int64_t some = rows - r < most ? rows - r : most;
+      hipLaunchKernelGGL((mxfp4_rows_kernel<T>), dim3(unit_blocks(some, steps)), dim3(256), 0, s,
+                         (uint32_t)some, cols, (uint32_t)steps, x + r * ldx, ldx, codes + r * ldq,
+                         ldq, scales + r * lds, lds);
+    }
+  } else {
+    constexpr int kC = sizeof(T) == 2 ? 2 : 1;
+    const int64_t tiles = (cols + 64 * kC - 1) / (64 * kC), most = 1 << 22;
+    // ids are 32 bits: lines past that many tiles go in launches of their own
+    for (int64_t t0 = 0; t0 < tiles; t0 += most) {
+      const int64_t nt = tiles - t0 < most ? tiles - t0 : most;
+      const int64_t c0 = t0 * 64 * kC, nc = cols - c0 < nt * 64 * kC ? cols - c0 : nt * 64 * kC;
+      for (int64_t st0 = 0; st0 < steps; st0 += most / nt) {
+        const int64_t ns = steps - st0 < most / nt ? steps - st0 : most / nt;
+        hipLaunchKernelGGL((mxfp4_cols_kernel<T, kC>), dim3((unsigned)(nt * ns)), dim3(512), 0, s,
+                           rows - st0 * 256, nc, (uint32_t)nt, x + st0 * 256 * ldx + c0, ldx,
+                           codes + c0 * ldq + st0 * 128, ldq, scales + c0 * lds + st0 * 8, lds);
+      }
+    }
+  }
+  return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
+}
+
+template <typename T>
+int values_t(int64_t lines, int64_t k, const uint8_t* codes, int64_t ldq, const uint8_t* scales,
+             int64_t lds, T* out, int64_t ldo, hipStream_t s) {
+  const int64_t steps = (k + 255) / 256, most = lines_at_once(steps);
+  for (int64_t r = 0; r < lines; r += most) {
+    const int64_t some = lines - r < most ? lines - r : most;
+    hipLaunchKernelGGL((mxfp4_values_kernel<T>), dim3(unit_blocks(some, steps)), dim3(256), 0, s,
+                       (uint32_t)some, k, (uint32_t)steps, codes + r * ldq, ldq, scales + r * lds,
+                       lds, out + r * ldo, ldo);
+  }
+  return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
+}
+
+}  // namespace
+
+int launch_mxfp4_quant(int64_t rows, int64_t cols, int type, const void* x, int64_t ldx, int axis,
+                       uint8_t* codes, int64_t ldq, uint8_t* scales, int64_t lds, hipStream_t s) {
+  switch (type) {
+    case OZK_F64:
+      return quant_t(rows, cols, (const double*)x, ldx, axis, codes, ldq, scales, lds, s);
+    case OZK_F32:
+      return quant_t(rows, cols, (const float*)x, ldx, axis, codes, ldq, scales, lds, s);
+    case OZK_F16:
+      return quant_t(rows, cols, (const f16_t*)x, ldx, axis, codes, ldq, scales, lds, s);
+    default:
+      return quant_t(rows, cols, (const bf16_t*)x, ldx, axis, codes, ldq, scales, lds, s);
+  }
+}
+
+int launch_mxfp4_values(int64_t lines, int64_t k, const uint8_t* codes, int64_t ldq,
+                        const uint8_t* scales, int64_t lds, int type, void* out, int64_t ldo,
+                        hipStream_t s) {
+  switch (type) {
+    case OZK_F64:
+      return values_t(lines, k, codes, ldq, scales, lds, (double*)out, ldo, s);
+    case OZK_F32:
+      return values_t(lines, k, codes, ldq, scales, lds, (float*)out, ldo, s);
+    case OZK_F16:
+      return values_t(lines, k, codes, ldq, scales, lds, (f16_t*)out, ldo, s);
+    default:
+      return values_t(lines, k, codes, ldq, scales, lds, (bf16_t*)out, ldo, s);
+  }
+}
+
+}  // namespace ozk

@@ -180,7 +180,19 @@ struct DgemmEpilogue {
 int launch_crt_epilogue(int64_t m, int64_t n, int r, const int8_t* res, int64_t ldr,
                         int64_t stride_r, const int32_t* ea, const int32_t* eb,
                         const DgemmEpilogue& E, double* c, int64_t ldc, hipStream_t s);
-// Its gradient's elementwise part: g (m x n, ld n, or null) = dc * act'(z), dbias (or null) =
+// The gated form: residues of m x 2 n products, those of the gate's projection before those of
+// the other; a row's ldr, at least n + round_up(n, 64), may all be read.  z (m x 2 n) = the products
+// + bias (2 n), c = act(z's first half) * its second.  E.residual is null.
+int launch_crt_gated(int64_t m, int64_t n, int r, const int8_t* res, int64_t ldr, int64_t stride_r,
+                     const int32_t* ea, const int32_t* eb, const DgemmEpilogue& E, double* c,
+                     int64_t ldc, hipStream_t s);
+// out[c] = the sums of column c of `chunks` rows of n partial sums, in a fixed order.
+void launch_column_join(int64_t n, int chunks, const double* part, double* out, hipStream_t s);
+// And its gradient's elementwise part: g (m x 2 n, ld 2 n, or null) and its column sums dbias (2 n,
+// or null) through part, act_grad_chunks(m) x 2 n sums.
+int launch_gate_grad(int64_t m, int64_t n, const double* dc, int64_t lddc, const double* z,
+                     int64_t ldz, int act, double* g, double* part, double* dbias, hipStream_t s);
+// The gradient's elementwise part without a gate: g (m x n, ld n, or null) = dc * act'(z), dbias (or null) =
 // column sums of g through part, act_grad_chunks(m) x n sums.
 int64_t act_grad_chunks(int64_t m);
 int launch_act_grad(int64_t m, int64_t n, const double* dc, int64_t lddc, const double* z,
@@ -229,6 +241,27 @@ int launch_int8linear(int64_t m, int64_t n, int64_t k, const int8_t* x, int64_t 
                       const float* sx, const int8_t* w, int64_t ldw, const float* sw,
                       const void* bias, int act, const void* residual, int64_t ldr, int type,
                       void* c, int64_t ldc, void* workspace, hipStream_t s);
+
+// Lines of MX FP4 codes (mxfp4_codes.hip) and the products on them (mxfp4_linear.hip); workspace:
+// mxfp4_linear_workspace(m, n, k, gated) bytes.  gated: w has 2 n lines, bias 2 n entries.
+int launch_mxfp4_quant(int64_t rows, int64_t cols, int type, const void* x, int64_t ldx, int axis,
+                       uint8_t* codes, int64_t ldq, uint8_t* scales, int64_t lds, hipStream_t s);
+int launch_mxfp4_values(int64_t lines, int64_t k, const uint8_t* codes, int64_t ldq,
+                        const uint8_t* scales, int64_t lds, int type, void* out, int64_t ldo,
+                        hipStream_t s);
+size_t mxfp4_linear_workspace(int64_t m, int64_t n, int64_t k, bool gated);
+int launch_mxfp4_linear(int64_t m, int64_t n, int64_t k, const uint8_t* x, int64_t ldx,
+                        const uint8_t* xs, int64_t ldxs, const uint8_t* w, int64_t ldw,
+                        const uint8_t* ws, int64_t ldws, bool gated, const void* bias, int act,
+                        const void* residual, int64_t ldr, int type, void* c, int64_t ldc,
+                        void* workspace, hipStream_t s);
+
+// Clipping of `count` tensors (pointers, sizes and types on the host) to a norm (clip.hip);
+// workspace: clip_norm_workspace(count) bytes.  scale: write out (else only the norm).
+size_t clip_norm_workspace(int64_t count);
+int launch_clip_norm(int64_t count, const void* const* x, void* const* out, const int64_t* sizes,
+                     const int* types, double max_norm, double* norm, void* workspace,
+                     hipStream_t s);
 
 // Rows of int8 codes and layer norm (layernorm.hip); gamma, beta, mean, rstd, dx, dgamma and
 // dbeta may each be null where ozk.h says so.  The backward pass leaves

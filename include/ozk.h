@@ -73,6 +73,7 @@ extern "C" {
 
 #define OZK_MAX_MODULI 20
 #define OZK_MAX_K 131071      /* |residue product| <= 2^14: int32 sums stay exact */
+#define OZK_MX_MAX_K 131072   /* inner dimension of the products on MX FP4 lines */
 #define OZK_PLANE_K 64        /* residue and limb planes pad K to a multiple of this */
 #define OZK_NOALLOC_SCRATCH_BYTES (64ull << 20)  /* scratch of ozk_dgemv_noalloc, per GPU */
 
@@ -231,6 +232,35 @@ int ozk_dgemm_epilogue_grad(int64_t m, int64_t n, int64_t k, const double* dC, i
                             const double* Z, int64_t ldz, int act, double* dA, int64_t ldda,
                             double* dB, int64_t lddb, double* dbias, int r, int scaling,
                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- emulated DGEMM: gated block
+ * The first half of a gated feed-forward block in emulated fp64 (no counterpart in the pages):
+ *     Z = A B + 1 bias^T  (m x 2 n),   C = act(Z[:, :n]) * Z[:, n:]  (m x n)
+ * B is k x 2 n, ldb >= 2 n: the gate's projection, then the other.  bias (2 n entries) may be
+ * NULL; Z, if not NULL, receives the pre-activations the gradient needs (ldz >= 2 n).  Both
+ * products are rounded once (as ozk_dgemm_ex), then the bias is added, the activation taken and the
+ * product formed, one fp64 rounding or fp64 function each, in the registers of the
+ * reconstruction.  Outputs overlap no input.  Other arguments and the errors are those of
+ * ozk_dgemm_epilogue; the workspace (256-byte aligned) takes ozk_dgemm_gated_workspace_size
+ * bytes.  OZK_EUNSUPPORTED from n = 2^40 on. */
+int ozk_dgemm_gated_workspace_size(int64_t m, int64_t n, int64_t k, int r, size_t* bytes);
+int ozk_dgemm_gated(int64_t m, int64_t n, int64_t k, const double* A, int64_t lda, const double* B,
+                    int64_t ldb, const double* bias, int act, double* Z, int64_t ldz, double* C,
+                    int64_t ldc, int r, int scaling, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+/* Its gradient: from dC (m x n), A, B and Z
+ *     G = [dC * Z[:, n:] * act'(Z[:, :n]),  dC * act(Z[:, :n])]  (m x 2 n),
+ *     dA = G B^T,   dB = A^T G,   dbias = column sums of G
+ * dA (m x k), dB (k x 2 n) and dbias (2 n entries) may each be NULL and are then not computed.  Both
+ * products are emulated with r moduli, inner dimensions 2 n and m; dbias is summed in fp64 in a
+ * fixed order.  m, 2 n and k at most OZK_MAX_K.  Otherwise as ozk_dgemm_epilogue_grad. */
+int ozk_dgemm_gated_grad_workspace_size(int64_t m, int64_t n, int64_t k, int r, size_t* bytes);
+int ozk_dgemm_gated_grad(int64_t m, int64_t n, int64_t k, const double* dC, int64_t lddc,
+                         const double* A, int64_t lda, const double* B, int64_t ldb,
+                         const double* Z, int64_t ldz, int act, double* dA, int64_t ldda,
+                         double* dB, int64_t lddb, double* dbias, int r, int scaling,
+                         void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------- emulated DGEMV
  * Y = A X for A m x k and X k x nrhs (1 <= nrhs <= 32): the memory-bound GEMV and
@@ -446,6 +476,74 @@ int ozk_layernorm_backward(int64_t rows, int64_t cols, int type, const void* dy,
                            const void* x, int64_t ldx, const void* gamma, const void* mean,
                            const void* rstd, void* dx, int64_t lddx, void* dgamma, void* dbeta,
                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- MX FP4: codes, products
+ * Microscaled 4-bit floating point (OCP MX FP4; no counterpart in the pages).  A line of k values
+ * is cut into blocks of 32; a block is 32 e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign in bit
+ * 3), two a byte with the even K index in the low nibble, and one scale byte s, which stands for
+ * 2^(s - 127), or NaN for 255.  Lines hold whole steps of 256 values: ozk_mxfp4_line_bytes(k) =
+ * 128 ceil(k / 256) bytes of codes and ozk_mxfp4_scale_bytes(k) = 8 ceil(k / 256) scales, the
+ * least leading dimensions; codes past k are 0 and scales past the last block are not 255, both as
+ * ozk_mxfp4_quant writes them (other codes there enter the products).  Codes start at multiples of
+ * 16 bytes with leading dimensions that are multiples of 16, scales at multiples of 8 with multiples
+ * of 8 (OZK_EINVAL otherwise).
+ *
+ * ozk_mxfp4_quant: codes and scales of the lines of x (rows x cols of `type`, an OZK_F* value;
+ *   ldx >= cols), axis 0: its rows, k = cols; axis 1: its columns, k = rows.  For a block with the
+ *   largest magnitude a, E = floor(log2 a) - 2 held to [-127, 127] and s = E + 127 (0 for a block of
+ *   zeros); the code is x 2^-E rounded to the nearest value, ties to the even code, magnitudes past
+ *   6 to 6, with the sign of x also where it is 0.  A block with an Inf or NaN, or with E above 127, has s
+ *   = 255 and codes 0.  k >= 1; rows and cols below 2^31 (OZK_EUNSUPPORTED beyond).
+ * ozk_mxfp4_values: the values of `lines` lines of k, rounded once to `type` (exact in
+ *   fp64, and in fp32 and bf16 but for magnitudes from 2^128 on, which are Inf); NaN where s = 255.  out lines x k, ldo >= k.
+ *
+ * ozk_mxfp4_linear: C = act(X W^T + 1 bias^T) + residual, X m lines and W n lines of k values,
+ *   C m x n.  bias (n), residual (m x n, ldr >= n) and C have `type`: OZK_F32, OZK_F16 or
+ *   OZK_BF16; bias and residual may be NULL, residual may be C itself.  Sums are fp32, in an order
+ *   that depends on m, n and k alone (results repeat bit for bit), and so is what follows, rounded once to
+ *   C's type, the activations as ozk_int8linear's.  Where a block's scale is NaN, so are the outputs it
+ *   touches; products past fp32's range are Inf or zero.
+ * ozk_mxfp4_gated: the first half of a gated feed-forward block, C = act(Zg) * Zu with
+ *   Zg = X Wg^T + 1 bias[:n]^T, Zu = X Wu^T + 1 bias[n:]^T; W has 2 n lines, Wg's before Wu's, bias 2 n
+ *   entries.
+ * Both: 1 <= k <= OZK_MX_MAX_K; a workspace (256-byte aligned) of the size the query returns, which
+ *   may be 0 (workspace may be NULL then); C overlaps no other operand.  OZK_EUNSUPPORTED from
+ *   m = 2^31 or n = 2^30 on, for leading dimensions of codes or scales from 2^24 on, and where a launch would pass
+ *   2^32 threads. */
+int64_t ozk_mxfp4_line_bytes(int64_t k);
+int64_t ozk_mxfp4_scale_bytes(int64_t k);
+int ozk_mxfp4_quant(int64_t rows, int64_t cols, int type, const void* x, int64_t ldx, int axis,
+                    uint8_t* codes, int64_t ldq, uint8_t* scales, int64_t lds, void* stream);
+int ozk_mxfp4_values(int64_t lines, int64_t k, const uint8_t* codes, int64_t ldq,
+                     const uint8_t* scales, int64_t lds, int type, void* out, int64_t ldo,
+                     void* stream);
+int ozk_mxfp4_linear_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes);
+int ozk_mxfp4_linear(int64_t m, int64_t n, int64_t k, const uint8_t* X, int64_t ldx,
+                     const uint8_t* scale_x, int64_t ldsx, const uint8_t* W, int64_t ldw,
+                     const uint8_t* scale_w, int64_t ldsw, const void* bias, int act,
+                     const void* residual, int64_t ldr, int type, void* C, int64_t ldc,
+                     void* workspace, size_t workspace_bytes, void* stream);
+int ozk_mxfp4_gated_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes);
+int ozk_mxfp4_gated(int64_t m, int64_t n, int64_t k, const uint8_t* X, int64_t ldx,
+                    const uint8_t* scale_x, int64_t ldsx, const uint8_t* W, int64_t ldw,
+                    const uint8_t* scale_w, int64_t ldsw, const void* bias, int act, int type,
+                    void* C, int64_t ldc, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- clipping to a norm
+ * The gradients of a training step (no counterpart in the pages): with N the 2-norm of all values
+ * of `count` tensors together, out[i] = x[i] min(1, max_norm / N).  x, out, sizes (elements) and
+ * types (OZK_F* values) are HOST arrays, read during the call; x[i] and out[i] point to
+ * contiguous device memory, aligned to their elements, out[i] of x[i]'s type.  out[i] may be x[i]
+ * (a norm within the bound then writes nothing); apart from that no output overlaps another, or an
+ * input (OZK_EINVAL).  norm (device, fp64) receives N.  Squares are summed in fp64 in a fixed order, without
+ * overflow or underflow of the squares of fp64 values; a value times the factor is formed in fp64
+ * and rounded to its type.  Where N is Inf or NaN the values are left as they are.  max_norm >= 0;
+ * with Inf only N is computed (and x copied where out is not x).  The workspace (256-byte aligned) takes
+ * ozk_clip_norm_workspace_size bytes.  OZK_EUNSUPPORTED from 2^23 tensors, or 2^44 bytes of one, on. */
+int ozk_clip_norm_workspace_size(int64_t count, size_t* bytes);
+int ozk_clip_norm(int64_t count, const void* const* x, void* const* out, const int64_t* sizes,
+                  const int* types, double max_norm, double* norm, void* workspace,
+                  size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------- measurement support
  * ozk_dgemm_ex_timed: ozk_dgemm_ex that also has the launch of the r residue products
