@@ -33,6 +33,17 @@ __device__ __forceinline__ void dma16_sbase(uint32_t voffset, uint64_t sbase, ui
       : "memory", "m0");
 }
 
+// Lane i copies 4 bytes from g into LDS bytes [lds_base + 4 i, +4).
+__device__ __forceinline__ void dma4(const void* g, uint32_t lds_base) {
+  asm volatile(
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dword %0, off"
+      :
+      : "v"(g), "s"(lds_base)
+      : "memory", "m0");
+}
+
 // Byte address of a __shared__ object in the LDS aperture.
 template <typename T>
 __device__ __forceinline__ uint32_t lds_address(T* p) {

@@ -59,6 +59,16 @@ __device__ __forceinline__ void put1(const MxEpilogue<O>& E, int64_t row, int64_
   E.c[row * E.ldc + col] = (O)z;
 }
 
+// The outputs from col to the row's end, fewer than eight, from staged sums (gated: the other
+// projection's `apart` further on).
+template <bool kGated, typename O>
+__device__ __forceinline__ void put_ragged(const MxEpilogue<O>& E, int64_t row, int64_t col,
+                                           const float* sums, int apart) {
+#pragma unroll 1
+  for (int u = 0; col + u < E.n; ++u)
+    put1<kGated>(E, row, col + u, sums[u], kGated ? sums[apart + u] : 0.0f);
+}
+
 // Four consecutive outputs of one row.
 template <bool kGated, typename O>
 __device__ __forceinline__ void put4(const MxEpilogue<O>& E, int64_t row, int64_t col,
@@ -94,124 +104,735 @@ __device__ __forceinline__ void put4(const MxEpilogue<O>& E, int64_t row, int64_
   }
 }
 
-// Any rows and columns: workgroup = 16 kMT rows x 16 kNT columns of C (gated: of both
-// projections), its eight waves taking the K steps of 256 codes in turn.  Operands go from global
-// memory to the matrix core's registers directly: a lane's 32 bytes of a step are two blocks.
-template <typename O, bool kGated, int kMT, int kNT>
-__global__ __launch_bounds__(512) void mxfp4_few_kernel(int64_t steps, Lines X, Lines W,
-                                                        MxEpilogue<O> E, int64_t tiles_n) {
-  constexpr int kWaves = 8, kG = kGated ? 2 : 1, kB = kNT * kG;
-  __shared__ v4f sums[kWaves][kMT * kB][64];
+// Four partial sums of a row of `wide`, the columns from col up to `end` of them.
+__device__ __forceinline__ void put_part(float* __restrict__ p, int64_t row, int64_t col,
+                                         int64_t m, int64_t end, int64_t wide, const v4f& acc) {
+  if (row >= m || col >= end) return;
+  if (col + 4 <= end) {
+    *reinterpret_cast<v4f_words*>(p + row * wide + col) = acc;
+    return;
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (col + u < end) p[row * wide + col + u] = acc[u];
+}
+
+// Both projections' partial sums of four columns (not gated: `up` is not used).
+template <bool kGated, typename O>
+__device__ __forceinline__ void put_parts(const MxEpilogue<O>& E, float* __restrict__ p, int64_t row,
+                                          int64_t col, const v4f& acc, const v4f& up) {
+  const int64_t wide = kGated ? 2 * E.n : E.n;
+  put_part(p, row, col, E.m, E.n, wide, acc);
+  if constexpr (kGated)
+    if (col < E.n) put_part(p + E.n, row, col, E.m, E.n, wide, up);
+}
+
+// Up to 16 rows: workgroup = 16 columns of C (gated: of both projections), its eight waves taking
+// the K steps of 256 codes in turn (of the workgroup's split of K).  Each wave streams its steps
+// through a ring of its own in LDS by direct loads of 8 lines x 128 bytes and of 32 lines' 8 scales.
+// No barriers: a wave waits for its own loads, reads its fragments and refills the slot.
+// kXR rows of X (8 for up to 8) travel with each step.
+template <typename O, bool kGated, int kXR, int kS>
+__global__ __launch_bounds__(512) void mxfp4_stream_kernel(int steps, Lines X, Lines W,
+                                                           MxEpilogue<O> E, int splits,
+                                                           float* __restrict__ part) {
+  constexpr int kG = kGated ? 2 : 1, kWaves = 8, kRows = 16 * kG + kXR;
+  constexpr int kCodes = kRows * 128, LC = kRows / 8, LS = (kRows + 31) / 32, L = LC + LS;
+  constexpr int kSlot = kCodes + LS * 256;
+  __shared__ __attribute__((aligned(1024))) int8_t lds[kWaves * kS * kSlot];
+  static_assert(kWaves * kG * 1024 <= kWaves * kS * kSlot, "the sums fit the ring");
+  static_assert(L * (kS - 1) <= 63, "the load counter's range");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t tile_m = blockIdx.x / tiles_n, tile_n = blockIdx.x - tile_m * tiles_n;
-  const int64_t row0 = tile_m * (16 * kMT), col0 = tile_n * (16 * kNT);
-  const int frow = lane & 15, quarter = lane >> 4;
-  const uint8_t *wp[kB], *wsp[kB], *xp[kMT], *xsp[kMT];
+  const int split = blockIdx.x % splits;
+  const int64_t col0 = (int64_t)(blockIdx.x / splits) * 16;
+  const int t0 = (int)((int64_t)steps * split / splits) + wave;
+  const int t1 = (int)((int64_t)steps * (split + 1) / splits);
+  const int own = t0 < t1 ? (t1 - t0 + kWaves - 1) / kWaves : 0;   // steps t0 + 8 i
+  // line r of a step: of W's gate, of its other projection, then of X; lines past the operand
+  // re-read its last
+  auto line = [&](int r, bool& is_w) -> int64_t {
+    is_w = r < 16 * kG;
+    if (!is_w) {
+      const int64_t row = r - 16 * kG;
+      return row < E.m ? row : E.m - 1;
+    }
+    const int64_t col = col0 + (r & 15);
+    return (col < E.n ? col : E.n - 1) + (kGated && r >= 16 ? E.n : 0);
+  };
+  // load q: lines 8 q .. 8 q + 7; lane i takes line i / 8 of them, physical chunk i % 8, which
+  // holds logical chunk (i % 8) ^ ((line >> 1) & 7)
+  const uint8_t* from[L];
 #pragma unroll
-  for (int j = 0; j < kB; ++j) {
-    const int64_t c = col0 + 16 * (j % kNT) + frow;
-    const int64_t r = (c < E.n ? c : E.n - 1) + (j / kNT) * E.n;
-    wp[j] = W.codes + r * W.ld + 32 * quarter;
-    wsp[j] = W.scales + r * W.lds + 2 * quarter;
+  for (int q = 0; q < LC; ++q) {
+    bool is_w;
+    const int64_t r = line(8 * q + (lane >> 3), is_w);
+    const int chunk = 16 * ((lane & 7) ^ ((4 * q + (lane >> 4)) & 7));
+    from[q] = (is_w ? W.codes + r * W.ld : X.codes + r * X.ld) + (int64_t)t0 * 128 + chunk;
   }
 #pragma unroll
-  for (int i = 0; i < kMT; ++i) {
-    const int64_t r = row0 + 16 * i + frow;
-    xp[i] = X.codes + (r < E.m ? r : E.m - 1) * X.ld + 32 * quarter;
-    xsp[i] = X.scales + (r < E.m ? r : E.m - 1) * X.lds + 2 * quarter;
+  for (int q = 0; q < LS; ++q) {
+    bool is_w;
+    const int at = 32 * q + (lane >> 1);
+    const int64_t r = line(at < kRows ? at : kRows - 1, is_w);
+    from[LC + q] = (is_w ? W.scales + r * W.lds : X.scales + r * X.lds) + (int64_t)t0 * 8 +
+                   4 * (lane & 1);
   }
-  v4f acc[kMT][kB];
+  const uint32_t ring = __builtin_amdgcn_readfirstlane(lds_address(lds) + wave * (kS * kSlot));
+  auto load = [&](int i) {
+    const uint32_t slot = ring + (uint32_t)(i % kS) * kSlot;
 #pragma unroll
-  for (int i = 0; i < kMT; ++i)
+    for (int q = 0; q < LC; ++q) dma16(from[q] + (int64_t)i * (kWaves * 128), slot + q * 1024);
 #pragma unroll
-    for (int j = 0; j < kB; ++j) acc[i][j] = v4f{0, 0, 0, 0};
-  for (int64_t t = wave; t < steps; t += kWaves) {
-    v4i fb[2][kB], fa[2][kMT];
-    int sb[kB], sa[kMT];
+    for (int q = 0; q < LS; ++q)
+      dma4(from[LC + q] + (int64_t)i * (kWaves * 8), slot + kCodes + q * 256);
+  };
+  const int frow = lane & 15, quarter = lane >> 4, xrow = 16 * kG + (frow & (kXR - 1));
+  v4f acc[kG];
 #pragma unroll
-    for (int j = 0; j < kB; ++j) {
-      fb[0][j] = *reinterpret_cast<const v4i*>(wp[j] + t * 128);
-      fb[1][j] = *reinterpret_cast<const v4i*>(wp[j] + t * 128 + 16);
-      sb[j] = *reinterpret_cast<const uint16_t*>(wsp[j] + t * 8);
+  for (int g = 0; g < kG; ++g) acc[g] = v4f{0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < kS; ++i)
+    if (i < own) load(i);
+  for (int i = 0; i < own; ++i) {
+    const int younger = own - 1 - i;
+    if (younger >= kS - 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L * (kS - 1)) : "memory");
+    else if (kS > 3 && younger == 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L * 2) : "memory");
+    else if (kS > 2 && younger == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const int8_t* slot = lds + wave * (kS * kSlot) + (i % kS) * kSlot;
+    auto codes = [&](int r, int h) {
+      return *reinterpret_cast<const v4i*>(slot + r * 128 +
+                                           (((2 * quarter + h) ^ ((r >> 1) & 7)) << 4));
+    };
+    auto scale = [&](int r) -> int {
+      return *reinterpret_cast<const uint16_t*>(slot + kCodes + r * 8 + 2 * quarter);
+    };
+    v4i fb[2][kG], fa[2];
+    int sb[kG];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int g = 0; g < kG; ++g) fb[h][g] = codes(16 * g + frow, h);
+      fa[h] = codes(xrow, h);
     }
 #pragma unroll
-    for (int i = 0; i < kMT; ++i) {
-      fa[0][i] = *reinterpret_cast<const v4i*>(xp[i] + t * 128);
-      fa[1][i] = *reinterpret_cast<const v4i*>(xp[i] + t * 128 + 16);
-      sa[i] = *reinterpret_cast<const uint16_t*>(xsp[i] + t * 8);
-    }
-#pragma unroll
-    for (int i = 0; i < kMT; ++i)
-#pragma unroll
-      for (int j = 0; j < kB; ++j) {
-        acc[i][j] = mfma_mx<0>(fb[0][j], sb[j], fa[0][i], sa[i], acc[i][j]);
-        acc[i][j] = mfma_mx<1>(fb[1][j], sb[j], fa[1][i], sa[i], acc[i][j]);
-      }
-  }
-#pragma unroll
-  for (int i = 0; i < kMT; ++i)
-#pragma unroll
-    for (int j = 0; j < kB; ++j) sums[wave][i * kB + j][lane] = acc[i][j];
-  __syncthreads();
-  for (int b = wave; b < kMT * kNT; b += kWaves) {
-    const int i = b / kNT, j = b % kNT;
-    v4f s[2];
+    for (int g = 0; g < kG; ++g) sb[g] = scale(16 * g + frow);
+    const int sa = scale(xrow);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    if (i + kS < own) load(i + kS);
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
-      s[g] = sums[0][i * kB + j + g * kNT][lane];
-#pragma unroll
-      for (int v = 1; v < kWaves; ++v) s[g] += sums[v][i * kB + j + g * kNT][lane];
+      acc[g] = mfma_mx<0>(fb[0][g], sb[g], fa[0], sa, acc[g]);
+      acc[g] = mfma_mx<1>(fb[1][g], sb[g], fa[1], sa, acc[g]);
     }
-    put4<kGated>(E, row0 + 16 * i + frow, col0 + 16 * j + 4 * quarter, s[0], s[kG - 1]);
   }
+  // every wave is past its ring: the sums take its first bytes
+  __syncthreads();
+  v4f* sums = reinterpret_cast<v4f*>(lds);
+#pragma unroll
+  for (int g = 0; g < kG; ++g) sums[(g * kWaves + wave) * 64 + lane] = acc[g];
+  __syncthreads();
+  if (wave) return;
+#pragma unroll
+  for (int g = 0; g < kG; ++g)
+#pragma unroll
+    for (int v = 1; v < kWaves; ++v) acc[g] += sums[(g * kWaves + v) * 64 + lane];
+  const int64_t row = frow, col = col0 + 4 * quarter;
+  if (part)
+    put_parts<kGated>(E, part + split * E.m * E.n * kG, row, col, acc[0], acc[kG - 1]);
+  else
+    put4<kGated>(E, row, col, acc[0], acc[kG - 1]);
+}
+
+// ------------------------------------------------------------------ tiles
+// Tiles as the int8 layer's (tile_walk.h), a K step being 128 bytes of each line, 256 codes, and the
+// line's 8 scales, whose ring stands behind the codes'.  Lane quarter q of a fragment takes
+// chunks 2 q and 2 q + 1 of a line's step, so that its two scales are one aligned word of 16 bits.
+// Gated: a wave's columns are half columns of the gate's projection and half the same columns of
+// the other, so that both meet in one wave; the tile has BN / 2 columns of C.
+template <typename TL, bool kGated>
+struct MxTile {
+  static constexpr int kCols = kGated ? TL::BN / 2 : TL::BN;     // of C, a tile's
+  static constexpr int kWaveCols = kGated ? TL::WN / 2 : TL::WN; // and a wave's
+  static constexpr int kScaleStage = (TL::BM + TL::BN) * 8;
+  // loads of 32 lines' scales a wave and step; waves without lines of their own repeat others'
+  static constexpr int kScaleLoads = (kScaleStage / 256 + TL::NW - 1) / TL::NW;
+  static constexpr int kLoads = TL::kLoads + kScaleLoads;
+  static constexpr int kBytes = TL::S * (TL::kStage + kScaleStage);
+  static_assert(kScaleStage % 256 == 0 && kBytes <= 160 * 1024, "LDS");
+  static_assert(kLoads * (TL::S - 1) <= 63, "the load counter's range");
+  static_assert(kWaveCols % 8 == 0, "a load's lines are of one projection");
+};
+
+template <typename TL, bool kGated>
+struct MxWalk {
+  using T = MxTile<TL, kGated>;
+  static constexpr int BM = TL::BM, BN = TL::BN, NW = TL::NW, S = TL::S, LC = TL::kLoads;
+  static constexpr int LS = T::kScaleLoads;
+  int8_t* lds;
+  int wave, lane;
+  int nk;                  // K steps
+  int64_t row0, col0;      // of C
+  uint64_t base[LC];       // of a load's lines (uniform)
+  uint32_t voff[LC];       // a lane's offset from there
+  const uint8_t* scale[LS];
+  uint32_t wave_lds, scale_lds[LS];
+
+  // Tile `tile` of tiles_m x tiles_n in groups of group_m tile rows (column, then row in group), K
+  // steps first .. first + count - 1.
+  __device__ __forceinline__ MxWalk(int8_t* ring, int64_t m, int64_t n, const Lines& X,
+                                    const Lines& W, int tile, int tiles_m, int tiles_n,
+                                    int group_m, int first, int count)
+      : lds(ring), nk(count) {
+    lane = threadIdx.x & 63;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int per_group = group_m * tiles_n, first_m = tile / per_group * group_m;
+    const int gsize = tiles_m - first_m < group_m ? tiles_m - first_m : group_m;
+    const int in_group = tile % per_group;
+    row0 = (int64_t)(first_m + in_group % gsize) * BM;
+    col0 = (int64_t)(in_group / gsize) * T::kCols;
+    // Load q of this wave: region rg = wave + NW q, lines 8 rg .. 8 rg + 7 of X's, then of W's; lane
+    // i takes line i / 8 of it, physical chunk i % 8, which holds logical chunk
+    // (i % 8) ^ ((line >> 1) & 7).  Lines past the matrix re-read its last.
+    const uint32_t chunk = 16 * ((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7));
+#pragma unroll
+    for (int q = 0; q < LC; ++q) {
+      const int rg = wave + NW * q, r = 8 * rg;
+      const bool is_w = r >= BM;
+      const int wr = r - BM, half = kGated && is_w ? wr % TL::WN / T::kWaveCols : 0;
+      const int at = !is_w ? r : (kGated ? wr / TL::WN * T::kWaveCols + wr % T::kWaveCols : wr);
+      const int64_t origin = is_w ? col0 : row0, last = (is_w ? n : m) - 1 - origin;
+      const int64_t ld = is_w ? W.ld : X.ld;
+      base[q] = (uint64_t)((is_w ? W.codes + half * (n * ld) : X.codes) + origin * ld +
+                           (int64_t)first * 128);
+      const int mine = at + (lane >> 3);
+      voff[q] = (uint32_t)((mine < last ? mine : last) * ld) + chunk;
+    }
+#pragma unroll
+    for (int q = 0; q < LS; ++q) {
+      const int rg = (wave + NW * q) % ((BM + BN) / 32);
+      const int r = 32 * rg + (lane >> 1), wr = r - BM;
+      const bool is_w = r >= BM;
+      const int half = kGated && is_w ? wr % TL::WN / T::kWaveCols : 0;
+      const int at = !is_w ? r : (kGated ? wr / TL::WN * T::kWaveCols + wr % T::kWaveCols : wr);
+      const int64_t g = (is_w ? col0 : row0) + at, last = (is_w ? n : m) - 1;
+      const int64_t l = (g < last ? g : last) + half * n;
+      scale[q] = (is_w ? W.scales + l * W.lds : X.scales + l * X.lds) + (int64_t)first * 8 +
+                 4 * (lane & 1);
+      scale_lds[q] = __builtin_amdgcn_readfirstlane(lds_address(lds) + S * TL::kStage + rg * 256);
+    }
+    wave_lds = __builtin_amdgcn_readfirstlane(lds_address(lds) + wave * 1024);
+  }
+
+  __device__ __forceinline__ const int8_t* stage(int t) const {
+    return lds + (t % S) * TL::kStage;
+  }
+  // A line's two scales of this lane's quarter of step t.
+  __device__ __forceinline__ const uint16_t* scales(int t) const {
+    return reinterpret_cast<const uint16_t*>(lds + S * TL::kStage + (t % S) * T::kScaleStage);
+  }
+
+  // Load q of step t: codes, then scales.
+  __device__ __forceinline__ void load(int t, int q) const {
+    if (q < LC)
+      dma16_sbase(voff[q], base[q] + (uint64_t)t * 128,
+                  wave_lds + (uint32_t)(t % S) * TL::kStage + q * (NW * 1024));
+    else
+      dma4(scale[q - LC] + (int64_t)t * 8, scale_lds[q - LC] + (uint32_t)(t % S) * T::kScaleStage);
+  }
+
+  // Waits until of this wave's loads at most those of the youngest `younger` steps are under
+  // way (kMost: the number that is asked for on every step but the last ones).
+  template <int kMost>
+  __device__ __forceinline__ void wait_loads(int younger) const {
+    constexpr int L = T::kLoads;
+    if (kMost == 0 || younger >= kMost) {
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L * kMost) : "memory");
+      return;
+    }
+    if (kMost > 3 && younger == 3) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L * 3) : "memory");
+    else if (kMost > 2 && younger == 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L * 2) : "memory");
+    else if (kMost > 1 && younger == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  }
+
+  // The ring's first stages asked for, step 0 in place for every wave.
+  __device__ __forceinline__ void begin() const {
+#pragma unroll
+    for (int t = 0; t < S; ++t)
+      if (t < nk)
+#pragma unroll
+        for (int q = 0; q < T::kLoads; ++q) load(t, q);
+    wait_loads<S - 1>(nk - 1);
+    wg_barrier();
+  }
+};
+
+// A workgroup's tile and split of K in the order (split, tile).
+struct Place {
+  int split, tile, t0, nk;
+  __device__ __forceinline__ Place(int steps, int tiles, int splits) {
+    const int id = xcd_order();
+    split = id / tiles;
+    tile = id - split * tiles;
+    t0 = (int)((int64_t)steps * split / splits);
+    nk = (int)((int64_t)steps * (split + 1) / splits) - t0;
+  }
+};
+
+// The outputs of a wave's NI x TJ blocks (lane l of block (i, j): row 16 i + l % 16, columns
+// 16 j + 4 (l / 16) .. + 3), or their partial sums.  The blocks are staged through this wave's
+// part `mine` of the ring so that a few lanes finish one row of the wave's columns, eight
+// consecutive outputs each.  Residuals are asked for four groups of rows ahead.  The loop over the
+// groups of a phase is kept a loop: written out, the epilogue does not fit the instruction cache.
+template <typename TL, bool kGated, typename O, int NI>
+__device__ __forceinline__ void put_tile(const MxEpilogue<O>& E, const v4f (&acc)[NI][TL::TJ],
+                                         int64_t wrow0, int64_t wcol0, int lane, float* mine,
+                                         float* __restrict__ part) {
+  using T = MxTile<TL, kGated>;
+  constexpr int TJ = TL::TJ, kPairs = kGated ? TJ / 2 : TJ;
+  const int frow = lane & 15, quarter = lane >> 4;
+  if (part) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j)
+        put_parts<kGated>(E, part, wrow0 + 16 * i + frow, wcol0 + 16 * j + 4 * quarter, acc[i][j],
+                          acc[i][(j + kPairs) % TJ]);
+    return;
+  }
+  typedef O V8 __attribute__((ext_vector_type(8), aligned(sizeof(O))));
+  constexpr int kLanes = T::kWaveCols / 8, kRows = 64 / kLanes;   // lanes of a row, rows at once
+  constexpr int kIters = TL::kPhase * 16 / kRows, kPhases = NI / TL::kPhase;
+  constexpr int kAhead = kIters * kPhases < 4 ? kIters * kPhases : 4;
+  static_assert(kIters >= 1 && kIters * kRows == TL::kPhase * 16, "whole groups of rows");
+  const int lrow = lane / kLanes, lcol = 8 * (lane % kLanes);
+  const int64_t col = wcol0 + lcol;
+  const bool whole = col + 8 <= E.n;
+  float b[8], bu[8];
+  V8 res[kAhead];
+  auto ahead = [&](int slot, int64_t row) {
+    if (!kGated && row < E.m && E.residual && whole)
+      res[slot] = *reinterpret_cast<const V8*>(E.residual + row * E.ldr + col);
+  };
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) ahead(u, wrow0 + u * kRows + lrow);
+#pragma unroll
+  for (int u = 0; u < 8; ++u) b[u] = bu[u] = 0.0f;
+  if (whole && E.bias) {
+    const V8 bv = *reinterpret_cast<const V8*>(E.bias + col);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) b[u] = (float)bv[u];
+    if constexpr (kGated) {
+      const V8 uv = *reinterpret_cast<const V8*>(E.bias + E.n + col);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) bu[u] = (float)uv[u];
+    }
+  }
+#pragma unroll
+  for (int ph = 0; ph < kPhases; ++ph) {
+#pragma unroll
+    for (int i = 0; i < TL::kPhase; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+        *reinterpret_cast<v4f*>(mine + (16 * i + frow) * TL::kPitch + 16 * j + 4 * quarter) =
+            acc[ph * TL::kPhase + i][j];
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll 1
+    for (int it = 0; it < kIters; ++it) {
+      const int64_t row = wrow0 + (ph * kIters + it) * kRows + lrow;
+      const float* from = mine + (it * kRows + lrow) * TL::kPitch + lcol;
+      const v4f lo = *reinterpret_cast<const v4f*>(from);
+      const v4f hi = *reinterpret_cast<const v4f*>(from + 4);
+      v4f ulo, uhi;
+      if constexpr (kGated) {
+        ulo = *reinterpret_cast<const v4f*>(from + T::kWaveCols);
+        uhi = *reinterpret_cast<const v4f*>(from + T::kWaveCols + 4);
+      }
+      const V8 r0 = res[0];
+#pragma unroll
+      for (int u = 0; u + 1 < kAhead; ++u) res[u] = res[u + 1];
+      if ((ph * kIters + it + kAhead) < kPhases * kIters) ahead(kAhead - 1, row + kAhead * kRows);
+      if (row >= E.m) continue;
+      if (!whole) {
+        put_ragged<kGated>(E, row, col, from, T::kWaveCols);
+        continue;
+      }
+      float z[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) z[u] = (u < 4 ? lo[u & 3] : hi[u & 3]) + b[u];
+      activate_all<sizeof(O) == 4>(z, E.act);
+      V8 o;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if constexpr (kGated) z[u] *= (u < 4 ? ulo[u & 3] : uhi[u & 3]) + bu[u];
+        else if (E.residual) z[u] += (float)r0[u];
+        o[u] = (O)z[u];
+      }
+      *reinterpret_cast<V8*>(E.c + row * E.ldc + col) = o;
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
+}
+
+// The large tile: per step every wave runs quarters of 2 x TJ blocks; before the last one it waits
+// for its loads of step t + 1 and for its reads of step t (the last quarter's operands are in
+// registers by then), so one barrier a step makes step t + 1 complete and step t's stage free
+// for step t + S, whose loads have S - 1 steps to land less a quarter.
+template <typename O, bool kGated, typename TL>
+__global__ __launch_bounds__(64 * TL::NW) void mxfp4_tile_kernel(int steps, Lines X, Lines W,
+                                                                 MxEpilogue<O> E, int tiles_m,
+                                                                 int tiles_n, int splits,
+                                                                 int group_m,
+                                                                 float* __restrict__ part) {
+  using T = MxTile<TL, kGated>;
+  constexpr int BM = TL::BM, TI = TL::TI, TJ = TL::TJ, S = TL::S, L = T::kLoads;
+  static_assert(TL::KG == 1, "one wave for both K halves");
+  __shared__ __attribute__((aligned(1024))) int8_t lds[T::kBytes];
+  const Place p(steps, tiles_m * tiles_n, splits);
+  const MxWalk<TL, kGated> K(lds, E.m, E.n, X, W, p.tile, tiles_m, tiles_n, group_m, p.t0, p.nk);
+  const int wr = K.wave / TL::WC, wc = K.wave % TL::WC, nk = K.nk;
+
+  v4f acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = v4f{0, 0, 0, 0};
+
+  const int frow = K.lane & 15, quarter = K.lane >> 4, sw = frow >> 1;
+  const int off0 = ((2 * quarter) ^ sw) << 4, off1 = ((2 * quarter + 1) ^ sw) << 4;
+  const int aline = wr * TL::WM + frow, bline = BM + wc * TL::WN + frow;
+  v4i fa[2][2][2], fb[2][TJ];   // fa[set][K half][row block of a quarter], fb[K half][block]
+  int sa[2][2], sb[TJ];         // scales of both K halves
+  auto read_a = [&](int set, int t, int kh, int rb, int ii) {
+    fa[set][kh][ii] = *reinterpret_cast<const v4i*>(K.stage(t) + (aline + 16 * rb) * kStepK +
+                                                    (kh ? off1 : off0));
+    if (kh == 0) sa[set][ii] = K.scales(t)[(aline + 16 * rb) * 4 + quarter];
+  };
+  auto read_b = [&](int t, int kh, int j) {
+    fb[kh][j] = *reinterpret_cast<const v4i*>(K.stage(t) + (bline + 16 * j) * kStepK +
+                                              (kh ? off1 : off0));
+  };
+  auto read_sb = [&](int t, int j) { sb[j] = K.scales(t)[(bline + 16 * j) * 4 + quarter]; };
+  // Quarter q (row blocks 2q and 2q + 1): MFMA idx is row block 2q + idx / (2 TJ), column block
+  // (idx / 2) % TJ, K half idx % 2, a block's two halves back to back.  Its first four MFMAs
+  // are followed by the reads of the next quarter's A fragments into the other set (the last
+  // quarter's: row blocks 0 and 1 of step `next`); the last quarter also replaces each B
+  // fragment after its last use and issues the loads of step t + S, if there is one.  (The empty
+  // asm keeps the compiler from moving MFMAs past that branch, out of their order.)
+  constexpr int NQ = TI / 2, kQuarter = 4 * TJ;
+  static_assert(NQ % 2 == 0 && L <= kQuarter, "sets alternate; loads fit a quarter");
+  auto quarter_of = [&](int q, int t, int next) {
+    const int as = q & 1;
+    const bool is_last = q == NQ - 1;
+#pragma unroll
+    for (int idx = 0; idx < kQuarter; ++idx) {
+      const int ii = idx / (2 * TJ), j = (idx >> 1) % TJ, kh = idx & 1;
+      v4f& a = acc[2 * q + ii][j];
+      a = kh ? mfma_mx<1>(fb[1][j], sb[j], fa[as][1][ii], sa[as][ii], a)
+             : mfma_mx<0>(fb[0][j], sb[j], fa[as][0][ii], sa[as][ii], a);
+      asm volatile("" : "+v"(a));
+      if (idx < 4) {
+        if (!is_last) read_a(as ^ 1, t, idx & 1, 2 * (q + 1) + (idx >> 1), idx >> 1);
+        else read_a(as ^ 1, next, idx & 1, idx >> 1, idx >> 1);
+      }
+      if (is_last && ii == 1) {
+        read_b(next, kh, j);
+        if (kh) read_sb(next, j);
+      }
+      if (is_last && (idx * L) / kQuarter != ((idx + 1) * L) / kQuarter && t + S < nk)
+        K.load(t + S, (idx * L) / kQuarter);
+      __builtin_amdgcn_sched_barrier(0);
+      // the wave that reaches the second half of a quarter first is preferred, so the two
+      // waves of a SIMD run apart
+      if (idx == kQuarter / 2 - 1) __builtin_amdgcn_s_setprio(1);
+    }
+    __builtin_amdgcn_s_setprio(0);
+  };
+
+  K.begin();
+#pragma unroll
+  for (int idx = 0; idx < 4; ++idx) read_a(0, 0, idx & 1, idx >> 1, idx >> 1);
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) {
+    read_b(0, 0, j);
+    read_b(0, 1, j);
+    read_sb(0, j);
+  }
+  for (int t = 0; t < nk; ++t) {
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int q = 0; q < NQ - 1; ++q) quarter_of(q, t, t);
+    // this wave's loads of step t + 1 have landed and it has read all of step t; past the
+    // barrier that holds for every wave
+    K.template wait_loads<S - 2>(nk - 2 - t);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    wg_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    // after the last step: a harmless re-read of it
+    quarter_of(NQ - 1, t, t + 1 < nk ? t + 1 : t);
+  }
+  wg_barrier();   // every wave is past its last read of the ring
+  put_tile<TL, kGated, O, TI>(
+      E, acc, K.row0 + wr * TL::WM, K.col0 + wc * T::kWaveCols, K.lane,
+      reinterpret_cast<float*>(lds) + K.wave * (TL::kPhase * 16 * TL::kPitch),
+      part ? part + (int64_t)p.split * E.m * E.n * (kGated ? 2 : 1) : nullptr);
+}
+
+// The smaller tiles, whose K steps take a fraction of a load's latency: as many stages as LDS
+// holds, and per step one barrier, one set of fragment reads and one run of MFMAs.  A pair of
+// waves shares the outputs of a wave and splits each step's K, a block of every two; the sums of both
+// meet in LDS at the end.  Behind the barrier of step t the wave reads step t + 1 and asks for step
+// t + S while step t's MFMAs run from registers.
+template <typename O, bool kGated, typename TL>
+__global__ __launch_bounds__(64 * TL::NW) void mxfp4_small_kernel(int steps, Lines X, Lines W,
+                                                                  MxEpilogue<O> E, int tiles_m,
+                                                                  int tiles_n, int splits,
+                                                                  int group_m,
+                                                                  float* __restrict__ part) {
+  using T = MxTile<TL, kGated>;
+  constexpr int BM = TL::BM, TI = TL::TI, TJ = TL::TJ, S = TL::S, L = T::kLoads, H = TI / 2;
+  static_assert(TL::KG == 2 && TI % 2 == 0 && L <= TI * TJ, "pairs of waves");
+  static_assert(TL::NW * H * TJ * 1024 <= S * TL::kStage, "halves fit the ring");
+  __shared__ __attribute__((aligned(1024))) int8_t lds[T::kBytes];
+  const Place p(steps, tiles_m * tiles_n, splits);
+  const MxWalk<TL, kGated> K(lds, E.m, E.n, X, W, p.tile, tiles_m, tiles_n, group_m, p.t0, p.nk);
+  const int kh = K.wave / (TL::WR * TL::WC), wt = K.wave % (TL::WR * TL::WC);
+  const int wr = wt / TL::WC, wc = wt % TL::WC, nk = K.nk;
+
+  v4f acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = v4f{0, 0, 0, 0};
+
+  const int frow = K.lane & 15, quarter = K.lane >> 4, sw = frow >> 1;
+  const int off = ((2 * quarter + kh) ^ sw) << 4, soff = 2 * quarter + kh;
+  const int aline = wr * TL::WM + frow, bline = BM + wc * TL::WN + frow;
+  v4i fa[2][TI], fb[2][TJ];
+  int sa[2][TI], sb[2][TJ];
+  auto read = [&](int set, int t) {
+    const int8_t* st = K.stage(t) + off;
+    const uint8_t* sc = reinterpret_cast<const uint8_t*>(K.scales(t)) + soff;
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      fb[set][j] = *reinterpret_cast<const v4i*>(st + (bline + 16 * j) * kStepK);
+      sb[set][j] = sc[(bline + 16 * j) * 8];
+    }
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      fa[set][i] = *reinterpret_cast<const v4i*>(st + (aline + 16 * i) * kStepK);
+      sa[set][i] = sc[(aline + 16 * i) * 8];
+    }
+  };
+  auto step = [&](int set, int t) {
+    K.template wait_loads<S - 2>(nk - 2 - t);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    wg_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    read(set ^ 1, t + 1 < nk ? t + 1 : t);   // after the last step: a harmless re-read
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int idx = 0; idx < TI * TJ; ++idx) {
+      const int i = idx / TJ, j = idx % TJ;
+      acc[i][j] = mfma_mx<0>(fb[set][j], sb[set][j], fa[set][i], sa[set][i], acc[i][j]);
+      // (without this the compiler moves MFMAs past the branch, out of their order)
+      asm volatile("" : "+v"(acc[i][j]));
+      if (idx < L && t + S < nk) K.load(t + S, idx);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  K.begin();
+  read(0, 0);
+  int t = 0;
+  for (; t + 1 < nk; t += 2) {
+    step(0, t);
+    step(1, t + 1);
+  }
+  if (t < nk) step(0, t);
+
+  // Wave kh of a pair finishes row blocks kh TI / 2 ..: the other half goes to its partner.
+  wg_barrier();   // every wave is past its last read of the ring
+  v4f own[H][TJ];
+  v4f* boxes = reinterpret_cast<v4f*>(lds);   // [wave][H][TJ][lane]
+#pragma unroll
+  for (int i = 0; i < H; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      boxes[((K.wave * H + i) * TJ + j) * 64 + K.lane] = kh ? acc[i][j] : acc[H + i][j];
+      own[i][j] = kh ? acc[H + i][j] : acc[i][j];
+    }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  wg_barrier();
+  const int partner = wt + (kh ? 0 : TL::WR * TL::WC);
+#pragma unroll
+  for (int i = 0; i < H; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) own[i][j] += boxes[((partner * H + i) * TJ + j) * 64 + K.lane];
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  wg_barrier();
+  put_tile<TL, kGated, O, H>(
+      E, own, K.row0 + wr * TL::WM + kh * 16 * H, K.col0 + wc * T::kWaveCols, K.lane,
+      reinterpret_cast<float*>(lds) + K.wave * (TL::kPhase * 16 * TL::kPitch),
+      part ? part + (int64_t)p.split * E.m * E.n * (kGated ? 2 : 1) : nullptr);
+}
+
+// The outputs of a product whose K was split: the partial sums added, then the epilogue.
+template <typename O, bool kGated>
+__global__ __launch_bounds__(256) void mxfp4_join_kernel(MxEpilogue<O> E, int splits,
+                                                         const float* __restrict__ part) {
+  constexpr int kG = kGated ? 2 : 1;
+  const int64_t quads = (E.n + 3) / 4;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= E.m * quads) return;
+  const int64_t row = id / quads, col = id % quads * 4;
+  v4f s[kG];
+#pragma unroll
+  for (int g = 0; g < kG; ++g) {
+    s[g] = v4f{0, 0, 0, 0};
+    const float* p = part + row * (kG * E.n) + g * E.n + col;
+    for (int k = 0; k < splits; ++k, p += E.m * E.n * kG) {
+      if (col + 4 <= E.n) {
+        s[g] += *reinterpret_cast<const v4f_words*>(p);
+      } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (col + u < E.n) s[g][u] += p[u];
+      }
+    }
+  }
+  put4<kGated>(E, row, col, s[0], s[kG - 1]);
+}
+
+typedef Tile<256, 256, 2, 4, 1, 2> MxLarge;
+typedef Tile<128, 128, 2, 2, 2, 4> MxMid;
+typedef Tile<64, 128, 1, 4, 2, 6> MxSmall;
+
+// How a product is run: by the kernel for few rows (a workgroup takes all rows) or by tiles of
+// one shape; K is split over `splits` workgroups where there are fewer tiles than the compute
+// units take.
+enum Shape { kStream, kSmall, kMid, kLarge };
+struct Plan {
+  Shape shape;
+  int64_t tiles_m, tiles_n;
+  int splits;
+};
+
+// Up to 16 rows: the stream kernel.  More: the tile shape and split of the least estimated time, in
+// microseconds, of rounds of 256 workgroups that each cost `fixed` and `step` per K step.  A split
+// costs the launch of the join and the partial sums' way out and back (5 TB/s).
+Plan plan_of(int64_t m, int64_t n, int64_t k, bool gated) {
+  const int64_t steps = (k + 255) / 256, wide = gated ? 2 * n : n;
+  if (m <= 16) {
+    Plan p{kStream, 1, (n + 15) / 16, 1};
+    // a workgroup's eight waves take four steps each at least
+    const int64_t s = 256 / p.tiles_n, most = steps / 32;
+    p.splits = (int)(s < most ? s : most);
+    if (p.splits < 1) p.splits = 1;
+    return p;
+  }
+  struct Cost {
+    Shape shape;
+    int64_t bm, bn;
+    double fixed, step;
+  };
+  const Cost costs[] = {{kSmall, 64, 128, 4.8, 0.55}, {kMid, 128, 128, 6.3, 0.72},
+                        {kLarge, 256, 256, 8.2, 1.65}};
+  Plan best{};
+  double least = 0;
+  for (const Cost& c : costs) {
+    const int64_t tm = (m + c.bm - 1) / c.bm, tn = (wide + c.bn - 1) / c.bn, tiles = tm * tn;
+    for (int64_t sp = 1; sp <= 16 && (sp == 1 || (tiles * sp <= 256 && steps / sp >= 4)); ++sp) {
+      const double rounds = (double)((tiles * sp + 255) / 256);
+      double t = rounds * (c.fixed + c.step * (double)((steps + sp - 1) / sp));
+      if (sp > 1) t += 3.0 + (double)sp * (double)m * (double)wide * 8.0 / 5e6;
+      if (least == 0 || t < least) {
+        least = t;
+        best = {c.shape, tm, tn, (int)sp};
+      }
+    }
+  }
+  return best;
+}
+
+template <typename O, bool kGated, typename TL>
+void launch_tiles(const Plan& p, int steps, const Lines& X, const Lines& W, const MxEpilogue<O>& E,
+                  float* part, hipStream_t s) {
+  const int group_m = 8;
+  const dim3 grid((unsigned)(p.tiles_m * p.tiles_n * p.splits)), block(64 * TL::NW);
+  if constexpr (TL::KG == 1)
+    hipLaunchKernelGGL((mxfp4_tile_kernel<O, kGated, TL>), grid, block, 0, s, steps, X, W, E,
+                       (int)p.tiles_m, (int)p.tiles_n, p.splits, group_m, part);
+  else
+    hipLaunchKernelGGL((mxfp4_small_kernel<O, kGated, TL>), grid, block, 0, s, steps, X, W, E,
+                       (int)p.tiles_m, (int)p.tiles_n, p.splits, group_m, part);
 }
 
 template <typename O, bool kGated>
 int linear_t(int64_t m, int64_t n, int64_t k, const Lines& X, const Lines& W, const void* bias,
-             int act, const void* residual, int64_t ldr, void* c, int64_t ldc, hipStream_t s) {
+             int act, const void* residual, int64_t ldr, void* c, int64_t ldc, void* workspace,
+             hipStream_t s) {
   const MxEpilogue<O> E{m, n, (const O*)bias, (const O*)residual, ldr, (O*)c, ldc, act};
-  const int64_t steps = (k + 255) / 256;
-  constexpr int kNT = kGated ? 1 : 2;
-  const int64_t tiles_n = (n + 16 * kNT - 1) / (16 * kNT);
-  const int64_t tiles_m = m <= 16 ? 1 : (m + 31) / 32;
+  const int steps = (int)((k + 255) / 256);
+  const Plan p = plan_of(m, n, k, kGated);
   // a launch takes fewer than 2^32 threads, 512 a workgroup
-  if (tiles_m * tiles_n >= 1 << 23) return OZK_EUNSUPPORTED;
-  const dim3 grid((unsigned)(tiles_m * tiles_n)), block(512);
-  if (m <= 16)
-    hipLaunchKernelGGL((mxfp4_few_kernel<O, kGated, 1, kNT>), grid, block, 0, s, steps, X, W, E,
-                       tiles_n);
-  else
-    hipLaunchKernelGGL((mxfp4_few_kernel<O, kGated, 2, kNT>), grid, block, 0, s, steps, X, W, E,
-                       tiles_n);
+  if (p.tiles_m * p.tiles_n * p.splits >= 1 << 23) return OZK_EUNSUPPORTED;
+  float* const part = p.splits > 1 ? static_cast<float*>(workspace) : nullptr;
+  if (p.shape == kStream) {
+    const dim3 grid((unsigned)(p.tiles_n * p.splits)), block(512);
+    if (m <= 8)
+      hipLaunchKernelGGL((mxfp4_stream_kernel<O, kGated, 8, 3>), grid, block, 0, s, steps, X, W, E,
+                         p.splits, part);
+    else
+      hipLaunchKernelGGL((mxfp4_stream_kernel<O, kGated, 16, 3>), grid, block, 0, s, steps, X, W, E,
+                         p.splits, part);
+  } else if (p.shape == kLarge) {
+    launch_tiles<O, kGated, MxLarge>(p, steps, X, W, E, part, s);
+  } else if (p.shape == kMid) {
+    launch_tiles<O, kGated, MxMid>(p, steps, X, W, E, part, s);
+  } else {
+    launch_tiles<O, kGated, MxSmall>(p, steps, X, W, E, part, s);
+  }
+  if (p.splits > 1)
+    hipLaunchKernelGGL((mxfp4_join_kernel<O, kGated>),
+                       dim3((unsigned)((m * ((n + 3) / 4) + 255) / 256)), dim3(256), 0, s, E,
+                       p.splits, part);
   return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
 }
 
 template <typename O>
 int linear_any(int64_t m, int64_t n, int64_t k, const Lines& X, const Lines& W, bool gated,
                const void* bias, int act, const void* residual, int64_t ldr, void* c, int64_t ldc,
-               hipStream_t s) {
-  return gated ? linear_t<O, true>(m, n, k, X, W, bias, act, residual, ldr, c, ldc, s)
-               : linear_t<O, false>(m, n, k, X, W, bias, act, residual, ldr, c, ldc, s);
+               void* workspace, hipStream_t s) {
+  return gated ? linear_t<O, true>(m, n, k, X, W, bias, act, residual, ldr, c, ldc, workspace, s)
+               : linear_t<O, false>(m, n, k, X, W, bias, act, residual, ldr, c, ldc, workspace, s);
 }
 
 }  // namespace
 
-size_t mxfp4_linear_workspace(int64_t, int64_t, int64_t, bool) { return 0; }
+size_t mxfp4_linear_workspace(int64_t m, int64_t n, int64_t k, bool gated) {
+  const Plan p = plan_of(m, n, k, gated);
+  return p.splits > 1 ? align256((size_t)p.splits * m * n * (gated ? 8 : 4)) : 0;
+}
 
 int launch_mxfp4_linear(int64_t m, int64_t n, int64_t k, const uint8_t* x, int64_t ldx,
                         const uint8_t* xs, int64_t ldxs, const uint8_t* w, int64_t ldw,
                         const uint8_t* ws, int64_t ldws, bool gated, const void* bias, int act,
-                        const void* residual, int64_t ldr, int type, void* c, int64_t ldc, void*,
-                        hipStream_t s) {
+                        const void* residual, int64_t ldr, int type, void* c, int64_t ldc,
+                        void* workspace, hipStream_t s) {
   const Lines X{x, ldx, xs, ldxs}, W{w, ldw, ws, ldws};
   switch (type) {
     case OZK_F32:
-      return linear_any<float>(m, n, k, X, W, gated, bias, act, residual, ldr, c, ldc, s);
+      return linear_any<float>(m, n, k, X, W, gated, bias, act, residual, ldr, c, ldc, workspace,
+                               s);
     case OZK_F16:
-      return linear_any<f16_t>(m, n, k, X, W, gated, bias, act, residual, ldr, c, ldc, s);
+      return linear_any<f16_t>(m, n, k, X, W, gated, bias, act, residual, ldr, c, ldc, workspace,
+                               s);
     default:
-      return linear_any<bf16_t>(m, n, k, X, W, gated, bias, act, residual, ldr, c, ldc, s);
+      return linear_any<bf16_t>(m, n, k, X, W, gated, bias, act, residual, ldr, c, ldc, workspace,
+                                s);
   }
 }
 
