@@ -44,6 +44,34 @@ __device__ __forceinline__ void dma4(const void* g, uint32_t lds_base) {
       : "memory", "m0");
 }
 
+// The same where `more` (wave-uniform) is not 0.  The branch stands inside the assembly: a loop
+// around it stays one basic block, which the compiler keeps in its written order.
+__device__ __forceinline__ void dma16_sbase_if(uint32_t more, uint32_t voffset, uint64_t sbase,
+                                               uint32_t lds_base) {
+  asm volatile(
+      "s_cmp_eq_u32 %3, 0\n\t"
+      "s_cbranch_scc1 .Lno_dma%=\n\t"
+      "s_mov_b32 m0, %2\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %0, %1\n"
+      ".Lno_dma%=:"
+      :
+      : "v"(voffset), "s"(sbase), "s"(lds_base), "s"(__builtin_amdgcn_readfirstlane(more))
+      : "memory", "m0", "scc");
+}
+__device__ __forceinline__ void dma16_if(uint32_t more, const void* g, uint32_t lds_base) {
+  asm volatile(
+      "s_cmp_eq_u32 %2, 0\n\t"
+      "s_cbranch_scc1 .Lno_dma%=\n\t"
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %0, off\n"
+      ".Lno_dma%=:"
+      :
+      : "v"(g), "s"(lds_base), "s"(__builtin_amdgcn_readfirstlane(more))
+      : "memory", "m0", "scc");
+}
+
 // Byte address of a __shared__ object in the LDS aperture.
 template <typename T>
 __device__ __forceinline__ uint32_t lds_address(T* p) {

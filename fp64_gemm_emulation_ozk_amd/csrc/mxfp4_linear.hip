@@ -25,6 +25,17 @@ __device__ __forceinline__ v4f mfma_mx(const v4i& w, int sw, const v4i& x, int s
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, x8, c, 4, 4, kH, sw, kH, sx);
 }
 
+// In LDS a line's step is 128 bytes, whose eight 16-byte chunks are XORed with swizzle(line).  A
+// fragment read of 16 bytes a lane is served 16 lanes at a time, eight lines of one quarter and the
+// other eight of its neighbour (lanes 0-3, 12-15, 20-27, and so on), which here read chunks two
+// apart: these 16 fall on all 64 banks if lines 4 .. 11 of 16 have swizzles that stay among
+// themselves under XOR with 2.  (With (line >> 1) & 7 alone, as where neighbours read chunks one
+// apart, 0.44 of the LDS's busy cycles were conflicts.)
+__device__ __forceinline__ int swizzle(int line) {
+  const int x = (line >> 1) & 7;
+  return x ^ ((x & 2) << 1);
+}
+
 // Lines of codes with their scales.
 struct Lines {
   const uint8_t* codes;
@@ -161,13 +172,13 @@ __global__ __launch_bounds__(512) void mxfp4_stream_kernel(int steps, Lines X, L
     return (col < E.n ? col : E.n - 1) + (kGated && r >= 16 ? E.n : 0);
   };
   // load q: lines 8 q .. 8 q + 7; lane i takes line i / 8 of them, physical chunk i % 8, which
-  // holds logical chunk (i % 8) ^ ((line >> 1) & 7)
+  // holds logical chunk (i % 8) ^ swizzle(line)
   const uint8_t* from[L];
 #pragma unroll
   for (int q = 0; q < LC; ++q) {
     bool is_w;
     const int64_t r = line(8 * q + (lane >> 3), is_w);
-    const int chunk = 16 * ((lane & 7) ^ ((4 * q + (lane >> 4)) & 7));
+    const int chunk = 16 * ((lane & 7) ^ swizzle(8 * q + (lane >> 3)));
     from[q] = (is_w ? W.codes + r * W.ld : X.codes + r * X.ld) + (int64_t)t0 * 128 + chunk;
   }
 #pragma unroll
@@ -203,7 +214,7 @@ __global__ __launch_bounds__(512) void mxfp4_stream_kernel(int steps, Lines X, L
     const int8_t* slot = lds + wave * (kS * kSlot) + (i % kS) * kSlot;
     auto codes = [&](int r, int h) {
       return *reinterpret_cast<const v4i*>(slot + r * 128 +
-                                           (((2 * quarter + h) ^ ((r >> 1) & 7)) << 4));
+                                           (((2 * quarter + h) ^ swizzle(r)) << 4));
     };
     auto scale = [&](int r) -> int {
       return *reinterpret_cast<const uint16_t*>(slot + kCodes + r * 8 + 2 * quarter);
@@ -247,45 +258,47 @@ __global__ __launch_bounds__(512) void mxfp4_stream_kernel(int steps, Lines X, L
 }
 
 // ------------------------------------------------------------------ tiles
-// Tiles as the int8 layer's (tile_walk.h), a K step being 128 bytes of each line, 256 codes, and the
-// line's 8 scales, whose ring stands behind the codes'.  Lane quarter q of a fragment takes
-// chunks 2 q and 2 q + 1 of a line's step, so that its two scales are one aligned word of 16 bits.
+// Tiles as the int8 layer's (tile_walk.h), a K step being 128 bytes of each line, 256 codes.  Lane
+// quarter q of a fragment takes chunks 2 q and 2 q + 1 of a line's step, so that its two scales are
+// one aligned word of 16 bits.  Scales come in groups of four steps, 32 bytes a line, in a ring of
+// kBufs groups behind the codes': 8 bytes of every line each step are as many requests to L2 again as
+// the codes are.
 // Gated: a wave's columns are half columns of the gate's projection and half the same columns of
 // the other, so that both meet in one wave; the tile has BN / 2 columns of C.
-template <typename TL, bool kGated>
+template <typename TL, bool kGated, int kBufs>
 struct MxTile {
   static constexpr int kCols = kGated ? TL::BN / 2 : TL::BN;     // of C, a tile's
   static constexpr int kWaveCols = kGated ? TL::WN / 2 : TL::WN; // and a wave's
-  static constexpr int kScaleStage = (TL::BM + TL::BN) * 8;
-  // loads of 32 lines' scales a wave and step; waves without lines of their own repeat others'
-  static constexpr int kScaleLoads = (kScaleStage / 256 + TL::NW - 1) / TL::NW;
-  static constexpr int kLoads = TL::kLoads + kScaleLoads;
-  static constexpr int kBytes = TL::S * (TL::kStage + kScaleStage);
-  static_assert(kScaleStage % 256 == 0 && kBytes <= 160 * 1024, "LDS");
-  static_assert(kLoads * (TL::S - 1) <= 63, "the load counter's range");
+  static constexpr int kScaleBufs = kBufs;
+  static constexpr int kScaleBuf = (TL::BM + TL::BN) * 32;
+  // loads of 32 lines' scales a wave and group; waves without lines of their own repeat others'
+  static constexpr int kScaleLoads = (kScaleBuf / 1024 + TL::NW - 1) / TL::NW;
+  static constexpr int kBytes = TL::S * TL::kStage + kBufs * kScaleBuf;
+  static_assert(kScaleBuf % 1024 == 0 && kBytes <= 160 * 1024, "LDS");
   static_assert(kWaveCols % 8 == 0, "a load's lines are of one projection");
 };
 
-template <typename TL, bool kGated>
+template <typename T, typename TL, bool kGated>
 struct MxWalk {
-  using T = MxTile<TL, kGated>;
   static constexpr int BM = TL::BM, BN = TL::BN, NW = TL::NW, S = TL::S, LC = TL::kLoads;
   static constexpr int LS = T::kScaleLoads;
   int8_t* lds;
   int wave, lane;
   int nk;                  // K steps
+  int last;                // the lines' last step, from this workgroup's first, if it is the 1st, 3rd, ...
   int64_t row0, col0;      // of C
   uint64_t base[LC];       // of a load's lines (uniform)
   uint32_t voff[LC];       // a lane's offset from there
   const uint8_t* scale[LS];
+  int scale_left;          // bytes of a line's scales from the lane's first on
   uint32_t wave_lds, scale_lds[LS];
 
   // Tile `tile` of tiles_m x tiles_n in groups of group_m tile rows (column, then row in group), K
-  // steps first .. first + count - 1.
+  // steps first .. first + count - 1 of `steps`.
   __device__ __forceinline__ MxWalk(int8_t* ring, int64_t m, int64_t n, const Lines& X,
                                     const Lines& W, int tile, int tiles_m, int tiles_n,
-                                    int group_m, int first, int count)
-      : lds(ring), nk(count) {
+                                    int group_m, int first, int count, int steps)
+      : lds(ring), nk(count), last((steps - first) % 2 && steps > 1 ? steps - 1 - first : -1) {
     lane = threadIdx.x & 63;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int per_group = group_m * tiles_n, first_m = tile / per_group * group_m;
@@ -295,21 +308,23 @@ struct MxWalk {
     col0 = (int64_t)(in_group / gsize) * T::kCols;
     // Load q of this wave: region rg = wave + NW q, lines 8 rg .. 8 rg + 7 of X's, then of W's; lane
     // i takes line i / 8 of it, physical chunk i % 8, which holds logical chunk
-    // (i % 8) ^ ((line >> 1) & 7).  Lines past the matrix re-read its last.
-    const uint32_t chunk = 16 * ((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7));
+    // (i % 8) ^ swizzle(line), which depends on the region's parity alone, the wave's.  Lines past
+    // the matrix re-read its last.
+    const uint32_t chunk = 16 * ((lane & 7) ^ swizzle(8 * wave + (lane >> 3)));
 #pragma unroll
     for (int q = 0; q < LC; ++q) {
       const int rg = wave + NW * q, r = 8 * rg;
       const bool is_w = r >= BM;
       const int wr = r - BM, half = kGated && is_w ? wr % TL::WN / T::kWaveCols : 0;
       const int at = !is_w ? r : (kGated ? wr / TL::WN * T::kWaveCols + wr % T::kWaveCols : wr);
-      const int64_t origin = is_w ? col0 : row0, last = (is_w ? n : m) - 1 - origin;
+      const int64_t origin = is_w ? col0 : row0, end = (is_w ? n : m) - 1 - origin;
       const int64_t ld = is_w ? W.ld : X.ld;
       base[q] = (uint64_t)((is_w ? W.codes + half * (n * ld) : X.codes) + origin * ld +
                            (int64_t)first * 128);
       const int mine = at + (lane >> 3);
-      voff[q] = (uint32_t)((mine < last ? mine : last) * ld) + chunk;
+      voff[q] = (uint32_t)((mine < end ? mine : end) * ld) + chunk;
     }
+    // Scales: 32 bytes of a line, four steps, by two lanes.
 #pragma unroll
     for (int q = 0; q < LS; ++q) {
       const int rg = (wave + NW * q) % ((BM + BN) / 32);
@@ -317,37 +332,50 @@ struct MxWalk {
       const bool is_w = r >= BM;
       const int half = kGated && is_w ? wr % TL::WN / T::kWaveCols : 0;
       const int at = !is_w ? r : (kGated ? wr / TL::WN * T::kWaveCols + wr % T::kWaveCols : wr);
-      const int64_t g = (is_w ? col0 : row0) + at, last = (is_w ? n : m) - 1;
-      const int64_t l = (g < last ? g : last) + half * n;
-      scale[q] = (is_w ? W.scales + l * W.lds : X.scales + l * X.lds) + (int64_t)first * 8 +
-                 4 * (lane & 1);
-      scale_lds[q] = __builtin_amdgcn_readfirstlane(lds_address(lds) + S * TL::kStage + rg * 256);
+      const int64_t g = (is_w ? col0 : row0) + at, end = (is_w ? n : m) - 1;
+      const int64_t l = (g < end ? g : end) + half * n;
+      scale[q] = (is_w ? W.scales + l * W.lds : X.scales + l * X.lds) + (int64_t)first * 8;
+      scale_lds[q] = __builtin_amdgcn_readfirstlane(lds_address(lds) + S * TL::kStage + rg * 1024);
     }
+    scale_left = (steps - first) * 8;
     wave_lds = __builtin_amdgcn_readfirstlane(lds_address(lds) + wave * 1024);
   }
 
   __device__ __forceinline__ const int8_t* stage(int t) const {
     return lds + (t % S) * TL::kStage;
   }
-  // A line's two scales of this lane's quarter of step t.
-  __device__ __forceinline__ const uint16_t* scales(int t) const {
-    return reinterpret_cast<const uint16_t*>(lds + S * TL::kStage + (t % S) * T::kScaleStage);
+  // Line 0's 8 scales of step t (a line's group is 32 bytes).
+  __device__ __forceinline__ const uint8_t* scales(int t) const {
+    return reinterpret_cast<const uint8_t*>(lds) + S * TL::kStage +
+           (t / 4 % T::kScaleBufs) * T::kScaleBuf + t % 4 * 8 + (t == last ? 8 : 0);
   }
 
-  // Load q of step t: codes, then scales.
-  __device__ __forceinline__ void load(int t, int q) const {
-    if (q < LC)
-      dma16_sbase(voff[q], base[q] + (uint64_t)t * 128,
-                  wave_lds + (uint32_t)(t % S) * TL::kStage + q * (NW * 1024));
-    else
-      dma4(scale[q - LC] + (int64_t)t * 8, scale_lds[q - LC] + (uint32_t)(t % S) * T::kScaleStage);
+  // Load q of step t's codes if `more`.
+  __device__ __forceinline__ void load(uint32_t more, int t, int q) const {
+    dma16_sbase_if(more, voff[q], base[q] + (uint64_t)t * 128,
+                   wave_lds + (uint32_t)(t % S) * TL::kStage + q * (NW * 1024));
+  }
+  // Load q of the scales of steps 4 g .. 4 g + 3 if `more`.  A lane whose 16 bytes would leave its
+  // line takes the line's last 16: a last step that is the 1st, 3rd, ... lies 8 bytes on (`last`).
+  __device__ __forceinline__ void load_scales(uint32_t more, int g, int q) const {
+    const uint32_t to = scale_lds[q] + (uint32_t)(g % T::kScaleBufs) * T::kScaleBuf;
+    const int at = 32 * g + 16 * (lane & 1), most = scale_left - 16;
+    dma16_if(more, scale[q] + (at < most ? at : most), to);
   }
 
-  // Waits until of this wave's loads at most those of the youngest `younger` steps are under
-  // way (kMost: the number that is asked for on every step but the last ones).
+  // Behind the barrier of step t, in which the scales of group t / 4 - 1 have been read for the last
+  // time where t begins a group: whether that asks for another, and which.
+  __device__ __forceinline__ int next_group(int t) const { return t / 4 + T::kScaleBufs - 1; }
+  __device__ __forceinline__ bool asks(int t) const {
+    return t % 4 == 0 && 4 * next_group(t) < nk;
+  }
+
+  // Waits until of this wave's loads of codes at most those of the youngest `younger` steps are under
+  // way (kMost: the number that is asked for on every step but the last ones), and of scales at most
+  // those asked for within these steps.
   template <int kMost>
   __device__ __forceinline__ void wait_loads(int younger) const {
-    constexpr int L = T::kLoads;
+    constexpr int L = LC;
     if (kMost == 0 || younger >= kMost) {
       asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L * kMost) : "memory");
       return;
@@ -358,14 +386,30 @@ struct MxWalk {
     else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   }
 
-  // The ring's first stages asked for, step 0 in place for every wave.
+  // The ring's first stages asked for, scales first, step 0 in place for every wave.
   __device__ __forceinline__ void begin() const {
+    // group G is asked for at step 4 (G - kBufs + 1) and read from behind the barrier of step
+    // 4 G - 1 on: 4 kBufs - 6 steps' codes later, of which S - 2 may still be under way
+    static_assert(4 * T::kScaleBufs - 6 >= S - 2, "a group's scales have landed");
+    if (scale_left == 8 && last < 0) {   // lines of one step: their 8 scales, no loads of 16 bytes
+      for (int q = 0; q < LS; ++q) {
+        const int rg = (wave + NW * q) % ((BM + BN) / 32);
+        if ((lane & 1) == 0)
+          *reinterpret_cast<uint2*>(lds + S * TL::kStage + rg * 1024 + 16 * lane) =
+              *reinterpret_cast<const uint2*>(scale[q]);
+      }
+    } else {
+#pragma unroll
+      for (int g = 0; g < T::kScaleBufs - 1; ++g)
+#pragma unroll
+        for (int q = 0; q < LS; ++q) load_scales(4 * g < nk, g, q);
+    }
 #pragma unroll
     for (int t = 0; t < S; ++t)
-      if (t < nk)
 #pragma unroll
-        for (int q = 0; q < T::kLoads; ++q) load(t, q);
+      for (int q = 0; q < LC; ++q) load(t < nk, t, q);
     wait_loads<S - 1>(nk - 1);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     wg_barrier();
   }
 };
@@ -391,7 +435,7 @@ template <typename TL, bool kGated, typename O, int NI>
 __device__ __forceinline__ void put_tile(const MxEpilogue<O>& E, const v4f (&acc)[NI][TL::TJ],
                                          int64_t wrow0, int64_t wcol0, int lane, float* mine,
                                          float* __restrict__ part) {
-  using T = MxTile<TL, kGated>;
+  constexpr int kWaveCols = kGated ? TL::WN / 2 : TL::WN;
   constexpr int TJ = TL::TJ, kPairs = kGated ? TJ / 2 : TJ;
   const int frow = lane & 15, quarter = lane >> 4;
   if (part) {
@@ -404,7 +448,7 @@ __device__ __forceinline__ void put_tile(const MxEpilogue<O>& E, const v4f (&acc
     return;
   }
   typedef O V8 __attribute__((ext_vector_type(8), aligned(sizeof(O))));
-  constexpr int kLanes = T::kWaveCols / 8, kRows = 64 / kLanes;   // lanes of a row, rows at once
+  constexpr int kLanes = kWaveCols / 8, kRows = 64 / kLanes;   // lanes of a row, rows at once
   constexpr int kIters = TL::kPhase * 16 / kRows, kPhases = NI / TL::kPhase;
   constexpr int kAhead = kIters * kPhases < 4 ? kIters * kPhases : 4;
   static_assert(kIters >= 1 && kIters * kRows == TL::kPhase * 16, "whole groups of rows");
@@ -448,8 +492,8 @@ __device__ __forceinline__ void put_tile(const MxEpilogue<O>& E, const v4f (&acc
       const v4f hi = *reinterpret_cast<const v4f*>(from + 4);
       v4f ulo, uhi;
       if constexpr (kGated) {
-        ulo = *reinterpret_cast<const v4f*>(from + T::kWaveCols);
-        uhi = *reinterpret_cast<const v4f*>(from + T::kWaveCols + 4);
+        ulo = *reinterpret_cast<const v4f*>(from + kWaveCols);
+        uhi = *reinterpret_cast<const v4f*>(from + kWaveCols + 4);
       }
       const V8 r0 = res[0];
 #pragma unroll
@@ -457,7 +501,7 @@ __device__ __forceinline__ void put_tile(const MxEpilogue<O>& E, const v4f (&acc
       if ((ph * kIters + it + kAhead) < kPhases * kIters) ahead(kAhead - 1, row + kAhead * kRows);
       if (row >= E.m) continue;
       if (!whole) {
-        put_ragged<kGated>(E, row, col, from, T::kWaveCols);
+        put_ragged<kGated>(E, row, col, from, kWaveCols);
         continue;
       }
       float z[8];
@@ -487,12 +531,13 @@ __global__ __launch_bounds__(64 * TL::NW) void mxfp4_tile_kernel(int steps, Line
                                                                  int tiles_n, int splits,
                                                                  int group_m,
                                                                  float* __restrict__ part) {
-  using T = MxTile<TL, kGated>;
-  constexpr int BM = TL::BM, TI = TL::TI, TJ = TL::TJ, S = TL::S, L = T::kLoads;
+  using T = MxTile<TL, kGated, 2>;
+  constexpr int BM = TL::BM, TI = TL::TI, TJ = TL::TJ, S = TL::S, L = TL::kLoads;
   static_assert(TL::KG == 1, "one wave for both K halves");
   __shared__ __attribute__((aligned(1024))) int8_t lds[T::kBytes];
   const Place p(steps, tiles_m * tiles_n, splits);
-  const MxWalk<TL, kGated> K(lds, E.m, E.n, X, W, p.tile, tiles_m, tiles_n, group_m, p.t0, p.nk);
+  const MxWalk<T, TL, kGated> K(lds, E.m, E.n, X, W, p.tile, tiles_m, tiles_n, group_m, p.t0, p.nk,
+                                steps);
   const int wr = K.wave / TL::WC, wc = K.wave % TL::WC, nk = K.nk;
 
   v4f acc[TI][TJ];
@@ -501,30 +546,33 @@ __global__ __launch_bounds__(64 * TL::NW) void mxfp4_tile_kernel(int steps, Line
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = v4f{0, 0, 0, 0};
 
-  const int frow = K.lane & 15, quarter = K.lane >> 4, sw = frow >> 1;
+  const int frow = K.lane & 15, quarter = K.lane >> 4, sw = swizzle(frow);
   const int off0 = ((2 * quarter) ^ sw) << 4, off1 = ((2 * quarter + 1) ^ sw) << 4;
   const int aline = wr * TL::WM + frow, bline = BM + wc * TL::WN + frow;
   v4i fa[2][2][2], fb[2][TJ];   // fa[set][K half][row block of a quarter], fb[K half][block]
   int sa[2][2], sb[TJ];         // scales of both K halves
+  auto two_scales = [&](int t, int line) -> int {
+    return *reinterpret_cast<const uint16_t*>(K.scales(t) + line * 32 + 2 * quarter);
+  };
   auto read_a = [&](int set, int t, int kh, int rb, int ii) {
     fa[set][kh][ii] = *reinterpret_cast<const v4i*>(K.stage(t) + (aline + 16 * rb) * kStepK +
                                                     (kh ? off1 : off0));
-    if (kh == 0) sa[set][ii] = K.scales(t)[(aline + 16 * rb) * 4 + quarter];
+    if (kh == 0) sa[set][ii] = two_scales(t, aline + 16 * rb);
   };
   auto read_b = [&](int t, int kh, int j) {
     fb[kh][j] = *reinterpret_cast<const v4i*>(K.stage(t) + (bline + 16 * j) * kStepK +
                                               (kh ? off1 : off0));
   };
-  auto read_sb = [&](int t, int j) { sb[j] = K.scales(t)[(bline + 16 * j) * 4 + quarter]; };
+  auto read_sb = [&](int t, int j) { sb[j] = two_scales(t, bline + 16 * j); };
   // Quarter q (row blocks 2q and 2q + 1): MFMA idx is row block 2q + idx / (2 TJ), column block
   // (idx / 2) % TJ, K half idx % 2, a block's two halves back to back.  Its first four MFMAs
   // are followed by the reads of the next quarter's A fragments into the other set (the last
   // quarter's: row blocks 0 and 1 of step `next`); the last quarter also replaces each B
-  // fragment after its last use and issues the loads of step t + S, if there is one.  (The empty
-  // asm keeps the compiler from moving MFMAs past that branch, out of their order.)
+  // fragment after its last use and issues the loads of step t + S, if there is one (more), and of
+  // scales (asks).
   constexpr int NQ = TI / 2, kQuarter = 4 * TJ;
   static_assert(NQ % 2 == 0 && L <= kQuarter, "sets alternate; loads fit a quarter");
-  auto quarter_of = [&](int q, int t, int next) {
+  auto quarter_of = [&](int q, int t, int next, uint32_t more, uint32_t asks) {
     const int as = q & 1;
     const bool is_last = q == NQ - 1;
 #pragma unroll
@@ -533,7 +581,6 @@ __global__ __launch_bounds__(64 * TL::NW) void mxfp4_tile_kernel(int steps, Line
       v4f& a = acc[2 * q + ii][j];
       a = kh ? mfma_mx<1>(fb[1][j], sb[j], fa[as][1][ii], sa[as][ii], a)
              : mfma_mx<0>(fb[0][j], sb[j], fa[as][0][ii], sa[as][ii], a);
-      asm volatile("" : "+v"(a));
       if (idx < 4) {
         if (!is_last) read_a(as ^ 1, t, idx & 1, 2 * (q + 1) + (idx >> 1), idx >> 1);
         else read_a(as ^ 1, next, idx & 1, idx >> 1, idx >> 1);
@@ -542,8 +589,10 @@ __global__ __launch_bounds__(64 * TL::NW) void mxfp4_tile_kernel(int steps, Line
         read_b(next, kh, j);
         if (kh) read_sb(next, j);
       }
-      if (is_last && (idx * L) / kQuarter != ((idx + 1) * L) / kQuarter && t + S < nk)
-        K.load(t + S, (idx * L) / kQuarter);
+      if (is_last && (idx * L) / kQuarter != ((idx + 1) * L) / kQuarter)
+        K.load(more, t + S, (idx * L) / kQuarter);
+      if (is_last && idx >= kQuarter - T::kScaleLoads)
+        K.load_scales(asks, K.next_group(t), idx - (kQuarter - T::kScaleLoads));
       __builtin_amdgcn_sched_barrier(0);
       // the wave that reaches the second half of a quarter first is preferred, so the two
       // waves of a SIMD run apart
@@ -564,7 +613,7 @@ __global__ __launch_bounds__(64 * TL::NW) void mxfp4_tile_kernel(int steps, Line
   for (int t = 0; t < nk; ++t) {
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int q = 0; q < NQ - 1; ++q) quarter_of(q, t, t);
+    for (int q = 0; q < NQ - 1; ++q) quarter_of(q, t, t, 0, 0);
     // this wave's loads of step t + 1 have landed and it has read all of step t; past the
     // barrier that holds for every wave
     K.template wait_loads<S - 2>(nk - 2 - t);
@@ -572,7 +621,7 @@ __global__ __launch_bounds__(64 * TL::NW) void mxfp4_tile_kernel(int steps, Line
     wg_barrier();
     __builtin_amdgcn_sched_barrier(0);
     // after the last step: a harmless re-read of it
-    quarter_of(NQ - 1, t, t + 1 < nk ? t + 1 : t);
+    quarter_of(NQ - 1, t, t + 1 < nk ? t + 1 : t, t + S < nk, K.asks(t));
   }
   wg_barrier();   // every wave is past its last read of the ring
   put_tile<TL, kGated, O, TI>(
@@ -586,19 +635,21 @@ __global__ __launch_bounds__(64 * TL::NW) void mxfp4_tile_kernel(int steps, Line
 // waves shares the outputs of a wave and splits each step's K, a block of every two; the sums of both
 // meet in LDS at the end.  Behind the barrier of step t the wave reads step t + 1 and asks for step
 // t + S while step t's MFMAs run from registers.
-template <typename O, bool kGated, typename TL>
+template <typename O, bool kGated, typename TL, int kBufs>
 __global__ __launch_bounds__(64 * TL::NW) void mxfp4_small_kernel(int steps, Lines X, Lines W,
                                                                   MxEpilogue<O> E, int tiles_m,
                                                                   int tiles_n, int splits,
                                                                   int group_m,
                                                                   float* __restrict__ part) {
-  using T = MxTile<TL, kGated>;
-  constexpr int BM = TL::BM, TI = TL::TI, TJ = TL::TJ, S = TL::S, L = T::kLoads, H = TI / 2;
-  static_assert(TL::KG == 2 && TI % 2 == 0 && L <= TI * TJ, "pairs of waves");
+  using T = MxTile<TL, kGated, kBufs>;
+  constexpr int BM = TL::BM, TI = TL::TI, TJ = TL::TJ, S = TL::S, L = TL::kLoads, H = TI / 2;
+  constexpr int LS = T::kScaleLoads;
+  static_assert(TL::KG == 2 && TI % 2 == 0 && L + LS <= TI * TJ, "pairs of waves");
   static_assert(TL::NW * H * TJ * 1024 <= S * TL::kStage, "halves fit the ring");
   __shared__ __attribute__((aligned(1024))) int8_t lds[T::kBytes];
   const Place p(steps, tiles_m * tiles_n, splits);
-  const MxWalk<TL, kGated> K(lds, E.m, E.n, X, W, p.tile, tiles_m, tiles_n, group_m, p.t0, p.nk);
+  const MxWalk<T, TL, kGated> K(lds, E.m, E.n, X, W, p.tile, tiles_m, tiles_n, group_m, p.t0, p.nk,
+                                steps);
   const int kh = K.wave / (TL::WR * TL::WC), wt = K.wave % (TL::WR * TL::WC);
   const int wr = wt / TL::WC, wc = wt % TL::WC, nk = K.nk;
 
@@ -608,23 +659,23 @@ __global__ __launch_bounds__(64 * TL::NW) void mxfp4_small_kernel(int steps, Lin
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = v4f{0, 0, 0, 0};
 
-  const int frow = K.lane & 15, quarter = K.lane >> 4, sw = frow >> 1;
+  const int frow = K.lane & 15, quarter = K.lane >> 4, sw = swizzle(frow);
   const int off = ((2 * quarter + kh) ^ sw) << 4, soff = 2 * quarter + kh;
   const int aline = wr * TL::WM + frow, bline = BM + wc * TL::WN + frow;
   v4i fa[2][TI], fb[2][TJ];
   int sa[2][TI], sb[2][TJ];
   auto read = [&](int set, int t) {
     const int8_t* st = K.stage(t) + off;
-    const uint8_t* sc = reinterpret_cast<const uint8_t*>(K.scales(t)) + soff;
+    const uint8_t* sc = K.scales(t) + soff;
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
       fb[set][j] = *reinterpret_cast<const v4i*>(st + (bline + 16 * j) * kStepK);
-      sb[set][j] = sc[(bline + 16 * j) * 8];
+      sb[set][j] = sc[(bline + 16 * j) * 32];
     }
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
       fa[set][i] = *reinterpret_cast<const v4i*>(st + (aline + 16 * i) * kStepK);
-      sa[set][i] = sc[(aline + 16 * i) * 8];
+      sa[set][i] = sc[(aline + 16 * i) * 32];
     }
   };
   auto step = [&](int set, int t) {
@@ -638,9 +689,8 @@ __global__ __launch_bounds__(64 * TL::NW) void mxfp4_small_kernel(int steps, Lin
     for (int idx = 0; idx < TI * TJ; ++idx) {
       const int i = idx / TJ, j = idx % TJ;
       acc[i][j] = mfma_mx<0>(fb[set][j], sb[set][j], fa[set][i], sa[set][i], acc[i][j]);
-      // (without this the compiler moves MFMAs past the branch, out of their order)
-      asm volatile("" : "+v"(acc[i][j]));
-      if (idx < L && t + S < nk) K.load(t + S, idx);
+      if (idx < L) K.load(t + S < nk, t + S, idx);
+      else if (idx < L + LS) K.load_scales(K.asks(t), K.next_group(t), idx - L);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -708,7 +758,7 @@ __global__ __launch_bounds__(256) void mxfp4_join_kernel(MxEpilogue<O> E, int sp
 
 typedef Tile<256, 256, 2, 4, 1, 2> MxLarge;
 typedef Tile<128, 128, 2, 2, 2, 4> MxMid;
-typedef Tile<64, 128, 1, 4, 2, 6> MxSmall;
+typedef Tile<64, 128, 1, 4, 2, 5> MxSmall;
 
 // How a product is run: by the kernel for few rows (a workgroup takes all rows) or by tiles of
 // one shape; K is split over `splits` workgroups where there are fewer tiles than the compute
@@ -766,7 +816,7 @@ void launch_tiles(const Plan& p, int steps, const Lines& X, const Lines& W, cons
     hipLaunchKernelGGL((mxfp4_tile_kernel<O, kGated, TL>), grid, block, 0, s, steps, X, W, E,
                        (int)p.tiles_m, (int)p.tiles_n, p.splits, group_m, part);
   else
-    hipLaunchKernelGGL((mxfp4_small_kernel<O, kGated, TL>), grid, block, 0, s, steps, X, W, E,
+    hipLaunchKernelGGL((mxfp4_small_kernel<O, kGated, TL, TL::S <= 4 ? 2 : 3>), grid, block, 0, s, steps, X, W, E,
                        (int)p.tiles_m, (int)p.tiles_n, p.splits, group_m, part);
 }
 
