@@ -427,12 +427,13 @@ struct Place {
 };
 
 // The outputs of a wave's NI x TJ blocks (lane l of block (i, j): row 16 i + l % 16, columns
-// 16 j + 4 (l / 16) .. + 3), or their partial sums.  The blocks are staged through this wave's
-// part `mine` of the ring so that a few lanes finish one row of the wave's columns, eight
-// consecutive outputs each.  Residuals are asked for four groups of rows ahead.  The loop over the
-// groups of a phase is kept a loop: written out, the epilogue does not fit the instruction cache.
+// 16 j + 4 (l / 16) .. + 3), or their partial sums.  A phase of the blocks is staged through this
+// wave's part `mine` of the ring so that a few lanes finish one row of the wave's columns, eight
+// consecutive outputs each; a phase's groups of rows are finished together, for their instructions'
+// latencies, and the next phase's residuals asked for meanwhile.  The phases are a loop, through
+// which the blocks move down: written out they would not fit the instruction cache.
 template <typename TL, bool kGated, typename O, int NI>
-__device__ __forceinline__ void put_tile(const MxEpilogue<O>& E, const v4f (&acc)[NI][TL::TJ],
+__device__ __forceinline__ void put_tile(const MxEpilogue<O>& E, v4f (&acc)[NI][TL::TJ],
                                          int64_t wrow0, int64_t wcol0, int lane, float* mine,
                                          float* __restrict__ part) {
   constexpr int kWaveCols = kGated ? TL::WN / 2 : TL::WN;
@@ -450,19 +451,14 @@ __device__ __forceinline__ void put_tile(const MxEpilogue<O>& E, const v4f (&acc
   typedef O V8 __attribute__((ext_vector_type(8), aligned(sizeof(O))));
   constexpr int kLanes = kWaveCols / 8, kRows = 64 / kLanes;   // lanes of a row, rows at once
   constexpr int kIters = TL::kPhase * 16 / kRows, kPhases = NI / TL::kPhase;
-  constexpr int kAhead = kIters * kPhases < 4 ? kIters * kPhases : 4;
   static_assert(kIters >= 1 && kIters * kRows == TL::kPhase * 16, "whole groups of rows");
   const int lrow = lane / kLanes, lcol = 8 * (lane % kLanes);
   const int64_t col = wcol0 + lcol;
   const bool whole = col + 8 <= E.n;
+  // every row and column of the wave's is C's (the usual case): no checks
+  const bool inside = wrow0 + 16 * NI <= E.m && wcol0 + kWaveCols <= E.n;
+  const float* const from = mine + lrow * TL::kPitch + lcol;
   float b[8], bu[8];
-  V8 res[kAhead];
-  auto ahead = [&](int slot, int64_t row) {
-    if (!kGated && row < E.m && E.residual && whole)
-      res[slot] = *reinterpret_cast<const V8*>(E.residual + row * E.ldr + col);
-  };
-#pragma unroll
-  for (int u = 0; u < kAhead; ++u) ahead(u, wrow0 + u * kRows + lrow);
 #pragma unroll
   for (int u = 0; u < 8; ++u) b[u] = bu[u] = 0.0f;
   if (whole && E.bias) {
@@ -475,47 +471,86 @@ __device__ __forceinline__ void put_tile(const MxEpilogue<O>& E, const v4f (&acc
       for (int u = 0; u < 8; ++u) bu[u] = (float)uv[u];
     }
   }
+  V8 res[kIters];
+  auto ask = [&](int64_t row0) {
+    if (kGated || !E.residual || !inside) return;
 #pragma unroll
+    for (int it = 0; it < kIters; ++it)
+      res[it] =
+          *reinterpret_cast<const V8*>(E.residual + (row0 + it * kRows + lrow) * E.ldr + col);
+  };
+  ask(wrow0);
+#pragma unroll 1
   for (int ph = 0; ph < kPhases; ++ph) {
+    const int64_t row0 = wrow0 + ph * (TL::kPhase * 16);
 #pragma unroll
     for (int i = 0; i < TL::kPhase; ++i)
 #pragma unroll
       for (int j = 0; j < TJ; ++j)
         *reinterpret_cast<v4f*>(mine + (16 * i + frow) * TL::kPitch + 16 * j + 4 * quarter) =
-            acc[ph * TL::kPhase + i][j];
+            acc[i][j];
+#pragma unroll
+    for (int i = 0; i + TL::kPhase < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) acc[i][j] = acc[i + TL::kPhase][j];
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll 1
-    for (int it = 0; it < kIters; ++it) {
-      const int64_t row = wrow0 + (ph * kIters + it) * kRows + lrow;
-      const float* from = mine + (it * kRows + lrow) * TL::kPitch + lcol;
-      const v4f lo = *reinterpret_cast<const v4f*>(from);
-      const v4f hi = *reinterpret_cast<const v4f*>(from + 4);
-      v4f ulo, uhi;
-      if constexpr (kGated) {
-        ulo = *reinterpret_cast<const v4f*>(from + kWaveCols);
-        uhi = *reinterpret_cast<const v4f*>(from + kWaveCols + 4);
-      }
-      const V8 r0 = res[0];
+    if (inside) {
+      float z[kIters * 8], up[kGated ? kIters * 8 : 1];
 #pragma unroll
-      for (int u = 0; u + 1 < kAhead; ++u) res[u] = res[u + 1];
-      if ((ph * kIters + it + kAhead) < kPhases * kIters) ahead(kAhead - 1, row + kAhead * kRows);
-      if (row >= E.m) continue;
-      if (!whole) {
-        put_ragged<kGated>(E, row, col, from, kWaveCols);
-        continue;
-      }
-      float z[8];
+      for (int it = 0; it < kIters; ++it)
 #pragma unroll
-      for (int u = 0; u < 8; ++u) z[u] = (u < 4 ? lo[u & 3] : hi[u & 3]) + b[u];
+        for (int h = 0; h < 2; ++h) {
+          const float* p = from + it * kRows * TL::kPitch + 4 * h;
+          const v4f v = *reinterpret_cast<const v4f*>(p);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) z[8 * it + 4 * h + u] = v[u] + b[4 * h + u];
+          if constexpr (kGated) {
+            const v4f w = *reinterpret_cast<const v4f*>(p + kWaveCols);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) up[8 * it + 4 * h + u] = w[u] + bu[4 * h + u];
+          }
+        }
       activate_all<sizeof(O) == 4>(z, E.act);
-      V8 o;
+      if (!kGated && E.residual)
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        if constexpr (kGated) z[u] *= (u < 4 ? ulo[u & 3] : uhi[u & 3]) + bu[u];
-        else if (E.residual) z[u] += (float)r0[u];
-        o[u] = (O)z[u];
+        for (int u = 0; u < kIters * 8; ++u) z[u] += (float)res[u / 8][u % 8];
+      if (ph + 1 < kPhases) ask(row0 + TL::kPhase * 16);
+#pragma unroll
+      for (int it = 0; it < kIters; ++it) {
+        V8 o;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          float y = z[8 * it + u];
+          if constexpr (kGated) y *= up[8 * it + u];
+          o[u] = (O)y;
+        }
+        *reinterpret_cast<V8*>(E.c + (row0 + it * kRows + lrow) * E.ldc + col) = o;
       }
-      *reinterpret_cast<V8*>(E.c + row * E.ldc + col) = o;
+    } else {
+#pragma unroll 1
+      for (int it = 0; it < kIters; ++it) {
+        const int64_t row = row0 + it * kRows + lrow;
+        const float* p = from + it * kRows * TL::kPitch;
+        if (row >= E.m || col >= E.n) continue;
+        if (!whole) {
+          put_ragged<kGated>(E, row, col, p, kWaveCols);
+          continue;
+        }
+        float z[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) z[u] = p[u] + b[u];
+        activate_all<sizeof(O) == 4>(z, E.act);
+        V8 o, r;
+        if (!kGated && E.residual)
+          r = *reinterpret_cast<const V8*>(E.residual + row * E.ldr + col);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          if constexpr (kGated) z[u] *= p[kWaveCols + u] + bu[u];
+          else if (E.residual) z[u] += (float)r[u];
+          o[u] = (O)z[u];
+        }
+        *reinterpret_cast<V8*>(E.c + row * E.ldc + col) = o;
+      }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
