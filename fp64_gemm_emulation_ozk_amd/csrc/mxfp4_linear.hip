@@ -138,38 +138,40 @@ __device__ __forceinline__ void put_parts(const MxEpilogue<O>& E, float* __restr
     if (col < E.n) put_part(p + E.n, row, col, E.m, E.n, wide, up);
 }
 
-// Up to 16 rows: workgroup = 16 columns of C (gated: of both projections), its eight waves taking
-// the K steps of 256 codes in turn (of the workgroup's split of K).  Each wave streams its steps
-// through a ring of its own in LDS by direct loads of 8 lines x 128 bytes and of 32 lines' 8 scales.
-// No barriers: a wave waits for its own loads, reads its fragments and refills the slot.
-// kXR rows of X (8 for up to 8) travel with each step.
-template <typename O, bool kGated, int kXR, int kS>
+// Few rows: workgroup = 16 kNT columns of C (gated: of both projections) and all rows, its eight
+// waves taking the K steps of 256 codes in turn (of the workgroup's split of K).  Each wave streams
+// its steps through a ring of its own in LDS by direct loads of 8 lines x 128 bytes and of 32 lines' 8
+// scales.  No barriers: a wave waits for its own loads, reads its fragments and refills the slot, so
+// that eight slots are under way even where a wave has but one.  kXR rows of X (8 to 64) travel
+// with each step.
+template <typename O, bool kGated, int kXR, int kNT, int kS>
 __global__ __launch_bounds__(512) void mxfp4_stream_kernel(int steps, Lines X, Lines W,
                                                            MxEpilogue<O> E, int splits,
                                                            float* __restrict__ part) {
-  constexpr int kG = kGated ? 2 : 1, kWaves = 8, kRows = 16 * kG + kXR;
+  constexpr int kG = kGated ? 2 : 1, kB = kNT * kG, kMT = kXR < 16 ? 1 : kXR / 16, kWaves = 8;
+  constexpr int kRows = 16 * kB + kXR;
   constexpr int kCodes = kRows * 128, LC = kRows / 8, LS = (kRows + 31) / 32, L = LC + LS;
   constexpr int kSlot = kCodes + LS * 256;
   __shared__ __attribute__((aligned(1024))) int8_t lds[kWaves * kS * kSlot];
-  static_assert(kWaves * kG * 1024 <= kWaves * kS * kSlot, "the sums fit the ring");
-  static_assert(L * (kS - 1) <= 63, "the load counter's range");
+  static_assert(kWaves * kMT * kB * 1024 <= kWaves * kS * kSlot, "the sums fit the ring");
+  static_assert(kS >= 1 && kS <= 3 && L * (kS - 1) <= 63, "the load counter's range");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int split = blockIdx.x % splits;
-  const int64_t col0 = (int64_t)(blockIdx.x / splits) * 16;
+  const int64_t col0 = (int64_t)(blockIdx.x / splits) * (16 * kNT);
   const int t0 = (int)((int64_t)steps * split / splits) + wave;
   const int t1 = (int)((int64_t)steps * (split + 1) / splits);
   const int own = t0 < t1 ? (t1 - t0 + kWaves - 1) / kWaves : 0;   // steps t0 + 8 i
   // line r of a step: of W's gate, of its other projection, then of X; lines past the operand
   // re-read its last
   auto line = [&](int r, bool& is_w) -> int64_t {
-    is_w = r < 16 * kG;
+    is_w = r < 16 * kB;
     if (!is_w) {
-      const int64_t row = r - 16 * kG;
+      const int64_t row = r - 16 * kB;
       return row < E.m ? row : E.m - 1;
     }
-    const int64_t col = col0 + (r & 15);
-    return (col < E.n ? col : E.n - 1) + (kGated && r >= 16 ? E.n : 0);
+    const int64_t col = col0 + r % (16 * kNT);
+    return (col < E.n ? col : E.n - 1) + (kGated && r >= 16 * kNT ? E.n : 0);
   };
   // load q: lines 8 q .. 8 q + 7; lane i takes line i / 8 of them, physical chunk i % 8, which
   // holds logical chunk (i % 8) ^ swizzle(line)
@@ -198,17 +200,18 @@ __global__ __launch_bounds__(512) void mxfp4_stream_kernel(int steps, Lines X, L
     for (int q = 0; q < LS; ++q)
       dma4(from[LC + q] + (int64_t)i * (kWaves * 8), slot + kCodes + q * 256);
   };
-  const int frow = lane & 15, quarter = lane >> 4, xrow = 16 * kG + (frow & (kXR - 1));
-  v4f acc[kG];
+  const int frow = lane & 15, quarter = lane >> 4, xrow = 16 * kB + (frow & (kXR - 1));
+  v4f acc[kMT][kB];
 #pragma unroll
-  for (int g = 0; g < kG; ++g) acc[g] = v4f{0, 0, 0, 0};
+  for (int i = 0; i < kMT; ++i)
+#pragma unroll
+    for (int j = 0; j < kB; ++j) acc[i][j] = v4f{0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < kS; ++i)
     if (i < own) load(i);
   for (int i = 0; i < own; ++i) {
     const int younger = own - 1 - i;
     if (younger >= kS - 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L * (kS - 1)) : "memory");
-    else if (kS > 3 && younger == 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L * 2) : "memory");
     else if (kS > 2 && younger == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L) : "memory");
     else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     const int8_t* slot = lds + wave * (kS * kSlot) + (i % kS) * kSlot;
@@ -219,42 +222,54 @@ __global__ __launch_bounds__(512) void mxfp4_stream_kernel(int steps, Lines X, L
     auto scale = [&](int r) -> int {
       return *reinterpret_cast<const uint16_t*>(slot + kCodes + r * 8 + 2 * quarter);
     };
-    v4i fb[2][kG], fa[2];
-    int sb[kG];
+    v4i fb[2][kB], fa[2][kMT];
+    int sb[kB], sa[kMT];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int g = 0; g < kG; ++g) fb[h][g] = codes(16 * g + frow, h);
-      fa[h] = codes(xrow, h);
+      for (int j = 0; j < kB; ++j) fb[h][j] = codes(16 * j + frow, h);
+#pragma unroll
+      for (int u = 0; u < kMT; ++u) fa[h][u] = codes(xrow + 16 * u, h);
     }
 #pragma unroll
-    for (int g = 0; g < kG; ++g) sb[g] = scale(16 * g + frow);
-    const int sa = scale(xrow);
+    for (int j = 0; j < kB; ++j) sb[j] = scale(16 * j + frow);
+#pragma unroll
+    for (int u = 0; u < kMT; ++u) sa[u] = scale(xrow + 16 * u);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
     if (i + kS < own) load(i + kS);
 #pragma unroll
-    for (int g = 0; g < kG; ++g) {
-      acc[g] = mfma_mx<0>(fb[0][g], sb[g], fa[0], sa, acc[g]);
-      acc[g] = mfma_mx<1>(fb[1][g], sb[g], fa[1], sa, acc[g]);
-    }
+    for (int u = 0; u < kMT; ++u)
+#pragma unroll
+      for (int j = 0; j < kB; ++j) {
+        acc[u][j] = mfma_mx<0>(fb[0][j], sb[j], fa[0][u], sa[u], acc[u][j]);
+        acc[u][j] = mfma_mx<1>(fb[1][j], sb[j], fa[1][u], sa[u], acc[u][j]);
+      }
   }
   // every wave is past its ring: the sums take its first bytes
   __syncthreads();
   v4f* sums = reinterpret_cast<v4f*>(lds);
 #pragma unroll
-  for (int g = 0; g < kG; ++g) sums[(g * kWaves + wave) * 64 + lane] = acc[g];
+  for (int i = 0; i < kMT; ++i)
+#pragma unroll
+    for (int j = 0; j < kB; ++j) sums[((i * kB + j) * kWaves + wave) * 64 + lane] = acc[i][j];
   __syncthreads();
-  if (wave) return;
+  for (int b = wave; b < kMT * kNT; b += kWaves) {
+    const int i = b / kNT, j = b % kNT;
+    v4f s[kG];
 #pragma unroll
-  for (int g = 0; g < kG; ++g)
+    for (int g = 0; g < kG; ++g) {
+      const v4f* p = sums + (i * kB + g * kNT + j) * kWaves * 64 + lane;
+      s[g] = p[0];
 #pragma unroll
-    for (int v = 1; v < kWaves; ++v) acc[g] += sums[(g * kWaves + v) * 64 + lane];
-  const int64_t row = frow, col = col0 + 4 * quarter;
-  if (part)
-    put_parts<kGated>(E, part + split * E.m * E.n * kG, row, col, acc[0], acc[kG - 1]);
-  else
-    put4<kGated>(E, row, col, acc[0], acc[kG - 1]);
+      for (int v = 1; v < kWaves; ++v) s[g] += p[v * 64];
+    }
+    const int64_t row = 16 * i + frow, col = col0 + 16 * j + 4 * quarter;
+    if (part)
+      put_parts<kGated>(E, part + split * E.m * E.n * kG, row, col, s[0], s[kG - 1]);
+    else
+      put4<kGated>(E, row, col, s[0], s[kG - 1]);
+  }
 }
 
 // ------------------------------------------------------------------ tiles
@@ -778,14 +793,22 @@ __global__ __launch_bounds__(256) void mxfp4_join_kernel(MxEpilogue<O> E, int sp
   for (int g = 0; g < kG; ++g) {
     s[g] = v4f{0, 0, 0, 0};
     const float* p = part + row * (kG * E.n) + g * E.n + col;
-    for (int k = 0; k < splits; ++k, p += E.m * E.n * kG) {
-      if (col + 4 <= E.n) {
-        s[g] += *reinterpret_cast<const v4f_words*>(p);
-      } else {
+    const int64_t apart = E.m * E.n * kG;
+    if (col + 4 <= E.n) {
+      int k = 0;
+      for (; k + 4 <= splits; k += 4, p += 4 * apart) {   // four asked for at once
+        v4f v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[u] = *reinterpret_cast<const v4f_words*>(p + u * apart);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) s[g] += v[u];
+      }
+      for (; k < splits; ++k, p += apart) s[g] += *reinterpret_cast<const v4f_words*>(p);
+    } else {
+      for (int k = 0; k < splits; ++k, p += apart)
 #pragma unroll
         for (int u = 0; u < 4; ++u)
           if (col + u < E.n) s[g][u] += p[u];
-      }
     }
   }
   put4<kGated>(E, row, col, s[0], s[kG - 1]);
@@ -805,13 +828,20 @@ struct Plan {
   int splits;
 };
 
-// Up to 16 rows: the stream kernel.  More: the tile shape and split of the least estimated time, in
-// microseconds, of rounds of 256 workgroups that each cost `fixed` and `step` per K step.  A split
-// costs the launch of the join and the partial sums' way out and back (5 TB/s).
+// Up to 64 rows: the stream kernel (32 and 64 rows of 8192 x 8192: 8.5 and 11.6 us, by tiles of 64
+// rows 15.1 and 16.4; of 4096 x 4096: 4.5 and 5.8 against 10.9 and 12.3).  More rows: the tile shape
+// and split of the least estimated time, in microseconds, of rounds of 256 workgroups that each cost
+// `fixed` and `step` per K step.  Measured, one round of 256 and of 4096 K values: small 5.5 and
+// 13.5, mid 7.9 and 19.6, large 10.4 and 36.3.  A split costs the launch of the join (4) and the
+// partial sums' way out and back (128 x 4096 x 4096, small, in 1, 2, 4 and 8: 13.5, 14.1, 14.7, 20.6;
+// 100 x 1024 x 8192: 21.8, 16.3, 12.3, 11.4).
 Plan plan_of(int64_t m, int64_t n, int64_t k, bool gated) {
   const int64_t steps = (k + 255) / 256, wide = gated ? 2 * n : n;
-  if (m <= 16) {
-    Plan p{kStream, 1, (n + 15) / 16, 1};
+  if (m <= 64) {
+    // 16 columns a workgroup, or 32 where that is more than the compute units take at once (16 rows of
+    // 8192 x 8192: 7.0 us with 32, 9.4 with 16; of 4096 x 4096: 4.4 and 3.9)
+    const int64_t bn = (n + 15) / 16 > (m <= 8 && !gated ? 512 : 256) ? 32 : 16;
+    Plan p{kStream, bn / 16, (n + bn - 1) / bn, 1};
     // a workgroup's eight waves take four steps each at least
     const int64_t s = 256 / p.tiles_n, most = steps / 32;
     p.splits = (int)(s < most ? s : most);
@@ -823,8 +853,8 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, bool gated) {
     int64_t bm, bn;
     double fixed, step;
   };
-  const Cost costs[] = {{kSmall, 64, 128, 4.8, 0.55}, {kMid, 128, 128, 6.3, 0.72},
-                        {kLarge, 256, 256, 8.2, 1.65}};
+  const Cost costs[] = {{kSmall, 64, 128, 5.0, 0.53}, {kMid, 128, 128, 7.2, 0.71},
+                        {kLarge, 256, 256, 9.5, 1.75}};
   Plan best{};
   double least = 0;
   for (const Cost& c : costs) {
@@ -832,7 +862,7 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, bool gated) {
     for (int64_t sp = 1; sp <= 16 && (sp == 1 || (tiles * sp <= 256 && steps / sp >= 4)); ++sp) {
       const double rounds = (double)((tiles * sp + 255) / 256);
       double t = rounds * (c.fixed + c.step * (double)((steps + sp - 1) / sp));
-      if (sp > 1) t += 3.0 + (double)sp * (double)m * (double)wide * 8.0 / 5e6;
+      if (sp > 1) t += 4.0 + (double)sp * (double)m * (double)wide * 4.0 / 3.5e6;
       if (least == 0 || t < least) {
         least = t;
         best = {c.shape, tm, tn, (int)sp};
@@ -867,12 +897,19 @@ int linear_t(int64_t m, int64_t n, int64_t k, const Lines& X, const Lines& W, co
   float* const part = p.splits > 1 ? static_cast<float*>(workspace) : nullptr;
   if (p.shape == kStream) {
     const dim3 grid((unsigned)(p.tiles_n * p.splits)), block(512);
-    if (m <= 8)
-      hipLaunchKernelGGL((mxfp4_stream_kernel<O, kGated, 8, 3>), grid, block, 0, s, steps, X, W, E,
-                         p.splits, part);
-    else
-      hipLaunchKernelGGL((mxfp4_stream_kernel<O, kGated, 16, 3>), grid, block, 0, s, steps, X, W, E,
-                         p.splits, part);
+#define OZK_STREAM(XR, NT, S)                                                              \
+  hipLaunchKernelGGL((mxfp4_stream_kernel<O, kGated, XR, NT, S>), grid, block, 0, s, steps, X, W, \
+                     E, p.splits, part)
+    const bool two = p.tiles_m == 2;
+    if (m <= 8 && two) OZK_STREAM(8, 2, 2);
+    else if (m <= 8) OZK_STREAM(8, 1, 3);
+    else if (m <= 16 && two) OZK_STREAM(16, 2, kGated ? 1 : 3);
+    else if (m <= 16) OZK_STREAM(16, 1, 3);
+    else if (m <= 32 && two) OZK_STREAM(32, 2, kGated ? 1 : 2);
+    else if (m <= 32) OZK_STREAM(32, 1, 2);
+    else if (two) OZK_STREAM(64, 2, 1);
+    else OZK_STREAM(64, 1, 1);
+#undef OZK_STREAM
   } else if (p.shape == kLarge) {
     launch_tiles<O, kGated, MxLarge>(p, steps, X, W, E, part, s);
   } else if (p.shape == kMid) {
