@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+from array import array
 
 import torch
 
@@ -1223,38 +1224,36 @@ def ozk_clip_norm(tensors, max_norm: float, out=None, norm: torch.Tensor | None 
     outs = tensors if out is None else list(out)
     if not tensors:
         raise ValueError("no tensors to clip")
-    if len(outs) != len(tensors):
-        raise ValueError(f"{len(tensors)} tensors, but {len(outs)} outputs")
+    n = len(tensors)
+    if len(outs) != n:
+        raise ValueError(f"{n} tensors, but {len(outs)} outputs")
     first = tensors[0]
-    if not isinstance(first, torch.Tensor):
-        raise TypeError("tensors must be CUDA/HIP tensors")
-    index = first.get_device() if first.is_cuda else None
-    kinds = []
-    for group in ((tensors,) if outs is tensors else (tensors, outs)):
-        for t in group:
-            if not isinstance(t, torch.Tensor) or not t.is_cuda:
-                raise TypeError("tensors must be CUDA/HIP tensors")
-            if t.get_device() != index:
-                raise ValueError(f"a tensor is on {t.device}, expected {first.device}")
-            if not t.is_contiguous():
-                raise ValueError("tensors must be contiguous")
+    for t in tensors if outs is tensors else (*tensors, *outs):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError("tensors must be CUDA/HIP tensors")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+    index = first.get_device()
+    sizes = array("q", [t.numel() for t in tensors])
+    kinds = array("i", [_type(t.dtype) for t in tensors])
+    xs = array("Q", [t.data_ptr() for t in tensors])
+    ys = xs if outs is tensors else array("Q", [t.data_ptr() for t in outs])
     for t, o in zip(tensors, outs):
+        if t.get_device() != index or o.get_device() != index:
+            raise ValueError(f"a tensor is on {t.device}, its output on {o.device}, expected "
+                             f"{first.device}")
         if o is not t and (o.dtype is not t.dtype or o.shape != t.shape):
             raise ValueError(f"an output is {o.dtype} {tuple(o.shape)}, its tensor {t.dtype} "
                              f"{tuple(t.shape)}")
-        kinds.append(_type(t.dtype))
-    _check_like(norm, (), torch.float64, "norm", first.device)
+    if norm is not None:
+        _check_like(norm, (), torch.float64, "norm", first.device)
     _check_workspace(workspace, first.device)
-    n = len(tensors)
-    xs = (_ptr * n)(*[t.data_ptr() for t in tensors])
-    ys = xs if outs is tensors else (_ptr * n)(*[t.data_ptr() for t in outs])
-    sizes = (_i64 * n)(*[t.numel() for t in tensors])
-    types = (_int * n)(*kinds)
     with _On(first.device) as on:
         if norm is None:
             norm = first.new_empty((), dtype=torch.float64)
         if workspace is None:
             workspace = _workspace(ozk_clip_norm_workspace_size(n), first.device)
-        _call("ozk_clip_norm", n, xs, ys, sizes, types, float(max_norm), _at(norm),
+        at = lambda a: a.buffer_info()[0]
+        _call("ozk_clip_norm", n, at(xs), at(ys), at(sizes), at(kinds), float(max_norm), _at(norm),
               _at(workspace), workspace.numel(), on.stream(stream, norm, workspace))
     return norm, outs
