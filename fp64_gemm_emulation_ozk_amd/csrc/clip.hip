@@ -1,11 +1,15 @@
 // Clipping of many tensors to a global norm: N = (sum of all |x|^2)^(1/2), y = x min(1, M / N).
 //
-// Two passes, each one launch for up to 128 tensors, whose addresses, sizes and types travel with the
-// launch (nothing is copied to the device, so a call can be captured).  The tensors are cut into
-// chunks of 32 KiB, dealt out to at most 512 workgroups (two per compute unit).  The first pass
-// leaves each workgroup's sums, the second's workgroups all add them in the same order and scale.
+// Two passes, each one launch for up to 128 tensors, whose addresses, sizes and types travel with
+// the launch (nothing is copied to the device, so a call can be captured).  The tensors are cut into
+// chunks, dealt out to at most 512 workgroups (two per compute unit).  The first pass leaves each
+// workgroup's sums, the second's workgroups all add them in the same order and scale.
 // Squares are summed in 64 bits.  Those of fp64 values may leave its range, so they are summed
 // three times, as they are and with the values scaled by 2^-600 and 2^600.
+//
+// Memory bounds both passes.  All of a chunk's loads are in flight at once: a thread has four of 16
+// bytes in the first pass, where eight took longer (166 -> 169 us over 1.0 GB of bf16), and eight
+// in the second (406 -> 380 us with its writes of as much).
 #include "ozk_internal.h"
 #include "rows.h"
 
@@ -13,7 +17,11 @@ namespace ozk {
 namespace {
 
 constexpr int kTensors = 128, kThreads = 512, kGroups = 512;
-constexpr int64_t kChunkBytes = 32768;
+// Vectors of 16 bytes a thread takes of a chunk, in the pass that sums and in that which scales.
+constexpr int kSumVectors = 4, kScaleVectors = 8;
+
+constexpr int chunk_bytes(int vectors) { return vectors * kThreads * 16; }
+
 constexpr double kDown = 0x1p-600, kUp = 0x1p+600;
 
 struct ClipTable {
@@ -54,23 +62,23 @@ __device__ __forceinline__ int tensor_of(const ClipTable& A, int chunk) {
 }
 
 // f(vector, how many of its elements, its first element) over the chunk's vectors of 16 bytes,
-// four loads of a thread at once; its last, short vector's elements alone.
-template <typename T, typename F>
+// kV loads of a thread at once; its last, short vector's elements alone.
+template <int kV, typename T, typename F>
 __device__ __forceinline__ void each_vector(const T* x, int64_t size, int chunk, F f) {
   constexpr int N = Vec<T>::N;
   typedef typename Vec<T>::type V;
   // which chunk is the last is compared in 32 bits: of a 64-bit comparison of uniform values this
   // compiler (clang of ROCm 7.2) took the branch from vcc and the selected count from a stale scc
-  constexpr int most = kChunkBytes / (int)sizeof(T);
+  constexpr int most = chunk_bytes(kV) / (int)sizeof(T);
   const int64_t begin = (int64_t)chunk * most;
   const T* p = x + begin;
   if (chunk < (int)((size - 1) / most)) {
-    V v[4];
+    V v[kV];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < kV; ++q)
       v[q] = *reinterpret_cast<const V*>(p + (q * kThreads + threadIdx.x) * N);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) f(v[q], N, begin + (q * kThreads + threadIdx.x) * N);
+    for (int q = 0; q < kV; ++q) f(v[q], N, begin + (q * kThreads + threadIdx.x) * N);
     return;
   }
   const int count = (int)(size - begin);   // 1 .. most
@@ -89,11 +97,11 @@ __device__ __forceinline__ void each_vector(const T* x, int64_t size, int chunk,
 template <typename T>
 __device__ __forceinline__ void sum_chunk(const ClipTable& A, int t, int chunk, Squares& sum) {
   Squares s;
-  each_vector((const T*)A.x[t], A.size[t], chunk,
-              [&](const typename Vec<T>::type& v, int, int64_t) {
+  each_vector<kSumVectors>((const T*)A.x[t], A.size[t], chunk,
+                           [&](const typename Vec<T>::type& v, int, int64_t) {
 #pragma unroll
-                for (int u = 0; u < Vec<T>::N; ++u) add_square(s, v[u]);
-              });
+                             for (int u = 0; u < Vec<T>::N; ++u) add_square(s, v[u]);
+                           });
   sum.mid += s.mid;
   // of the other types nothing is past the range but Inf itself, and nothing below 2^-298
   sum.low += sizeof(T) == 8 ? s.low : s.mid * kDown * kDown;
@@ -103,8 +111,6 @@ __device__ __forceinline__ void sum_chunk(const ClipTable& A, int t, int chunk, 
 __device__ __forceinline__ double block_sum(double v, double* slot) {
   return row_all<kThreads>(v, SumOp(), slot);
 }
-
-static_assert(kChunkBytes == 4 * kThreads * 16, "four vectors a thread");
 
 __global__ __launch_bounds__(kThreads) void clip_sums_kernel(ClipTable A,
                                                              double* __restrict__ part) {
@@ -134,23 +140,25 @@ template <typename T>
 __device__ __forceinline__ void scale_chunk(const ClipTable& A, int t, int chunk,
                                             double coef) {
   T* out = (T*)A.out[t];
-  each_vector((const T*)A.x[t], A.size[t], chunk,
-              [&](const typename Vec<T>::type& v, int count, int64_t at) {
-                typename Vec<T>::type o;
+  each_vector<kScaleVectors>(
+      (const T*)A.x[t], A.size[t], chunk,
+      [&](const typename Vec<T>::type& v, int count, int64_t at) {
+        typename Vec<T>::type o;
 #pragma unroll
-                for (int u = 0; u < Vec<T>::N; ++u) {
-                  const double y = (double)v[u] * coef;
-                  if constexpr (sizeof(T) == 8) o[u] = y;
-                  else o[u] = (T)(float)y;
-                }
-                if (count == Vec<T>::N) {
-                  *reinterpret_cast<typename Vec<T>::type*>(out + at) = o;
-                } else {
+        for (int u = 0; u < Vec<T>::N; ++u) {
+          const double y = (double)v[u] * coef;
+          // to 16 bits by way of fp32, which is off a direct rounding by 2^-24 at most
+          if constexpr (sizeof(T) == 8) o[u] = y;
+          else o[u] = (T)(float)y;
+        }
+        if (count == Vec<T>::N) {
+          *reinterpret_cast<typename Vec<T>::type*>(out + at) = o;
+        } else {
 #pragma unroll
-                  for (int u = 0; u < Vec<T>::N; ++u)
-                    if (u < count) out[at + u] = o[u];
-                }
-              });
+          for (int u = 0; u < Vec<T>::N; ++u)
+            if (u < count) out[at + u] = o[u];
+        }
+      });
 }
 
 // in_place: every out is its x, so that a norm within the bound leaves nothing to do.  Chunks are
@@ -194,9 +202,10 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable A,
 
 int64_t element_size(int type) { return type == OZK_F64 ? 8 : (type == OZK_F32 ? 4 : 2); }
 
-// The tensors [t, t + returned) of a launch: those that are not empty, up to kTensors of them.
+// The tensors [t, t + returned) of a launch: those that are not empty, up to kTensors of them,
+// in chunks of `bytes`.
 int64_t fill_table(ClipTable& A, int64_t t, int64_t count, const void* const* x, void* const* out,
-                   const int64_t* sizes, const int* types, bool* in_place) {
+                   const int64_t* sizes, const int* types, int64_t bytes, bool* in_place) {
   A.count = A.chunks = 0;
   int64_t i = t;
   for (; i < count && A.count < kTensors; ++i) {
@@ -206,7 +215,7 @@ int64_t fill_table(ClipTable& A, int64_t t, int64_t count, const void* const* x,
     A.size[A.count] = sizes[i];
     A.type[A.count] = (uint8_t)types[i];
     A.first[A.count] = A.chunks;
-    A.chunks += (int)((sizes[i] * element_size(types[i]) + kChunkBytes - 1) / kChunkBytes);
+    A.chunks += (int)((sizes[i] * element_size(types[i]) + bytes - 1) / bytes);
     *in_place = *in_place && x[i] == out[i];
     ++A.count;
   }
@@ -227,7 +236,7 @@ int launch_clip_norm(int64_t count, const void* const* x, void* const* out, cons
   int parts = 0;
   bool in_place = true;
   for (int64_t t = 0; t < count;) {
-    t += fill_table(A, t, count, x, out, sizes, types, &in_place);
+    t += fill_table(A, t, count, x, out, sizes, types, chunk_bytes(kSumVectors), &in_place);
     if (A.chunks == 0) continue;
     const int groups = A.chunks < kGroups ? A.chunks : kGroups;
     hipLaunchKernelGGL(clip_sums_kernel, dim3(groups), dim3(kThreads), 0, s, A,
@@ -236,7 +245,7 @@ int launch_clip_norm(int64_t count, const void* const* x, void* const* out, cons
   }
   bool first = true;
   for (int64_t t = 0; t < count || first;) {
-    t += fill_table(A, t, count, x, out, sizes, types, &in_place);
+    t += fill_table(A, t, count, x, out, sizes, types, chunk_bytes(kScaleVectors), &in_place);
     if (A.chunks == 0 && !(first && t >= count)) continue;
     const int groups = A.chunks < kGroups ? (A.chunks > 0 ? A.chunks : 1) : kGroups;
     hipLaunchKernelGGL(clip_scale_kernel, dim3(groups), dim3(kThreads), 0, s, A, part, parts,
