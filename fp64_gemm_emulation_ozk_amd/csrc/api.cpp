@@ -1277,10 +1277,13 @@ struct Span {
   bool operator<(const Span& o) const { return from < o.from; }
 };
 
-// Whether an output overlaps another, or an input other than the one it is.
+// Whether an output, norm among them, overlaps another, or an input other than the one it is.
+// spans: count + 1 of them.
 bool clip_overlaps(int64_t count, const void* const* x, void* const* out, const int64_t* sizes,
-                   const int* types, Span* spans) {
+                   const int* types, const double* norm, Span* spans) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(norm);
   int64_t n = 0;
+  spans[n++] = {at, at + sizeof(double), -1};
   for (int64_t i = 0; i < count; ++i)
     if (sizes[i] > 0) {
       const uintptr_t p = reinterpret_cast<uintptr_t>(out[i]);
@@ -1323,10 +1326,10 @@ int ozk_clip_norm(int64_t count, const void* const* x, void* const* out, const i
   if (need > workspace_bytes || (need > 0 && !workspace)) return OZK_EWORKSPACE;
   if (need > 0 && !aligned(workspace, 256)) return OZK_EINVAL;
   if (count > 0) {
-    Span few[64];
-    Span* spans = count <= 64 ? few : new (std::nothrow) Span[count];
+    Span few[65];
+    Span* spans = count <= 64 ? few : new (std::nothrow) Span[count + 1];
     if (!spans) return OZK_EUNSUPPORTED;
-    const bool bad = clip_overlaps(count, x, out, sizes, types, spans);
+    const bool bad = clip_overlaps(count, x, out, sizes, types, norm, spans);
     if (spans != few) delete[] spans;
     if (bad) return OZK_EINVAL;
   }

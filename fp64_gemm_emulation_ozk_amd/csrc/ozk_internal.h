@@ -192,8 +192,8 @@ void launch_column_join(int64_t n, int chunks, const double* part, double* out, 
 // or null) through part, act_grad_chunks(m) x 2 n sums.
 int launch_gate_grad(int64_t m, int64_t n, const double* dc, int64_t lddc, const double* z,
                      int64_t ldz, int act, double* g, double* part, double* dbias, hipStream_t s);
-// The gradient's elementwise part without a gate: g (m x n, ld n, or null) = dc * act'(z), dbias (or null) =
-// column sums of g through part, act_grad_chunks(m) x n sums.
+// The gradient's elementwise part without a gate: g (m x n, ld n, or null) = dc * act'(z), dbias
+// (or null) = column sums of g through part, act_grad_chunks(m) x n sums.
 int64_t act_grad_chunks(int64_t m);
 int launch_act_grad(int64_t m, int64_t n, const double* dc, int64_t lddc, const double* z,
                     int64_t ldz, int act, double* g, double* part, double* dbias,
@@ -257,7 +257,7 @@ int launch_mxfp4_linear(int64_t m, int64_t n, int64_t k, const uint8_t* x, int64
                         void* workspace, hipStream_t s);
 
 // Clipping of `count` tensors (pointers, sizes and types on the host) to a norm (clip.hip);
-// workspace: clip_norm_workspace(count) bytes.  scale: write out (else only the norm).
+// workspace: clip_norm_workspace(count) bytes.
 size_t clip_norm_workspace(int64_t count);
 int launch_clip_norm(int64_t count, const void* const* x, void* const* out, const int64_t* sizes,
                      const int* types, double max_norm, double* norm, void* workspace,

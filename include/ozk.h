@@ -485,31 +485,33 @@ int ozk_layernorm_backward(int64_t rows, int64_t cols, int type, const void* dy,
  * 128 ceil(k / 256) bytes of codes and ozk_mxfp4_scale_bytes(k) = 8 ceil(k / 256) scales, the
  * least leading dimensions; codes past k are 0 and scales past the last block are not 255, both as
  * ozk_mxfp4_quant writes them (other codes there enter the products).  Codes start at multiples of
- * 16 bytes with leading dimensions that are multiples of 16, scales at multiples of 8 with multiples
- * of 8 (OZK_EINVAL otherwise).
+ * 16 bytes with leading dimensions that are multiples of 16, scales at multiples of 8 with
+ * multiples of 8 (OZK_EINVAL otherwise).
  *
  * ozk_mxfp4_quant: codes and scales of the lines of x (rows x cols of `type`, an OZK_F* value;
  *   ldx >= cols), axis 0: its rows, k = cols; axis 1: its columns, k = rows.  For a block with the
- *   largest magnitude a, E = floor(log2 a) - 2 held to [-127, 127] and s = E + 127 (0 for a block of
- *   zeros); the code is x 2^-E rounded to the nearest value, ties to the even code, magnitudes past
- *   6 to 6, with the sign of x also where it is 0.  A block with an Inf or NaN, or with E above 127, has s
- *   = 255 and codes 0.  k >= 1; rows and cols below 2^31 (OZK_EUNSUPPORTED beyond).
- * ozk_mxfp4_values: the values of `lines` lines of k, rounded once to `type` (exact in
- *   fp64, and in fp32 and bf16 but for magnitudes from 2^128 on, which are Inf); NaN where s = 255.  out lines x k, ldo >= k.
+ *   largest magnitude a, E = floor(log2 a) - 2 held to [-127, 127] and s = E + 127 (0 for a block
+ *   of zeros); the code is x 2^-E rounded to the nearest value, ties to the even code, magnitudes
+ *   past 6 to 6, with the sign of x also where it is 0.  A block with an Inf or NaN, or with E
+ *   above 127, has s = 255 and codes 0.  k >= 1; rows and cols below 2^31 (OZK_EUNSUPPORTED
+ *   beyond).
+ * ozk_mxfp4_values: the values of `lines` lines of k, rounded once to `type` (exact in fp64, and
+ *   in fp32 and bf16 but for magnitudes from 2^128 on, which are Inf); NaN where s = 255.  out
+ *   lines x k, ldo >= k.
  *
  * ozk_mxfp4_linear: C = act(X W^T + 1 bias^T) + residual, X m lines and W n lines of k values,
  *   C m x n.  bias (n), residual (m x n, ldr >= n) and C have `type`: OZK_F32, OZK_F16 or
  *   OZK_BF16; bias and residual may be NULL, residual may be C itself.  Sums are fp32, in an order
- *   that depends on m, n and k alone (results repeat bit for bit), and so is what follows, rounded once to
- *   C's type, the activations as ozk_int8linear's.  Where a block's scale is NaN, so are the outputs it
- *   touches; products past fp32's range are Inf or zero.
+ *   that depends on m, n and k alone (results repeat bit for bit), and so is what follows, rounded
+ *   once to C's type, the activations as ozk_int8linear's.  Where a block's scale is NaN, so are
+ *   the outputs it touches; products past fp32's range are Inf or zero.
  * ozk_mxfp4_gated: the first half of a gated feed-forward block, C = act(Zg) * Zu with
- *   Zg = X Wg^T + 1 bias[:n]^T, Zu = X Wu^T + 1 bias[n:]^T; W has 2 n lines, Wg's before Wu's, bias 2 n
- *   entries.
- * Both: 1 <= k <= OZK_MX_MAX_K; a workspace (256-byte aligned) of the size the query returns, which
- *   may be 0 (workspace may be NULL then); C overlaps no other operand.  OZK_EUNSUPPORTED from
- *   m = 2^31 or n = 2^30 on, for leading dimensions of codes or scales from 2^24 on, and where a launch would pass
- *   2^32 threads. */
+ *   Zg = X Wg^T + 1 bias[:n]^T, Zu = X Wu^T + 1 bias[n:]^T; W has 2 n lines, Wg's before Wu's,
+ *   bias 2 n entries.
+ * Both: 1 <= k <= OZK_MX_MAX_K; a workspace (256-byte aligned) of the size the query returns,
+ *   which may be 0 (workspace may be NULL then); C overlaps no other operand.  OZK_EUNSUPPORTED
+ *   from m = 2^31 or n = 2^30 on, for leading dimensions of codes or scales from 2^24 on, and
+ *   where a launch would pass 2^32 threads. */
 int64_t ozk_mxfp4_line_bytes(int64_t k);
 int64_t ozk_mxfp4_scale_bytes(int64_t k);
 int ozk_mxfp4_quant(int64_t rows, int64_t cols, int type, const void* x, int64_t ldx, int axis,
@@ -533,13 +535,14 @@ int ozk_mxfp4_gated(int64_t m, int64_t n, int64_t k, const uint8_t* X, int64_t l
  * The gradients of a training step (no counterpart in the pages): with N the 2-norm of all values
  * of `count` tensors together, out[i] = x[i] min(1, max_norm / N).  x, out, sizes (elements) and
  * types (OZK_F* values) are HOST arrays, read during the call; x[i] and out[i] point to
- * contiguous device memory, aligned to their elements, out[i] of x[i]'s type.  out[i] may be x[i]
- * (a norm within the bound then writes nothing); apart from that no output overlaps another, or an
- * input (OZK_EINVAL).  norm (device, fp64) receives N.  Squares are summed in fp64 in a fixed order, without
- * overflow or underflow of the squares of fp64 values; a value times the factor is formed in fp64
- * and rounded to its type.  Where N is Inf or NaN the values are left as they are.  max_norm >= 0;
- * with Inf only N is computed (and x copied where out is not x).  The workspace (256-byte aligned) takes
- * ozk_clip_norm_workspace_size bytes.  OZK_EUNSUPPORTED from 2^23 tensors, or 2^44 bytes of one, on. */
+ * contiguous device memory, aligned to their elements, out[i] of x[i]'s type.  norm (device, fp64)
+ * receives N.  out[i] may be x[i] (a norm within the bound then writes nothing); apart from that no
+ * output, norm among them, overlaps another or an input (OZK_EINVAL).  Squares are summed in fp64
+ * in a fixed order, without overflow or underflow of the squares of fp64 values; a value times the
+ * factor is formed in fp64 and rounded to its type (to 16 bits by way of fp32).  Where N is Inf or
+ * NaN the values are left as they are.  max_norm >= 0; with Inf only N is computed (and x copied
+ * where out is not x).  The workspace (256-byte aligned) takes ozk_clip_norm_workspace_size bytes.
+ * OZK_EUNSUPPORTED from 2^23 tensors, or 2^44 bytes of one, on. */
 int ozk_clip_norm_workspace_size(int64_t count, size_t* bytes);
 int ozk_clip_norm(int64_t count, const void* const* x, void* const* out, const int64_t* sizes,
                   const int* types, double max_norm, double* norm, void* workspace,

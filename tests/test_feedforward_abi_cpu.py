@@ -186,6 +186,8 @@ def test_clip_norm_refusals(lib):
     for kw in (dict(max_norm=-1.0), dict(max_norm=float("nan")), dict(norm=None),
                dict(norm=ctypes.c_void_p(0x1004)), dict(ws=ODD)):
         assert _clip(lib, [good], **kw) == EINVAL, kw
+    for at in (a, a + 56, b, b + 56):                          # the norm among the values
+        assert _clip(lib, [good], norm=ctypes.c_void_p(at)) == EINVAL, at
     assert _clip(lib, [good], wsb=16) == EWORKSPACE and _clip(lib, [good], ws=None) == EWORKSPACE
     assert _clip(lib, [(a, b, 1 << 43, 1)]) == EUNSUPPORTED
     f = lib.ozk_clip_norm

@@ -144,6 +144,23 @@ def test_quant_many_lines():
     assert torch.equal(v.view(-1, 1021, 3), wv[None].expand(rows // 1021, -1, -1))
 
 
+@pytest.mark.parametrize("kind,cols", [("bfloat16", (1 << 29) + 1), ("float64", (1 << 28) + 70)])
+def test_quant_many_columns(kind, cols):
+    """Columns of several launches, the last one of a single column."""
+    announce(f"mxfp4 quant many columns {kind}")
+    if torch.cuda.mem_get_info()[0] < cols * 160:
+        pytest.skip("needs 160 bytes of device memory a column")
+    block = matrix(1, 1021, TYPES[kind], 6).to(device())
+    x = block.repeat(1, cols // 1021 + 1)[:, :cols]
+    q, s = ozk.ozk_mxfp4_quant(x, 1)
+    wq, ws = ozk.ozk_mxfp4_quant(block, 1)
+    whole = cols // 1021 * 1021
+    for got, want in ((q, wq), (s, ws)):
+        for part in got[:whole].view(-1, 1021, got.shape[1]).split(20000):
+            assert torch.equal(part, want[None].expand(len(part), -1, -1))
+        assert torch.equal(got[whole:], want[:cols - whole])
+
+
 @pytest.mark.parametrize("kind", list(TYPES))
 def test_values_every_code_and_scale(kind):
     """All 16 codes under all 256 scales, rounded once to the type (fp16 overflows to Inf)."""
@@ -741,6 +758,37 @@ def test_training_step():
         torch.cuda.synchronize()
         for a, e in zip(out, eager):
             assert torch.equal(a, e)
+
+
+def test_graphs_share_a_workspace():
+    """Two graphs that were captured with one workspace, replayed in turn on one stream."""
+    announce("feed-forward graphs with one workspace")
+    rng = np.random.default_rng(31)
+    a, b = to_dev(rng.standard_normal((70, 300))), to_dev(rng.standard_normal((300, 130)))
+    x, w = [ozk.ozk_mxfp4_quant(to_dev(rng.standard_normal((s, 16384)))) for s in (90, 100)]
+    grads = [to_dev(rng.standard_normal(s)) for s in (70000, 3)]
+    ws = torch.empty(max(ozk.ozk_dgemm_gated_workspace_size(70, 65, 300, 14),
+                         ozk.ozk_mxfp4_linear_workspace_size(90, 100, 16384),
+                         ozk.ozk_clip_norm_workspace_size(2)), dtype=torch.uint8, device=device())
+    kw = dict(workspace=ws)
+
+    def first(a, b):
+        outs = [torch.empty_like(g) for g in grads]
+        norm, _ = ozk.ozk_clip_norm(grads, 1.0, out=outs, **kw)
+        return ozk.ozk_dgemm_gated(a, b, 14, **kw), norm, *outs
+
+    def second(*lines):
+        return (ozk.ozk_mxfp4_linear(*lines, **kw),)
+
+    graphs = [(captured(first, [a, b]), first(a, b)), (captured(second, [*x, *w]), second(*x, *w))]
+    for turn in range(4):
+        ws.fill_(255)
+        for (graph, out), want in graphs:
+            for o in out:
+                o.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(o, e) for o, e in zip(out, want))
 
 
 def test_linear_gradients_on_codes():
