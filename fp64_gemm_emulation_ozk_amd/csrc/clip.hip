@@ -1,15 +1,15 @@
 // Clipping of many tensors to a global norm: N = (sum of all |x|^2)^(1/2), y = x min(1, M / N).
 //
 // Two passes, each one launch for up to 128 tensors, whose addresses, sizes and types travel with
-// the launch (nothing is copied to the device, so a call can be captured).  The tensors are cut into
-// chunks, dealt out to at most 512 workgroups (two per compute unit).  The first pass leaves each
-// workgroup's sums, the second's workgroups all add them in the same order and scale.
+// the launch (nothing is copied to the device, so a call can be captured).  The tensors are cut
+// into chunks, dealt out to at most 512 workgroups (two per compute unit).  The first pass leaves
+// each workgroup's sums, the second's workgroups all add them in the same order and scale.
 // Squares are summed in 64 bits.  Those of fp64 values may leave its range, so they are summed
 // three times, as they are and with the values scaled by 2^-600 and 2^600.
 //
-// Memory bounds both passes.  All of a chunk's loads are in flight at once: a thread has four of 16
-// bytes in the first pass, where eight took longer (166 -> 169 us over 1.0 GB of bf16), and eight
-// in the second (406 -> 380 us with its writes of as much).
+// Memory bounds both passes.  All of a chunk's loads are in flight at once: a thread has four of
+// 16 bytes in the first pass, where eight took longer (166 -> 169 us over 1.0 GB of bf16), and
+// eight in the second (406 -> 380 us with its writes of as much).
 #include "ozk_internal.h"
 #include "rows.h"
 

@@ -25,7 +25,11 @@ __device__ __forceinline__ double activate_of(double z, int act) {
 }
 
 // Waves as in crt_outputs, 64 columns of C a group; the second projection's residues start at any
-// address, n bytes on.
+// address, n bytes on.  Bound as the ungated reconstruction, by the latency of residues from r
+// planes with vector instructions close behind: 4096 x 2 8192, r = 16, silu, Z kept 482 to 499 us
+// (1.9 GB, 3.8 TB/s); no activation takes as long.  Inside the product of 64 inner values (865 us
+// in all), asking for the next group's residues before this one's lift 876, 4096 workgroups in
+// place of 16384 885.
 template <int R, ActSet kSet>
 __global__ __launch_bounds__(256) void crt_gated_kernel(
     int64_t m, int64_t n, const int8_t* __restrict__ res, int64_t ldr, int64_t stride_r,
@@ -100,6 +104,7 @@ __device__ __forceinline__ Pair gate_grad(double dc, double zg, double zu, int a
 }
 
 // A column c of both halves of G per thread, a chunk of rows per workgroup, and the chunk's sums.
+// Bound by memory: 1500 x 1025 (61 MB) 17.4 us, of which launch and latency are 4.
 __global__ __launch_bounds__(256) void gate_grad_kernel(
     int64_t m, int64_t n, int64_t chunk, const double* __restrict__ dc, int64_t lddc,
     const double* __restrict__ z, int64_t ldz, int act, double* __restrict__ g,

@@ -3,6 +3,12 @@
 // X m x k and W n (2n) x k as MX FP4 lines.  A v_mfma_scale_f32_16x16x128_f8f6f4 takes 32 codes
 // and their scale from every lane, so a lane's 16 bytes of a line are one block; sums are fp32,
 // and what follows them is fp32, rounded once to the output's type.
+//
+// Few rows are bound by the bytes of W: the stream kernel.  Many are bound by the matrix cores and
+// by what feeds them: the tile kernels.  (us, bf16, MI355X; a replayed graph)
+//   rows of 8192 x 8192:  1: 6.2   16: 7.0   32: 8.5   64: 11.6   128: 19.4   256: 23   512: 29
+//   8192^3: 251 (4.4 PFLOP/s); 4096 x 16384 x 4096: 145, with gelu 173, with a residual 178, with
+//   both 191; gated 4096 x 2 8192 x 4096: 145
 #include "activation.h"
 #include "ozk_internal.h"
 #include "rows.h"
@@ -16,8 +22,8 @@ typedef float v4f_words __attribute__((ext_vector_type(4), aligned(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
 
 // One block's worth of a step for every lane: half kH of the lane's 32 bytes of the step, scale
-// byte kH of its two.  Lane (row lane % 16, quarter lane / 16) gives 32 codes of its line; lane l of
-// the sum holds line l % 16 of x and lines 4 (l / 16) .. + 3 of w.
+// byte kH of its two.  Lane (row lane % 16, quarter lane / 16) gives 32 codes of its line; lane l
+// of the sum holds line l % 16 of x and lines 4 (l / 16) .. + 3 of w.
 template <int kH>
 __device__ __forceinline__ v4f mfma_mx(const v4i& w, int sw, const v4i& x, int sx, const v4f& c) {
   const v8i w8 = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
@@ -26,9 +32,9 @@ __device__ __forceinline__ v4f mfma_mx(const v4i& w, int sw, const v4i& x, int s
 }
 
 // In LDS a line's step is 128 bytes, whose eight 16-byte chunks are XORed with swizzle(line).  A
-// fragment read of 16 bytes a lane is served 16 lanes at a time, eight lines of one quarter and the
-// other eight of its neighbour (lanes 0-3, 12-15, 20-27, and so on), which here read chunks two
-// apart: these 16 fall on all 64 banks if lines 4 .. 11 of 16 have swizzles that stay among
+// fragment read of 16 bytes a lane is served 16 lanes at a time, eight lines of one quarter and
+// the other eight of its neighbour (lanes 0-3, 12-15, 20-27, and so on), which here read chunks
+// two apart: these 16 fall on all 64 banks if lines 4 .. 11 of 16 have swizzles that stay among
 // themselves under XOR with 2.  (With (line >> 1) & 7 alone, as where neighbours read chunks one
 // apart, 0.44 of the LDS's busy cycles were conflicts.)
 __device__ __forceinline__ int swizzle(int line) {
@@ -130,8 +136,9 @@ __device__ __forceinline__ void put_part(float* __restrict__ p, int64_t row, int
 
 // Both projections' partial sums of four columns (not gated: `up` is not used).
 template <bool kGated, typename O>
-__device__ __forceinline__ void put_parts(const MxEpilogue<O>& E, float* __restrict__ p, int64_t row,
-                                          int64_t col, const v4f& acc, const v4f& up) {
+__device__ __forceinline__ void put_parts(const MxEpilogue<O>& E, float* __restrict__ p,
+                                          int64_t row, int64_t col, const v4f& acc,
+                                          const v4f& up) {
   const int64_t wide = kGated ? 2 * E.n : E.n;
   put_part(p, row, col, E.m, E.n, wide, acc);
   if constexpr (kGated)
@@ -139,11 +146,11 @@ __device__ __forceinline__ void put_parts(const MxEpilogue<O>& E, float* __restr
 }
 
 // Few rows: workgroup = 16 kNT columns of C (gated: of both projections) and all rows, its eight
-// waves taking the K steps of 256 codes in turn (of the workgroup's split of K).  Each wave streams
-// its steps through a ring of its own in LDS by direct loads of 8 lines x 128 bytes and of 32 lines' 8
-// scales.  No barriers: a wave waits for its own loads, reads its fragments and refills the slot, so
-// that eight slots are under way even where a wave has but one.  kXR rows of X (8 to 64) travel
-// with each step.
+// waves taking the K steps of 256 codes in turn (of the workgroup's split of K).  Each wave
+// streams its steps through a ring of its own in LDS by direct loads of 8 lines x 128 bytes and
+// of 32 lines' 8 scales.  No barriers: a wave waits for its own loads, reads its fragments and
+// refills the slot, so that eight slots are under way even where a wave has but one.  kXR rows of
+// X (8 to 64) travel with each step.
 template <typename O, bool kGated, int kXR, int kNT, int kS>
 __global__ __launch_bounds__(512) void mxfp4_stream_kernel(int steps, Lines X, Lines W,
                                                            MxEpilogue<O> E, int splits,
@@ -274,10 +281,11 @@ __global__ __launch_bounds__(512) void mxfp4_stream_kernel(int steps, Lines X, L
 
 // ------------------------------------------------------------------ tiles
 // Tiles as the int8 layer's (tile_walk.h), a K step being 128 bytes of each line, 256 codes.  Lane
-// quarter q of a fragment takes chunks 2 q and 2 q + 1 of a line's step, so that its two scales are
-// one aligned word of 16 bits.  Scales come in groups of four steps, 32 bytes a line, in a ring of
-// kBufs groups behind the codes': 8 bytes of every line each step are as many requests to L2 again as
-// the codes are.
+// quarter q of a fragment takes chunks 2 q and 2 q + 1 of a line's step, so that its two scales
+// are one aligned word of 16 bits.  Scales come in groups of four steps, 32 bytes a line, in a
+// ring of kBufs groups behind the codes': 8 bytes of every line each step are as many requests to
+// L2 again as the codes are (8192^3: 271 us so, 260 with groups and with K steps of one basic
+// block).
 // Gated: a wave's columns are half columns of the gate's projection and half the same columns of
 // the other, so that both meet in one wave; the tile has BN / 2 columns of C.
 template <typename TL, bool kGated, int kBufs>
@@ -300,7 +308,7 @@ struct MxWalk {
   int8_t* lds;
   int wave, lane;
   int nk;                  // K steps
-  int last;                // the lines' last step, from this workgroup's first, if it is the 1st, 3rd, ...
+  int last;   // the lines' last step, from this workgroup's first, if it is the 1st, 3rd, ...
   int64_t row0, col0;      // of C
   uint64_t base[LC];       // of a load's lines (uniform)
   uint32_t voff[LC];       // a lane's offset from there
@@ -321,10 +329,10 @@ struct MxWalk {
     const int in_group = tile % per_group;
     row0 = (int64_t)(first_m + in_group % gsize) * BM;
     col0 = (int64_t)(in_group / gsize) * T::kCols;
-    // Load q of this wave: region rg = wave + NW q, lines 8 rg .. 8 rg + 7 of X's, then of W's; lane
-    // i takes line i / 8 of it, physical chunk i % 8, which holds logical chunk
-    // (i % 8) ^ swizzle(line), which depends on the region's parity alone, the wave's.  Lines past
-    // the matrix re-read its last.
+    // Load q of this wave: region rg = wave + NW q, lines 8 rg .. 8 rg + 7 of X's, then of W's;
+    // lane i takes line i / 8 of it, physical chunk i % 8, which holds logical chunk (i % 8) ^
+    // swizzle(line), which depends on the region's parity alone, the wave's.  Lines past the
+    // matrix re-read its last.
     const uint32_t chunk = 16 * ((lane & 7) ^ swizzle(8 * wave + (lane >> 3)));
 #pragma unroll
     for (int q = 0; q < LC; ++q) {
@@ -378,16 +386,16 @@ struct MxWalk {
     dma16_if(more, scale[q] + (at < most ? at : most), to);
   }
 
-  // Behind the barrier of step t, in which the scales of group t / 4 - 1 have been read for the last
-  // time where t begins a group: whether that asks for another, and which.
+  // Behind the barrier of step t, in which the scales of group t / 4 - 1 have been read for the
+  // last time where t begins a group: whether that asks for another, and which.
   __device__ __forceinline__ int next_group(int t) const { return t / 4 + T::kScaleBufs - 1; }
   __device__ __forceinline__ bool asks(int t) const {
     return t % 4 == 0 && 4 * next_group(t) < nk;
   }
 
-  // Waits until of this wave's loads of codes at most those of the youngest `younger` steps are under
-  // way (kMost: the number that is asked for on every step but the last ones), and of scales at most
-  // those asked for within these steps.
+  // Waits until of this wave's loads of codes at most those of the youngest `younger` steps are
+  // under way (kMost: the number that is asked for on every step but the last ones), and of scales
+  // at most those asked for within these steps.
   template <int kMost>
   __device__ __forceinline__ void wait_loads(int younger) const {
     constexpr int L = LC;
@@ -441,12 +449,12 @@ struct Place {
   }
 };
 
-// The outputs of a wave's NI x TJ blocks (lane l of block (i, j): row 16 i + l % 16, columns
-// 16 j + 4 (l / 16) .. + 3), or their partial sums.  A phase of the blocks is staged through this
+// The outputs of a wave's NI x TJ blocks (lane l of block (i, j): row 16 i + l % 16, columns 16 j
+// + 4 (l / 16) .. + 3), or their partial sums.  A phase of the blocks is staged through this
 // wave's part `mine` of the ring so that a few lanes finish one row of the wave's columns, eight
-// consecutive outputs each; a phase's groups of rows are finished together, for their instructions'
-// latencies, and the next phase's residuals asked for meanwhile.  The phases are a loop, through
-// which the blocks move down: written out they would not fit the instruction cache.
+// consecutive outputs each; a phase's groups of rows are finished together, for their
+// instructions' latencies, and the next phase's residuals asked for meanwhile.  The phases are a
+// loop, through which the blocks move down: written out they would not fit the instruction cache.
 template <typename TL, bool kGated, typename O, int NI>
 __device__ __forceinline__ void put_tile(const MxEpilogue<O>& E, v4f (&acc)[NI][TL::TJ],
                                          int64_t wrow0, int64_t wcol0, int lane, float* mine,
@@ -575,6 +583,10 @@ __device__ __forceinline__ void put_tile(const MxEpilogue<O>& E, v4f (&acc)[NI][
 // for its loads of step t + 1 and for its reads of step t (the last quarter's operands are in
 // registers by then), so one barrier a step makes step t + 1 complete and step t's stage free
 // for step t + S, whose loads have S - 1 steps to land less a quarter.
+//
+// 4096^2 x 32768 takes 224 to 230 us: the matrix instructions alone 164, the loads alone 147,
+// everything but the loads 203.  The clock falls to 1.8 GHz under it.  Two workgroups a compute
+// unit with tiles of 256 x 128, whose epilogues could overlap, took 338.
 template <typename O, bool kGated, typename TL>
 __global__ __launch_bounds__(64 * TL::NW) void mxfp4_tile_kernel(int steps, Lines X, Lines W,
                                                                  MxEpilogue<O> E, int tiles_m,
@@ -682,9 +694,9 @@ __global__ __launch_bounds__(64 * TL::NW) void mxfp4_tile_kernel(int steps, Line
 
 // The smaller tiles, whose K steps take a fraction of a load's latency: as many stages as LDS
 // holds, and per step one barrier, one set of fragment reads and one run of MFMAs.  A pair of
-// waves shares the outputs of a wave and splits each step's K, a block of every two; the sums of both
-// meet in LDS at the end.  Behind the barrier of step t the wave reads step t + 1 and asks for step
-// t + S while step t's MFMAs run from registers.
+// waves shares the outputs of a wave and splits each step's K, a block of every two; the sums of
+// both meet in LDS at the end.  Behind the barrier of step t the wave reads step t + 1 and asks
+// for step t + S while step t's MFMAs run from registers.
 template <typename O, bool kGated, typename TL, int kBufs>
 __global__ __launch_bounds__(64 * TL::NW) void mxfp4_small_kernel(int steps, Lines X, Lines W,
                                                                   MxEpilogue<O> E, int tiles_m,
@@ -828,18 +840,18 @@ struct Plan {
   int splits;
 };
 
-// Up to 64 rows: the stream kernel (32 and 64 rows of 8192 x 8192: 8.5 and 11.6 us, by tiles of 64
-// rows 15.1 and 16.4; of 4096 x 4096: 4.5 and 5.8 against 10.9 and 12.3).  More rows: the tile shape
-// and split of the least estimated time, in microseconds, of rounds of 256 workgroups that each cost
-// `fixed` and `step` per K step.  Measured, one round of 256 and of 4096 K values: small 5.5 and
-// 13.5, mid 7.9 and 19.6, large 10.4 and 36.3.  A split costs the launch of the join (4) and the
-// partial sums' way out and back (128 x 4096 x 4096, small, in 1, 2, 4 and 8: 13.5, 14.1, 14.7, 20.6;
-// 100 x 1024 x 8192: 21.8, 16.3, 12.3, 11.4).
+// Up to 64 rows: the stream kernel (32 and 64 rows of 8192 x 8192: 8.5 and 11.6 us, by tiles of
+// 64 rows 15.1 and 16.4; of 4096 x 4096: 4.5 and 5.8 against 10.9 and 12.3).  More rows: the tile
+// shape and split of the least estimated time, in microseconds, of rounds of 256 workgroups that
+// each cost `fixed` and `step` per K step.  Measured, one round of 256 and of 4096 K values:
+// small 5.5 and 13.5, mid 7.9 and 19.6, large 10.4 and 36.3.  A split costs the launch of the
+// join (4) and the partial sums' way out and back (128 x 4096 x 4096, small, in 1, 2, 4 and 8:
+// 13.5, 14.1, 14.7, 20.6; 100 x 1024 x 8192: 21.8, 16.3, 12.3, 11.4).
 Plan plan_of(int64_t m, int64_t n, int64_t k, bool gated) {
   const int64_t steps = (k + 255) / 256, wide = gated ? 2 * n : n;
   if (m <= 64) {
-    // 16 columns a workgroup, or 32 where that is more than the compute units take at once (16 rows of
-    // 8192 x 8192: 7.0 us with 32, 9.4 with 16; of 4096 x 4096: 4.4 and 3.9)
+    // 16 columns a workgroup, or 32 where that is more than the compute units take at once (16
+    // rows of 8192 x 8192: 7.0 us with 32, 9.4 with 16; of 4096 x 4096: 4.4 and 3.9)
     const int64_t bn = (n + 15) / 16 > (m <= 8 && !gated ? 512 : 256) ? 32 : 16;
     Plan p{kStream, bn / 16, (n + bn - 1) / bn, 1};
     // a workgroup's eight waves take four steps each at least
@@ -881,8 +893,8 @@ void launch_tiles(const Plan& p, int steps, const Lines& X, const Lines& W, cons
     hipLaunchKernelGGL((mxfp4_tile_kernel<O, kGated, TL>), grid, block, 0, s, steps, X, W, E,
                        (int)p.tiles_m, (int)p.tiles_n, p.splits, group_m, part);
   else
-    hipLaunchKernelGGL((mxfp4_small_kernel<O, kGated, TL, TL::S <= 4 ? 2 : 3>), grid, block, 0, s, steps, X, W, E,
-                       (int)p.tiles_m, (int)p.tiles_n, p.splits, group_m, part);
+    hipLaunchKernelGGL((mxfp4_small_kernel<O, kGated, TL, TL::S <= 4 ? 2 : 3>), grid, block, 0, s,
+                       steps, X, W, E, (int)p.tiles_m, (int)p.tiles_n, p.splits, group_m, part);
 }
 
 template <typename O, bool kGated>

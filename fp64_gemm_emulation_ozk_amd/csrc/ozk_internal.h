@@ -181,8 +181,8 @@ int launch_crt_epilogue(int64_t m, int64_t n, int r, const int8_t* res, int64_t 
                         int64_t stride_r, const int32_t* ea, const int32_t* eb,
                         const DgemmEpilogue& E, double* c, int64_t ldc, hipStream_t s);
 // The gated form: residues of m x 2 n products, those of the gate's projection before those of
-// the other; a row's ldr, at least n + round_up(n, 64), may all be read.  z (m x 2 n) = the products
-// + bias (2 n), c = act(z's first half) * its second.  E.residual is null.
+// the other; a row's ldr, at least n + round_up(n, 64), may all be read.  z (m x 2 n) = the
+// products + bias (2 n), c = act(z's first half) * its second.  E.residual is null.
 int launch_crt_gated(int64_t m, int64_t n, int r, const int8_t* res, int64_t ldr, int64_t stride_r,
                      const int32_t* ea, const int32_t* eb, const DgemmEpilogue& E, double* c,
                      int64_t ldc, hipStream_t s);

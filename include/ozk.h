@@ -252,9 +252,9 @@ int ozk_dgemm_gated(int64_t m, int64_t n, int64_t k, const double* A, int64_t ld
 /* Its gradient: from dC (m x n), A, B and Z
  *     G = [dC * Z[:, n:] * act'(Z[:, :n]),  dC * act(Z[:, :n])]  (m x 2 n),
  *     dA = G B^T,   dB = A^T G,   dbias = column sums of G
- * dA (m x k), dB (k x 2 n) and dbias (2 n entries) may each be NULL and are then not computed.  Both
- * products are emulated with r moduli, inner dimensions 2 n and m; dbias is summed in fp64 in a
- * fixed order.  m, 2 n and k at most OZK_MAX_K.  Otherwise as ozk_dgemm_epilogue_grad. */
+ * dA (m x k), dB (k x 2 n) and dbias (2 n entries) may each be NULL and are then not computed.
+ * Both products are emulated with r moduli, inner dimensions 2 n and m; dbias is summed in fp64 in
+ * a fixed order.  m, 2 n and k at most OZK_MAX_K.  Otherwise as ozk_dgemm_epilogue_grad. */
 int ozk_dgemm_gated_grad_workspace_size(int64_t m, int64_t n, int64_t k, int r, size_t* bytes);
 int ozk_dgemm_gated_grad(int64_t m, int64_t n, int64_t k, const double* dC, int64_t lddc,
                          const double* A, int64_t lda, const double* B, int64_t ldb,
