@@ -442,6 +442,11 @@ __device__ __forceinline__ void store_residues_direct(
 // 12 panels of A and B for 32 tiles in that XCD's L2.  All XCDs work on the same modulus
 // and the same 8 tile rows at once, so the A panels and (from one group of rows to the
 // next) the B panels they share come from the 256 MB last-level cache rather than HBM.
+//
+// Two products whose tiles are one list (the gradients of a layer): the tiles of the one with more
+// K steps, then the other's, walked by the same workgroups, so that the ragged last rounds of
+// both become one (1500 x 1024 x 2176 and 1001 x 2112 x 1536, r = 16: 110 to 115 us, one after the
+// other 2 x 68).
 constexpr int kPairRow = 128;                       // bytes per row of a pair stage
 constexpr int kPairGroupM = 8;                      // tile rows per group of the tile order
 constexpr int kPairBytes = (BM + BN) * kPairRow;    // 64 KiB
@@ -496,11 +501,24 @@ __device__ __forceinline__ void store_residues16(const v4i (&acc)[8][4], int64_t
   }
 }
 
-template <int kEpi, int NW>
-__global__ __launch_bounds__(64 * NW, 1) void gemm_i8_pairs_kernel(
-    int64_t m, int64_t n, int64_t kp, const int8_t* __restrict__ pa, int64_t stride_a,
-    const int8_t* __restrict__ pb, int64_t stride_b, void* __restrict__ out, int64_t ldo,
-    int64_t stride_o, int tiles_m, int tiles_n, int tiles, EpiModuli E, int vec_out) {
+struct PairsProduct {
+  int64_t m, n, kp;
+  const int8_t* pa;
+  int64_t stride_a;
+  const int8_t* pb;
+  int64_t stride_b;
+  void* out;
+  int64_t ldo, stride_o;
+  int tiles_m, tiles_n, tiles, vec_out;
+};
+template <int kCount>
+struct PairsArgs {
+  PairsProduct p[kCount];
+  EpiModuli E;
+};
+
+template <int kEpi, int NW, int kCount>
+__global__ __launch_bounds__(64 * NW, 1) void gemm_i8_pairs_kernel(PairsArgs<kCount> A) {
   __shared__ __attribute__((aligned(1024))) int8_t lds[2 * kPairBytes];
 
   constexpr int kWaves = NW;
@@ -518,41 +536,49 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm_i8_pairs_kernel(
 
   // This workgroup's tiles: first, first + G, ... below tiles (all uniform).
   const int G = gridDim.x;
-  const int t_end = tiles;
+  const int t_end = A.p[0].tiles + (kCount > 1 ? A.p[kCount - 1].tiles : 0);
   const int step = G;
   int t = G % kXcds == 0 ? (int)(blockIdx.x % kXcds) * (G / kXcds) + (int)(blockIdx.x / kXcds)
                          : (int)blockIdx.x;
   if (t >= t_end) return;
 
-  // Tile -> (modulus, tile row, tile column), tile rows grouped by kPairGroupM.
+  // Tile -> (product, modulus, tile row, tile column), tile rows grouped by kPairGroupM.
   struct Tile {
+    int which;                          // 0 of a single product
     int l;
     int64_t row0, col0;
     uint64_t base_a, base_b;            // tile origins of A_l and B_l (uniform)
     uint32_t voff[kLoadsPerWave];       // per-lane source offsets of the loads
   };
-  const int per_mod = tiles_m * tiles_n;
-  const int per_group = kPairGroupM * tiles_n;
+  auto product = [&](int which) -> const PairsProduct& {
+    return A.p[kCount > 1 ? which : 0];
+  };
   // Region rg = wave + NW q: rows 8 (rg % 32) .. +7 of A (q < 4) or B; lane i lands at
   // row 8 (rg % 32) + i / 8, physical chunk i % 8, which holds logical chunk
   // (i % 8) ^ ((row >> 1) & 7); rows past the matrix re-read its last row.
   auto make_tile = [&](int tt, Tile& d) {
+    d.which = kCount > 1 && tt >= A.p[0].tiles;
+    if (d.which) tt -= A.p[0].tiles;
+    const PairsProduct& P = product(d.which);
+    const int per_mod = P.tiles_m * P.tiles_n;
+    const int per_group = kPairGroupM * P.tiles_n;
+    const int64_t kp = P.kp;
     d.l = tt / per_mod;
     const int rem = tt - d.l * per_mod;
     const int first_m = (rem / per_group) * kPairGroupM;
-    const int gsize = tiles_m - first_m < kPairGroupM ? tiles_m - first_m : kPairGroupM;
+    const int gsize = P.tiles_m - first_m < kPairGroupM ? P.tiles_m - first_m : kPairGroupM;
     const int in_group = rem % per_group;
     d.row0 = (int64_t)(first_m + in_group % gsize) * BM;
     d.col0 = (int64_t)(in_group / gsize) * BN;
-    d.base_a = (uint64_t)(pa + d.l * stride_a + d.row0 * kp);
-    d.base_b = (uint64_t)(pb + d.l * stride_b + d.col0 * kp);
+    d.base_a = (uint64_t)(P.pa + d.l * P.stride_a + d.row0 * kp);
+    d.base_b = (uint64_t)(P.pb + d.l * P.stride_b + d.col0 * kp);
 #pragma unroll
     for (int q = 0; q < kLoadsPerWave; ++q) {
       const bool is_b = q >= kLoadsPerWave / 2;
       const int row = 8 * ((wave + kWaves * q) & 31) + (lane >> 3);
       const int chunk = (lane & 7) ^ ((row >> 1) & 7);
       const int64_t origin = is_b ? d.col0 : d.row0;
-      const int64_t last = (is_b ? n : m) - 1;
+      const int64_t last = (is_b ? P.n : P.m) - 1;
       const int64_t gr = origin + row < last ? origin + row : last;
       d.voff[q] = (uint32_t)((gr - origin) * kp + 16 * chunk);
     }
@@ -560,7 +586,6 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm_i8_pairs_kernel(
 
   const uint32_t lds0 = lds_address(lds);
   const uint32_t wave_lds = __builtin_amdgcn_readfirstlane(lds0 + wave * 1024);
-  const int np = (int)(kp / kPairRow);
   // Load q of pair `pair` of the current tile (next: of the next tile) into LDS buffer
   // `buf`.
   Tile cur, nxt;
@@ -649,6 +674,7 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm_i8_pairs_kernel(
     const int t_next = t + step;
     const bool has_next = t_next < t_end;
     if (has_next) make_tile(t_next, nxt);
+    const int np = (int)(product(cur.which).kp / kPairRow);
     for (int p = 0; p < np; ++p) {
       __builtin_amdgcn_sched_barrier(0);
       const int b0 = (par + p) & 1;      // pair p's buffer (and pair p+2's)
@@ -677,10 +703,13 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm_i8_pairs_kernel(
       quarter(3, st, sn, wrap, wrap ? p + 2 - np : p + 2, b0, q3_loads ? kLoadsPerWave : 0);
     }
     // Epilogue of tile `cur`: exactly kStores stores per wave when the tile is full.
+    const PairsProduct& P = product(cur.which);
+    const int64_t m = P.m, n = P.n, ldo = P.ldo;
+    const int vec_out = P.vec_out;
     const bool full = vec_out && cur.row0 + BM <= m && cur.col0 + BN <= n;
     if (kEpi == kEpiProducts) {
       // lane l of block (i, j): row 16 i + l % 16, columns 16 j + 4 (l / 16) + 0..3
-      int32_t* o = reinterpret_cast<int32_t*>(out) + cur.l * stride_o;
+      int32_t* o = reinterpret_cast<int32_t*>(P.out) + cur.l * P.stride_o;
 #pragma unroll
       for (int i = 0; i < TI; ++i) {
         const int64_t row = cur.row0 + grp * 128 + 16 * i + (lane & 15);
@@ -702,9 +731,9 @@ __global__ __launch_bounds__(64 * NW, 1) void gemm_i8_pairs_kernel(
         }
       }
     } else {
-      store_residues16<NW>(acc, m, n, cur.row0, cur.col0, grp, wq, lane, E.mod[cur.l],
-                           E.inv[cur.l], reinterpret_cast<int8_t*>(out) + cur.l * stride_o, ldo,
-                           full, vec_out);
+      store_residues16<NW>(acc, m, n, cur.row0, cur.col0, grp, wq, lane, A.E.mod[cur.l],
+                           A.E.inv[cur.l], reinterpret_cast<int8_t*>(P.out) + cur.l * P.stride_o,
+                           ldo, full, vec_out);
     }
     if (!has_next) break;
 #pragma unroll
@@ -739,50 +768,85 @@ int compute_units() {
   return cus;
 }
 
-}  // namespace
-
-int launch_gemm_i8(int64_t m, int64_t n, int64_t kp, int r, const int8_t* pa, int64_t stride_a,
-                   const int8_t* pb, int64_t stride_b, void* out, int64_t ldo, int64_t stride_o,
-                   int epilogue, hipStream_t s, hipEvent_t ev_start, hipEvent_t ev_stop) {
-  if (m <= 0 || n <= 0) return OZK_OK;
-  const int tiles_m = (int)((m + BM - 1) / BM);
-  const int tiles_n = (int)((n + BN - 1) / BN);
+EpiModuli epi_moduli(int r) {
   EpiModuli E;
   const CrtConsts* C = crt_consts(r);
   for (int i = 0; i < kMaxModuli; ++i) {
     E.mod[i] = i < r ? C->mod[i] : 1;
     E.inv[i] = i < r ? C->inv[i] : 1.0;
   }
-  const int64_t blocks = (int64_t)tiles_m * tiles_n * r;
-  if (blocks > 0x7fffffff) return OZK_EUNSUPPORTED;
+  return E;
+}
+
+// A product as the persistent kernel takes it; tiles < 0 where they are more than 32 bits count.
+PairsProduct pairs_product(int64_t m, int64_t n, int64_t kp, int r, const int8_t* pa,
+                           int64_t stride_a, const int8_t* pb, int64_t stride_b, void* out,
+                           int64_t ldo, int64_t stride_o, int epilogue) {
+  const int64_t tiles_m = (m + BM - 1) / BM, tiles_n = (n + BN - 1) / BN;
+  const int64_t tiles = tiles_m * tiles_n * r;
   const int64_t elem = epilogue == kEpiProducts ? 4 : 1;
   const int64_t vbytes = 16;
   const int vec_out = (reinterpret_cast<uintptr_t>(out) % vbytes) == 0 &&
                       (ldo * elem) % vbytes == 0 && (stride_o * elem) % vbytes == 0;
+  return {m, n, kp, pa, stride_a, pb, stride_b, out, ldo, stride_o, (int)tiles_m, (int)tiles_n,
+          tiles > 0x7fffffff ? -1 : (int)tiles, vec_out};
+}
+
+// Whole-line loads need K in steps of 128; the tile pipeline needs two of them.
+bool in_pairs(int64_t kp) { return kp % kPairRow == 0 && kp >= 2 * kPairRow; }
+
+}  // namespace
+
+int launch_gemm_i8(int64_t m, int64_t n, int64_t kp, int r, const int8_t* pa, int64_t stride_a,
+                   const int8_t* pb, int64_t stride_b, void* out, int64_t ldo, int64_t stride_o,
+                   int epilogue, hipStream_t s, hipEvent_t ev_start, hipEvent_t ev_stop) {
+  if (m <= 0 || n <= 0) return OZK_OK;
+  const PairsArgs<1> A{{pairs_product(m, n, kp, r, pa, stride_a, pb, stride_b, out, ldo, stride_o,
+                                      epilogue)},
+                       epi_moduli(r)};
+  const PairsProduct& P = A.p[0];
+  if (P.tiles < 0) return OZK_EUNSUPPORTED;
   constexpr int NW = kWavesDefault;
   const dim3 block(64 * NW);
-  // whole-line loads need K in steps of 128; the tile pipeline needs two of them
-  const bool pairs = kp % kPairRow == 0 && kp >= 2 * kPairRow;
   const int cus = compute_units();
   if (cus <= 0) return OZK_EHIP;
-  const dim3 grid((unsigned)blocks);
-  const dim3 grid_p((unsigned)(blocks < cus ? blocks : cus));  // one workgroup per CU
-  const int tiles = (int)blocks;
+  const dim3 grid((unsigned)P.tiles);
+  const dim3 grid_p((unsigned)(P.tiles < cus ? P.tiles : cus));  // one workgroup per CU
 #define OZK_GEMM(EPI)                                                                        \
-  if (pairs)                                                                                 \
-    hipExtLaunchKernelGGL((gemm_i8_pairs_kernel<EPI, NW>), grid_p, block, 0, s, ev_start,    \
-                          ev_stop, 0, m, n, kp, pa, stride_a, pb, stride_b, out, ldo,         \
-                          stride_o, tiles_m, tiles_n, tiles, E, vec_out);                     \
+  if (in_pairs(kp))                                                                          \
+    hipExtLaunchKernelGGL((gemm_i8_pairs_kernel<EPI, NW, 1>), grid_p, block, 0, s, ev_start, \
+                          ev_stop, 0, A);                                                    \
   else                                                                                       \
     hipExtLaunchKernelGGL((gemm_i8_kernel<EPI, NW>), grid, block, 0, s, ev_start, ev_stop, 0, \
-                          m, n, kp, pa, stride_a, pb, stride_b, out, ldo, stride_o, tiles_m,  \
-                          tiles_n, E, vec_out)
+                          m, n, kp, pa, stride_a, pb, stride_b, out, ldo, stride_o,           \
+                          P.tiles_m, P.tiles_n, A.E, P.vec_out)
   if (epilogue == kEpiProducts) {
     OZK_GEMM(kEpiProducts);
   } else {
     OZK_GEMM(kEpiResidues);
   }
 #undef OZK_GEMM
+  return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
+}
+
+int launch_gemm_i8_two(const PlaneProduct* P, int r, hipStream_t s) {
+  PairsArgs<2> A;
+  const int first = P[1].kp > P[0].kp ? 1 : 0;   // the longer tiles go first
+  int64_t tiles = 0;
+  for (int i = 0; i < 2; ++i) {
+    const PlaneProduct& Q = P[i ^ first];
+    A.p[i] = pairs_product(Q.m, Q.np, Q.kp, r, Q.left, Q.m * Q.kp, Q.right, Q.n * Q.kp, Q.res,
+                           Q.np, Q.m * Q.np, kEpiResidues);
+    if (A.p[i].tiles < 0) return OZK_EUNSUPPORTED;
+    tiles += A.p[i].tiles;
+  }
+  if (tiles > 0x7fffffff || !in_pairs(P[0].kp) || !in_pairs(P[1].kp)) return OZK_EUNSUPPORTED;
+  A.E = epi_moduli(r);
+  const int cus = compute_units();
+  if (cus <= 0) return OZK_EHIP;
+  hipLaunchKernelGGL((gemm_i8_pairs_kernel<kEpiResidues, kWavesDefault, 2>),
+                     dim3((unsigned)(tiles < cus ? tiles : cus)), dim3(64 * kWavesDefault), 0, s,
+                     A);
   return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
 }
 

@@ -220,6 +220,10 @@ struct PlaneProduct {
   const int8_t* right;
   int8_t* res;
 };
+// Estimated microseconds of launch_products.
+double products_time(const PlaneProduct* P, int count, int r);
+// Residues of two products in one launch of the large tiles, kp at least 256 each.
+int launch_gemm_i8_two(const PlaneProduct* P, int r, hipStream_t s);
 // Whether a product's operands are small: at most `lines` lines of kdim values each; columns:
 // both operands' lines are columns.
 bool small_operands(int64_t lines, int64_t kdim, bool columns);

@@ -329,6 +329,43 @@ double rounds_time(const PlaneProduct* P, int count, int r, int64_t bm, int64_t 
   return (double)((tiles + 255) / 256) * (fixed + step * (double)steps);
 }
 
+// The same for two products' large tiles in one list, the longer ones first.
+double list_time(const PlaneProduct* P, int r, double fixed, double step) {
+  const int first = P[1].kp > P[0].kp ? 1 : 0;
+  const double rounds =
+      rounds_time(P + first, 1, r, 256, 256, 1.0, 0.0);   // of the longer tiles
+  const double all = rounds_time(P, 2, r, 256, 256, 1.0, 0.0);
+  return 2.5 + rounds * (fixed + step * (double)(P[first].kp / kStepK)) +
+         (all - rounds) * (fixed + step * (double)(P[1 - first].kp / kStepK));
+}
+
+// The tiles of the least estimated time.
+enum TileChoice { kTilesSmall, kTilesMid, kTilesLarge };
+struct Choice {
+  TileChoice tiles;
+  bool one_list;   // large: both products in one launch
+  double time;
+};
+
+// One round: fixed + step per 128 K values (the int8 layer's measured rounds, without the launch).
+// Whole calls, r = 16, by the small, mid and large tiles: 256^3 13.6, 15.0, 16.4; 512^3 28.7,
+// 25.5, 28.5; 768^3 55.8, 49.4, 39.8; 60 x 60 x 8192 60.6, 66.2, 106; 384 x 384 x 8192 107, 82.3,
+// 124; 1024^3 86.2, 67.7, 51.0.  Over 26 shapes of 64 to 16384 the choice costs 0.8 % on average,
+// 12 % at worst (300 x 1000 x 300: mid 30.2, large 26.9).
+Choice choose_tiles(const PlaneProduct* P, int count, int r) {
+  const double small = rounds_time(P, count, r, 64, 128, 2.5, 0.55);
+  const double mid = rounds_time(P, count, r, 128, 128, 3.8, 0.72);
+  // gemm_i8.hip: two products are one list of tiles unless a line is a single step
+  const bool one_list = count == 2 && P[0].kp >= 256 && P[1].kp >= 256;
+  double large = 0;
+  if (one_list) large = list_time(P, r, 5.0, 1.5);
+  else
+    for (int o = 0; o < count; ++o) large += 2.5 + rounds_time(P + o, 1, r, 256, 256, 5.0, 1.5);
+  if (large < small && large < mid) return {kTilesLarge, one_list, large};
+  if (small < mid) return {kTilesSmall, false, small};
+  return {kTilesMid, false, mid};
+}
+
 }  // namespace
 
 // Lines of at most 2048 values, and 2^21 values in the larger operand; 2^25 where its lines have at
@@ -390,7 +427,22 @@ int launch_small_deconstruct(const SmallOperand* op, int count, int r, int scali
   return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
 }
 
+double products_time(const PlaneProduct* P, int count, int r) {
+  return choose_tiles(P, count, r).time;
+}
+
 int launch_products(const PlaneProduct* P, int count, int r, hipStream_t s) {
+  const Choice choice = choose_tiles(P, count, r);
+  if (choice.one_list) return launch_gemm_i8_two(P, r, s);
+  if (choice.tiles == kTilesLarge) {
+    for (int o = 0; o < count; ++o) {
+      const int st = launch_gemm_i8(P[o].m, P[o].np, P[o].kp, r, P[o].left, P[o].m * P[o].kp,
+                                    P[o].right, P[o].n * P[o].kp, P[o].res, P[o].np,
+                                    P[o].m * P[o].np, kEpiResidues, s);
+      if (st != OZK_OK) return st;
+    }
+    return OZK_OK;
+  }
   ProductArgs A;
   A.count = count;
   A.r = r;
@@ -400,26 +452,7 @@ int launch_products(const PlaneProduct* P, int count, int r, hipStream_t s) {
     A.inv[l] = l < r ? C->inv[l] : 1.0;
   }
   for (int o = 0; o < count; ++o) A.P[o] = P[o];
-  // One round: fixed + step per 128 K values (the int8 layer's measured rounds, without the launch).
-  // Whole calls, r = 16, by the small, mid and large tiles: 256^3 13.6, 15.0, 16.4; 512^3 28.7,
-  // 25.5, 28.5; 768^3 55.8, 49.4, 39.8; 60 x 60 x 8192 60.6, 66.2, 106; 384 x 384 x 8192 107, 82.3,
-  // 124; 1024^3 86.2, 67.7, 51.0.  Over 26 shapes of 64 to 16384 the choice costs 0.8 % on average,
-  // 12 % at worst (300 x 1000 x 300: mid 30.2, large 26.9).
-  const double small = rounds_time(P, count, r, 64, 128, 2.5, 0.55);
-  const double mid = rounds_time(P, count, r, 128, 128, 3.8, 0.72);
-  double large = 0;   // gemm_i8.hip, one launch a product
-  for (int o = 0; o < count; ++o)
-    large += 2.5 + rounds_time(P + o, 1, r, 256, 256, 5.0, 1.5);
-  if (large < small && large < mid) {
-    for (int o = 0; o < count; ++o) {
-      const int st = launch_gemm_i8(P[o].m, P[o].np, P[o].kp, r, P[o].left, P[o].m * P[o].kp,
-                                    P[o].right, P[o].n * P[o].kp, P[o].res, P[o].np,
-                                    P[o].m * P[o].np, kEpiResidues, s);
-      if (st != OZK_OK) return st;
-    }
-    return OZK_OK;
-  }
-  if (small < mid) launch_small_t<TileSmall>(A, s);
+  if (choice.tiles == kTilesSmall) launch_small_t<TileSmall>(A, s);
   else launch_small_t<TileMid>(A, s);
   return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
 }

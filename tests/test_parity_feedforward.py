@@ -525,6 +525,38 @@ def test_dgemm_gated_grad_parts():
     assert not da.any() and (wide[:, 30:] == 2.0).all() and dbias.shape == (0,)
 
 
+@pytest.mark.parametrize("m,n,k,r", [(1500, 1025, 1001, 16), (1344, 270, 1314, 16),
+                                     (1997, 504, 303, 20), (640, 167, 1227, 8),
+                                     (700, 700, 2000, 14), (2330, 716, 777, 14)])
+def test_two_gradients_in_one_list_of_tiles(m, n, k, r):
+    """Sizes whose two products are walked as one list of tiles, either of them the longer: the
+    bits of each alone, in a workspace of the queried size and replayed from a graph."""
+    announce(f"gradients in one list m={m} n={n} k={k} r={r}")
+    rng = np.random.default_rng(m)
+    a, b, dc, z = [to_dev(rng.standard_normal(s)) for s in ((m, k), (k, 2 * n), (m, n),
+                                                            (m, 2 * n))]
+    wide = torch.cat([dc, dc], 1)
+    calls = [(lambda **kw: ozk.ozk_dgemm_gated_grad(dc, a, b, r, z, **kw),
+              ozk.ozk_dgemm_gated_grad_workspace_size(m, n, k, r)),
+             (lambda **kw: ozk.ozk_dgemm_epilogue_grad(wide, a, b, r, preact=z, act="silu", **kw),
+              ozk.ozk_dgemm_epilogue_grad_workspace_size(m, 2 * n, k, r))]
+    for f, need in calls:
+        ws = torch.full((need + 1024,), 255, dtype=torch.uint8, device=device())
+        whole = f(workspace=ws[:need])
+        assert (ws[need:] == 255).all()
+        da = f(need_db=False, need_dbias=False)[0]
+        db = f(need_da=False, need_dbias=False)[1]
+        assert torch.equal(whole[0], da) and torch.equal(whole[1], db)
+        graph, out = captured(lambda: f(workspace=ws[:need]), [])
+        for _ in range(3):
+            for o in out:
+                o.zero_()
+            ws.fill_(255)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(o, w) for o, w in zip(out, whole))
+
+
 # ------------------------------------------------------------------ clipping
 def clip_inputs(sizes, kinds, seed, size=1.0):
     rng = np.random.default_rng(seed)
