@@ -1123,17 +1123,22 @@ def _line_ld(t: torch.Tensor, width: int) -> int:
 
 
 def _check_lines(codes, scales, name: str, device=None):
-    """Lines of codes and their scales, whole steps of both: (lines, values of a line)."""
+    """Lines of codes and their scales, whole steps of both: (lines, values of a line, leading
+    dimensions of codes and scales)."""
     _check_rows(codes, torch.uint8, name)
     lines, lb = codes.shape
     if lb % 128 or lb == 0:
         raise ValueError(f"{name} must hold whole steps of 128 bytes a line, got {lb}")
-    if device is not None and codes.device != device:
-        raise ValueError(f"{name} is on {codes.device}, expected {device}")
+    on = codes.device
+    if device is not None and on != device:
+        raise ValueError(f"{name} is on {on}, expected {device}")
     if scales is None:
         raise ValueError(f"{name}'s scales are missing")
-    _check_like(scales, (lines, lb // 16), torch.uint8, f"{name}'s scales", codes.device)
-    return lines, 2 * lb
+    sb = lb // 16
+    _check_like(scales, (lines, sb), torch.uint8, f"{name}'s scales", on)
+    if lines > 1:
+        return lines, 2 * lb, codes.stride(0), scales.stride(0)
+    return lines, 2 * lb, lb, sb   # a single line may have any stride
 
 
 def ozk_mxfp4_values(codes: torch.Tensor, scales: torch.Tensor, k: int | None = None,
@@ -1144,7 +1149,7 @@ def ozk_mxfp4_values(codes: torch.Tensor, scales: torch.Tensor, k: int | None = 
     if out is not None:
         dtype = out.dtype
     kind = _type(dtype)
-    lines, most = _check_lines(codes, scales, "codes")
+    lines, most, ldq, lds = _check_lines(codes, scales, "codes")
     k = most if k is None else k
     if not most - 256 < k <= most:
         raise ValueError(f"lines of {most} values do not hold {k}")
@@ -1152,9 +1157,8 @@ def ozk_mxfp4_values(codes: torch.Tensor, scales: torch.Tensor, k: int | None = 
     with _On(codes.device) as on:
         if out is None:
             out = codes.new_empty((lines, k), dtype=dtype)
-        _call("ozk_mxfp4_values", lines, k, _at(codes), _line_ld(codes, most // 2), _at(scales),
-              _line_ld(scales, most // 32), kind, _at(out), _line_ld(out, k),
-              on.stream(stream, out))
+        _call("ozk_mxfp4_values", lines, k, _at(codes), ldq, _at(scales), lds, kind, _at(out),
+              _line_ld(out, k), on.stream(stream, out))
     return out
 
 
@@ -1165,25 +1169,25 @@ def _mx_product(name, size, gated, x, scale_x, w, scale_w, bias, act, residual, 
     kind = _type(dtype)
     if kind == OZK_F64:
         raise TypeError("the output is float32, float16 or bfloat16")
-    m, k = _check_lines(x, scale_x, "X")
-    wide, kw = _check_lines(w, scale_w, "W", x.device)
+    m, k, ldx, ldsx = _check_lines(x, scale_x, "X")
+    device = x.device
+    wide, kw, ldw, ldsw = _check_lines(w, scale_w, "W", device)
     if k != kw:
         raise ValueError(f"X's lines hold {k} values, W's {kw}")
     n = _check_halves(wide, "W's lines") if gated else wide
-    _check_like(bias, (wide,), dtype, "bias", x.device)
-    _check_like(residual, (m, n), dtype, "residual", x.device)
-    _check_like(out, (m, n), dtype, "out", x.device)
-    _check_workspace(workspace, x.device)
-    with _On(x.device) as on:
+    _check_like(bias, (wide,), dtype, "bias", device)
+    _check_like(residual, (m, n), dtype, "residual", device)
+    _check_like(out, (m, n), dtype, "out", device)
+    _check_workspace(workspace, device)
+    with _On(device) as on:
         if out is None:
             out = x.new_empty((m, n), dtype=dtype)
         ws_bytes = size(m, n, k)
         if workspace is None and ws_bytes > 0:
-            workspace = _workspace(ws_bytes, x.device)
+            workspace = _workspace(ws_bytes, device)
         rest = () if gated else (_at(residual), _ld_opt(residual))
-        _call(name, m, n, k, _at(x), _line_ld(x, k // 2), _at(scale_x), _line_ld(scale_x, k // 32),
-              _at(w), _line_ld(w, k // 2), _at(scale_w), _line_ld(scale_w, k // 32), _at(bias),
-              _act(act), *rest, kind, _at(out), _ld(out), _at(workspace),
+        _call(name, m, n, k, _at(x), ldx, _at(scale_x), ldsx, _at(w), ldw, _at(scale_w), ldsw,
+              _at(bias), _act(act), *rest, kind, _at(out), _ld(out), _at(workspace),
               0 if workspace is None else workspace.numel(), on.stream(stream, out, workspace))
     return out
 
@@ -1228,23 +1232,24 @@ def ozk_clip_norm(tensors, max_norm: float, out=None, norm: torch.Tensor | None 
     if len(outs) != n:
         raise ValueError(f"{n} tensors, but {len(outs)} outputs")
     first = tensors[0]
-    for t in tensors if outs is tensors else (*tensors, *outs):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError("tensors must be CUDA/HIP tensors")
-        if not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
-    index = first.get_device()
+    on_gpu = isinstance(first, torch.Tensor) and first.is_cuda
+    index = first.get_device() if on_gpu else None   # -1 of a host tensor
+    for t in tensors if outs is tensors else tensors + outs:
+        if not isinstance(t, torch.Tensor) or t.get_device() != index or not t.is_contiguous():
+            if not isinstance(t, torch.Tensor) or not t.is_cuda:
+                raise TypeError("tensors must be CUDA/HIP tensors")
+            if not t.is_contiguous():
+                raise ValueError("tensors must be contiguous")
+            raise ValueError(f"a tensor is on {t.device}, expected {first.device}")
+    if outs is not tensors:
+        for t, o in zip(tensors, outs):
+            if o.dtype is not t.dtype or not o.is_same_size(t):
+                raise ValueError(f"an output is {o.dtype} {tuple(o.shape)}, its tensor {t.dtype} "
+                                 f"{tuple(t.shape)}")
     sizes = array("q", [t.numel() for t in tensors])
     kinds = array("i", [_type(t.dtype) for t in tensors])
     xs = array("Q", [t.data_ptr() for t in tensors])
     ys = xs if outs is tensors else array("Q", [t.data_ptr() for t in outs])
-    for t, o in zip(tensors, outs):
-        if t.get_device() != index or o.get_device() != index:
-            raise ValueError(f"a tensor is on {t.device}, its output on {o.device}, expected "
-                             f"{first.device}")
-        if o is not t and (o.dtype is not t.dtype or o.shape != t.shape):
-            raise ValueError(f"an output is {o.dtype} {tuple(o.shape)}, its tensor {t.dtype} "
-                             f"{tuple(t.shape)}")
     if norm is not None:
         _check_like(norm, (), torch.float64, "norm", first.device)
     _check_workspace(workspace, first.device)
