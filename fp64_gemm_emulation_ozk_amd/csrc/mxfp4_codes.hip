@@ -6,8 +6,9 @@
 // finds.  A code is RNE(x 2^-E) on {0, 0.5, 1, 1.5, 2, 3, 4, 6}, 6 beyond, which gfx950's
 // conversions to FP4 compute with the scale as their operand.
 //
-// Memory bounds all of them.  4096 x 16384 bf16: rows 32.3 us (170 MB, 5.3 TB/s), values 26.5;
-// 4099 x 5001 fp32: columns 19.1 us (93 MB, 4.9 TB/s), values 16.2.
+// Memory bounds all of them.  From operands in no cache, us: 4096 x 16384 bf16 rows 33.3, columns
+// 37.5, values 25.9 (170 MB each, 5.1, 4.5 and 6.6 TB/s); 4099 x 5001 fp32 rows 20.3, columns
+// 21.9, values 22.1 (93 MB).  In the last-level cache: 27, 26 and 26; 16.3, 18.1 and 16.2.
 #include "ozk_internal.h"
 #include "rows.h"
 
@@ -216,14 +217,22 @@ __global__ __launch_bounds__(512) void mxfp4_cols_kernel(int64_t rows, int64_t c
   const int64_t col0 = (int64_t)(id - step * tiles) * kLines, row0 = (int64_t)step * 256 + 32 * w;
   const int64_t c = col0 + kC * lane;
   // All rows asked for without a branch between: what lies past the matrix reads its last row or
-  // column, and is made zero below (rows) or not stored (columns).  kC <= cols.
+  // column, and is made zero below (rows) or not stored (columns).  kC <= cols.  Whole blocks have
+  // code of their own: 32 clamped row addresses did not fit the scalar registers (4096 x 16384
+  // bf16 38.2 us so, else 37.5; 1500 x 2000 fp32 8.4 and 7.8).
   const int64_t from = col0 + kC <= cols ? col0 : cols - kC;   // uniform, as a row's address
   const uint32_t off = (uint32_t)((c + kC <= cols ? c : cols - kC) - from);
   V raw[32];
+  if (row0 + 32 <= rows) {   // uniform
+    const T* p = x + row0 * ldx + from;
 #pragma unroll
-  for (int r = 0; r < 32; ++r) {
-    const T* p = x + (row0 + r < rows ? row0 + r : rows - 1) * ldx + from;
-    raw[r] = *reinterpret_cast<const V*>(p + off);
+    for (int r = 0; r < 32; ++r) raw[r] = *reinterpret_cast<const V*>(p + r * ldx + off);
+  } else {
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+      const T* p = x + (row0 + r < rows ? row0 + r : rows - 1) * ldx + from;
+      raw[r] = *reinterpret_cast<const V*>(p + off);
+    }
   }
   T v[kC][32];
 #pragma unroll
@@ -296,8 +305,11 @@ __device__ __forceinline__ void take_codes(uint32_t c, uint32_t byte, A (&v)[N])
 }
 
 // A half wave writes a unit in 8 / N stores of 16 bytes a lane, each whole lines of memory (32
-// bytes a lane in two stores of every other 16: 8192^2 to fp32 72 us).
-template <typename T>
+// bytes a lane in two stores of every other 16: 8192^2 to fp32 72 us).  kWhole: rows start at
+// multiples of 16 bytes, so that no two stores share a line; then they are marked as not to be
+// read soon.  4096 x 16384 to bf16 25.9 us so, else 32.1, and with a reader behind 58.0 and 57.5;
+// 8192^2 to fp32 48.5 and 57.4, 102 and 114.  (Rows of 4099 fp32, marked: 25.3, not marked 22.0.)
+template <typename T, bool kWhole>
 __global__ __launch_bounds__(256) void mxfp4_values_kernel(uint32_t lines, int64_t k,
                                                            uint32_t steps,
                                                            const uint8_t* __restrict__ codes,
@@ -306,6 +318,7 @@ __global__ __launch_bounds__(256) void mxfp4_values_kernel(uint32_t lines, int64
                                                            int64_t lds, T* __restrict__ out,
                                                            int64_t ldo) {
   constexpr int N = Vec<T>::N, kQ = 8 / N;
+  typedef T V __attribute__((ext_vector_type(N)));
   typedef typename AccOf<T>::type A;
   const int lane = threadIdx.x & 63, sub = lane & 31;
   const uint32_t wave = blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -335,8 +348,16 @@ __global__ __launch_bounds__(256) void mxfp4_values_kernel(uint32_t lines, int64
       for (int u = 0; u < kQ; ++u) {
         A v[N];
         take_codes<N>(c[i][u], s[i][u], v);
-        store_vec(out + (int64_t)at.line * ldo,
-                  (int64_t)at.step * 256 + u * (32 * N) + N * sub, k, v);
+        T* const row = out + (int64_t)at.line * ldo;
+        const int64_t col = (int64_t)at.step * 256 + u * (32 * N) + N * sub;
+        if (kWhole && col + N <= k) {
+          V o;
+#pragma unroll
+          for (int e = 0; e < N; ++e) o[e] = (T)v[e];
+          __builtin_nontemporal_store(o, reinterpret_cast<V*>(row + col));
+        } else {
+          store_vec(row, col, k, v);
+        }
       }
     }
     at.two_on(steps);
@@ -399,11 +420,17 @@ template <typename T>
 int values_t(int64_t lines, int64_t k, const uint8_t* codes, int64_t ldq, const uint8_t* scales,
              int64_t lds, T* out, int64_t ldo, hipStream_t s) {
   const int64_t steps = (k + 255) / 256, most = lines_at_once(steps);
+  const bool whole = reinterpret_cast<uintptr_t>(out) % 16 == 0 && ldo * sizeof(T) % 16 == 0;
   for (int64_t r = 0; r < lines; r += most) {
     const int64_t some = lines - r < most ? lines - r : most;
-    hipLaunchKernelGGL((mxfp4_values_kernel<T>), dim3(unit_blocks(some, steps)), dim3(256), 0, s,
-                       (uint32_t)some, k, (uint32_t)steps, codes + r * ldq, ldq, scales + r * lds,
-                       lds, out + r * ldo, ldo);
+    const dim3 grid(unit_blocks(some, steps)), block(256);
+#define OZK_VALUES(WHOLE)                                                                         \
+  hipLaunchKernelGGL((mxfp4_values_kernel<T, WHOLE>), grid, block, 0, s, (uint32_t)some, k,       \
+                     (uint32_t)steps, codes + r * ldq, ldq, scales + r * lds, lds, out + r * ldo, \
+                     ldo)
+    if (whole) OZK_VALUES(true);
+    else OZK_VALUES(false);
+#undef OZK_VALUES
   }
   return hipGetLastError() == hipSuccess ? OZK_OK : OZK_EHIP;
 }

@@ -7,8 +7,8 @@
 // Few rows are bound by the bytes of W: the stream kernel.  Many are bound by the matrix cores and
 // by what feeds them: the tile kernels.  (us, bf16, MI355X; a replayed graph)
 //   rows of 8192 x 8192:  1: 6.2   16: 7.0   32: 8.5   64: 11.6   128: 19.4   256: 23   512: 29
-//   8192^3: 251 (4.4 PFLOP/s); 4096 x 16384 x 4096: 145, with gelu 173, with a residual 178, with
-//   both 191; gated 4096 x 2 8192 x 4096: 145
+//   8192^3: 251 (4.4 PFLOP/s); 4096 x 16384 x 4096: 143, with gelu 171, with a residual 165, with
+//   both 184; gated 4096 x 2 8192 x 4096: 139
 #include "activation.h"
 #include "ozk_internal.h"
 #include "rows.h"
@@ -455,6 +455,11 @@ struct Place {
 // consecutive outputs each; a phase's groups of rows are finished together, for their
 // instructions' latencies, and the next phase's residuals asked for meanwhile.  The phases are a
 // loop, through which the blocks move down: written out they would not fit the instruction cache.
+// A residual is read once and marked so; without one the outputs are marked as not to be read
+// soon (bf16, cold, and with a reader of the outputs behind: 4096 x 16384 x 4096 with a residual
+// 191 -> 174 us and 219 -> 205, with gelu too 194 -> 190 and 227 -> 215; gelu alone 175 -> 172
+// and 208 -> 205; gated 147 -> 139 and 159 -> 153.  Outputs marked beside a residual: 179 and
+// 211, 194 and 228).
 template <typename TL, bool kGated, typename O, int NI>
 __device__ __forceinline__ void put_tile(const MxEpilogue<O>& E, v4f (&acc)[NI][TL::TJ],
                                          int64_t wrow0, int64_t wcol0, int lane, float* mine,
@@ -499,8 +504,8 @@ __device__ __forceinline__ void put_tile(const MxEpilogue<O>& E, v4f (&acc)[NI][
     if (kGated || !E.residual || !inside) return;
 #pragma unroll
     for (int it = 0; it < kIters; ++it)
-      res[it] =
-          *reinterpret_cast<const V8*>(E.residual + (row0 + it * kRows + lrow) * E.ldr + col);
+      res[it] = __builtin_nontemporal_load(
+          reinterpret_cast<const V8*>(E.residual + (row0 + it * kRows + lrow) * E.ldr + col));
   };
   ask(wrow0);
 #pragma unroll 1
@@ -547,7 +552,9 @@ __device__ __forceinline__ void put_tile(const MxEpilogue<O>& E, v4f (&acc)[NI][
           if constexpr (kGated) y *= up[8 * it + u];
           o[u] = (O)y;
         }
-        *reinterpret_cast<V8*>(E.c + (row0 + it * kRows + lrow) * E.ldc + col) = o;
+        V8* const to = reinterpret_cast<V8*>(E.c + (row0 + it * kRows + lrow) * E.ldc + col);
+        if (!kGated && E.residual) *to = o;
+        else __builtin_nontemporal_store(o, to);
       }
     } else {
 #pragma unroll 1
