@@ -2,6 +2,8 @@
 
 Tolerances count roundings, as in the layer operators' tests: u = 2^-24 (2^-53) is half a step
 of the fp32 (fp64) arithmetic, eps / 2 of the output's type one rounding to it."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -821,6 +823,41 @@ def test_graphs_share_a_workspace():
             graph.replay()
             torch.cuda.synchronize()
             assert all(torch.equal(o, e) for o, e in zip(out, want))
+
+
+def test_threads_on_streams_of_their_own():
+    """Four host threads, each with a stream, run a serving block, a training step and a clipping
+    at once: the bits of each alone."""
+    announce("feed-forward threads")
+    dtype = torch.bfloat16
+    p = serve_weights(520, 700, dtype, 5)
+    rng = np.random.default_rng(6)
+    n, hid = 96, 128
+    jobs = []
+    for i in range(4):
+        x = torch.from_numpy(rng.standard_normal((5 + 40 * i, 520))).to(dtype).to(device())
+        args = [to_dev(rng.standard_normal(s)) for s in ((200, n), (200, n), (n,), (n,),
+                                                         (n, 2 * hid), (2 * hid,), (hid, n), (n,))]
+        jobs.append((x, args))
+    want = [(serve(x, p, dtype), train_step(*args)) for x, args in jobs]
+    torch.cuda.synchronize()
+    got = [None] * 4
+
+    def work(i):
+        x, args = jobs[i]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(5):
+                got[i] = (serve(x, p, dtype), train_step(*args))
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for g, w in zip(got, want):
+        assert torch.equal(g[0], w[0])
+        assert all(torch.equal(a, b) for a, b in zip(g[1], w[1]))
 
 
 def test_linear_gradients_on_codes():
