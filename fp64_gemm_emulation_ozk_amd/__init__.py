@@ -1247,7 +1247,10 @@ def ozk_clip_norm(tensors, max_norm: float, out=None, norm: torch.Tensor | None 
                 raise ValueError(f"an output is {o.dtype} {tuple(o.shape)}, its tensor {t.dtype} "
                                  f"{tuple(t.shape)}")
     sizes = array("q", [t.numel() for t in tensors])
-    kinds = array("i", [_type(t.dtype) for t in tensors])
+    try:
+        kinds = array("i", [_TYPES[t.dtype] for t in tensors])
+    except KeyError as e:
+        raise TypeError(f"unsupported element type {e.args[0]}") from None
     xs = array("Q", [t.data_ptr() for t in tensors])
     ys = xs if outs is tensors else array("Q", [t.data_ptr() for t in outs])
     if norm is not None:
