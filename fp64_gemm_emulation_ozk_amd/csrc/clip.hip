@@ -142,9 +142,22 @@ __global__ __launch_bounds__(kThreads) void clip_sums_kernel(ClipTable A,
   }
 }
 
+// M / N as one number, and for fp64 values as step coef step: where the quotient is subnormal, so
+// that it holds few bits or none, step is 2^-512 and coef M 2^512 / (N 2^-512); else step is 1,
+// which changes nothing.  A value times 2^-512 loses bits only below 2^-510, where its output is 0.
+// The other types' outputs are below 2^-894 there, 0 in any of them.
+struct Factor {
+  double whole, step, coef;
+};
+__device__ __forceinline__ Factor factor_of(double max_norm, double total) {
+  const double c = max_norm / total;
+  if (c >= 0x1p-1022) return {c, 1.0, c};
+  return {c, 0x1p-512, (max_norm * 0x1p512) / (total * 0x1p-512)};
+}
+
 template <typename T>
 __device__ __forceinline__ void scale_chunk(const ClipTable& A, int t, int chunk,
-                                            double coef) {
+                                            Factor by) {
   T* out = (T*)A.out[t];
   each_vector<kScaleVectors>(
       (const T*)A.x[t], A.size[t], chunk,
@@ -152,10 +165,9 @@ __device__ __forceinline__ void scale_chunk(const ClipTable& A, int t, int chunk
         typename Vec<T>::type o;
 #pragma unroll
         for (int u = 0; u < Vec<T>::N; ++u) {
-          const double y = (double)v[u] * coef;
           // to 16 bits by way of fp32, which is off a direct rounding by 2^-24 at most
-          if constexpr (sizeof(T) == 8) o[u] = y;
-          else o[u] = (T)(float)y;
+          if constexpr (sizeof(T) == 8) o[u] = v[u] * by.step * by.coef * by.step;
+          else o[u] = (T)(float)((double)v[u] * by.whole);
         }
         if (count == Vec<T>::N) {
           __builtin_nontemporal_store(o, reinterpret_cast<typename Vec<T>::type*>(out + at));
@@ -193,15 +205,15 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable A,
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
   const bool clips = total > max_norm && !__builtin_isinf(total);
   if (!clips && in_place) return;
-  const double coef = clips ? max_norm / total : 1.0;
+  const Factor by = clips ? factor_of(max_norm, total) : Factor{1.0, 1.0, 1.0};
   for (int c = A.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
     const int t = tensor_of(A, c);
     const int chunk = c - A.first[t];
     switch (A.type[t]) {
-      case OZK_F64: scale_chunk<double>(A, t, chunk, coef); break;
-      case OZK_F32: scale_chunk<float>(A, t, chunk, coef); break;
-      case OZK_F16: scale_chunk<f16_t>(A, t, chunk, coef); break;
-      default: scale_chunk<bf16_t>(A, t, chunk, coef); break;
+      case OZK_F64: scale_chunk<double>(A, t, chunk, by); break;
+      case OZK_F32: scale_chunk<float>(A, t, chunk, by); break;
+      case OZK_F16: scale_chunk<f16_t>(A, t, chunk, by); break;
+      default: scale_chunk<bf16_t>(A, t, chunk, by); break;
     }
   }
 }

@@ -646,6 +646,32 @@ def test_clip_norm_range():
     assert float(norm) == 0
 
 
+@pytest.mark.parametrize("size,max_norm", [(1e300, 1e-20), (1e300, 1e-30), (1e305, 1e-305),
+                                           (1e300, 3e-8), (1e10, 1e-310), (1e305, 5e-324),
+                                           (1e300, 0.0)])
+def test_clip_norm_small_factor(size, max_norm):
+    """Factors below fp64's normal range, down to none at all: the outputs are at most max_norm and
+    as precise as where the factor is normal (test_clip_norm_range), to two steps of 2^-1074.  The
+    values beside them in other types become 0."""
+    announce(f"clip {size} to {max_norm}")
+    xs = [x.to(device()) for x in clip_inputs([40000, 3], ["float64"] * 2, 7, size)]
+    xs.append(torch.tensor([3e38, -1.0, 0.0], device=device()))
+    xs.append(torch.tensor([6e4, -6e-8], dtype=torch.float16, device=device()))
+    outs = [torch.full_like(x, 2.0) for x in xs]
+    norm, _ = ozk.ozk_clip_norm(xs, max_norm, out=outs)
+    # size is taken out of the values before squaring, and so of the factor
+    units = [host(x) / size for x in xs]
+    total = np.sqrt(sum((u * u).sum() for u in units))
+    assert abs(float(norm) / size - total) <= 2.0 ** -43 * total
+    for o, u in zip(outs[:2], units):
+        want = u / total * max_norm
+        assert_near(host(o), want, 2.0 ** -42 * np.abs(want) + 2.0 ** -1073, "clipped")
+    assert not any(o.any() for o in outs[2:])
+    keep = [x.clone() for x in xs]
+    ozk.ozk_clip_norm(xs, max_norm)
+    assert all(torch.equal(x, o) for x, o in zip(xs, outs)) and not torch.equal(keep[0], xs[0])
+
+
 def test_clip_norm_large():
     """A tensor of more than 2^32 bytes and 2^31 elements among small ones."""
     announce("clip large")
