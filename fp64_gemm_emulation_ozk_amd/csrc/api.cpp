@@ -1005,7 +1005,7 @@ int ozk_dgemm_epilogue_grad(int64_t m, int64_t n, int64_t k, const double* dC, i
 int ozk_dgemm_gated_workspace_size(int64_t m, int64_t n, int64_t k, int r, size_t* bytes) {
   if (!bytes || m < 0 || n < 0 || k < 1 || check_r(r) != OZK_OK) return OZK_EINVAL;
   if (k > OZK_MAX_K) return OZK_ERANGE;
-  if (n > (int64_t)1 << 40) return OZK_EUNSUPPORTED;
+  if (n >= (int64_t)1 << 40) return OZK_EUNSUPPORTED;
   *bytes = product_layout(gated_product(m, n, k, nullptr, k, nullptr, 2 * n), r).total();
   return OZK_OK;
 }
@@ -1018,7 +1018,7 @@ int ozk_dgemm_gated(int64_t m, int64_t n, int64_t k, const double* A, int64_t ld
   if (scaling != OZK_SCALING_MAX && scaling != OZK_SCALING_NORM) return OZK_EINVAL;
   if (m < 0 || n < 0 || k < 1) return OZK_EINVAL;
   if (k > OZK_MAX_K) return OZK_ERANGE;
-  if (n > (int64_t)1 << 40) return OZK_EUNSUPPORTED;
+  if (n >= (int64_t)1 << 40) return OZK_EUNSUPPORTED;
   const int64_t n1 = n > 0 ? n : 1;
   if (lda < k || ldb < 2 * n1 || ldc < n1 || (Z && ldz < 2 * n1)) return OZK_EINVAL;
   int wa = 0, wb = 0;
@@ -1343,9 +1343,9 @@ int ozk_clip_norm(int64_t count, const void* const* x, void* const* out, const i
     const size_t e = type_size(types[i]);
     if (!x[i] || !out[i] || !aligned(x[i], e) || !aligned(out[i], e)) return OZK_EINVAL;
     // chunks are counted in 32 bits
-    if (sizes[i] > ((int64_t)1 << 44) / (int64_t)e) return OZK_EUNSUPPORTED;
+    if (sizes[i] >= ((int64_t)1 << 44) / (int64_t)e) return OZK_EUNSUPPORTED;
     bytes += sizes[i] * e + 32768;
-    if (bytes > (int64_t)1 << 45) return OZK_EUNSUPPORTED;
+    if (bytes >= (int64_t)1 << 45) return OZK_EUNSUPPORTED;
   }
   const size_t need = clip_norm_workspace(count);
   if (need > workspace_bytes || (need > 0 && !workspace)) return OZK_EWORKSPACE;

@@ -511,7 +511,7 @@ int ozk_layernorm_backward(int64_t rows, int64_t cols, int type, const void* dy,
  * Both: 1 <= k <= OZK_MX_MAX_K; a workspace (256-byte aligned) of the size the query returns,
  *   which may be 0 (workspace may be NULL then); C overlaps no other operand.  OZK_EUNSUPPORTED
  *   from m = 2^31 or n = 2^30 on, for leading dimensions of codes or scales from 2^24 on, and
- *   where a launch would pass 2^32 threads. */
+ *   where a launch would come to 2^32 threads. */
 int64_t ozk_mxfp4_line_bytes(int64_t k);
 int64_t ozk_mxfp4_scale_bytes(int64_t k);
 int ozk_mxfp4_quant(int64_t rows, int64_t cols, int type, const void* x, int64_t ldx, int axis,
@@ -542,7 +542,8 @@ int ozk_mxfp4_gated(int64_t m, int64_t n, int64_t k, const uint8_t* X, int64_t l
  * factor is formed in fp64 and rounded to its type (to 16 bits by way of fp32).  Where N is Inf or
  * NaN the values are left as they are.  max_norm >= 0; with Inf only N is computed (and x copied
  * where out is not x).  The workspace (256-byte aligned) takes ozk_clip_norm_workspace_size bytes.
- * OZK_EUNSUPPORTED from 2^23 tensors, or 2^44 bytes of one, on. */
+ * OZK_EUNSUPPORTED from 2^23 tensors, 2^44 bytes of one tensor, or 2^45 bytes of all that are not
+ * empty, with 2^15 added for each, on. */
 int ozk_clip_norm_workspace_size(int64_t count, size_t* bytes);
 int ozk_clip_norm(int64_t count, const void* const* x, void* const* out, const int64_t* sizes,
                   const int* types, double max_norm, double* norm, void* workspace,

@@ -204,6 +204,39 @@ def test_clip_norm_refusals(lib):
                  ws=None) == EWORKSPACE
 
 
+def test_limits_are_where_they_are_stated(lib):
+    """The first value that is refused as unsupported, and the last that is not: with no
+    workspace the latter are refused for that.  No call gets past the checks."""
+    call = _caller(lib.ozk_dgemm_gated,
+                   "m n k A lda B ldb bias act Z ldz C ldc r scaling ws wsb stream", dict(
+                       m=1, n=4, k=4, A=FAKE, lda=4, B=FAKE, ldb=1 << 42, bias=None, act=4, Z=None,
+                       ldz=0, C=FAKE, ldc=1 << 42, r=14, scaling=0, ws=None, wsb=0, stream=None))
+    out = ctypes.c_size_t()
+    size = lib.ozk_dgemm_gated_workspace_size
+    for n, unsupported in ((1 << 40, True), ((1 << 40) - 1, False)):
+        assert call(n=n) == (EUNSUPPORTED if unsupported else EWORKSPACE)
+        assert size(1, n, 4, 14, ctypes.byref(out)) == (EUNSUPPORTED if unsupported else OK)
+
+    a = 1 << 50
+    for kind, e in ((0, 8), (1, 4), (2, 2), (3, 2)):
+        most = (1 << 44) // e
+        assert _clip(lib, [(a, a, most, kind)], ws=None) == EUNSUPPORTED
+        assert _clip(lib, [(a, a, most - 1, kind)], ws=None) == EWORKSPACE
+    # of all: 2^45 bytes with 2^15 for each tensor
+    for last, status in (((1 << 43) - 3 * 32768, EUNSUPPORTED),
+                         ((1 << 43) - 3 * 32768 - 8, EWORKSPACE)):
+        each = [1 << 43, 1 << 43, 1 << 43, last - 32768]
+        tensors = [(a + (i << 44), a + (i << 44), b // 8, 0) for i, b in enumerate(each)]
+        assert _clip(lib, tensors + [(a, a, 0, 0)], ws=None) == status
+
+    for f in (lib.ozk_mxfp4_linear_workspace_size, lib.ozk_mxfp4_gated_workspace_size):
+        for m, n, status in (((1 << 31) - 1, 1, OK), (1 << 31, 1, EUNSUPPORTED),
+                             (1, (1 << 30) - 1, OK), (1, 1 << 30, EUNSUPPORTED)):
+            assert f(m, n, 256, ctypes.byref(out)) == status
+    size = lib.ozk_clip_norm_workspace_size
+    assert size((1 << 23) - 1, ctypes.byref(out)) == OK
+
+
 def test_binding_refuses_host_tensors_and_names():
     a = torch.zeros(4, 4, dtype=torch.float64)
     q = torch.zeros(4, 128, dtype=torch.uint8)
