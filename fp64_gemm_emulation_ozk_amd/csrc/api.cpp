@@ -798,9 +798,10 @@ struct Job {
 };
 
 // One or two products in emulated fp64, each with its epilogue.  Small ones run together, each
-// in a workspace of its own (in `workspace` one after the other); others one after the other,
-// over the same workspace.
-int run_jobs(Job* jobs, int count, int r, int scaling, void* workspace, hipStream_t s) {
+// in a workspace of its own (in `workspace` one after the other), and so do those that `joined`
+// names if `bytes` of workspace hold both; others one after the other, over the same workspace.
+int run_jobs(Job* jobs, int count, int r, int scaling, void* workspace, size_t bytes,
+             hipStream_t s) {
   int st, wl = 0, wr = 0;
   bool together = true;
   for (int i = 0; i < count; ++i) together = together && small(jobs[i].P);
@@ -833,7 +834,9 @@ int run_jobs(Job* jobs, int count, int r, int scaling, void* workspace, hipStrea
     if ((st = launch_products(prod, count, r, s))) return st;
     return jobs[0].reconstruct(r, s);
   }
-  const bool join = count == 2 && joined(jobs[0].P, jobs[1].P, r);
+  const bool join = count == 2 && joined(jobs[0].P, jobs[1].P, r) &&
+                    product_layout(jobs[0].P, r).total() +
+                            product_layout(jobs[1].P, r).total() <= bytes;
   PlaneProduct prod[2];
   Carver cv(workspace);
   for (int i = 0; i < count; ++i) {
@@ -893,10 +896,13 @@ Product grad_b(int64_t m, int64_t n, int64_t k, const double* A, int64_t lda,
 }
 
 // Workspace of the gradient: G, the chunks' sums of its columns, and the two products' (side
-// by side where they run together, else the larger one).
+// by side where they run together, else the larger one).  Of products that are not small the
+// larger one's is enough (least): then they run one after the other.
 struct EpilogueGradLayout {
-  size_t g, part, products;
-  size_t total() const { return align256(g) + align256(part) + align256(products); }
+  size_t g, part, products, least_products;
+  size_t before() const { return align256(g) + align256(part); }   // the products'
+  size_t total() const { return before() + align256(products); }
+  size_t least() const { return before() + align256(least_products); }
 };
 
 EpilogueGradLayout epilogue_grad_layout(int64_t m, int64_t n, int64_t k, int r) {
@@ -906,7 +912,8 @@ EpilogueGradLayout epilogue_grad_layout(int64_t m, int64_t n, int64_t k, int r) 
   const Product pa = grad_a(m, n, k, nullptr, n, nullptr, n);
   const Product pb = grad_b(m, n, k, nullptr, k, nullptr, n);
   const size_t a = product_layout(pa, r).total(), b = product_layout(pb, r).total();
-  L.products = joined(pa, pb, r) ? a + b : (a > b ? a : b);
+  L.least_products = small(pa) && small(pb) ? a + b : (a > b ? a : b);
+  L.products = joined(pa, pb, r) ? a + b : L.least_products;
   return L;
 }
 
@@ -943,7 +950,7 @@ int ozk_dgemm_epilogue(int64_t m, int64_t n, int64_t k, const double* A, int64_t
   if (!aligned(workspace, 256)) return OZK_EINVAL;
   if ((size_t)m * n > (size_t)0x7fffffffffffull) return OZK_EUNSUPPORTED;
   Job job{P, {bias, residual, ldr, Z, ldz, act}, C, ldc};
-  return run_jobs(&job, 1, r, scaling, workspace, as_stream(stream));
+  return run_jobs(&job, 1, r, scaling, workspace, workspace_bytes, as_stream(stream));
 }
 
 int ozk_dgemm_epilogue_grad_workspace_size(int64_t m, int64_t n, int64_t k, int r,
@@ -979,12 +986,13 @@ int ozk_dgemm_epilogue_grad(int64_t m, int64_t n, int64_t k, const double* dC, i
   if (!dA && !dB && !dbias) return OZK_OK;
   if (!dC || (act != OZK_ACT_NONE && !Z) || (dA && !B) || (dB && !A)) return OZK_EINVAL;
   const EpilogueGradLayout L = epilogue_grad_layout(m, n, k, r);
-  if (!workspace || workspace_bytes < L.total()) return OZK_EWORKSPACE;
+  if (!workspace || workspace_bytes < L.least()) return OZK_EWORKSPACE;
   if (!aligned(workspace, 256)) return OZK_EINVAL;
   Carver cv(workspace);
   double* g = static_cast<double*>(cv.take(L.g));
   double* part = static_cast<double*>(cv.take(L.part));
-  void* products = cv.take(L.products);
+  const size_t room = workspace_bytes - L.before();
+  void* products = cv.take(room);
   hipStream_t s = as_stream(stream);
   // without an activation G is dC itself
   const bool own_g = act != OZK_ACT_NONE && (dA || dB);
@@ -998,7 +1006,7 @@ int ozk_dgemm_epilogue_grad(int64_t m, int64_t n, int64_t k, const double* dC, i
   int count = 0;
   if (dA) jobs[count++] = Job{grad_a(m, n, k, gp, ldg, B, ldb), none, dA, ldda};
   if (dB) jobs[count++] = Job{grad_b(m, n, k, A, lda, gp, ldg), none, dB, lddb};
-  return count ? run_jobs(jobs, count, r, scaling, products, s) : OZK_OK;
+  return count ? run_jobs(jobs, count, r, scaling, products, room, s) : OZK_OK;
 }
 
 // ---------------------------------------------------------------- gated block in emulated fp64
@@ -1031,7 +1039,7 @@ int ozk_dgemm_gated(int64_t m, int64_t n, int64_t k, const double* A, int64_t ld
   if (!aligned(workspace, 256)) return OZK_EINVAL;
   if ((size_t)m * n > (size_t)0x3fffffffffffull) return OZK_EUNSUPPORTED;
   Job job{P, {bias, nullptr, 0, Z, ldz, act}, C, ldc, true};
-  return run_jobs(&job, 1, r, scaling, workspace, as_stream(stream));
+  return run_jobs(&job, 1, r, scaling, workspace, workspace_bytes, as_stream(stream));
 }
 
 int ozk_dgemm_gated_grad_workspace_size(int64_t m, int64_t n, int64_t k, int r, size_t* bytes) {
@@ -1065,12 +1073,13 @@ int ozk_dgemm_gated_grad(int64_t m, int64_t n, int64_t k, const double* dC, int6
   if (!dA && !dB && !dbias) return OZK_OK;
   if (!dC || !Z || (dA && !B) || (dB && !A)) return OZK_EINVAL;
   const EpilogueGradLayout L = epilogue_grad_layout(m, w, k, r);
-  if (!workspace || workspace_bytes < L.total()) return OZK_EWORKSPACE;
+  if (!workspace || workspace_bytes < L.least()) return OZK_EWORKSPACE;
   if (!aligned(workspace, 256)) return OZK_EINVAL;
   Carver cv(workspace);
   double* g = static_cast<double*>(cv.take(L.g));
   double* part = static_cast<double*>(cv.take(L.part));
-  void* products = cv.take(L.products);
+  const size_t room = workspace_bytes - L.before();
+  void* products = cv.take(room);
   if ((st = launch_gate_grad(m, n, dC, lddc, Z, ldz, act, dA || dB ? g : nullptr, part, dbias, s)))
     return st;
   const DgemmEpilogue none{nullptr, nullptr, 0, nullptr, 0, OZK_ACT_NONE};
@@ -1078,7 +1087,7 @@ int ozk_dgemm_gated_grad(int64_t m, int64_t n, int64_t k, const double* dC, int6
   int count = 0;
   if (dA) jobs[count++] = Job{grad_a(m, w, k, g, w, B, ldb), none, dA, ldda};
   if (dB) jobs[count++] = Job{grad_b(m, w, k, A, lda, g, w), none, dB, lddb};
-  return count ? run_jobs(jobs, count, r, scaling, products, s) : OZK_OK;
+  return count ? run_jobs(jobs, count, r, scaling, products, room, s) : OZK_OK;
 }
 
 // ---------------------------------------------------------------- int8 linear layer

@@ -225,7 +225,9 @@ int ozk_dgemm_epilogue(int64_t m, int64_t n, int64_t k, const double* A, int64_t
  * with r moduli like ozk_dgemm_ex, inner dimensions n and m; dbias is summed in fp64 in a
  * fixed order.  m, n and k at most OZK_MAX_K.  m = 0 or n = 0 gives zero gradients.  The
  * workspace (256-byte aligned, ozk_dgemm_epilogue_grad_workspace_size bytes) serves any
- * choice of outputs.  No output overlaps an input. */
+ * choice of outputs.  For some sizes the query counts the space of both products, which then run
+ * as one; unless both are small, one with room for G, its column sums and the larger product alone
+ * serves too, with the same bits (OZK_EWORKSPACE below that).  No output overlaps an input. */
 int ozk_dgemm_epilogue_grad_workspace_size(int64_t m, int64_t n, int64_t k, int r, size_t* bytes);
 int ozk_dgemm_epilogue_grad(int64_t m, int64_t n, int64_t k, const double* dC, int64_t lddc,
                             const double* A, int64_t lda, const double* B, int64_t ldb,

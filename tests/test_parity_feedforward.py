@@ -559,6 +559,47 @@ def test_two_gradients_in_one_list_of_tiles(m, n, k, r):
             assert all(torch.equal(o, w) for o, w in zip(out, whole))
 
 
+@pytest.mark.parametrize("m,n,k,r,both_small", [(1500, 1025, 1001, 16, False),
+                                                (1997, 504, 303, 20, True),
+                                                (700, 700, 2000, 14, False)])
+def test_gradients_in_the_larger_product_s_workspace(m, n, k, r, both_small):
+    """Where the query counts both products' space, one that holds the larger alone gives the same
+    bits, for both gradients and for either, and nothing past it is written; less is refused, and
+    so is this much where both products are small (2^21 values in their operands at most).
+    The products' own sizes are at least their planes and residues."""
+    announce(f"gradients in less workspace m={m} n={n} k={k} r={r}")
+    rng = np.random.default_rng(m)
+    a, b, dc, z = [to_dev(rng.standard_normal(s)) for s in ((m, k), (k, 2 * n), (m, n),
+                                                            (m, 2 * n))]
+    wide = torch.cat([dc, dc], 1)
+    up = lambda v, by: -(-v // by) * by
+    least = lambda rows, cols, inner: r * up(inner, 128) * (rows + cols) + r * rows * up(cols, 64)
+    one, two = sorted((least(m, k, 2 * n), least(k, 2 * n, m)))
+    g = 16 * m * n
+    calls = [(lambda **kw: ozk.ozk_dgemm_gated_grad(dc, a, b, r, z, **kw),
+              ozk.ozk_dgemm_gated_grad_workspace_size(m, n, k, r)),
+             (lambda **kw: ozk.ozk_dgemm_epilogue_grad(wide, a, b, r, preact=z, act="silu", **kw),
+              ozk.ozk_dgemm_epilogue_grad_workspace_size(m, 2 * n, k, r))]
+    for f, need in calls:
+        assert need >= g + one + two                  # both are counted
+        less = (need - one) // 256 * 256
+        want = f()
+        ws = torch.full((need,), 255, dtype=torch.uint8, device=device())
+        if both_small:
+            with pytest.raises(ozk.OzkError) as e:
+                f(workspace=ws[:less])
+            assert e.value.status == -2
+            continue
+        got = f(workspace=ws[:less])
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        assert (ws[less:] == 255).all()
+        assert torch.equal(f(workspace=ws[:less], need_db=False, need_dbias=False)[0], want[0])
+        assert torch.equal(f(workspace=ws[:less], need_da=False, need_dbias=False)[1], want[1])
+        with pytest.raises(ozk.OzkError) as e:
+            f(workspace=ws[:g + two - 256])
+        assert e.value.status == -2
+
+
 # ------------------------------------------------------------------ clipping
 def clip_inputs(sizes, kinds, seed, size=1.0):
     rng = np.random.default_rng(seed)
