@@ -2,11 +2,14 @@
 arguments before any HIP call, the binding checks tensors before it calls them."""
 import ctypes
 import os
+import random
 
 import pytest
 import torch
 
 import fp64_gemm_emulation_ozk_amd as ozk
+
+import mx_plan
 
 OK, EINVAL, EWORKSPACE, ERANGE, EUNSUPPORTED = 0, -1, -2, -3, -5
 FAKE = ctypes.c_void_p(0x1000)   # never dereferenced: every call below fails validation
@@ -159,6 +162,51 @@ def test_mxfp4_product_refusals(lib, gated):
             assert call(**args) == EWORKSPACE and call(**args, ws=FAKE) == EWORKSPACE
             assert call(**args, ws=FAKE, wsb=out.value - 1) == EWORKSPACE
             assert call(**args, ws=ODD, wsb=out.value) == EINVAL
+
+
+def test_the_plan_of_the_tests_is_the_library_s(lib):
+    """How often K is split shows in the workspace, over sizes spread over the whole range."""
+    rng = random.Random(5)
+    out = ctypes.c_size_t()
+    sizes = mx_plan.TILES + mx_plan.STREAM + [
+        [int(2 ** rng.uniform(0, top)) for top in (13, 14, 17)] for _ in range(4000)]
+    split = 0
+    for m, n, k in sizes:
+        for gated, f in ((False, lib.ozk_mxfp4_linear_workspace_size),
+                         (True, lib.ozk_mxfp4_gated_workspace_size)):
+            assert f(m, n, k, ctypes.byref(out)) == OK
+            splits = mx_plan.plan(m, n, k, gated)[1]
+            split += splits > 1
+            need = splits * m * n * (8 if gated else 4) if splits > 1 else 0
+            assert out.value == (need + 255) // 256 * 256, (m, n, k, gated, splits)
+    assert split > 1000
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_sizes_take_every_kernel_into_its_steady_state(gated):
+    """Each tile, K whole and split, over more steps than twice what its rings of codes and of
+    scales hold, in odd and even numbers; each width of the streams over more steps a wave than
+    any ring of theirs (three)."""
+    tiles, streams = {}, {}
+    for m, n, k in mx_plan.TILES:
+        shape, splits = mx_plan.plan(m, n, k, gated)
+        steps = mx_plan.steps_of(k)
+        firsts = [steps * s // splits for s in range(splits + 1)]
+        tiles.setdefault((shape, splits > 1), []).extend(
+            (firsts[s] % 2, firsts[s + 1] - firsts[s]) for s in range(splits))
+    assert set(tiles) == {(s, split) for s in ("small", "mid", "large") for split in (False, True)}
+    for (shape, split), runs in tiles.items():
+        around = 2 * max(4 * mx_plan.SCALE_BUFFERS[shape], mx_plan.CODE_STAGES[shape])
+        assert any(count > around for _, count in runs), (shape, split)
+        assert not split or {odd for odd, _ in runs} == {0, 1}
+    for shape in ("mid", "large"):
+        assert {5, 8, 9, 13, 17} <= {count for _, count in tiles[shape, False]}
+    for m, n, k in mx_plan.STREAM:
+        kernel, splits = mx_plan.plan(m, n, k, gated)
+        streams.setdefault(kernel, []).append(-(-(mx_plan.steps_of(k) // splits) // 8))
+    assert set(streams) == {("stream", r, c) for r in (8, 16, 32, 64) for c in (1, 2)}
+    for waves in streams.values():
+        assert 1 in waves and max(waves) > 3
 
 
 def _clip(lib, tensors, max_norm=1.0, norm=FAKE, ws=FAKE, wsb=1 << 20):

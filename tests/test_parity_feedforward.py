@@ -13,6 +13,7 @@ import ozk_inputs
 from oracle import feedforward as ff
 from oracle import layers
 
+import mx_plan
 from gpu_common import announce, device, to_dev
 from test_parity_layers import (TYPES, U32, U64, act_error, assert_near, half_step, host, padded,
                                 tiny)
@@ -311,6 +312,71 @@ def test_product(m, n, k, kind, gated):
     plain = (ozk.ozk_mxfp4_gated(*args, act="silu", dtype=dtype) if gated else
              ozk.ozk_mxfp4_linear(*args, dtype=dtype))
     check_mx(plain, xv, wv, None, "silu" if gated else "none", None, gated)
+
+
+def mx_operand_on_gpu(gen, lines, k):
+    """As mx_operand with scales 2^-1 .. 2^1, a block's of its own: (packed, scales, values)."""
+    kp = ff.padded_k(k)
+    draw = lambda *a: torch.randint(*a, generator=gen, device=device())
+    codes = draw(0, 16, (lines, kp))
+    codes[:, k:] = 0
+    scales = draw(126, 129, (lines, kp // 32))
+    grid = torch.from_numpy(np.concatenate((ff.GRID, -ff.GRID))).to(device())
+    values = grid[codes].view(lines, -1, 32) * torch.exp2((scales - 127).double())[:, :, None]
+    codes = codes.to(torch.uint8)
+    return codes[:, 0::2] | codes[:, 1::2] << 4, scales.to(torch.uint8), values.view(lines, kp)
+
+
+def check_mx_exact(m, n, k, gated):
+    """fp32 sums that are exact in every order, since the magnitudes of their terms, multiples of
+    2^-4, sum to less than 2^20; then fp32 steps, the same here, and one rounding to the type.  The
+    last step before fp16 may be one instruction with the rounding, which then rounds the exact
+    product or sum once; by way of fp32 it is off by 2^-24 and by 2^-11 of what that gives (below
+    fp16's normal range by 2^-25)."""
+    gen = torch.Generator(device()).manual_seed(m * n + k)
+    wide = 2 * n if gated else n
+    xq, xs, xv = mx_operand_on_gpu(gen, m, k)
+    wq, ws, wv = mx_operand_on_gpu(gen, wide, k)
+    wt = wv.t().contiguous()
+    assert torch.matmul(xv.abs(), wt.abs()).amax() < 2.0 ** 20
+    z = torch.matmul(xv, wt).float()
+    f = ozk.ozk_mxfp4_gated if gated else ozk.ozk_mxfp4_linear
+    args = (xq, xs, wq, ws)
+    want = z[:, :n] * z[:, n:] if gated else z
+    for _ in range(2):
+        out = torch.full((m, n + 3), 7.0, device=device())
+        f(*args, act="none", out=out[:, :n])
+        assert torch.equal(out[:, :n], want) and (out[:, n:] == 7.0).all()
+    for dtype in SHORT.values():
+        normal = lambda *s: torch.randn(s, generator=gen, device=device()).to(dtype)
+        bias, res = normal(wide), normal(m, n)
+        zb = z + bias.float()
+        y, last = zb[:, :n].relu(), zb[:, n:] if gated else res.float()
+        join = torch.mul if gated else torch.add
+        kw = {} if gated else dict(residual=res)
+        got = f(*args, bias=bias, act="relu", dtype=dtype, **kw)
+        same = got == join(y, last).to(dtype)
+        if dtype is torch.float16:
+            exact = join(y.double(), last.double())
+            same |= ((got.double() - exact).abs()
+                     <= (2.0 ** -11 * (1 + 2.0 ** -24) + 2.0 ** -24) * exact.abs() + 2.0 ** -25)
+        assert same.all()
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("m,n,k", mx_plan.TILES)
+def test_product_through_the_tiles_rings(m, n, k, gated):
+    """Every tile, K whole and split, over many turns of its rings."""
+    announce(f"mxfp4 tiles m={m} n={n} k={k} gated={gated} {mx_plan.plan(m, n, k, gated)}")
+    check_mx_exact(m, n, k, gated)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("m,n,k", mx_plan.STREAM)
+def test_product_through_the_streams_rings(m, n, k, gated):
+    """Few rows: each number of rows and columns a workgroup takes."""
+    announce(f"mxfp4 stream m={m} n={n} k={k} gated={gated} {mx_plan.plan(m, n, k, gated)}")
+    check_mx_exact(m, n, k, gated)
 
 
 @pytest.mark.parametrize("m", [1, 12, 40, 100, 300])
