@@ -1199,7 +1199,9 @@ def ozk_mxfp4_linear(x: torch.Tensor, scale_x: torch.Tensor, w: torch.Tensor,
                      stream=None) -> torch.Tensor:
     """C = act(X W^T + bias) + residual for m lines X and n lines W in MX FP4 (as
     ozk_mxfp4_quant gives them); C, bias and residual in `dtype` (float32, float16 or bfloat16;
-    the type of `out` where that is given).  residual may be out."""
+    the type of `out` where that is given).  residual may be out.  What X and W hold a line of is
+    whole steps of 256 values, and only that is compared: a shorter line ends in zeros, so that
+    lines of 300 and of 400 values (two steps both) give the products over the first 300."""
     return _mx_product("ozk_mxfp4_linear", ozk_mxfp4_linear_workspace_size, False, x, scale_x, w,
                        scale_w, bias, act, residual, dtype, out, workspace, stream)
 
@@ -1209,7 +1211,7 @@ def ozk_mxfp4_gated(x: torch.Tensor, scale_x: torch.Tensor, w: torch.Tensor,
                     dtype=torch.bfloat16, out: torch.Tensor | None = None,
                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """C = act(X Wg^T + bias[:n]) * (X Wu^T + bias[n:]) for W = [Wg; Wu] of 2 n lines, in MX
-    FP4 as ozk_mxfp4_linear's operands."""
+    FP4 as ozk_mxfp4_linear's operands, of which whole steps are compared here too."""
     return _mx_product("ozk_mxfp4_gated", ozk_mxfp4_gated_workspace_size, True, x, scale_x, w,
                        scale_w, bias, act, None, dtype, out, workspace, stream)
 

@@ -510,7 +510,8 @@ int ozk_layernorm_backward(int64_t rows, int64_t cols, int type, const void* dy,
  * ozk_mxfp4_gated: the first half of a gated feed-forward block, C = act(Zg) * Zu with
  *   Zg = X Wg^T + 1 bias[:n]^T, Zu = X Wu^T + 1 bias[n:]^T; W has 2 n lines, Wg's before Wu's,
  *   bias 2 n entries.
- * Both: 1 <= k <= OZK_MX_MAX_K; a workspace (256-byte aligned) of the size the query returns,
+ * Both: 1 <= k <= OZK_MX_MAX_K, and whole steps are multiplied: lines of fewer values than k
+ *   stand for lines that end in zeros; a workspace (256-byte aligned) of the size the query returns,
  *   which may be 0 (workspace may be NULL then); C overlaps no other operand.  OZK_EUNSUPPORTED
  *   from m = 2^31 or n = 2^30 on, for leading dimensions of codes or scales from 2^24 on, and
  *   where a launch would come to 2^32 threads. */

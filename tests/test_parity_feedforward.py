@@ -447,6 +447,24 @@ def test_product_without_sums(m):
     assert (got == 131072 * 2.25).all()
 
 
+@pytest.mark.parametrize("m", [3, 100])
+def test_product_of_lines_of_fewer_values(m):
+    """Operands of different k in as many steps: the shorter lines end in zeros.  Of different
+    steps they are refused."""
+    announce(f"mxfp4 lines of 300 and 400, m={m}")
+    rng = np.random.default_rng(m)
+    x, w = rng.integers(-3, 4, (m, 300)).astype(float), rng.integers(-3, 4, (70, 400)).astype(float)
+    xq, wq = ozk.ozk_mxfp4_quant(to_dev(x)), ozk.ozk_mxfp4_quant(to_dev(w))
+    want = x @ w[:, :300].T      # the values are codes times 2^-1 .. 2^0, and so are not rounded
+    np.testing.assert_array_equal(host(ozk.ozk_mxfp4_values(*wq, 400)), w)
+    np.testing.assert_array_equal(host(ozk.ozk_mxfp4_linear(*xq, *wq, dtype=torch.float32)), want)
+    got = ozk.ozk_mxfp4_gated(*xq, *wq, act="none", dtype=torch.float32)
+    np.testing.assert_array_equal(host(got), want[:, :35] * want[:, 35:])
+    for f in (ozk.ozk_mxfp4_linear, ozk.ozk_mxfp4_gated):
+        with pytest.raises(ValueError):
+            f(*xq, *ozk.ozk_mxfp4_quant(to_dev(w[:, :256].copy())))
+
+
 def test_product_far_rows():
     """C of more than 2^31 elements, and lines past 2^32 bytes."""
     announce("mxfp4 far rows")
