@@ -1221,11 +1221,27 @@ def ozk_clip_norm_workspace_size(count: int) -> int:
     return _layer_size("ozk_clip_norm_workspace_size", count)
 
 
+def _fills_a_run(t: torch.Tensor) -> bool:
+    """Whether t's elements are one run of memory, whatever the order of its dimensions."""
+    step = 1
+    for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n != 1):
+        if stride != step:
+            return False
+        step *= size
+    return True
+
+
+def _layout(t: torch.Tensor):
+    """The strides that say where elements lie."""
+    return [s for s, n in zip(t.stride(), t.shape) if n != 1] if t.numel() else []
+
+
 def ozk_clip_norm(tensors, max_norm: float, out=None, norm: torch.Tensor | None = None,
                   workspace: torch.Tensor | None = None, stream=None):
-    """(N, outputs): the 2-norm N of all values of a list of contiguous tensors (float64,
-    float32, float16 or bfloat16, any shapes, one device) as a float64 tensor of no dimensions,
-    and the tensors times min(1, max_norm / N): in place, or in the tensors of `out`."""
+    """(N, outputs): the 2-norm N of all values of a list of dense tensors (float64, float32,
+    float16 or bfloat16, any shapes, their dimensions in any order in memory, one device) as a
+    float64 tensor of no dimensions, and the tensors times min(1, max_norm / N): in place, or in
+    the tensors of `out`, each with its tensor's strides."""
     tensors = list(tensors)
     outs = tensors if out is None else list(out)
     if not tensors:
@@ -1236,18 +1252,23 @@ def ozk_clip_norm(tensors, max_norm: float, out=None, norm: torch.Tensor | None 
     first = tensors[0]
     on_gpu = isinstance(first, torch.Tensor) and first.is_cuda
     index = first.get_device() if on_gpu else None   # -1 of a host tensor
+    ordered = True   # every tensor's dimensions are in memory as they are written
     for t in tensors if outs is tensors else tensors + outs:
         if not isinstance(t, torch.Tensor) or t.get_device() != index or not t.is_contiguous():
             if not isinstance(t, torch.Tensor) or not t.is_cuda:
                 raise TypeError("tensors must be CUDA/HIP tensors")
-            if not t.is_contiguous():
-                raise ValueError("tensors must be contiguous")
-            raise ValueError(f"a tensor is on {t.device}, expected {first.device}")
+            if t.get_device() != index:
+                raise ValueError(f"a tensor is on {t.device}, expected {first.device}")
+            if not _fills_a_run(t):
+                raise ValueError("tensors must be dense: one run of memory each")
+            ordered = False
     if outs is not tensors:
         for t, o in zip(tensors, outs):
             if o.dtype is not t.dtype or not o.is_same_size(t):
                 raise ValueError(f"an output is {o.dtype} {tuple(o.shape)}, its tensor {t.dtype} "
                                  f"{tuple(t.shape)}")
+            if not ordered and _layout(o) != _layout(t):
+                raise ValueError(f"an output has strides {o.stride()}, its tensor {t.stride()}")
     sizes = array("q", [t.numel() for t in tensors])
     try:
         kinds = array("i", [_TYPES[t.dtype] for t in tensors])

@@ -739,6 +739,37 @@ def test_clip_norm_unaligned():
         assert torch.equal(buf[mask], keep[mask])
 
 
+def test_clip_norm_of_other_orders():
+    """Dense tensors whose dimensions lie in another order, as gradients of transposed weights: in
+    place and into outputs of the same strides; outputs of others and gaps are refused."""
+    announce("clip other orders")
+    rng = np.random.default_rng(3)
+    base = [to_dev(rng.standard_normal(s)).to(d) for s, d in (
+        ((130, 70), torch.float32), ((3, 5, 7, 11), torch.bfloat16), ((6, 1, 9), torch.float64),
+        ((257,), torch.float16))]
+    views = [base[0].t(), base[1].permute(0, 3, 1, 2), base[2].permute(2, 1, 0), base[3]]
+    assert not any(v.is_contiguous() for v in views[:3])
+    norm, want = ozk.ozk_clip_norm(base, 1.0, out=[torch.empty_like(b) for b in base])
+    outs = [torch.empty_like(v) for v in views]      # empty_like keeps the strides
+    for o, v in zip(outs, views):
+        assert o.stride() == v.stride()
+    got, _ = ozk.ozk_clip_norm(views, 1.0, out=outs)
+    assert torch.equal(got, norm)
+    moved = [want[0].t(), want[1].permute(0, 3, 1, 2), want[2].permute(2, 1, 0), want[3]]
+    assert all(torch.equal(o, w) for o, w in zip(outs, moved))
+    for bad in (dict(tensors=views, out=[torch.empty_like(v).contiguous() for v in views]),
+                dict(tensors=base[:1], out=[torch.empty(70, 130, device=device()).t()]),
+                dict(tensors=[base[0][:, :69]]), dict(tensors=[base[0].t()[:69, ::2]]),
+                dict(tensors=[base[0][:1].expand(4, 70)])):
+        with pytest.raises(ValueError):
+            ozk.ozk_clip_norm(**bad, max_norm=1.0)
+    none = [base[0][:0].t(), torch.empty(70, 0, device=device())]   # empty: any strides
+    ozk.ozk_clip_norm(views + none[:1], 1.0, out=outs + none[1:])
+    assert all(torch.equal(o, w) for o, w in zip(outs, moved))
+    ozk.ozk_clip_norm(views, 1.0)
+    assert all(torch.equal(b, w) for b, w in zip(base, want))
+
+
 def test_clip_norm_range():
     """Squares past fp64's range on either side; Inf and NaN leave the values as they are."""
     announce("clip range")
