@@ -11,7 +11,8 @@
 // 16 bytes in the first pass, where eight took longer (166 -> 169 us over 1.0 GB of bf16), and
 // eight in the second (406 -> 380 us with its writes of as much).  The second pass's loads and
 // stores are marked as not to be read soon: the whole of 1.1 GB 581 -> 541 us, 134 MB 84 -> 68,
-// 25 MB 22.5 -> 19.2; with a reader of the outputs behind 761 -> 713, 98 -> 101 and 32.8 -> 32.0.
+// 25 MB 22.5 -> 19.2; with a reader of the outputs behind 761 -> 713, 98 -> 101 and 32.8 -> 32.0
+// (tensors at odd elements, 1.0 GB: bf16 630 -> 622, fp32 604 -> 582, fp64 614 -> 592).
 #include "ozk_internal.h"
 #include "rows.h"
 
@@ -142,20 +143,20 @@ __global__ __launch_bounds__(kThreads) void clip_sums_kernel(ClipTable A,
   }
 }
 
-// M / N as one number, and for fp64 values as step coef step: where the quotient is subnormal, so
-// that it holds few bits or none, step is 2^-512 and coef M 2^512 / (N 2^-512); else step is 1,
-// which changes nothing.  A value times 2^-512 loses bits only below 2^-510, where its output is 0.
-// The other types' outputs are below 2^-894 there, 0 in any of them.
+// M / N as one number, and for fp64 values where it is subnormal, so that it holds few bits or
+// none, as 2^-512 coef 2^-512, coef = M 2^512 / (N 2^-512), or 0 for coef elsewhere.  A value times
+// 2^-512 loses bits only below 2^-510, where its output is 0.  The other types' outputs are below
+// 2^-894 there, 0 in any of them.
 struct Factor {
-  double whole, step, coef;
+  double whole, coef;
 };
 __device__ __forceinline__ Factor factor_of(double max_norm, double total) {
   const double c = max_norm / total;
-  if (c >= 0x1p-1022) return {c, 1.0, c};
-  return {c, 0x1p-512, (max_norm * 0x1p512) / (total * 0x1p-512)};
+  return {c, c < 0x1p-1022 ? (max_norm * 0x1p512) / (total * 0x1p-512) : 0.0};
 }
 
-template <typename T>
+// kSteps: the factor in its parts (taken so for all values, 1.0 GB of fp64 takes 519 us for 516).
+template <typename T, bool kSteps = false>
 __device__ __forceinline__ void scale_chunk(const ClipTable& A, int t, int chunk,
                                             Factor by) {
   T* out = (T*)A.out[t];
@@ -166,7 +167,8 @@ __device__ __forceinline__ void scale_chunk(const ClipTable& A, int t, int chunk
 #pragma unroll
         for (int u = 0; u < Vec<T>::N; ++u) {
           // to 16 bits by way of fp32, which is off a direct rounding by 2^-24 at most
-          if constexpr (sizeof(T) == 8) o[u] = v[u] * by.step * by.coef * by.step;
+          if constexpr (kSteps) o[u] = v[u] * 0x1p-512 * by.coef * 0x1p-512;
+          else if constexpr (sizeof(T) == 8) o[u] = v[u] * by.whole;
           else o[u] = (T)(float)((double)v[u] * by.whole);
         }
         if (count == Vec<T>::N) {
@@ -205,12 +207,15 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable A,
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
   const bool clips = total > max_norm && !__builtin_isinf(total);
   if (!clips && in_place) return;
-  const Factor by = clips ? factor_of(max_norm, total) : Factor{1.0, 1.0, 1.0};
+  const Factor by = clips ? factor_of(max_norm, total) : Factor{1.0, 0.0};
   for (int c = A.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
     const int t = tensor_of(A, c);
     const int chunk = c - A.first[t];
     switch (A.type[t]) {
-      case OZK_F64: scale_chunk<double>(A, t, chunk, by); break;
+      case OZK_F64:
+        if (by.coef == 0.0) scale_chunk<double>(A, t, chunk, by);
+        else scale_chunk<double, true>(A, t, chunk, by);
+        break;
       case OZK_F32: scale_chunk<float>(A, t, chunk, by); break;
       case OZK_F16: scale_chunk<f16_t>(A, t, chunk, by); break;
       default: scale_chunk<bf16_t>(A, t, chunk, by); break;
