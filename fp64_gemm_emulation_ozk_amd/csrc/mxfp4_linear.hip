@@ -455,11 +455,13 @@ struct Place {
 // consecutive outputs each; a phase's groups of rows are finished together, for their
 // instructions' latencies, and the next phase's residuals asked for meanwhile.  The phases are a
 // loop, through which the blocks move down: written out they would not fit the instruction cache.
-// A residual is read once and marked so; without one the outputs are marked as not to be read
-// soon (bf16, cold, and with a reader of the outputs behind: 4096 x 16384 x 4096 with a residual
-// 191 -> 174 us and 219 -> 205, with gelu too 194 -> 190 and 227 -> 215; gelu alone 175 -> 172
-// and 208 -> 205; gated 147 -> 139 and 159 -> 153.  Outputs marked beside a residual: 179 and
-// 211, 194 and 228).
+// A residual is read once and marked so (4096 x 16384 x 4096, gelu, bf16, cold, and with a reader of
+// the outputs behind: 231 -> 217 us and 280 -> 266, rows at odd elements 207 -> 199 and 260 -> 252;
+// fp32 325 -> 297 and 404 -> 389).  Outputs are marked as not to be read soon behind a gate, where a
+// wave's rows are half lines of memory, if they have 16 bits and rows at multiples of 16 bytes:
+// 8192 x 2 4096 x 1024, bf16, silu 57.5 us so, else 61.9, with the quantiser behind 82.5 and 87 cold;
+// 4096 x 2 8192 x 4096 140 and 143, 172 and 178.  Rows at odd elements 147 marked and 140 not,
+// fp32 outputs 169 and 149 (cold 192 and 158); without a gate the two are the same.
 template <typename TL, bool kGated, typename O, int NI>
 __device__ __forceinline__ void put_tile(const MxEpilogue<O>& E, v4f (&acc)[NI][TL::TJ],
                                          int64_t wrow0, int64_t wcol0, int lane, float* mine,
@@ -483,6 +485,8 @@ __device__ __forceinline__ void put_tile(const MxEpilogue<O>& E, v4f (&acc)[NI][
   const int lrow = lane / kLanes, lcol = 8 * (lane % kLanes);
   const int64_t col = wcol0 + lcol;
   const bool whole = col + 8 <= E.n;
+  const bool marked = kGated && sizeof(O) == 2 &&
+                      (reinterpret_cast<uintptr_t>(E.c) | (uintptr_t)E.ldc * sizeof(O)) % 16 == 0;
   // every row and column of the wave's is C's (the usual case): no checks
   const bool inside = wrow0 + 16 * NI <= E.m && wcol0 + kWaveCols <= E.n;
   const float* const from = mine + lrow * TL::kPitch + lcol;
@@ -543,18 +547,26 @@ __device__ __forceinline__ void put_tile(const MxEpilogue<O>& E, v4f (&acc)[NI][
 #pragma unroll
         for (int u = 0; u < kIters * 8; ++u) z[u] += (float)res[u / 8][u % 8];
       if (ph + 1 < kPhases) ask(row0 + TL::kPhase * 16);
+      V8 o[kIters];
 #pragma unroll
-      for (int it = 0; it < kIters; ++it) {
-        V8 o;
+      for (int it = 0; it < kIters; ++it)
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           float y = z[8 * it + u];
           if constexpr (kGated) y *= up[8 * it + u];
-          o[u] = (O)y;
+          o[it][u] = (O)y;
         }
-        V8* const to = reinterpret_cast<V8*>(E.c + (row0 + it * kRows + lrow) * E.ldc + col);
-        if (!kGated && E.residual) *to = o;
-        else __builtin_nontemporal_store(o, to);
+      const auto to = [&](int it) {
+        return reinterpret_cast<V8*>(E.c + (row0 + it * kRows + lrow) * E.ldc + col);
+      };
+      if (marked) {
+        asm volatile("");   // without these the compiler makes unmarked stores of both branches
+#pragma unroll
+        for (int it = 0; it < kIters; ++it) __builtin_nontemporal_store(o[it], to(it));
+        asm volatile("");
+      } else {
+#pragma unroll
+        for (int it = 0; it < kIters; ++it) *to(it) = o[it];
       }
     } else {
 #pragma unroll 1

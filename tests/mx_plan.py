@@ -34,11 +34,13 @@ def plan(m, n, k, gated):
     return best[1], best[2]
 
 
-# Tiles: from one ring's steps to many times around it, odd and even, ragged everywhere; K whole,
-# then split, with odd first steps among the splits.
+# Tiles: from one ring's steps to many times around it, odd and even, ragged everywhere, and with
+# rows of 16-bit outputs at multiples of 16 bytes; K whole, then split, with odd first steps among
+# the splits.
 TILES = ([(m, n, 256 * steps - 57) for m, n in ((2900, 4501), (1500, 1300), (1025, 1030))
           for steps in (5, 8, 9, 13, 17, 33)]
          + [(2900, 300, 6343), (65, 4500, 6343)]
+         + [(2900, 4504, 2247), (1500, 1304, 2247), (1025, 1032, 2247)]
          + [(513, 4500, 18119), (2050, 130, 32455), (130, 3001, 19143), (130, 4500, 32455),
             (65, 4500, 12999), (130, 2050, 12999), (2050, 2050, 17000), (1001, 513, 30001),
             (100, 75, 60001)])
