@@ -73,6 +73,7 @@ __device__ __forceinline__ void each_vector(const T* x, int64_t size, int chunk,
   typedef typename Vec<T>::type V;
   // which chunk is the last is compared in 32 bits: of a 64-bit comparison of uniform values this
   // compiler (clang of ROCm 7.2) took the branch from vcc and the selected count from a stale scc
+  // (in the code of the library's other kernels every select and branch follows what sets its scc)
   constexpr int most = chunk_bytes(kV) / (int)sizeof(T);
   const int64_t begin = (int64_t)chunk * most;
   const T* p = x + begin;

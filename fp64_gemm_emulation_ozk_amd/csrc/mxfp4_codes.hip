@@ -210,7 +210,7 @@ __global__ __launch_bounds__(512) void mxfp4_cols_kernel(int64_t rows, int64_t c
   typedef T V __attribute__((ext_vector_type(kC), aligned(sizeof(T))));
   constexpr int kLines = 64 * kC;
   __shared__ uint4 box[kLines * 8];
-  __shared__ uint8_t sbox[kLines][8];
+  __shared__ __attribute__((aligned(8))) uint8_t sbox[kLines][8];   // read as words of 8
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t id = blockIdx.x, step = id / tiles;
