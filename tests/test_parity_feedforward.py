@@ -12,6 +12,7 @@ import fp64_gemm_emulation_ozk_amd as ozk
 import ozk_inputs
 from oracle import feedforward as ff
 from oracle import layers
+from oracle import rns
 
 import mx_plan
 from gpu_common import announce, device, to_dev
@@ -519,6 +520,29 @@ def test_dgemm_gated(m, n, k, r, scaling):
         assert_near(host(c[:, :n]), y * up, tol, name)
         assert (z[:, 2 * n:] == 5.0).all() and (c[:, n:] == 5.0).all()
         assert torch.equal(ozk.ozk_dgemm_gated(*args, **kw), c[:, :n])   # Z not kept
+
+
+@pytest.mark.parametrize("r", range(1, 21))
+def test_dgemm_gated_every_r(r):
+    """The reconstruction of both projections and of both gradients is compiled for every number
+    of moduli: the bits of ozk_dgemm_ex.  Without an activation G is dC times the other half of Z,
+    rounded once."""
+    size = 300
+    while rns.budget_q(r) - rns.ceil_log2(size) < 4:
+        size //= 2
+    m, n, k = size, max(size // 2, 1), max(size - 3, 1)
+    announce(f"dgemm gated r={r} m={m} n={n} k={k}")
+    a, b = [to_dev(x) for x in ozk_inputs.gemm_operands(m, 2 * n, k, seed=r, dist="phi", phi=1.0)]
+    dc = to_dev(np.random.default_rng(r).standard_normal((m, n)))
+    for scaling in ("max", "norm"):
+        z = torch.empty((m, 2 * n), dtype=torch.float64, device=device())
+        c = ozk.ozk_dgemm_gated(a, b, r, act="none", scaling=scaling, preact=z)
+        assert torch.equal(z, ozk.ozk_dgemm_ex(a, b, r, scaling))
+        assert torch.equal(c, z[:, :n] * z[:, n:])
+        da, db, _ = ozk.ozk_dgemm_gated_grad(dc, a, b, r, z, act="none", scaling=scaling)
+        g = torch.cat((dc * z[:, n:], dc * z[:, :n]), 1)
+        assert torch.equal(da, ozk.ozk_dgemm_ex(g, b.t().contiguous(), r, scaling))
+        assert torch.equal(db, ozk.ozk_dgemm_ex(a.t().contiguous(), g, r, scaling))
 
 
 def test_dgemm_gated_edges():
