@@ -235,8 +235,13 @@ def _check(t: torch.Tensor, dtype, name: str, ndim: int = 2):
         raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
     if t.dim() != ndim:
         raise ValueError(f"{name} must be {ndim}-D")
-    if ndim == 2 and t.numel() > 0 and t.stride(1) != 1:
-        raise ValueError(f"{name} must be row-major with unit column stride")
+    if ndim == 2 and t.numel() > 0:
+        if t.stride(1) != 1:
+            raise ValueError(f"{name} must be row-major with unit column stride")
+        # rows that overlap (an expanded or unfolded view) have no leading dimension the library
+        # takes
+        if t.stride(0) < t.shape[1] and t.shape[0] > 1:
+            raise ValueError(f"{name}'s rows overlap")
     if ndim == 1 and t.numel() > 1 and t.stride(0) != 1:
         raise ValueError(f"{name} must be contiguous")
 
@@ -681,14 +686,11 @@ def ozk_int4int8gemm_fp4awe(a: torch.Tensor, b: torch.Tensor, out: torch.Tensor 
 
 # ------------------------------------------------------------ layers around the products
 def _check_rows(t: torch.Tensor, dtype, name: str):
-    """A matrix operand of the layer operators.  Rows that overlap (an expanded or unfolded
-    view) have no leading dimension the library takes."""
+    """A matrix operand of the layer operators: what holds is found out at once."""
     if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.dim() == 2
             and t.is_contiguous()):
         return
     _check(t, dtype, name)
-    if t.shape[0] > 1 and t.shape[1] > 0 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name}'s rows overlap")
 
 
 def _check_like(t: torch.Tensor | None, shape: tuple, dtype, name: str, device):

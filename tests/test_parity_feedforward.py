@@ -1124,6 +1124,31 @@ def test_given_stream_and_workspace():
             assert e.value.status == -2
 
 
+def test_rows_that_overlap_are_refused():
+    """By every binding of a matrix: as leading dimension of an expanded row the library would take
+    its length, and read past its end."""
+    announce("rows that overlap")
+    row = torch.zeros(1, 8, dtype=torch.float64, device=device())
+    a, good = row.expand(8, 8), torch.zeros(8, 8, dtype=torch.float64, device=device())
+    slid = torch.zeros(40, dtype=torch.float64, device=device()).unfold(0, 8, 4)[:8]
+    i8 = torch.zeros(1, 8, dtype=torch.int8, device=device()).expand(8, 8)
+    for bad in (a, slid, row[:, :1].expand(8, 1)):
+        for f in (lambda t: ozk.ozk_dgemm(t, good[:t.shape[1]], 14),
+                  lambda t: ozk.ozk_dgemm(good[:, :8], t, 14),
+                  lambda t: ozk.ozk_dgemm_ex(t, good[:t.shape[1]], 14),
+                  lambda t: ozk.ozk_dgemv(t, good[:t.shape[1], :2], 14),
+                  lambda t: ozk.ozk_dgemv(good, t, 14), lambda t: ozk.ozk_deconstruct(t, 0, 14),
+                  lambda t: ozk.ozk_dgemm_gated(t, good[:t.shape[1]], 14),
+                  lambda t: ozk.ozk_mxfp4_quant(t), lambda t: ozk.ozk_layernorm(t)):
+            with pytest.raises(ValueError):
+                f(bad)
+    for f in (ozk.ozk_int8gemm_fp4limb, ozk.ozk_int8gemm_fp4awe, ozk.ozk_int4int8gemm_fp4awe):
+        with pytest.raises(ValueError):
+            f(i8, i8.contiguous())
+        with pytest.raises(ValueError):
+            f(i8.contiguous(), i8)
+
+
 def test_binding_refusals():
     """Shapes, types, strides and devices the binding refuses before any call."""
     announce("feed-forward binding refusals")
