@@ -236,7 +236,7 @@ def _check(t: torch.Tensor, dtype, name: str, ndim: int = 2):
     if t.dim() != ndim:
         raise ValueError(f"{name} must be {ndim}-D")
     if ndim == 2 and t.numel() > 0:
-        if t.stride(1) != 1:
+        if t.stride(1) != 1 and t.shape[1] > 1:
             raise ValueError(f"{name} must be row-major with unit column stride")
         # rows that overlap (an expanded or unfolded view) have no leading dimension the library
         # takes

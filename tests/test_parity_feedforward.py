@@ -1124,6 +1124,20 @@ def test_given_stream_and_workspace():
             assert e.value.status == -2
 
 
+def test_matrices_of_one_column():
+    """Their column stride says nothing: a transposed row is as good as a column."""
+    announce("one column of any stride")
+    rng = np.random.default_rng(2)
+    a, b = to_dev(rng.standard_normal((1, 40))).t(), to_dev(rng.standard_normal((1, 12)))
+    assert a.shape == (40, 1) and a.stride(1) == 40
+    dc, z = to_dev(rng.standard_normal((40, 6))), to_dev(rng.standard_normal((40, 12)))
+    for f in (lambda a: ozk.ozk_dgemm_gated(a, b, 14),
+              lambda a: ozk.ozk_dgemm_gated_grad(dc, a, b, 14, z)[1],
+              lambda a: ozk.ozk_dgemm_ex(a, b, 14, "norm"),
+              lambda a: ozk.ozk_mxfp4_quant(a)[0], lambda a: ozk.ozk_mxfp4_quant(a, 1)[1]):
+        assert torch.equal(f(a), f(a.clone(memory_format=torch.contiguous_format).view(-1)[:, None]))
+
+
 def test_rows_that_overlap_are_refused():
     """By every binding of a matrix: as leading dimension of an expanded row the library would take
     its length, and read past its end."""
