@@ -715,7 +715,9 @@ __global__ __launch_bounds__(64 * TL::NW) void mxfp4_tile_kernel(int steps, Line
 // holds, and per step one barrier, one set of fragment reads and one run of MFMAs.  A pair of
 // waves shares the outputs of a wave and splits each step's K, a block of every two; the sums of
 // both meet in LDS at the end.  Behind the barrier of step t the wave reads step t + 1 and asks
-// for step t + S while step t's MFMAs run from registers.
+// for step t + S while step t's MFMAs run from registers.  (The waits, barriers and the exchange of
+// halves are small_product's in tile_walk.h, with scales beside the codes: a fault in one is to be
+// looked for in the other.)
 template <typename O, bool kGated, typename TL, int kBufs>
 __global__ __launch_bounds__(64 * TL::NW) void mxfp4_small_kernel(int steps, Lines X, Lines W,
                                                                   MxEpilogue<O> E, int tiles_m,

@@ -165,7 +165,7 @@ struct Walk {
 // Behind the barrier of step t the wave reads step t + 1 and asks for step t + S while step
 // t's MFMAs run from registers.
 // Wave kh of a pair ends with row blocks kh TI / 2 .. of the wave's tile in `own`, and all waves
-// past their last use of the ring.
+// past their last use of the ring.  mxfp4_small_kernel (mxfp4_linear.hip) keeps the same order.
 template <typename TL>
 __device__ __forceinline__ void small_product(const Walk<TL>& W, v4i (&own)[TL::TI / 2][TL::TJ]) {
   constexpr int BM = TL::BM, TI = TL::TI, TJ = TL::TJ, S = TL::S, L = TL::kLoads;
